@@ -37,6 +37,8 @@ EXPORTS = [
     "gqa_decode_noalloc", "gqa_decode_noalloc_scratch_bytes",
     "gqa_decode_host", "gqa_decode_paged_fp8", "gqa_decode_paged_fp8_dev_scales", "gqa_decode_paged", "gqa_decode_paged_ex",
     "gqa_decode_paged_num_splits", "gqa_decode_paged_workspace_bytes", "gqa_decode_paged_dev_scales",
+    "gqa_decode_paged_int4", "gqa_decode_paged_int4_num_splits", "gqa_decode_paged_int4_workspace_bytes",
+    "gqa_paged_append", "gqa_paged_gather",
     "gqa_paged_gather_fp8", "gqa_fp8_e4m3fn_to_f32", "gqa_device_status", "gqa_set_wait_limit_ns",
     "gqa_debug_set_fault_mode", "gqa_debug_set_kernel_events", "gqa_debug_read_stream",
     "gqa_decode_paged_engine", "gqa_debug_set_paged_engine",
@@ -101,6 +103,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gqa_decode_paged_num_splits.argtypes = [i] * 8
     lib.gqa_decode_paged_workspace_bytes.restype = sz
     lib.gqa_decode_paged_workspace_bytes.argtypes = [i] * 9
+    ll = ctypes.c_longlong
+    lib.gqa_decode_paged_int4.restype = st
+    lib.gqa_decode_paged_int4.argtypes = [vp] * 8 + [i] * 8 + [f, i, vp, sz, vp]
+    lib.gqa_decode_paged_int4_num_splits.restype = i
+    lib.gqa_decode_paged_int4_num_splits.argtypes = [i] * 7
+    lib.gqa_decode_paged_int4_workspace_bytes.restype = sz
+    lib.gqa_decode_paged_int4_workspace_bytes.argtypes = [i] * 8
+    lib.gqa_paged_append.restype = st
+    lib.gqa_paged_append.argtypes = ([vp, ll, vp, vp, ll, vp, ll, i, vp, vp, vp, f, f, vp, vp, i, vp, vp, vp, vp]
+                                     + [i] * 11 + [vp])
+    lib.gqa_paged_gather.restype = st
+    lib.gqa_paged_gather.argtypes = [i, vp, vp, vp, f, f, vp, vp, i, vp, vp, vp, vp, vp] + [i] * 7 + [vp]
     lib.gqa_paged_gather_fp8.restype = st
     lib.gqa_paged_gather_fp8.argtypes = [vp, vp, vp, vp] + [i] * 7 + [vp]
     lib.gqa_fp8_e4m3fn_to_f32.restype = st
@@ -462,6 +476,222 @@ def gqa_decode_paged_num_splits(B, Sq, Hq, Hkv, D, kv_dtype, page_size, pages_pe
 def gqa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D, kv_dtype, page_size, pages_per_req, num_splits=0) -> int:
     return load_library().gqa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D, kv_dtype, page_size, pages_per_req,
                                                            num_splits)
+
+
+# ---------------------------------------------------------------------------
+# the paged cache: 4-bit decode, append, gather
+# ---------------------------------------------------------------------------
+GQA_KV_INT4 = 3
+
+
+def _on_device_of(t: torch.Tensor, stream):
+    """(guard, stream pointer) of a call on t's device: the stream given, or that device's current one.  The guard is
+    entered around the call where another device is current."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    s = torch.cuda.current_stream(t.device) if stream is None else stream
+    if s.device != t.device:
+        raise ValueError(f"stream on {s.device}, tensors on {t.device}")
+    guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return guard, s.cuda_stream
+
+
+def _guarded(guard, fn, *args):
+    if guard is None:
+        return fn(*args)
+    with guard:
+        return fn(*args)
+
+
+def _need_on(t: torch.Tensor, name: str, dtype, like: torch.Tensor, shape=None):
+    """As _need_shape, for an argument that must be there; shape None: any."""
+    if t.dtype != dtype or t.device != like.device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: expected contiguous {dtype}{'' if shape is None else ' ' + str(tuple(shape))} on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cache(fn: str, k_pool, v_pool, kv_params, page_table, seq_lens, k_scales, v_scales):
+    """Checks the cache's tensors against each other; returns (kv_dtype, num_pages, page_size, Hkv, D, B,
+    pages_per_req, n_scales)."""
+    if k_pool.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"{fn}: pools [num_pages,page_size,Hkv,D or D/2], page_table 2-D")
+    num_pages, page_size, Hkv, width = k_pool.shape
+    kvd, D = (_kv_dtype(k_pool), width) if kv_params is None else (GQA_KV_INT4, 2 * width)
+    if kv_params is not None:
+        _need_on(k_pool, "k_pool", torch.uint8, k_pool)
+        _need_on(kv_params, "kv_params", torch.float16, k_pool, (num_pages, page_size, Hkv, 4))
+    _need_on(k_pool, "k_pool", k_pool.dtype, k_pool)
+    _need_on(v_pool, "v_pool", k_pool.dtype, k_pool, k_pool.shape)
+    _need_on(page_table, "page_table", torch.int32, k_pool)
+    B, pages_per_req = page_table.shape
+    _need_on(seq_lens, "seq_lens", torch.int32, k_pool, (B,))
+    n_scales = 0
+    if k_scales is not None or v_scales is not None:
+        if k_scales is None or v_scales is None:
+            raise ValueError(f"{fn}: k_scales and v_scales go together")
+        n_scales = k_scales.numel()
+        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _need_on(t, n, torch.float32, k_pool)
+        if v_scales.numel() != n_scales:
+            raise ValueError(f"{fn}: k_scales and v_scales need the same number of values")
+    return kvd, num_pages, page_size, Hkv, D, B, pages_per_req, n_scales
+
+
+def gqa_decode_paged_int4(q, k_pool, v_pool, kv_params, page_table, seq_lens, out=None, lse=None, scale=None,
+                          num_splits=0, workspace=None, stream=None, with_lse=True):
+    """Paged decode over every token of each request from a 4-bit cache.
+
+    q [B,Sq,Hq,D] bf16; pools uint8 [num_pages, page_size, Hkv, D/2] (element 2i in the low half of byte i);
+    kv_params fp16 [num_pages, page_size, Hkv, 4] (K scale, K zero, V scale, V zero; value = code * scale + zero);
+    page_table int32 [B, pages_per_req]; seq_lens int32 [B].  num_splits 0 = automatic; workspace: optional CUDA uint8
+    tensor of gqa_decode_paged_int4_workspace_bytes.
+    Returns (out [B,Sq,Hq,D] bf16, lse [B,Hq,Sq] fp32 or None).
+    """
+    lib = _lib_handle or load_library()
+    guard, cs = _on_device_of(q, stream)
+    if kv_params is None or q.dim() != 4:
+        raise ValueError("gqa_decode_paged_int4: q [B,Sq,Hq,D] and kv_params are needed")
+    _, num_pages, page_size, Hkv, D, B, ppr, _ = _cache("gqa_decode_paged_int4", k_pool, v_pool, kv_params,
+                                                        page_table, seq_lens, None, None)
+    _, Sq, Hq, _ = q.shape
+    _need_on(q, "q", torch.bfloat16, k_pool, (B, Sq, Hq, D))
+    if out is None:
+        out = torch.empty_like(q)
+        if stream is not None:
+            out.record_stream(stream)
+    else:
+        _need_on(out, "out", torch.bfloat16, q, q.shape)
+    if lse is not None:
+        _need_on(lse, "lse", torch.float32, q, (B, Hq, Sq))
+    elif with_lse:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        if stream is not None:
+            lse.record_stream(stream)
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != q.device:
+            raise ValueError(f"workspace: expected a contiguous tensor on {q.device}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = _guarded(guard, lib.gqa_decode_paged_int4, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+                  kv_params.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _data(lse), B, Sq,
+                  Hq, Hkv, D, page_size, ppr, num_pages, _scale_arg(scale), int(num_splits), _data(workspace),
+                  ws_bytes, cs)
+    _check(st, "gqa_decode_paged_int4")
+    return out, lse
+
+
+def gqa_decode_paged_int4_num_splits(B, Sq, Hq, Hkv, D, page_size, pages_per_req) -> int:
+    n = load_library().gqa_decode_paged_int4_num_splits(B, Sq, Hq, Hkv, D, page_size, pages_per_req)
+    if n < 0:
+        raise GQAError(-n, "gqa_decode_paged_int4_num_splits")
+    return n
+
+
+def gqa_decode_paged_int4_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, pages_per_req, num_splits=0) -> int:
+    return int(load_library().gqa_decode_paged_int4_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, pages_per_req,
+                                                                    int(num_splits)))
+
+
+def _heads_of(fn: str, t, name: str, T, heads, D, like):
+    """Token stride of t [T, heads, D] bf16 whose heads are contiguous."""
+    if t.dtype != torch.bfloat16 or t.device != like.device or t.dim() != 3 or t.shape != (T, heads, D):
+        raise ValueError(f"{fn}: {name} must be bfloat16 [{T},{heads},{D}] on {like.device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    s0, s1, s2 = t.stride()
+    if T and (s2 != 1 or (heads > 1 and s1 != D)):
+        raise ValueError(f"{fn}: the heads of a token of {name} must be contiguous")
+    return s0 if T > 1 else heads * D
+
+
+def gqa_paged_append(k, v, k_pool, v_pool, page_table, seq_lens, cu_tokens=None, q=None, q_out=None, cos_sin=None,
+                     interleaved=False, kv_params=None, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None,
+                     stream=None):
+    """Writes T new tokens' k and v [T,Hkv,D] bf16 into a paged cache, k (and q [T,Hq,D]) rotated on the way.
+
+    The token stride of q, k and v is free (slices of a fused projection).  cu_tokens int32 [B+1]: request b owns rows
+    cu_tokens[b] .. cu_tokens[b+1]-1 (None: T / B each); seq_lens int32 [B] counts the new tokens too.  cos_sin fp32
+    [max_pos, rot_dim]: cosines, then sines (None: no rotation); interleaved: neighbouring pairs instead of i and
+    i + rot_dim / 2.  Pools bf16, uint8 (E4M3FN codes), int8, or uint8 of 4-bit codes with kv_params; 8-bit pools take
+    k_scale / v_scale or CUDA fp32 k_scales / v_scales of 1 or Hkv values.
+    Returns q_out (bf16 [T,Hq,D], allocated when None) or None without q.
+    """
+    lib = _lib_handle or load_library()
+    fn = "gqa_paged_append"
+    guard, cs = _on_device_of(k, stream)
+    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, k_pool, v_pool, kv_params, page_table, seq_lens,
+                                                                 k_scales, v_scales)
+    T = k.shape[0]
+    k_stride = _heads_of(fn, k, "k", T, Hkv, D, k_pool)
+    v_stride = _heads_of(fn, v, "v", T, Hkv, D, k_pool)
+    Hq = q_stride = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        q_stride = _heads_of(fn, q, "q", T, Hq, D, k_pool)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            if stream is not None:
+                q_out.record_stream(stream)
+        else:
+            _need_on(q_out, "q_out", torch.bfloat16, k_pool, (T, Hq, D))
+    elif q_out is not None:
+        raise ValueError(f"{fn}: q_out without q")
+    if cu_tokens is not None:
+        _need_on(cu_tokens, "cu_tokens", torch.int32, k_pool, (B + 1,))
+    rot_dim = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError(f"{fn}: cos_sin must be [max_pos, rot_dim]")
+        _need_on(cos_sin, "cos_sin", torch.float32, k_pool)
+        max_pos, rot_dim = cos_sin.shape
+    st = _guarded(guard, lib.gqa_paged_append, _data(q), q_stride, _data(q_out), k.data_ptr(), k_stride, v.data_ptr(),
+                  v_stride, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params), float(k_scale),
+                  float(v_scale), _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(),
+                  seq_lens.data_ptr(), _data(cu_tokens), _data(cos_sin), rot_dim, max_pos, int(bool(interleaved)), T,
+                  B, Hq, Hkv, D, page_size, ppr, num_pages, cs)
+    _check(st, fn)
+    return q_out
+
+
+def gqa_paged_gather(k_pool, v_pool, page_table, seq_lens, k_out=None, v_out=None, rows=None, starts=None,
+                     kv_params=None, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None, stream=None):
+    """Tokens starts[b] .. seq_lens[b]-1 of each request of a paged cache, dense: k_out, v_out [B,rows,Hkv,D] bf16.
+
+    Output rows past a request's tokens are left as they were.  k_out and v_out None: allocated with zeros, for which
+    rows is needed.  Pools, scales and kv_params as gqa_paged_append; starts int32 [B] (None: 0).
+    Returns (k_out, v_out).
+    """
+    lib = _lib_handle or load_library()
+    fn = "gqa_paged_gather"
+    guard, cs = _on_device_of(k_pool, stream)
+    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, k_pool, v_pool, kv_params, page_table, seq_lens,
+                                                                 k_scales, v_scales)
+    if (k_out is None) != (v_out is None):
+        raise ValueError(f"{fn}: k_out and v_out go together")
+    if k_out is None:
+        if rows is None:
+            raise ValueError(f"{fn}: k_out and v_out, or rows, are needed")
+        on = torch.cuda.current_stream(k_pool.device) if stream is None else stream
+        with torch.cuda.stream(on):  # zeroed on the stream that writes them
+            k_out, v_out = (torch.zeros((B, rows, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
+                            for _ in range(2))
+    else:
+        if k_out.dim() != 4 or (rows is not None and rows != k_out.shape[1]):
+            raise ValueError(f"{fn}: k_out must be [B,rows,Hkv,D]")
+        rows = k_out.shape[1]
+        _need_on(k_out, "k_out", torch.bfloat16, k_pool, (B, rows, Hkv, D))
+        _need_on(v_out, "v_out", torch.bfloat16, k_pool, (B, rows, Hkv, D))
+    if starts is not None:
+        _need_on(starts, "starts", torch.int32, k_pool, (B,))
+    st = _guarded(guard, lib.gqa_paged_gather, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params),
+                  float(k_scale), float(v_scale), _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(),
+                  seq_lens.data_ptr(), _data(starts), k_out.data_ptr(), v_out.data_ptr(), B, int(rows), Hkv, D,
+                  page_size, ppr, num_pages, cs)
+    _check(st, fn)
+    return k_out, v_out
 
 
 def gqa_paged_gather_fp8(pool, page_table, topk_idx, out=None, stream=None):

@@ -11,6 +11,7 @@
 
 #include "../../include/gqa_decode.h"
 #include "../../include/gqa_decode_debug.h"
+#include "gqa_host.h"
 #include "gqa_launch.h"
 
 namespace gqa {
@@ -525,6 +526,20 @@ void paged_bind_workspace(const PagedShape &s, int workers, void *ws, PagedArgs 
 }
 
 }  // namespace
+
+bool host_current_device(int *dev) { return current_device(dev); }
+int host_sm_count(int dev) { return sm_count(dev); }
+unsigned *host_error_word(int dev) { return error_word(dev); }
+cudaError_t host_pool_alloc(void **p, size_t bytes, int dev, cudaStream_t stream) {
+    return pool_alloc(p, bytes, dev, stream);
+}
+uint64_t host_wait_limit_ns() { return g_wait_limit_ns.load(); }
+int host_fault_mode() { return g_fault_mode.load(); }
+void host_kernel_events(cudaEvent_t *before, cudaEvent_t *after) {
+    *before = g_ev_before.load();
+    *after = g_ev_after.load();
+}
+float host_resolve_scale(float scale, int D) { return resolve_scale(scale, D); }
 
 // K or V as a 4-D tensor (d, kv head, key, batch) with a box of 64 head-dim
 // elements (128 bytes, one swizzle atom) x 1 head x box_keys keys x 1 batch.

@@ -342,7 +342,12 @@ gqa_status gqa_decode_paged_fp8_dev_scales(const void *q, const void *gate,
  *   (256-byte aligned, at least gqa_decode_paged_workspace_bytes; NULL =
  *   library pool).
  * ------------------------------------------------------------------------ */
-typedef enum { GQA_KV_BF16 = 0, GQA_KV_FP8_E4M3FN = 1, GQA_KV_INT8 = 2 } gqa_kv_dtype;
+typedef enum {
+    GQA_KV_BF16 = 0,
+    GQA_KV_FP8_E4M3FN = 1,
+    GQA_KV_INT8 = 2,
+    GQA_KV_INT4 = 3 /* gqa_paged_append, gqa_paged_gather; decoded by gqa_decode_paged_int4 */
+} gqa_kv_dtype;
 
 gqa_status gqa_decode_paged(const void *q, const void *k_pool, const void *v_pool, int kv_dtype,
                             float k_scale, float v_scale, const int32_t *page_table,
@@ -381,6 +386,117 @@ int gqa_decode_paged_num_splits(int B, int Sq, int Hq, int Hkv, int D, int kv_dt
  * 0 when no workspace is needed or the arguments are invalid. */
 size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int kv_dtype,
                                         int page_size, int pages_per_req, int num_splits);
+
+/* ------------------------------------------------------------------------
+ * Paged decode over whole requests from a cache held in 4 bits.
+ *
+ * gqa_decode_paged's operation over pools of 4-bit codes.  Each token and KV
+ * head has its own scale and zero for K and for V, so a code u in 0..15 stands
+ * for u * scale + zero:
+ *   K^_t = u_k * ks_t + kz_t,  V^_t = u_v * vs_t + vz_t.
+ *
+ * k_pool, v_pool : device uint8 [num_pages, page_size, Hkv, D / 2]; element
+ *   2 i of a row is the low half of byte i, element 2 i + 1 the high half.
+ * kv_params : device fp16 [num_pages, page_size, Hkv, 4]: ks, kz, vs, vz.
+ *   Scales are >= 0; a V scale below 2^-24 (the smallest fp16 value: 0) is
+ *   taken as 2^-24, which changes an element by less than 1e-6.
+ * q, out, lse, page_table, seq_lens, scale, causal rows, empty rows (out = 0,
+ *   lse = -inf) and device checks as gqa_decode_paged.  A row whose scores are
+ *   NaN gives NaN; other rows are not touched by it, and what the pools hold
+ *   in slots past a request's length is never used.
+ * Limits: D in {64, 128}; (Hq / Hkv) * Sq <= 128; the rest as
+ *   gqa_decode_paged.  kv_params 16-byte aligned.
+ * num_splits = workers per block of KV heads (0 = automatic); workspace as
+ *   gqa_decode_paged_ex (NULL = library pool; otherwise 256-byte aligned,
+ *   gqa_decode_paged_int4_workspace_bytes, not in use by other work in
+ *   flight).  The same split count gives the same bits.
+ * ------------------------------------------------------------------------ */
+gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, const void *v_pool, const void *kv_params,
+                                 const int32_t *page_table, const int32_t *seq_lens, void *out, float *lse,
+                                 int B, int Sq, int Hq, int Hkv, int D, int page_size, int pages_per_req,
+                                 int num_pages, float scale, int num_splits, void *workspace,
+                                 size_t workspace_bytes, gqa_stream_t stream);
+
+/* Workers per block of KV heads of the automatic choice (negative gqa_status
+ * on invalid arguments). */
+int gqa_decode_paged_int4_num_splits(int B, int Sq, int Hq, int Hkv, int D, int page_size, int pages_per_req);
+
+/* Workspace bytes for num_splits (0 = automatic); 0 when none is needed or the
+ * arguments are invalid. */
+size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size,
+                                             int pages_per_req, int num_splits);
+
+/* ------------------------------------------------------------------------
+ * Appending keys and values to a paged cache, rotated on the way.
+ *
+ * T new tokens lie in rows 0 .. T-1 of q, k and v: request b owns the rows
+ * cu_tokens[b] .. cu_tokens[b+1]-1 (cu_tokens NULL: T / B rows each, in
+ * order; rows at or past cu_tokens[B] are left alone).  seq_lens[b] counts the
+ * request's tokens INCLUDING the new ones (what the decode call after it
+ * takes), so with n_b new ones the j-th has position t = seq_lens[b] - n_b + j
+ * and goes to page page_table[b, t / page_size], slot t % page_size.
+ *
+ * Rotation, of the first rot_dim elements of every q and k head: the pair
+ * (x, y) -- elements i and i + rot_dim / 2, or 2 i and 2 i + 1 when interleaved
+ * is non-zero -- becomes (x c - y s, y c + x s) with c = cos_sin[t, i] and
+ * s = cos_sin[t, rot_dim / 2 + i], in fp32, rounded after each product and sum.
+ * rot_dim = 0: no rotation (cos_sin and max_pos ignored).  v is never rotated.
+ *
+ * q_out receives the rotated q (bf16, [T, Hq, D]); q and q_out both NULL: no
+ * queries.  q_out may be q itself when q_stride = Hq * D.  The pools receive
+ * the rotated k and v as kv_dtype:
+ *   GQA_KV_BF16        rounded to nearest even
+ *   GQA_KV_FP8_E4M3FN  e4m3(x * (1 / scale)), saturated at +-448, NaN kept
+ *   GQA_KV_INT8        nearest even of x * (1 / scale), clamped to +-127, NaN as 0
+ *   GQA_KV_INT4        per token and head (x clamped to the fp16 range, NaN as
+ *                      0): zero = fp16(min x), scale = fp16((max x - zero) / 15),
+ *                      code = nearest even of (x - zero) * (1 / scale), clamped to 0..15
+ *                      (all 0 when the scale is 0), into kv_params as for
+ *                      gqa_decode_paged_int4.
+ * 8-bit pools take host scales k_scale, v_scale (finite, > 0) or, with
+ * k_scales and v_scales non-NULL, n_scales (1 or Hkv) device scales each.
+ *
+ * q, k, v : device bf16 [T, heads, D], heads contiguous, tokens q_stride,
+ *   k_stride, v_stride elements apart (multiples of 8, at least heads * D, so
+ *   that slices of a fused projection need no copy); 16-byte aligned.
+ * cos_sin : device fp32 [max_pos, rot_dim], 16-byte aligned.
+ * kv_params : 8-byte aligned, for GQA_KV_INT4 only (else NULL).
+ * Limits: D in {64, 128}; rot_dim a multiple of 16, at most D; T >= 0; page
+ *   limits as gqa_decode_paged.
+ * Device-checked (GQA_ERR_DEVICE_INDEX in the device error word): a token
+ *   whose position is outside the request's pages or past max_pos is skipped
+ *   whole; one whose page id is out of range gets its q_out row only.  Two
+ *   tokens sent to the same slot leave one of the two, unspecified which.
+ * ------------------------------------------------------------------------ */
+gqa_status gqa_paged_append(const void *q, long long q_stride, void *q_out, const void *k, long long k_stride,
+                            const void *v, long long v_stride, int kv_dtype, void *k_pool, void *v_pool,
+                            void *kv_params, float k_scale, float v_scale, const float *k_scales,
+                            const float *v_scales, int n_scales, const int32_t *page_table,
+                            const int32_t *seq_lens, const int32_t *cu_tokens, const float *cos_sin, int rot_dim,
+                            int max_pos, int interleaved, int T, int B, int Hq, int Hkv, int D, int page_size,
+                            int pages_per_req, int num_pages, gqa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gathering requests from a paged cache into dense bf16 K and V, as the dense
+ * calls read them (a prompt chunk with more query rows than the paged calls
+ * take attends to its request's cache this way).
+ *
+ *   k_out[b, j, g, :] = K^ of token starts[b] + j   (v_out alike)
+ * for j < min(rows, seq_lens[b] - starts[b]); output rows past that are left
+ * as they were.  starts NULL: all 0.  Values: bf16 pools as they are, 8-bit
+ * code * scale, 4-bit code * scale + zero, computed in fp32 and rounded to bf16.
+ *
+ * k_out, v_out : device bf16 [B, rows, Hkv, D], 16-byte aligned.  Pools,
+ *   scales, kv_params, page_table and limits as gqa_paged_append.
+ * Device-checked (GQA_ERR_DEVICE_INDEX): a seq_lens[b] outside
+ *   [0, pages_per_req * page_size] or a negative starts[b] is clamped; a token
+ *   whose page id is out of range reads as zeros.
+ * ------------------------------------------------------------------------ */
+gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const void *v_pool, const void *kv_params,
+                            float k_scale, float v_scale, const float *k_scales, const float *v_scales,
+                            int n_scales, const int32_t *page_table, const int32_t *seq_lens,
+                            const int32_t *starts, void *k_out, void *v_out, int B, int rows, int Hkv, int D,
+                            int page_size, int pages_per_req, int num_pages, gqa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Test hooks.  They run the paged kernel's own index mapping and FP8

@@ -1,0 +1,298 @@
+"""GPU parity of paged decode over a 4-bit cache, through the Python binding, against a plain 64-bit computation on
+the same codes, scales and zeros."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gq():
+    from gqa_decode_attention_gb300 import build as gbuild
+    gbuild.build()
+    import gqa_decode_attention_gb300 as m
+    m.load_library()
+    assert torch.cuda.is_available()
+    return m
+
+
+def make(B, Sq, Hq, Hkv, D, ps, lens, seed, ppr=None, extra=3, v_gain=1.0):
+    """A cache in use.  Slots that hold no token of a request carry NaN and infinite parameters, and table entries past
+    a request's pages are out of range: neither may be read into a result."""
+    g = torch.Generator().manual_seed(seed)
+    ppr = max(1, -(-max(lens) // ps)) if ppr is None else ppr
+    num_pages = B * ppr + extra
+    q = torch.randn(B, Sq, Hq, D, generator=g).to(torch.bfloat16)
+    x = torch.randn(2, num_pages, ps, Hkv, D, generator=g)
+    x[1] *= v_gain
+    kc, kp = ref.encode_int4(x[0])
+    vc, vp = ref.encode_int4(x[1])
+    params = torch.cat([kp, vp], -1)
+    table = torch.randperm(num_pages, generator=g)[:B * ppr].view(B, ppr).to(torch.int32)
+    used = torch.zeros(num_pages * ps, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        if n:
+            used[ref.slots(table[b], ps, range(n))] = True
+        table[b, -(-n // ps):] = 2 ** 31 - 1 if b % 2 else -7
+    flat = params.view(-1, Hkv, 4)
+    flat[~used] = torch.tensor([float("nan"), float("inf"), float("inf"), float("nan")]).half()
+    return dict(q=q, k_pool=kc, v_pool=vc, params=params, table=table, lens=torch.tensor(lens, dtype=torch.int32))
+
+
+def run(gq, d, **kw):
+    c = {n: t.cuda() for n, t in d.items()}
+    out, lse = gq.gqa_decode_paged_int4(c["q"], c["k_pool"], c["v_pool"], c["params"], c["table"], c["lens"], **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), lse.cpu()
+
+
+def check(d, out, lse, rows=None, what="", skip=None):
+    """Every query row (or the batch rows given) against 64 bits, within the bounds of cache_ref.int4_bounds."""
+    B, Sq, Hq, D = d["q"].shape
+    ps, Hkv = d["k_pool"].shape[1:3]
+    for b in range(B) if rows is None else rows:
+        n = int(d["lens"][b])
+        at = ref.slots(d["table"][b], ps, range(n)) if n else torch.zeros(0, dtype=torch.long)
+        p = d["params"].flatten(0, 1)[at]
+        k = ref.value_int4(d["k_pool"].flatten(0, 1)[at], p[..., :2])
+        v = ref.value_int4(d["v_pool"].flatten(0, 1)[at], p[..., 2:])
+        if skip is not None and n:
+            keep = skip(b, n)
+            k, v, p = k[keep], v[keep], p[keep]
+        ds, v_range, v_mag = ref.int4_bounds(d["q"][b], p, D)
+        for i in range(Sq):
+            seen = n - Sq + i + 1
+            if skip is not None and n:
+                seen = int(skip(b, n)[:max(seen, 0)].sum())
+            o, s = ref.attend(d["q"][b, i], k, v, seen)
+            if seen <= 0:
+                assert torch.all(out[b, i] == 0) and torch.all(torch.isneginf(lse[b, :, i])), what
+                continue
+            # a weight is off by its score's error (twice: numerator and sum) and its fp16 rounding; the sum of fp32
+            # terms over the tokens by 2^-23 a step of a pairwise-merged walk (2^-17 covers any walk here)
+            tol = 2 * ds * v_mag + 2.0 ** -11 * v_range + 2.0 ** -17 * v_mag + 2.0 ** -8 * o.abs()
+            err = (out[b, i].double() - o).abs()
+            assert torch.all(err <= tol), f"{what}: request {b} row {i}: out off by {float((err - tol).max())} over {float(tol.max())}"
+            el = (lse[b, :, i].double() - s).abs()
+            assert torch.all(el <= ds + 2.0 ** -17), f"{what}: request {b} row {i}: lse off by {float(el.max())}, bound {ds}"
+
+
+# (B, Sq, Hq, Hkv, D, page_size, lens)
+SHAPES = [
+    (1, 1, 1, 1, 64, 1, (1,)),                        # one token, one head, pages of one
+    (1, 1, 8, 2, 64, 5, (1000,)),
+    (3, 1, 32, 8, 128, 16, (128, 77, 1)),
+    (4, 1, 64, 8, 128, 16, (0, 640, 33, 0)),          # empty requests
+    (2, 4, 32, 8, 128, 32, (300, 2)),                 # 16 rows a KV head; two rows see nothing
+    (2, 3, 10, 2, 128, 24, (97, 500)),                # 15 rows, page size 8 x 3
+    (1, 2, 12, 12, 128, 16, (700,)),                  # 12 KV heads: a last block of 4
+    (2, 1, 3, 3, 64, 8, (65, 31)),                    # 3 KV heads
+    (1, 1, 32, 1, 64, 16, (3001,)),                   # 32 rows on one KV head
+    (2, 4, 16, 1, 128, 16, (513, 40)),                # 64 rows on one KV head
+    (1, 2, 128, 2, 64, 64, (900,)),                   # 128 rows a KV head
+    (2, 16, 8, 1, 128, 7, (150, 10)),                 # 128 rows, odd pages, rows that see nothing
+    (1, 1, 48, 16, 64, 128, (260,)),                  # 16 KV heads
+    (5, 1, 5, 1, 128, 3, (95, 96, 97, 31, 32)),       # around the stage's 32 tokens
+    (1, 1, 20, 20, 64, 2, (333,)),
+    (40, 1, 16, 4, 128, 16, tuple(range(1, 41))),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "b%d_sq%d_h%dx%d_d%d_ps%d" % s[:6])
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_matches_64_bits(gq, shape, splits):
+    d = make(*shape[:6], list(shape[6]), seed=sum(shape[:6]))
+    out, lse = run(gq, d, num_splits=splits)
+    assert gq.gqa_device_status() == 0
+    check(d, out, lse, what=f"{shape} splits {splits}")
+
+
+@pytest.mark.parametrize("splits", [0, 2, 9])
+def test_same_splits_same_bits(gq, splits):
+    d = make(6, 2, 32, 8, 128, 16, [700, 0, 15, 1200, 64, 333], seed=5)
+    first = run(gq, d, num_splits=splits)
+    for _ in range(5):
+        again = run(gq, d, num_splits=splits)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_workers_than_steps(gq, D):
+    d = make(2, 1, 8, 2, D, 16, [40, 3], seed=6)
+    out, lse = run(gq, d, num_splits=64)
+    check(d, out, lse)
+
+
+def test_bad_pages_and_lengths_are_flagged(gq):
+    """An out-of-range page inside a request: its tokens are skipped and the device error word says so; a length past
+    the table's capacity or below zero is clamped, and flagged."""
+    d = make(3, 1, 16, 4, 128, 16, [100, 64, 90], seed=7)
+    d["table"][0, 2] = 10 ** 6
+    d["table"][2, 0] = -1
+    out, lse = run(gq, d)
+    assert gq.gqa_device_status() == 7
+
+    def skip(b, n):
+        keep = torch.ones(n, dtype=torch.bool)
+        if b == 0:
+            keep[32:48] = False
+        if b == 2:
+            keep[0:16] = False
+        return keep
+
+    safe = {**d, "table": d["table"].clamp(0, d["k_pool"].shape[0] - 1)}
+    check(safe, out, lse, skip=skip)
+    d = make(3, 1, 16, 4, 128, 16, [96, 64, 0], seed=8)
+    over = {**d, "lens": torch.tensor([97, 64, -5], dtype=torch.int32)}
+    out, lse = run(gq, over)
+    assert gq.gqa_device_status() == 7
+    check(d, out, lse)
+
+
+def test_all_pages_bad(gq):
+    d = make(1, 2, 8, 2, 64, 16, [100], seed=9)
+    d["table"][:] = -1
+    out, lse = run(gq, d, num_splits=3)
+    assert gq.gqa_device_status() == 7
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+@pytest.mark.parametrize("gain", [2.0 ** -20, 1e-3, 300.0, 2e4])
+def test_value_magnitudes(gq, gain):
+    """V scales from the subnormal end of fp16 to its top."""
+    d = make(2, 1, 16, 2, 128, 16, [400, 1000], seed=10, v_gain=gain)
+    out, lse = run(gq, d, num_splits=5)
+    assert gq.gqa_device_status() == 0
+    check(d, out, lse, what=f"gain {gain}")
+
+
+def test_mixed_value_scales(gq):
+    """Tokens whose V scales differ by 2^20, constant rows (scale 0) among them."""
+    d = make(2, 1, 16, 2, 128, 16, [600, 900], seed=11)
+    g = torch.Generator().manual_seed(12)
+    e = torch.randint(-14, 7, d["params"].shape[:-1], generator=g).float()
+    p = d["params"].float()
+    p[..., 2:] = p[..., 2:] * (2.0 ** e)[..., None]
+    zero = torch.rand(d["params"].shape[:-1], generator=g) < 0.2
+    p[..., 2][zero] = 0.0
+    d["params"] = p.half()
+    d["v_pool"][zero] = 0
+    out, lse = run(gq, d)
+    check(d, out, lse)
+
+
+def test_peaked_and_growing_scores(gq):
+    """Scores that grow along the request by hundreds (the running maximum moves at every step), and one token far
+    above all others."""
+    d = make(2, 1, 8, 1, 64, 16, [800, 800], seed=13)
+    p = d["params"].float()
+    for b, f in ((0, lambda t: 1.0 + t.float() / 8), (1, lambda t: torch.where(t == 417, 200.0, 1.0))):
+        t = torch.arange(800)
+        at = ref.slots(d["table"][b], 16, t)
+        p.view(-1, 1, 4)[at, :, :2] *= f(t)[:, None, None]
+    d["params"] = p.half()
+    for splits in (0, 1, 4):
+        out, lse = run(gq, d, num_splits=splits)
+        check(d, out, lse, what=f"splits {splits}")
+
+
+def test_large_and_small_queries(gq):
+    d = make(1, 1, 8, 2, 128, 16, [300], seed=14)
+    scale = torch.tensor([2.0 ** -60, 2.0 ** -20, 1.0, 2.0 ** 6, 1.0, 2.0 ** -100, 0.0, 1.0]).view(1, 1, 8, 1)
+    d["q"] = (d["q"].float() * scale).to(torch.bfloat16)
+    out, lse = run(gq, d)
+    check(d, out, lse)
+
+
+def test_nan_rows_stay_their_own(gq):
+    """A query row with NaN or infinity gives NaN; the other rows keep every bit."""
+    d = make(2, 2, 16, 2, 128, 16, [300, 500], seed=15)
+    clean = run(gq, d, num_splits=3)
+    bad = {**d, "q": d["q"].clone()}
+    bad["q"][0, 1, 3, 17] = float("nan")
+    bad["q"][1, 0, 9, 100] = float("inf")
+    out, lse = run(gq, bad, num_splits=3)
+    hit = torch.zeros(2, 2, 16, dtype=torch.bool)
+    hit[0, 1, 3] = hit[1, 0, 9] = True
+    assert torch.all(torch.isnan(out[hit])) and torch.all(torch.isnan(lse.permute(0, 2, 1)[hit]))
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse.permute(0, 2, 1)[~hit], clean[1].permute(0, 2, 1)[~hit])
+
+
+def test_codes_beyond_four_gib(gq):
+    """Pools of more than 4 GiB each, the request's pages at their far end."""
+    num_pages, ps, Hkv, D = 540_000, 16, 8, 128
+    assert num_pages * ps * Hkv * D // 2 > 2 ** 32
+    small = make(2, 1, 16, Hkv, D, ps, [130, 50], seed=16)
+    n = small["k_pool"].shape[0]
+    big = {k: v.cuda() for k, v in small.items()}
+    for name in ("k_pool", "v_pool", "params"):
+        t = torch.empty((num_pages,) + tuple(small[name].shape[1:]), dtype=small[name].dtype, device="cuda")
+        t[num_pages - n:] = big[name]
+        big[name] = t
+    far = torch.where((small["table"] >= 0) & (small["table"] < n), small["table"] + (num_pages - n), small["table"])
+    out, lse = gq.gqa_decode_paged_int4(big["q"], big["k_pool"], big["v_pool"], big["params"], far.cuda(), big["lens"])
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 0
+    check(small, out.cpu(), lse.cpu())
+
+
+def test_long_request(gq):
+    d = make(2, 1, 8, 1, 64, 64, [200_000, 1], seed=17)
+    out, lse = run(gq, d)
+    check(d, out, lse)
+
+
+def test_outputs_given_and_without_lse(gq):
+    d = make(2, 1, 16, 2, 64, 16, [90, 200], seed=18)
+    want = run(gq, d, num_splits=4)
+    c = {n: t.cuda() for n, t in d.items()}
+    a = (c["q"], c["k_pool"], c["v_pool"], c["params"], c["table"], c["lens"])
+    out = torch.full_like(c["q"], 7.0)
+    got, lse = gq.gqa_decode_paged_int4(*a, out=out, with_lse=False, num_splits=4)
+    assert got is out and lse is None
+    ws = torch.empty(max(256, gq.gqa_decode_paged_int4_workspace_bytes(2, 1, 16, 2, 64, 16, c["table"].shape[1], 4)),
+                     dtype=torch.uint8, device="cuda")
+    o2, l2 = gq.gqa_decode_paged_int4(*a, workspace=ws, num_splits=4)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu(), want[0]) and torch.equal(o2.cpu(), want[0]) and torch.equal(l2.cpu(), want[1])
+    scaled, _ = gq.gqa_decode_paged_int4(*a, scale=1 / math.sqrt(64), num_splits=4)
+    assert torch.equal(scaled.cpu(), want[0])
+
+
+def test_other_streams_and_graphs(gq):
+    """Two captured graphs and eager calls on streams of their own, run at once and again with new lengths: each call's
+    partial results are its own."""
+    ds = [make(4, 1, 32, 8, 128, 16, [600, 200, 0, 900], seed=19), make(3, 2, 16, 2, 64, 16, [1000, 10, 350], seed=20)]
+    cs = [{n: t.cuda() for n, t in d.items()} for d in ds]
+    call = lambda c, **kw: gq.gqa_decode_paged_int4(c["q"], c["k_pool"], c["v_pool"], c["params"], c["table"], c["lens"], **kw)  # noqa: E731
+    want = [tuple(t.cpu() for t in call(c)) for c in cs]
+    graphs, outs = [], []
+    for c in cs:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(call(c))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    eager = []
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        for c, s in zip(cs, streams[2:]):
+            eager.append(call(c, stream=s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o[0].cpu(), want[i][0]) and torch.equal(o[1].cpu(), want[i][1])
+    for n, o in enumerate(eager):
+        assert torch.equal(o[0].cpu(), want[n % 2][0]) and torch.equal(o[1].cpu(), want[n % 2][1])
+    cs[0]["lens"].copy_(torch.tensor([10, 0, 0, 33], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    check({**ds[0], "lens": cs[0]["lens"].cpu()}, outs[0][0].cpu(), outs[0][1].cpu(), what="replayed with other lengths")
