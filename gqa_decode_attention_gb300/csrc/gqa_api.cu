@@ -540,6 +540,18 @@ void host_kernel_events(cudaEvent_t *before, cudaEvent_t *after) {
     *after = g_ev_after.load();
 }
 float host_resolve_scale(float scale, int D) { return resolve_scale(scale, D); }
+bool host_int4_tensor_map(CUtensorMap *map, const void *base, long long rows, int heads, int row_bytes, int box_rows,
+                          int box_heads) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(row_bytes), cuuint64_t(rows), cuuint64_t(heads)};
+    const cuuint64_t strides[2] = {cuuint64_t(heads) * row_bytes, cuuint64_t(row_bytes)};
+    const cuuint32_t box[3] = {cuuint32_t(row_bytes), cuuint32_t(box_rows), cuuint32_t(box_heads)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // K or V as a 4-D tensor (d, kv head, key, batch) with a box of 64 head-dim
 // elements (128 bytes, one swizzle atom) x 1 head x box_keys keys x 1 batch.

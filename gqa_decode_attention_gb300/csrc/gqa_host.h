@@ -2,6 +2,7 @@
 // translation units that hold C entry points.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -23,6 +24,12 @@ int host_fault_mode();
 void host_kernel_events(cudaEvent_t *before, cudaEvent_t *after);
 // scale, or 1 / sqrt(D) where scale is not a positive finite number.
 float host_resolve_scale(float scale, int D);
+
+// TMA descriptor of one 4-bit pool: bytes [rows, heads, row_bytes] seen as
+// (byte, row, head), boxes of (row_bytes, box_rows, box_heads), the 64-byte
+// swizzle for rows of 64 bytes.  Rows and heads past the end read as zeros.
+bool host_int4_tensor_map(CUtensorMap *map, const void *base, long long rows, int heads, int row_bytes, int box_rows,
+                          int box_heads);
 
 inline bool host_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t host_align256(size_t x) { return (x + 255) & ~size_t(255); }

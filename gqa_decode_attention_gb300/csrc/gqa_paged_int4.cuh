@@ -1,0 +1,742 @@
+// gqa_paged_int4.cuh -- paged decode over whole requests from a 4-bit cache
+// (sm_103a): the main kernel and the merge of partial results.
+//
+// Mathematics.  With codes u in 0..15 and a token's own scale and zero,
+// K^_t = u_t ks_t + kz_t and V^_t = v_t vs_t + vz_t, a row's scores and output are
+//   s_t = scale (ks_t sum_d q_d u_td + kz_t sum_d q_d)
+//   O_d = (sum_t p_t vs_t v_td + sum_t p_t vz_t) / sum_t p_t,  p_t = e^(s_t).
+// So the tensor cores multiply plain codes: q.u, and (p vs).v; scale and zero
+// of K enter the scores, those of V the weights and one extra sum a row.
+//
+// What bounds it.  A token costs 2 (D/2 + 4) bytes per KV head, a quarter of a
+// bf16 cache, so the walk must turn codes into operands at four times the
+// pace per byte.  The operand's cost is the kernel's budget:
+//  - A 4-bit code masked out of its 16-bit half is the fp16 subnormal u 2^-24
+//    (or 16 u 2^-24 for the second code of the half): an MMA operand of two
+//    codes is one AND of the stored word, with no conversion, bias or
+//    subtraction, and the factors (2^24, 2^20) come off once, in q for K and in
+//    the epilogue for V.
+//  - q's order along D and the output's order are free, so K's operands take
+//    the codes in the order in which they lie in the word.  V's operands pair
+//    two tokens of one element: a byte permute merges two tokens' halves, then
+//    the same masks apply.
+//  - The running maximum is a lazy reference: the row's maximum is only
+//    reduced over the warp (and O rescaled) when some weight would pass 2^9,
+//    which after the first steps of a walk is rare; a step otherwise costs one vote.
+//
+// Layout.  As in the other paged kernels a CTA takes a block of KV heads and
+// one worker's share of all requests' steps (here of 32 tokens), one consumer
+// warp per head (and per 16 query rows), a producer warp filling a ring of
+// shared-memory stages.  K and V come by TMA as boxes of (row bytes) x (up to
+// 16 tokens of one page) x (heads of the block): shared memory then holds each
+// head's rows back to back, and with the 64-byte swizzle (D = 128) and the
+// token order of `tok_of` every fragment read is free of bank conflicts.
+// Parameters come by 8-byte cp.async, [head][token].  Consumers never wait for
+// one another: each works out its segments from the lengths, and the producer
+// runs ahead across request borders.
+#pragma once
+
+#include "gqa_common.cuh"
+#include "gqa_params.h"
+
+namespace gqa {
+
+constexpr int kInt4Step = 32;       // tokens a stage
+constexpr int kInt4MaxStages = 8;
+constexpr int kInt4MaxWarps = 8;    // consumer warps of a CTA
+constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
+
+struct Int4Args {
+    const __nv_bfloat16 *q;   // [B, Sq, Hq, D]
+    const __half *params;     // [num_pages, page_size, Hkv, 4]
+    const int32_t *page_table, *seq_lens;
+    __nv_bfloat16 *out;
+    float *lse;
+    float *o_part;            // [head block, worker, 2 slots, HB, Mq, D] fp32, O / l
+    float *lse_part;          // [head block, worker, 2 slots, HB, Mq] fp32, log2 domain
+    long long *step_prefix;   // [B + 1] first step of each request (several workers)
+    int B, Sq, Hq, Hkv, G, Mq, page_size, pages_per_req, num_pages;
+    int workers, HB, RG;      // workers per head block, heads and row groups of 16 (8) rows a CTA
+    int stages, box_rows, box_pitch, stage_bytes;
+    float alpha;              // scale * log2(e)
+    unsigned long long wait_limit_ns;
+    int fault_mode;           // test hook: 1 = the producer never issues the first stage
+    unsigned *err;
+};
+
+// Shared memory of a CTA: the ring, then barriers, masks, schedule, flag.
+__host__ __device__ constexpr int int4_ring_bytes(int stages, int stage_bytes) { return stages * stage_bytes; }
+constexpr int kInt4TailBytes = 256;
+static_assert(2 * kInt4MaxStages * 8 + 4 * 8 + kInt4MaxStages * 4 + 2 * 4 <= kInt4TailBytes, "tail");
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t prmt4(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// d = A(16x16 f16) * B(16x8 f16), starting from zero
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 3-D tiled bulk tensor load into shared memory, completing on an mbarrier.
+__device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap, uint64_t *bar, int c0, int c1,
+                                            int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+__device__ __forceinline__ void cp_async8(uint32_t smem_dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+// Arrives on the barrier (one of its expected arrivals) once every cp.async of
+// this thread has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// Token (of a group of 8) in MMA row g.  A K fragment is read by the lanes of
+// rows g, g + 1 together (16 bytes a lane; D = 64: rows g .. g + 3, 8 bytes a
+// lane), a V fragment by the lanes of rows 0, 2, 4, 6 or 1, 3, 5, 7.  Rows lie
+// D/2 bytes apart, so with D = 64 each of these sets must cover the four rows
+// of a 128-byte line, and with D = 128 (two rows a line, the 64-byte swizzle
+// xoring the 16-byte unit with bits 7-8 of the address) pairs of rows must
+// differ in parity and V's even (odd) rows in bit 2.
+template <int D>
+__device__ __forceinline__ int tok_of(int g) {
+    return D == 128 ? g ^ ((g >> 1) & 1) : g ^ (g >> 2);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
+    gqa_paged_int4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                          const Int4Args a) {
+    constexpr int ROWB = D / 2;     // bytes of a row
+    constexpr int KW = D / 32;      // K words a lane holds of a token
+    constexpr int VW = D / 64;      // V words a lane holds of a token
+    constexpr int DB = D / 16;      // output blocks: block j holds elements (D/8) gi + 2 j, + 2 j + 1
+    constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+    extern __shared__ __align__(1024) uint8_t smem4[];
+    uint8_t *tail = smem4 + int4_ring_bytes(a.stages, a.stage_bytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(tail);
+    uint64_t *empty = full + kInt4MaxStages;
+    long long *sched = reinterpret_cast<long long *>(empty + kInt4MaxStages);  // begin, end, first step of `first`
+    uint32_t *vmask = reinterpret_cast<uint32_t *>(sched + 4);
+    int *first_s = reinterpret_cast<int *>(vmask + kInt4MaxStages);
+    volatile int *abort_flag = first_s + 1;
+    long long *warp_sum = reinterpret_cast<long long *>(smem4);  // the ring is not in use yet
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int consumers = a.HB * a.RG;
+    const int hb0 = blockIdx.x * a.HB;
+    const int nh = min(a.HB, a.Hkv - hb0);
+    const int cap = a.pages_per_req * a.page_size;
+    const uint32_t ring = smem_u32(smem4);
+
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < a.stages; ++st) {
+            mbar_init(full + st, 33);  // the producer's expect, and its 32 lanes' parameter copies
+            mbar_init(empty + st, nh * a.RG);
+        }
+        *first_s = a.B;
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == consumers && lane == 0) {
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
+    }
+    pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
+
+    // ---- schedule.  Request b takes ceil(len_b / 32) steps; worker w takes
+    // steps [w T / W, (w + 1) T / W) of the T steps of all requests in order.
+    // Each thread sums a run of requests, a scan over the CTA gives their first
+    // steps.  An empty request belongs to the worker whose range holds its
+    // step (the last worker for those at the very end).
+    bool bad = false;
+    {
+        const int run = (a.B + int(blockDim.x) - 1) / int(blockDim.x);
+        const int b0 = min(a.B, int(threadIdx.x) * run), b1 = min(a.B, b0 + run);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(a.seq_lens + b);
+            bad |= len < 0 || len > cap;
+            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step;
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        long long T = 0, P = incl - mine;
+        for (int w = 0; w <= consumers; ++w) {
+            const long long s = warp_sum[w];
+            T += s;
+            if (w < warp) P += s;
+        }
+        const unsigned long long W = a.workers, w = blockIdx.y;
+        const bool narrow = (unsigned long long)T * (W + 1) < (1ull << 32);
+        const long long begin = narrow ? unsigned(w * T) / unsigned(W) : w * T / W;
+        const long long end = narrow ? unsigned((w + 1) * T) / unsigned(W) : (w + 1) * T / W;
+        const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
+        int hit = a.B;
+        long long hit_p = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
+            const long long n = (len + kInt4Step - 1) / kInt4Step;
+            if (record) a.step_prefix[b] = P;
+            if (hit == a.B && P + (n > 0 ? n : 1) > begin) hit = b, hit_p = P;
+            P += n;
+        }
+        if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
+        if (hit < a.B) atomicMin(first_s, hit);
+        if (threadIdx.x == 0) sched[0] = begin, sched[1] = end, sched[2] = T;
+        __syncthreads();  // also: every warp is done with warp_sum, which lies in the ring
+        if (hit < a.B && hit == *first_s) sched[2] = hit_p;
+        if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
+        bad = false;
+        fence_proxy_async_shared();  // warp_sum's place is written by TMA next
+        __syncthreads();
+    }
+    const long long w_begin = sched[0], w_end = sched[1];
+    int seg_b = *first_s;
+    long long seg_p = sched[2], seg_t = w_begin;
+    const bool last_worker = int(blockIdx.y) == a.workers - 1;
+
+    // Segment of the worker's share: steps [seg_t, seg_next) of request seg_b.
+    auto more = [&] { return seg_b < a.B && (seg_t < w_end || (last_worker && seg_t == w_end)); };
+
+    // =============================================================== producer
+    if (warp == consumers) {
+        const int R = a.box_rows;
+        const uint32_t box_bytes = uint32_t(a.HB) * R * ROWB;
+        const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
+        const uint32_t p_off = 2 * v_off;
+        int gs = 0, st = 0;
+        uint32_t phase = 0;  // of the stage's empty barrier
+        bool failed = false;
+        while (more() && !failed) {
+            const int len = min(max(__ldg(a.seq_lens + seg_b), 0), cap);
+            const long long steps_b = (len + kInt4Step - 1) / kInt4Step;
+            const long long seg_next = min(w_end, seg_p + steps_b);
+            const int t_begin = int(seg_t - seg_p) * kInt4Step;
+            const int t_end = min(int(seg_next - seg_p) * kInt4Step, len);
+            const int32_t *table = a.page_table + size_t(seg_b) * a.pages_per_req;
+            int t = t_begin + lane;
+            int page = t < t_end ? __ldg(table + t / a.page_size) : 0;
+            for (int s0 = t_begin; s0 < t_end; s0 += kInt4Step, ++gs) {
+                const bool in = t < t_end;
+                const bool ok = in && page >= 0 && page < a.num_pages;
+                bad |= in && !ok;
+                const int row = ok ? page * a.page_size + t % a.page_size : 0;
+                // the next step's page is on its way while this one is issued
+                t += kInt4Step;
+                if (t < t_end) page = __ldg(table + t / a.page_size);
+                if (gs >= a.stages) {
+                    bool free = true;
+                    if (lane == 0) free = mbar_wait_bounded(empty + st, phase ^ 1, a.wait_limit_ns, abort_flag);
+                    if (!__shfl_sync(0xffffffffu, free, 0)) {
+                        failed = true;
+                        break;
+                    }
+                }
+                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                if (!(a.fault_mode == 1 && gs == 0)) {
+                    const bool issue = ok && lane % R == 0;  // a box's first token: its page holds all of the box
+                    const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
+                    if (lane == 0) {
+                        vmask[st] = valid;
+                        mbar_arrive_expect_tx(full + st, 2 * boxes * box_bytes);
+                    }
+                    __syncwarp();
+                    const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
+                    if (issue) {
+                        const uint32_t dst = base + uint32_t(lane / R) * a.box_pitch;
+                        tma_load_3d(dst, &k_map, full + st, 0, row, hb0);
+                        tma_load_3d(dst + v_off, &v_map, full + st, 0, row, hb0);
+                    }
+                    if (ok) {
+                        const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
+                        for (int h = 0; h < nh; ++h) cp_async8(base + p_off + uint32_t(h * kInt4Step + lane) * 8, src + h * 4);
+                    }
+                    cp_async_arrive(full + st);
+                }
+                if (++st == a.stages) st = 0, phase ^= 1;
+            }
+            if (seg_next == seg_p + steps_b) {
+                seg_p = seg_next;
+                ++seg_b;
+            }
+            seg_t = seg_next;
+        }
+        if (bad) flag_error(a.err, kErrIndex);
+        if (failed && lane == 0) {
+            flag_error(a.err, kErrTimeout);
+            *abort_flag = 1;
+        }
+        // Every copy must land before the CTA's shared memory is released;
+        // after an abort some may not have been waited for.
+        for (int i = 0; i < a.stages && i < gs; ++i) {
+            const int last = i + ((gs - 1 - i) / a.stages) * a.stages;  // last step issued into stage i
+            if (a.fault_mode == 1 && last == 0) continue;
+            if (lane == 0 && !mbar_wait_bounded(full + i, (last / a.stages) & 1, a.wait_limit_ns, nullptr))
+                flag_error(a.err, kErrTimeout);
+        }
+        return;
+    }
+
+    // ============================================================== consumers
+    const int lh = warp / a.RG, rg = warp - lh * a.RG;
+    if (lh >= nh) return;
+    const int g = hb0 + lh;
+    const int gi = lane >> 2, c = lane & 3;
+    const int R = a.box_rows;
+    // Offsets in a stage: a token's row lies in box t / R, head lh, row t % R.
+    const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
+    auto row_off = [&](int t) { return uint32_t(t / R) * a.box_pitch + uint32_t(lh * R + t % R) * ROWB; };
+    auto swz = [&](uint32_t off, int unit) { return D == 128 ? (uint32_t(unit) ^ ((off >> 7) & 3u)) << 4 : uint32_t(unit) << 4; };
+    const uint32_t d8 = R == 16 ? 8 * ROWB : uint32_t(8 / R) * a.box_pitch;     // to the token 8 later (keeps the swizzle)
+    const uint32_t d16 = R == 16 ? a.box_pitch : uint32_t(16 / R) * a.box_pitch;  // 16 later
+    const uint32_t k_row = row_off(tok_of<D>(gi));
+    const uint32_t k_off = D == 128 ? k_row + swz(k_row, c) : k_row + 8 * c;
+    uint32_t vo[2];  // tokens of MMA columns 2 c, 2 c + 1
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t r = row_off(tok_of<D>(2 * c + e));
+        vo[e] = v_off + (D == 128 ? r + swz(r, gi >> 1) + (gi & 1) * 8 : r + 4 * gi);
+    }
+    const uint32_t p_off = 2 * v_off + uint32_t(lh * kInt4Step + tok_of<D>(gi)) * 8;
+    const int tok0 = tok_of<D>(gi);
+
+    int st = 0;
+    uint32_t phase = 0;
+    bool failed = false;
+    while (more() && !failed) {
+        const int b = seg_b;
+        const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
+        const long long steps_b = (len + kInt4Step - 1) / kInt4Step;
+        const long long seg_next = min(w_end, seg_p + steps_b);
+        const int t_begin = int(seg_t - seg_p) * kInt4Step;
+        const int t_end = min(int(seg_next - seg_p) * kInt4Step, len);
+        const bool complete = seg_t == seg_p && seg_next == seg_p + steps_b;
+        const int slot = seg_t == w_begin ? 0 : 1;
+
+        // ---- queries.  Lane gi holds row gi (+ 8 a tile) at the elements of
+        // its quarter c, times a power of two that brings the row's largest
+        // element near 2^14 (bf16 values stay exact in fp16 down to 2^-28 of
+        // it).  The second code of a half is 16 u, so its q is q / 16.
+        uint32_t qf[NT][2 * KW][2];
+        float A[NT][2], qs[NT][2], R_[NT][2], l[NT][2], z[NT][2];
+        float o[NT][DB][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = (rg * NT + nt) * 8 + gi;
+            const bool real = r < a.Mq;
+            const int i = real ? r / a.G : 0;
+            const __nv_bfloat16 *qrow =
+                a.q + ((size_t(b) * a.Sq + i) * a.Hq + g * a.G + (real ? r - i * a.G : 0)) * D + (D / 4) * c;
+            float x[KW][8];
+            float mx = 0.f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                const uint4 raw = real ? *reinterpret_cast<const uint4 *>(qrow + 8 * w) : make_uint4(0, 0, 0, 0);
+                const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[w][2 * j] = __uint_as_float(rw[j] << 16);
+                    x[w][2 * j + 1] = __uint_as_float(rw[j] & 0xffff0000u);
+                    mx = fmaxf(mx, fmaxf(fabsf(x[w][2 * j]), fabsf(x[w][2 * j + 1])));
+                }
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // exponent of mx, kept where 2^-ex and 2^ex are normal; a row with an
+            // infinity or only zeros stays as it is
+            int ex = int(__float_as_uint(mx) >> 23) - 127 - 14;
+            ex = mx == 0.f || mx > 3.4e38f ? 0 : max(ex, -100);
+            const float down = __uint_as_float(uint32_t(127 - ex) << 23);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x[w][j] *= down;
+                    sum += x[w][j];
+                }
+                qf[nt][2 * w][0] = pack_f16x2(x[w][0], x[w][4]);
+                qf[nt][2 * w][1] = pack_f16x2(x[w][1] * 0.0625f, x[w][5] * 0.0625f);
+                qf[nt][2 * w + 1][0] = pack_f16x2(x[w][2], x[w][6]);
+                qf[nt][2 * w + 1][1] = pack_f16x2(x[w][3] * 0.0625f, x[w][7] * 0.0625f);
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            // score in the log2 domain = A (ks acc + kz qs), acc = 2^-24 sum q u
+            const float row_a = fmaxf(a.alpha * __uint_as_float(uint32_t(127 + ex) << 23) * 16777216.f, 1e-37f);
+            const float row_qs = sum * (1.f / 16777216.f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // rows of this lane's scores: 2 c + e
+                A[nt][e] = __shfl_sync(0xffffffffu, row_a, 4 * (2 * c + e));
+                qs[nt][e] = __shfl_sync(0xffffffffu, row_qs, 4 * (2 * c + e));
+                R_[nt][e] = kInt4NoRef;
+                l[nt][e] = z[nt][e] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < DB; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+        }
+        // first token that some row does not see (all see those before it)
+        const int t_causal = a.Sq > 1 ? len - a.Sq + 1 : 0x7fffffff;
+
+        for (int s0 = t_begin; s0 < t_end; s0 += kInt4Step) {
+            const bool ok = mbar_wait_bounded(full + st, phase, a.wait_limit_ns, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;
+                break;
+            }
+            const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
+            const uint32_t mask = vmask[st];
+            uint32_t kw[4][KW];  // token group j: tokens tok0 + 8 j
+            uint2 par[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = base + k_off + (j & 1) * d8 + (j >> 1) * d16;
+                if constexpr (KW == 4) {
+                    const uint4 x = lds128(at);
+                    kw[j][0] = x.x, kw[j][1] = x.y, kw[j][2] = x.z, kw[j][3] = x.w;
+                } else {
+                    const uint2 x = lds64(at);
+                    kw[j][0] = x.x, kw[j][1] = x.y;
+                }
+                par[j] = lds64(base + p_off + j * 64);
+            }
+            uint32_t vw[8][VW];  // token pair j: tokens of columns 2 c, 2 c + 1, 8 j later
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t at = base + vo[e] + (j & 1) * d8 + (j >> 1) * d16;
+                    if constexpr (VW == 2) {
+                        const uint2 x = lds64(at);
+                        vw[2 * j + e][0] = x.x, vw[2 * j + e][1] = x.y;
+                    } else {
+                        vw[2 * j + e][0] = lds32(at);
+                    }
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st);
+            if (++st == a.stages) st = 0, phase ^= 1;
+
+            // ---- scores of 2 x 16 tokens
+            float acc[NT][2][4];
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t x0 = h ? kw[2 * t][w] >> 8 : kw[2 * t][w];
+                        const uint32_t x1 = h ? kw[2 * t + 1][w] >> 8 : kw[2 * t + 1][w];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t b0 = qf[nt][2 * w + h][0], b1 = qf[nt][2 * w + h][1];
+                            if (w == 0 && h == 0)
+                                mma_f16_zero(acc[nt][t], x0 & M0, x1 & M0, x0 & M1, x1 & M1, b0, b1);
+                            else
+                                mma_f16_add(acc[nt][t], x0 & M0, x1 & M0, x0 & M1, x1 & M1, b0, b1);
+                        }
+                    }
+
+            // ---- weights.  acc[t][2 i + e]: token group j = 2 t + i, row 2 c + e.
+            float vs[4], vz[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].x));
+                const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].y));
+                vs[j] = fmaxf(v2.x, 5.9604644775390625e-8f);  // fp16's smallest: a weight of 0 would hide its score
+                vz[j] = v2.y;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &y = acc[nt][j >> 1][2 * (j & 1) + e];
+                        y = fmaf(y, k2.x, k2.y * qs[nt][e]);
+                    }
+            }
+            if (mask != 0xffffffffu || s0 + kInt4Step > t_causal) {  // tokens that are not there, or not seen by all rows
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool there = (mask >> (tok0 + 8 * j)) & 1u;
+                    if (!there) vs[j] = vz[j] = 0.f;  // the slot may hold anything
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = (rg * NT + nt) * 8 + 2 * c + e;
+                            const bool seen = there && s0 + tok0 + 8 * j <= len - a.Sq + (r < a.Mq ? r / a.G : a.Sq);
+                            if (!seen) acc[nt][j >> 1][2 * (j & 1) + e] = -INFINITY;
+                        }
+                }
+            }
+            float p[NT][4][2], wt[NT][4][2];
+            float top = 0.f;
+            auto weigh = [&] {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            p[nt][j][e] = fast_exp2(fmaf(acc[nt][j >> 1][2 * (j & 1) + e], A[nt][e], -R_[nt][e]));
+                            wt[nt][j][e] = p[nt][j][e] * vs[j];
+                        }
+                        top = fmax3(top, wt[nt][j][0], wt[nt][j][1]);
+                    }
+            };
+            weigh();
+            if (__any_sync(0xffffffffu, top > 512.f)) {
+                // Move the references up to the step's largest score + log2(V
+                // scale): the largest weight of the row is then 1.
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float corr[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = kInt4NoRef;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float y = acc[nt][j >> 1][2 * (j & 1) + e];
+                            if (vs[j] > 0.f) m = fmaxf(m, fmaf(y, A[nt][e], log2f(vs[j])));
+                        }
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        m = fmaxf(m, R_[nt][e]);
+                        corr[e] = fast_exp2(R_[nt][e] - m);
+                        R_[nt][e] = m;
+                        l[nt][e] *= corr[e];
+                        z[nt][e] *= corr[e];
+                    }
+#pragma unroll
+                    for (int j = 0; j < DB; ++j) {
+                        o[nt][j][0] *= corr[0];
+                        o[nt][j][1] *= corr[1];
+                        o[nt][j][2] *= corr[0];
+                        o[nt][j][3] *= corr[1];
+                    }
+                }
+                weigh();
+            }
+            uint32_t pb[NT][4];  // weights of row gi for the tokens of columns 2 c, 2 c + 1 of group j
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        l[nt][e] += p[nt][j][e];
+                        z[nt][e] = fmaf(p[nt][j][e], vz[j], z[nt][e]);
+                    }
+                    pb[nt][j] = movmatrix_trans(pack_f16x2(wt[nt][j][0], wt[nt][j][1]));
+                }
+
+            // ---- O^T += V^T . weights
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int w = 0; w < VW; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sel = h ? 0x7632u : 0x5410u;
+                        const uint32_t x = prmt4(vw[4 * t][w], vw[4 * t + 1][w], sel);
+                        const uint32_t y = prmt4(vw[4 * t + 2][w], vw[4 * t + 3][w], sel);
+                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int j = 4 * w + 2 * h;
+                            mma_f16_add(o[nt][j], x & M0, x & M1, y & M0, y & M1, pb[nt][2 * t], pb[nt][2 * t + 1]);
+                            mma_f16_add(o[nt][j + 1], x8 & M0, x8 & M1, y8 & M0, y8 & M1, pb[nt][2 * t], pb[nt][2 * t + 1]);
+                        }
+                    }
+        }
+        if (failed) break;
+
+        // ---- epilogue of the segment: row 2 c + e of a tile, elements (D/8) gi .. + D/8 - 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float L = l[nt][e], Z = z[nt][e];
+#pragma unroll
+                for (int off = 4; off < 32; off *= 2) {
+                    L += __shfl_xor_sync(0xffffffffu, L, off);
+                    Z += __shfl_xor_sync(0xffffffffu, Z, off);
+                }
+                const int r = (rg * NT + nt) * 8 + 2 * c + e;
+                if (r >= a.Mq) continue;
+                const float f = L == 0.f ? 0.f : 1.f / L;  // NaN stays
+                const float lse2 = L == 0.f ? -INFINITY : R_[nt][e] + log2f(L);
+                float x[2 * DB];
+#pragma unroll
+                for (int j = 0; j < DB; ++j) {
+                    x[2 * j] = fmaf(o[nt][j][e], 16777216.f, Z) * f;
+                    x[2 * j + 1] = fmaf(o[nt][j][2 + e], 1048576.f, Z) * f;
+                }
+                if (!complete) {
+                    const size_t prow = ((((size_t(blockIdx.x) * a.workers + blockIdx.y) * 2 + slot) * a.HB + lh) * a.Mq) + r;
+                    float *dst = a.o_part + prow * D + (D / 8) * gi;
+#pragma unroll
+                    for (int j = 0; j < 2 * DB; j += 4)
+                        *reinterpret_cast<float4 *>(dst + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    if (gi == 0) a.lse_part[prow] = lse2;
+                    continue;
+                }
+                const int i = r / a.G, h = g * a.G + (r - i * a.G);
+                __nv_bfloat16 *dst = a.out + ((size_t(b) * a.Sq + i) * a.Hq + h) * D + (D / 8) * gi;
+#pragma unroll
+                for (int j = 0; j < 2 * DB; j += 8)
+                    *reinterpret_cast<uint4 *>(dst + j) =
+                        make_uint4(pack_bf16x2(x[j], x[j + 1]), pack_bf16x2(x[j + 2], x[j + 3]),
+                                   pack_bf16x2(x[j + 4], x[j + 5]), pack_bf16x2(x[j + 6], x[j + 7]));
+                if (a.lse != nullptr && gi == 0)
+                    a.lse[(size_t(b) * a.Hq + h) * a.Sq + i] = lse2 * 0.69314718055994530942f;
+            }
+        if (seg_next == seg_p + steps_b) {
+            seg_p = seg_next;
+            ++seg_b;
+        }
+        seg_t = seg_next;
+    }
+    if (failed && lane == 0) {
+        flag_error(a.err, kErrTimeout);
+        *abort_flag = 1;
+    }
+}
+
+// Merge of the partials of requests that several workers share.  CTA (row, b):
+// the workers that hold request b are dealt to its warps in runs, each warp
+// merges its run in order (8 partials in flight), and the warps' results are
+// merged in warp order: the same bits every time.
+constexpr int kInt4MergeWarps = 4;
+constexpr int kInt4MergeBatch = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kInt4MergeWarps) gqa_paged_int4_merge_kernel(const Int4Args a) {
+    constexpr int V = D / 32;
+    __shared__ float sm_m[kInt4MergeWarps], sm_l[kInt4MergeWarps], sm_o[kInt4MergeWarps][D];
+    pdl_wait_primary();
+    const int b = blockIdx.y, rr = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long W = a.workers;
+    const long long P = a.step_prefix[b], n = a.step_prefix[b + 1] - P, T = a.step_prefix[a.B];
+    if (n == 0) return;  // an empty request: written by the main kernel
+    const bool narrow = (unsigned long long)(T + 1) * (unsigned long long)(W + 1) < (1ull << 32);
+    auto div = [narrow](long long x, long long y) -> long long { return narrow ? (long long)(unsigned(x) / unsigned(y)) : x / y; };
+    // worker of step s: the largest w with floor(w T / W) <= s
+    const long long w_first = div((P + 1) * W - 1, T), w_last = div((P + n) * W - 1, T);
+    if (w_first == w_last) return;  // one worker: written by the main kernel
+    const int g = rr / a.Mq, r = rr - g * a.Mq;
+    const int hb = g / a.HB, lh = g - hb * a.HB;
+    const long long each = (w_last - w_first + kInt4MergeWarps) / kInt4MergeWarps;
+    const long long from = w_first + warp * each, to = min(w_last + 1, from + each);
+    const bool before = div(w_first * T, W) < P;  // the first worker starts in an earlier request: its last slot
+
+    float m = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (long long w0 = from; w0 < to; w0 += kInt4MergeBatch) {
+        float l2[kInt4MergeBatch], x[kInt4MergeBatch][V];
+#pragma unroll
+        for (int k = 0; k < kInt4MergeBatch; ++k) {
+            const long long w = w0 + k;
+            l2[k] = -INFINITY;
+            // a worker without a step (T < W) holds nothing
+            if (w >= to || (T < W && div(w * T, W) == div((w + 1) * T, W))) continue;
+            const int slot = w == w_first && before ? 1 : 0;
+            const size_t prow = ((((size_t(hb) * W + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
+            l2[k] = __ldg(a.lse_part + prow);
+            if constexpr (V == 4) {
+                const float4 t = __ldg(reinterpret_cast<const float4 *>(a.o_part + prow * D) + lane);
+                x[k][0] = t.x, x[k][1] = t.y, x[k][2] = t.z, x[k][3] = t.w;
+            } else {
+                const float2 t = __ldg(reinterpret_cast<const float2 *>(a.o_part + prow * D) + lane);
+                x[k][0] = t.x, x[k][1] = t.y;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kInt4MergeBatch; ++k) {
+            if (l2[k] == -INFINITY) continue;
+            const float mn = fmaxf(m, l2[k]);
+            const float sc = fast_exp2(m - mn), wgt = fast_exp2(l2[k] - mn);
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = acc[v] * sc + wgt * x[k][v];
+            L = L * sc + wgt;
+            m = mn;
+        }
+    }
+    if (lane == 0) sm_m[warp] = m, sm_l[warp] = L;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = acc[v];
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kInt4MergeWarps; ++w) M = fmaxf(M, sm_m[w]);
+    float S = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kInt4MergeWarps; ++w) {
+        if (sm_l[w] == 0.f) continue;
+        const float f = fast_exp2(sm_m[w] - M);
+        S += f * sm_l[w];
+        x0 += f * sm_o[w][2 * threadIdx.x];
+        x1 += f * sm_o[w][2 * threadIdx.x + 1];
+    }
+    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const int i = r / a.G, h = g * a.G + (r - i * a.G);
+    const size_t row = (size_t(b) * a.Sq + i) * a.Hq + h;
+    *reinterpret_cast<uint32_t *>(a.out + row * D + 2 * threadIdx.x) = pack_bf16x2(x0 * inv, x1 * inv);
+    if (a.lse != nullptr && threadIdx.x == 0)
+        a.lse[(size_t(b) * a.Hq + h) * a.Sq + i] = S == 0.f ? -INFINITY : (M + log2f(S)) * 0.69314718055994530942f;
+}
+
+}  // namespace gqa

@@ -26,7 +26,7 @@ def attend(lib, q=A, kp=A, vp=A, par=A, pt=A, sl=A, out=A, lse=A, B=2, Sq=1, Hq=
     (dict(Hq=6, Hkv=4), 1), (dict(B=0), 1), (dict(Sq=0), 1), (dict(ps=0), 1), (dict(ppr=0), 1), (dict(num_pages=0), 1),
     (dict(splits=-1), 1), (dict(q=None), 1), (dict(par=None), 1), (dict(pt=None), 1), (dict(sl=None), 1), (dict(out=None), 1),
     (dict(D=96), 2), (dict(D=256), 2), (dict(Hq=258, Hkv=2), 2), (dict(Sq=33), 2), (dict(B=65536), 2),
-    (dict(ps=1 << 16, ppr=1 << 15), 2), (dict(ps=1 << 16, num_pages=1 << 15), 2),
+    (dict(ps=1 << 16, ppr=1 << 15), 2), (dict(ps=1, ppr=(1 << 31) - 63), 2), (dict(ps=1 << 16, num_pages=1 << 15), 2),
     (dict(q=A + 2), 3), (dict(kp=A + 8), 3), (dict(vp=A + 4), 3), (dict(par=A + 8), 3), (dict(out=A + 2), 3), (dict(lse=A + 2), 3),
     (dict(pt=A + 1), 3), (dict(sl=A + 2), 3),
 ])
