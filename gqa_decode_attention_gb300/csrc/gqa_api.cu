@@ -553,6 +553,18 @@ bool host_int4_tensor_map(CUtensorMap *map, const void *base, long long rows, in
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool host_int4_param_map(CUtensorMap *map, const void *base, long long rows, int heads, int box_rows, int box_heads) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(heads) * 4, cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(heads) * 8};
+    const cuuint32_t box[2] = {cuuint32_t(box_heads) * 4, cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // K or V as a 4-D tensor (d, kv head, key, batch) with a box of 64 head-dim
 // elements (128 bytes, one swizzle atom) x 1 head x box_keys keys x 1 batch.
 // Keys past Skv read as zeros.

@@ -31,6 +31,10 @@ float host_resolve_scale(float scale, int D);
 bool host_int4_tensor_map(CUtensorMap *map, const void *base, long long rows, int heads, int row_bytes, int box_rows,
                           int box_heads);
 
+// TMA descriptor of the 4-bit cache's parameters: fp16 [rows, heads, 4] seen as
+// rows of heads * 4, boxes of (box_heads * 4, box_rows).
+bool host_int4_param_map(CUtensorMap *map, const void *base, long long rows, int heads, int box_rows, int box_heads);
+
 inline bool host_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t host_align256(size_t x) { return (x + 255) & ~size_t(255); }
 

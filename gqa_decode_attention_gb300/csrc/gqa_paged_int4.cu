@@ -19,7 +19,8 @@ struct Int4Plan {
     int NT;      // tiles of 8 query rows a consumer warp holds
     int RG, HB;  // consumer warps per head, heads per CTA
     int R;       // tokens of a TMA box: the largest power of two, at most 16, that divides the page size
-    int pitch, stage_bytes, stages, smem, threads, nhb;
+    int pitch, par_pitch, stage_bytes, stages, smem, threads, nhb;
+    bool param_tma;
     long long max_steps;
 };
 
@@ -43,24 +44,34 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     while (page_size % p->R != 0) p->R /= 2;
     const int row = D / 2;
     p->pitch = (hb * p->R * row + 127) / 128 * 128;  // TMA writes to 128-byte boundaries
+    p->par_pitch = (hb * p->R * 8 + 127) / 128 * 128;
+    p->param_tma = Hkv % 2 == 0 && hb > 1;           // a box's rows, and their stride, in whole 16 bytes
     const int align = D == 128 ? 512 : 128;          // the swizzle repeats every 512 bytes
-    p->stage_bytes = (2 * (kInt4Step / p->R) * p->pitch + hb * kInt4Step * 8 + align - 1) / align * align;
-    const int budget = 100 * 1024;
-    p->stages = budget / p->stage_bytes;
-    if (p->stages > 4) p->stages = 4;
+    p->stage_bytes = ((kInt4Step / p->R) * (2 * p->pitch + p->par_pitch) + align - 1) / align * align;
+    // shared memory of an SM over the CTAs that registers allow (16 warps of 8
+    // rows, 12 of 16), less what the system keeps
+    const int warps = hb * p->RG, ctas = p->NT == 1 ? 16 / warps : warps <= 4 ? 12 / warps : 1;
+    p->stages = (228 * 1024 / ctas - 1024 - kInt4HeadBytes) / p->stage_bytes;
+    if (p->stages > kInt4MaxStages) p->stages = kInt4MaxStages;
     if (p->stages < 2) p->stages = 2;
-    p->smem = p->stages * p->stage_bytes + kInt4TailBytes;
+    p->smem = p->stages * p->stage_bytes + kInt4HeadBytes;
     p->threads = 32 * (hb * p->RG + 1);
     p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
+    if (p->max_steps >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
     return GQA_OK;
 }
 
+// Instances: 8 query rows a warp and up to 8 warps; 16 rows a warp and up to 4
+// warps (three CTAs an SM); 16 rows and 5 to 8 warps (65 to 128 rows a head).
+int instance_of(const Int4Plan &p) { return p.NT == 1 ? 0 : p.HB * p.RG <= 4 ? 1 : 2; }
+
 const void *kernel_of(const Int4Plan &p) {
-    if (p.D == 64)
-        return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 1>)
-                         : reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2>);
-    return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 1>)
-                     : reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2>);
+    static const void *const kernels[2][3] = {
+        {reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 1, 8>), reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2, 4>),
+         reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2, 8>)},
+        {reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 1, 8>), reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2, 4>),
+         reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2, 8>)}};
+    return kernels[p.D == 128][instance_of(p)];
 }
 
 // Resident CTAs per SM of the plan's instance on `dev`, the current device;
@@ -70,11 +81,11 @@ int int4_occupancy(int dev, const Int4Plan &p) {
         int smem, threads, ctas;
     };
     static std::mutex mu;
-    static Entry table[kMaxDevices][2][2][64];
-    static int used[kMaxDevices][2][2];
-    static bool raised[kMaxDevices][2][2];
+    static Entry table[kMaxDevices][2][3][64];
+    static int used[kMaxDevices][2][3];
+    static bool raised[kMaxDevices][2][3];
     std::lock_guard<std::mutex> lk(mu);
-    const int d = p.D == 128, n = p.NT - 1;
+    const int d = p.D == 128, n = instance_of(p);
     Entry *t = table[dev][d][n];
     for (int i = 0; i < used[dev][d][n]; ++i)
         if (t[i].smem == p.smem && t[i].threads == p.threads) return t[i].ctas;
@@ -109,7 +120,7 @@ size_t int4_workspace(const Int4Plan &p, int workers) {
     if (workers <= 1) return 0;
     const size_t rows = size_t(p.nhb) * workers * 2 * p.HB * p.Mq;
     return host_align256(rows * p.D * sizeof(float)) + host_align256(rows * sizeof(float)) +
-           host_align256((size_t(p.B) + 1) * sizeof(long long));
+           host_align256((size_t(p.B) + 1) * sizeof(int));
 }
 
 cudaError_t launch(const void *kern, dim3 grid, int threads, int smem, void **args, cudaStream_t stream) {
@@ -152,10 +163,11 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
         return GQA_ERR_ALIGNMENT;
     int dev = 0;
     if (!host_current_device(&dev)) return GQA_ERR_CUDA;
-    CUtensorMap k_map, v_map;
+    CUtensorMap k_map, v_map, p_map = {};
     const long long rows = (long long)num_pages * page_size;
     if (int4_occupancy(dev, p) < 1 || !host_int4_tensor_map(&k_map, k_pool, rows, Hkv, D / 2, p.R, p.HB) ||
-        !host_int4_tensor_map(&v_map, v_pool, rows, Hkv, D / 2, p.R, p.HB)) {
+        !host_int4_tensor_map(&v_map, v_pool, rows, Hkv, D / 2, p.R, p.HB) ||
+        (p.param_tma && !host_int4_param_map(&p_map, kv_params, rows, Hkv, p.R, p.HB))) {
         cudaGetLastError();
         return GQA_ERR_CUDA;
     }
@@ -189,7 +201,7 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
         a.o_part = reinterpret_cast<float *>(w);
         w += host_align256(part_rows * D * sizeof(float));
         a.lse_part = reinterpret_cast<float *>(w);
-        a.step_prefix = reinterpret_cast<long long *>(w + host_align256(part_rows * sizeof(float)));
+        a.step_prefix = reinterpret_cast<int *>(w + host_align256(part_rows * sizeof(float)));
     }
     a.B = B;
     a.Sq = Sq;
@@ -207,6 +219,12 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.box_rows = p.R;
     a.box_pitch = p.pitch;
     a.stage_bytes = p.stage_bytes;
+    a.tok8 = p.R == 16 ? 8 * (D / 2) : (8 / p.R) * p.pitch;
+    a.tok16 = p.R == 16 ? p.pitch : (16 / p.R) * p.pitch;
+    a.param_tma = p.param_tma;
+    a.param_pitch = p.par_pitch;
+    a.par8 = p.R == 16 ? 8 * p.HB * 8 : (8 / p.R) * p.par_pitch;
+    a.par16 = p.R == 16 ? p.par_pitch : (16 / p.R) * p.par_pitch;
     a.alpha = host_resolve_scale(scale, D) * 1.4426950408889634f;
     a.wait_limit_ns = host_wait_limit_ns();
     a.fault_mode = host_fault_mode();
@@ -215,7 +233,7 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     host_kernel_events(&before, &after);
     const bool timed = before != nullptr && after != nullptr;
     if (timed) cudaEventRecord(before, cs);
-    void *args[] = {&k_map, &v_map, &a};
+    void *args[] = {&k_map, &v_map, &p_map, &a};
     cudaError_t e = launch(kernel_of(p), dim3(unsigned(p.nhb), unsigned(workers)), p.threads, p.smem, args, cs);
     if (timed) cudaEventRecord(after, cs);
     if (e == cudaSuccess && workers > 1) {

@@ -25,15 +25,16 @@
 //    which after the first steps of a walk is rare; a step otherwise costs one vote.
 //
 // Layout.  As in the other paged kernels a CTA takes a block of KV heads and
-// one worker's share of all requests' steps (here of 32 tokens), one consumer
-// warp per head (and per 16 query rows), a producer warp filling a ring of
-// shared-memory stages.  K and V come by TMA as boxes of (row bytes) x (up to
-// 16 tokens of one page) x (heads of the block): shared memory then holds each
+// one worker's share of all requests' steps (here of 32 tokens), one warp per
+// head (and per 16 query rows), over a ring of shared-memory stages that the
+// warps fill in turns.  K and V come by TMA as boxes of (row bytes) x (up to 16
+// tokens of one page) x (heads of the block): shared memory then holds each
 // head's rows back to back, and with the 64-byte swizzle (D = 128) and the
 // token order of `tok_of` every fragment read is free of bank conflicts.
-// Parameters come by 8-byte cp.async, [head][token].  Consumers never wait for
-// one another: each works out its segments from the lengths, and the producer
-// runs ahead across request borders.
+// Parameters come by TMA too, [token][head] (by cp.async where their rows are
+// not 16 bytes).  The warps never wait for
+// one another beyond the ring: each works out its segments from the lengths,
+// and the loads run ahead across request borders.
 #pragma once
 
 #include "gqa_common.cuh"
@@ -54,20 +55,24 @@ struct Int4Args {
     float *lse;
     float *o_part;            // [head block, worker, 2 slots, HB, Mq, D] fp32, O / l
     float *lse_part;          // [head block, worker, 2 slots, HB, Mq] fp32, log2 domain
-    long long *step_prefix;   // [B + 1] first step of each request (several workers)
+    int *step_prefix;         // [B + 1] first step of each request (several workers)
     int B, Sq, Hq, Hkv, G, Mq, page_size, pages_per_req, num_pages;
-    int workers, HB, RG;      // workers per head block, heads and row groups of 16 (8) rows a CTA
+    int workers, HB, RG;      // workers per head block; heads of a CTA, warps (of 8 or 16 query rows) a head
     int stages, box_rows, box_pitch, stage_bytes;
+    int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
+    unsigned param_pitch;     // of a box's parameters in a stage
+    unsigned par8, par16;     // as tok8, tok16, of the parameters
+    unsigned tok8, tok16;     // bytes from a token's row in a stage to that of the token 8, 16 later (8, 16 keep the swizzle)
     float alpha;              // scale * log2(e)
     unsigned long long wait_limit_ns;
     int fault_mode;           // test hook: 1 = the producer never issues the first stage
     unsigned *err;
 };
 
-// Shared memory of a CTA: the ring, then barriers, masks, schedule, flag.
-__host__ __device__ constexpr int int4_ring_bytes(int stages, int stage_bytes) { return stages * stage_bytes; }
-constexpr int kInt4TailBytes = 256;
-static_assert(2 * kInt4MaxStages * 8 + 4 * 8 + kInt4MaxStages * 4 + 2 * 4 <= kInt4TailBytes, "tail");
+// Shared memory of a CTA: barriers, masks, schedule and flag, then the ring
+// (at constant addresses, and on the swizzle's 512-byte period).
+constexpr int kInt4HeadBytes = 512;
+static_assert(2 * kInt4MaxStages * 8 + kInt4MaxStages * 4 + 5 * 4 <= kInt4HeadBytes, "head");
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -79,6 +84,18 @@ __device__ __forceinline__ uint32_t prmt4(uint32_t a, uint32_t b, uint32_t sel) 
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
+}
+
+// Larger of two fp16 pairs, half by half (a NaN gives way to the other).
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Whether a half of x, which is not negative, is above 2^9 (a NaN is not).
+__device__ __forceinline__ bool above_512(uint32_t x) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return fmaxf(f.x, f.y) > 512.f;
 }
 
 // d = A(16x16 f16) * B(16x8 f16), starting from zero
@@ -109,6 +126,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t smem_dst, const void *tmap,
         : "memory");
 }
 
+// 2-D form of it.
+__device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const void *tmap, uint64_t *bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+
 __device__ __forceinline__ void cp_async8(uint32_t smem_dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_dst), "l"(src) : "memory");
 }
@@ -134,6 +160,31 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
     return v;
 }
 
+// As mbar_wait_bounded, by the barrier's shared-memory address.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait_bounded(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                 volatile int *abort) {
+    if (bar_try(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (bar_try(bar, parity)) return true;
+        if ((it & 63u) == 0u && ((abort != nullptr && *abort) || globaltimer_ns() - t0 > limit_ns)) return false;
+    }
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+
 // Token (of a group of 8) in MMA row g.  A K fragment is read by the lanes of
 // rows g, g + 1 together (16 bytes a lane; D = 64: rows g .. g + 3, 8 bytes a
 // lane), a V fragment by the lanes of rows 0, 2, 4, 6 or 1, 3, 5, 7.  Rows lie
@@ -146,44 +197,49 @@ __device__ __forceinline__ int tok_of(int g) {
     return D == 128 ? g ^ ((g >> 1) & 1) : g ^ (g >> 2);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
+// First step of worker w's share of T steps over W workers: floor(w T / W).
+__device__ __forceinline__ int int4_share(unsigned w, int T, int W) {
+    const unsigned long long x = (unsigned long long)w * unsigned(T);
+    return x < (1ull << 32) ? int(unsigned(x) / unsigned(W)) : int(x / unsigned(W));
+}
+
+template <int D, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 1)
     gqa_paged_int4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                          const Int4Args a) {
+                          const __grid_constant__ CUtensorMap p_map, const Int4Args a) {
     constexpr int ROWB = D / 2;     // bytes of a row
     constexpr int KW = D / 32;      // K words a lane holds of a token
     constexpr int VW = D / 64;      // V words a lane holds of a token
     constexpr int DB = D / 16;      // output blocks: block j holds elements (D/8) gi + 2 j, + 2 j + 1
     constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
     extern __shared__ __align__(1024) uint8_t smem4[];
-    uint8_t *tail = smem4 + int4_ring_bytes(a.stages, a.stage_bytes);
-    uint64_t *full = reinterpret_cast<uint64_t *>(tail);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem4);
     uint64_t *empty = full + kInt4MaxStages;
-    long long *sched = reinterpret_cast<long long *>(empty + kInt4MaxStages);  // begin, end, first step of `first`
-    uint32_t *vmask = reinterpret_cast<uint32_t *>(sched + 4);
-    int *first_s = reinterpret_cast<int *>(vmask + kInt4MaxStages);
-    volatile int *abort_flag = first_s + 1;
-    long long *warp_sum = reinterpret_cast<long long *>(smem4);  // the ring is not in use yet
+    uint32_t *vmask = reinterpret_cast<uint32_t *>(empty + kInt4MaxStages);
+    int *sched = reinterpret_cast<int *>(vmask + kInt4MaxStages);  // begin, end, first request, its first step
+    volatile int *abort_flag = sched + 4;
+    int *warp_sum = reinterpret_cast<int *>(smem4 + kInt4HeadBytes);  // the ring is not in use yet
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int consumers = a.HB * a.RG;
+    const int warps = int(blockDim.x) >> 5;
     const int hb0 = blockIdx.x * a.HB;
     const int nh = min(a.HB, a.Hkv - hb0);
     const int cap = a.pages_per_req * a.page_size;
-    const uint32_t ring = smem_u32(smem4);
+    const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes;
 
     if (threadIdx.x == 0) {
         for (int st = 0; st < a.stages; ++st) {
-            mbar_init(full + st, 33);  // the producer's expect, and its 32 lanes' parameter copies
+            mbar_init(full + st, a.param_tma ? 1 : 33);  // the filling warp's expect, and its 32 lanes' parameter copies
             mbar_init(empty + st, nh * a.RG);
         }
-        *first_s = a.B;
+        sched[2] = a.B;
         *abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == consumers && lane == 0) {
+    if (threadIdx.x == 0) {
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
+        if (a.param_tma) prefetch_tmap(&p_map);
     }
     pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
 
@@ -196,84 +252,84 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
     {
         const int run = (a.B + int(blockDim.x) - 1) / int(blockDim.x);
         const int b0 = min(a.B, int(threadIdx.x) * run), b1 = min(a.B, b0 + run);
-        long long mine = 0;
+        int mine = 0;
         for (int b = b0; b < b1; ++b) {
             const int len = __ldg(a.seq_lens + b);
             bad |= len < 0 || len > cap;
             mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step;
         }
-        long long incl = mine;
+        int incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += y;
         }
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        long long T = 0, P = incl - mine;
-        for (int w = 0; w <= consumers; ++w) {
-            const long long s = warp_sum[w];
+        int T = 0, P = incl - mine;
+        for (int w = 0; w < warps; ++w) {
+            const int s = warp_sum[w];
             T += s;
             if (w < warp) P += s;
         }
-        const unsigned long long W = a.workers, w = blockIdx.y;
-        const bool narrow = (unsigned long long)T * (W + 1) < (1ull << 32);
-        const long long begin = narrow ? unsigned(w * T) / unsigned(W) : w * T / W;
-        const long long end = narrow ? unsigned((w + 1) * T) / unsigned(W) : (w + 1) * T / W;
+        const int begin = int4_share(blockIdx.y, T, a.workers), end = int4_share(blockIdx.y + 1, T, a.workers);
         const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
-        int hit = a.B;
-        long long hit_p = 0;
+        int hit = a.B, hit_p = 0;
         for (int b = b0; b < b1; ++b) {
             const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
-            const long long n = (len + kInt4Step - 1) / kInt4Step;
+            const int n = (len + kInt4Step - 1) / kInt4Step;
             if (record) a.step_prefix[b] = P;
             if (hit == a.B && P + (n > 0 ? n : 1) > begin) hit = b, hit_p = P;
             P += n;
         }
         if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
-        if (hit < a.B) atomicMin(first_s, hit);
-        if (threadIdx.x == 0) sched[0] = begin, sched[1] = end, sched[2] = T;
+        if (hit < a.B) atomicMin(sched + 2, hit);
+        if (threadIdx.x == 0) sched[0] = begin, sched[1] = end, sched[3] = 0;
         __syncthreads();  // also: every warp is done with warp_sum, which lies in the ring
-        if (hit < a.B && hit == *first_s) sched[2] = hit_p;
+        if (hit < a.B && hit == sched[2]) sched[3] = hit_p;
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
         bad = false;
         fence_proxy_async_shared();  // warp_sum's place is written by TMA next
         __syncthreads();
     }
-    const long long w_begin = sched[0], w_end = sched[1];
-    int seg_b = *first_s;
-    long long seg_p = sched[2], seg_t = w_begin;
+    const int w_begin = sched[0], w_end = sched[1];
+    int seg_b = sched[2], seg_p = sched[3], seg_t = w_begin;
     const bool last_worker = int(blockIdx.y) == a.workers - 1;
 
-    // Segment of the worker's share: steps [seg_t, seg_next) of request seg_b.
-    auto more = [&] { return seg_b < a.B && (seg_t < w_end || (last_worker && seg_t == w_end)); };
+    const int R = a.box_rows;
+    // Offsets in a stage: a token's row lies in box t / R, head h, row t % R.
+    const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
+    auto par_off = [&](int t, int h) { return 2 * v_off + uint32_t(t / R) * a.param_pitch + uint32_t((t % R) * a.HB + h) * 8; };
 
     // =============================================================== producer
-    if (warp == consumers) {
-        const int R = a.box_rows;
-        const uint32_t box_bytes = uint32_t(a.HB) * R * ROWB;
-        const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
-        const uint32_t p_off = 2 * v_off;
-        int gs = 0, st = 0;
-        uint32_t phase = 0;  // of the stage's empty barrier
+    if (warp == warps - 1) {
+        const uint32_t box_bytes = uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
+        const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
+        const bool first = lane % R == 0;  // of a box
+        int st = 0, gs = 0;
+        uint32_t phase = 0;
         bool failed = false;
-        while (more() && !failed) {
+        while (seg_t < w_end && !failed) {
             const int len = min(max(__ldg(a.seq_lens + seg_b), 0), cap);
-            const long long steps_b = (len + kInt4Step - 1) / kInt4Step;
-            const long long seg_next = min(w_end, seg_p + steps_b);
-            const int t_begin = int(seg_t - seg_p) * kInt4Step;
-            const int t_end = min(int(seg_next - seg_p) * kInt4Step, len);
+            const int steps_b = (len + kInt4Step - 1) / kInt4Step;
+            const int seg_next = min(w_end, seg_p + steps_b);
             const int32_t *table = a.page_table + size_t(seg_b) * a.pages_per_req;
-            int t = t_begin + lane;
+            const int t_end = min((seg_next - seg_p) * kInt4Step, len);
+            int t = (seg_t - seg_p) * kInt4Step + lane;
+            int slot = t % a.page_size;
             int page = t < t_end ? __ldg(table + t / a.page_size) : 0;
-            for (int s0 = t_begin; s0 < t_end; s0 += kInt4Step, ++gs) {
+            for (; t - lane < t_end; ++gs) {
                 const bool in = t < t_end;
                 const bool ok = in && page >= 0 && page < a.num_pages;
                 bad |= in && !ok;
-                const int row = ok ? page * a.page_size + t % a.page_size : 0;
+                const int row = ok ? page * a.page_size + slot : 0;
                 // the next step's page is on its way while this one is issued
                 t += kInt4Step;
+                slot = t % a.page_size;
                 if (t < t_end) page = __ldg(table + t / a.page_size);
+                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                const bool box = ok && first;  // its first token's page holds all of a box
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
                 if (gs >= a.stages) {
                     bool free = true;
                     if (lane == 0) free = mbar_wait_bounded(empty + st, phase ^ 1, a.wait_limit_ns, abort_flag);
@@ -282,26 +338,25 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
                         break;
                     }
                 }
-                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
                 if (!(a.fault_mode == 1 && gs == 0)) {
-                    const bool issue = ok && lane % R == 0;  // a box's first token: its page holds all of the box
-                    const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
                     if (lane == 0) {
                         vmask[st] = valid;
-                        mbar_arrive_expect_tx(full + st, 2 * boxes * box_bytes);
+                        mbar_arrive_expect_tx(full + st, boxes * box_bytes);
                     }
                     __syncwarp();
                     const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
-                    if (issue) {
-                        const uint32_t dst = base + uint32_t(lane / R) * a.box_pitch;
-                        tma_load_3d(dst, &k_map, full + st, 0, row, hb0);
-                        tma_load_3d(dst + v_off, &v_map, full + st, 0, row, hb0);
+                    if (box) {
+                        tma_load_3d(base + box_at, &k_map, full + st, 0, row, hb0);
+                        tma_load_3d(base + box_at + v_off, &v_map, full + st, 0, row, hb0);
+                        if (a.param_tma) tma_load_2d(base + par_at, &p_map, full + st, hb0 * 4, row);
                     }
-                    if (ok) {
-                        const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
-                        for (int h = 0; h < nh; ++h) cp_async8(base + p_off + uint32_t(h * kInt4Step + lane) * 8, src + h * 4);
+                    if (!a.param_tma) {
+                        if (ok) {
+                            const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
+                            for (int h = 0; h < nh; ++h) cp_async8(base + par_at + h * 8, src + h * 4);
+                        }
+                        cp_async_arrive(full + st);
                     }
-                    cp_async_arrive(full + st);
                 }
                 if (++st == a.stages) st = 0, phase ^= 1;
             }
@@ -332,13 +387,8 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
     if (lh >= nh) return;
     const int g = hb0 + lh;
     const int gi = lane >> 2, c = lane & 3;
-    const int R = a.box_rows;
-    // Offsets in a stage: a token's row lies in box t / R, head lh, row t % R.
-    const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
     auto row_off = [&](int t) { return uint32_t(t / R) * a.box_pitch + uint32_t(lh * R + t % R) * ROWB; };
     auto swz = [&](uint32_t off, int unit) { return D == 128 ? (uint32_t(unit) ^ ((off >> 7) & 3u)) << 4 : uint32_t(unit) << 4; };
-    const uint32_t d8 = R == 16 ? 8 * ROWB : uint32_t(8 / R) * a.box_pitch;     // to the token 8 later (keeps the swizzle)
-    const uint32_t d16 = R == 16 ? a.box_pitch : uint32_t(16 / R) * a.box_pitch;  // 16 later
     const uint32_t k_row = row_off(tok_of<D>(gi));
     const uint32_t k_off = D == 128 ? k_row + swz(k_row, c) : k_row + 8 * c;
     uint32_t vo[2];  // tokens of MMA columns 2 c, 2 c + 1
@@ -347,19 +397,20 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
         const uint32_t r = row_off(tok_of<D>(2 * c + e));
         vo[e] = v_off + (D == 128 ? r + swz(r, gi >> 1) + (gi & 1) * 8 : r + 4 * gi);
     }
-    const uint32_t p_off = 2 * v_off + uint32_t(lh * kInt4Step + tok_of<D>(gi)) * 8;
     const int tok0 = tok_of<D>(gi);
+    const uint32_t p_off = par_off(tok0, lh);
+
+    const uint32_t bars = smem_u32(full);  // full, empty, then the stages' token masks
 
     int st = 0;
     uint32_t phase = 0;
     bool failed = false;
-    while (more() && !failed) {
+    // Segment of the share: steps [seg_t, seg_next) of request seg_b.
+    while (seg_b < a.B && (seg_t < w_end || (last_worker && seg_t == w_end))) {
         const int b = seg_b;
         const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
-        const long long steps_b = (len + kInt4Step - 1) / kInt4Step;
-        const long long seg_next = min(w_end, seg_p + steps_b);
-        const int t_begin = int(seg_t - seg_p) * kInt4Step;
-        const int t_end = min(int(seg_next - seg_p) * kInt4Step, len);
+        const int steps_b = (len + kInt4Step - 1) / kInt4Step;
+        const int seg_next = min(w_end, seg_p + steps_b);
         const bool complete = seg_t == seg_p && seg_next == seg_p + steps_b;
         const int slot = seg_t == w_begin ? 0 : 1;
 
@@ -425,22 +476,24 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < DB; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
         }
-        // first token that some row does not see (all see those before it)
-        const int t_causal = a.Sq > 1 ? len - a.Sq + 1 : 0x7fffffff;
+        const int n_seg = seg_next - seg_t;
+        // from this many steps before the segment's end some row may not see a
+        // token (row 0 sees none past len - Sq)
+        const int n_causal = a.Sq > 1 ? min(n_seg, n_seg - (max(len - a.Sq + 1, 0) / kInt4Step - (seg_t - seg_p))) : 0;
 
-        for (int s0 = t_begin; s0 < t_end; s0 += kInt4Step) {
-            const bool ok = mbar_wait_bounded(full + st, phase, a.wait_limit_ns, abort_flag);
+        for (int left = n_seg; left > 0; --left) {
+            const bool ok = bar_wait_bounded(bars + 8 * st, phase, a.wait_limit_ns, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
             }
             const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
-            const uint32_t mask = vmask[st];
+            const uint32_t mask = lds32(bars + 16 * kInt4MaxStages + 4 * st);
             uint32_t kw[4][KW];  // token group j: tokens tok0 + 8 j
             uint2 par[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t at = base + k_off + (j & 1) * d8 + (j >> 1) * d16;
+                const uint32_t at = base + k_off + (j & 1) * a.tok8 + (j >> 1) * a.tok16;
                 if constexpr (KW == 4) {
                     const uint4 x = lds128(at);
                     kw[j][0] = x.x, kw[j][1] = x.y, kw[j][2] = x.z, kw[j][3] = x.w;
@@ -448,25 +501,8 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
                     const uint2 x = lds64(at);
                     kw[j][0] = x.x, kw[j][1] = x.y;
                 }
-                par[j] = lds64(base + p_off + j * 64);
+                par[j] = lds64(base + p_off + (j & 1) * a.par8 + (j >> 1) * a.par16);
             }
-            uint32_t vw[8][VW];  // token pair j: tokens of columns 2 c, 2 c + 1, 8 j later
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t at = base + vo[e] + (j & 1) * d8 + (j >> 1) * d16;
-                    if constexpr (VW == 2) {
-                        const uint2 x = lds64(at);
-                        vw[2 * j + e][0] = x.x, vw[2 * j + e][1] = x.y;
-                    } else {
-                        vw[2 * j + e][0] = lds32(at);
-                    }
-                }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + st);
-            if (++st == a.stages) st = 0, phase ^= 1;
-
             // ---- scores of 2 x 16 tokens
             float acc[NT][2][4];
 #pragma unroll
@@ -503,7 +539,8 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
                         y = fmaf(y, k2.x, k2.y * qs[nt][e]);
                     }
             }
-            if (mask != 0xffffffffu || s0 + kInt4Step > t_causal) {  // tokens that are not there, or not seen by all rows
+            if (mask != 0xffffffffu || left <= n_causal) {  // tokens that are not there, or not seen by all rows
+                const int s0 = (seg_next - seg_p - left) * kInt4Step;  // the step's first token
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool there = (mask >> (tok0 + 8 * j)) & 1u;
@@ -518,23 +555,31 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
                         }
                 }
             }
-            float p[NT][4][2], wt[NT][4][2];
-            float top = 0.f;
+            // Weights of V as fp16 pairs (rows 2 c, 2 c + 1), the step's sums of
+            // p and p vz, and the largest weight.
+            uint32_t wt[NT][4], top = 0;
+            float sp[NT][2], sz[NT][2];
             auto weigh = [&] {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sp[nt][e] = sz[nt][e] = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        float p[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            p[nt][j][e] = fast_exp2(fmaf(acc[nt][j >> 1][2 * (j & 1) + e], A[nt][e], -R_[nt][e]));
-                            wt[nt][j][e] = p[nt][j][e] * vs[j];
+                            p[e] = fast_exp2(fmaf(acc[nt][j >> 1][2 * (j & 1) + e], A[nt][e], -R_[nt][e]));
+                            sp[nt][e] += p[e];
+                            sz[nt][e] = fmaf(p[e], vz[j], sz[nt][e]);
                         }
-                        top = fmax3(top, wt[nt][j][0], wt[nt][j][1]);
+                        wt[nt][j] = pack_f16x2(p[0] * vs[j], p[1] * vs[j]);
+                        top = hmax2(top, wt[nt][j]);
                     }
+                }
             };
             weigh();
-            if (__any_sync(0xffffffffu, top > 512.f)) {
+            if (__any_sync(0xffffffffu, above_512(top))) {
                 // Move the references up to the step's largest score + log2(V
                 // scale): the largest weight of the row is then 1.
 #pragma unroll
@@ -567,18 +612,34 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
                 }
                 weigh();
             }
-            uint32_t pb[NT][4];  // weights of row gi for the tokens of columns 2 c, 2 c + 1 of group j
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        l[nt][e] += p[nt][j][e];
-                        z[nt][e] = fmaf(p[nt][j][e], vz[j], z[nt][e]);
-                    }
-                    pb[nt][j] = movmatrix_trans(pack_f16x2(wt[nt][j][0], wt[nt][j][1]));
+                for (int e = 0; e < 2; ++e) {
+                    l[nt][e] += sp[nt][e];
+                    z[nt][e] += sz[nt][e];
                 }
+                // to row gi's weights for the tokens of columns 2 c, 2 c + 1 of group j
+#pragma unroll
+                for (int j = 0; j < 4; ++j) wt[nt][j] = movmatrix_trans(wt[nt][j]);
+            }
+
+            uint32_t vw[8][VW];  // token pair j: tokens of columns 2 c, 2 c + 1, 8 j later
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t at = base + vo[e] + (j & 1) * a.tok8 + (j >> 1) * a.tok16;
+                    if constexpr (VW == 2) {
+                        const uint2 x = lds64(at);
+                        vw[2 * j + e][0] = x.x, vw[2 * j + e][1] = x.y;
+                    } else {
+                        vw[2 * j + e][0] = lds32(at);
+                    }
+                }
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars + 8 * (kInt4MaxStages + st));
+            if (++st == a.stages) st = 0, phase ^= 1;
 
             // ---- O^T += V^T . weights
 #pragma unroll
@@ -594,8 +655,8 @@ __global__ void __launch_bounds__(32 * (kInt4MaxWarps + 1), NT == 1 ? 2 : 1)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const int j = 4 * w + 2 * h;
-                            mma_f16_add(o[nt][j], x & M0, x & M1, y & M0, y & M1, pb[nt][2 * t], pb[nt][2 * t + 1]);
-                            mma_f16_add(o[nt][j + 1], x8 & M0, x8 & M1, y8 & M0, y8 & M1, pb[nt][2 * t], pb[nt][2 * t + 1]);
+                            mma_f16_add(o[nt][j], x & M0, x & M1, y & M0, y & M1, wt[nt][2 * t], wt[nt][2 * t + 1]);
+                            mma_f16_add(o[nt][j + 1], x8 & M0, x8 & M1, y8 & M0, y8 & M1, wt[nt][2 * t], wt[nt][2 * t + 1]);
                         }
                     }
         }
@@ -667,31 +728,33 @@ __global__ void __launch_bounds__(32 * kInt4MergeWarps) gqa_paged_int4_merge_ker
     pdl_wait_primary();
     const int b = blockIdx.y, rr = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long W = a.workers;
-    const long long P = a.step_prefix[b], n = a.step_prefix[b + 1] - P, T = a.step_prefix[a.B];
+    const int W = a.workers;
+    const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P, T = a.step_prefix[a.B];
     if (n == 0) return;  // an empty request: written by the main kernel
-    const bool narrow = (unsigned long long)(T + 1) * (unsigned long long)(W + 1) < (1ull << 32);
-    auto div = [narrow](long long x, long long y) -> long long { return narrow ? (long long)(unsigned(x) / unsigned(y)) : x / y; };
     // worker of step s: the largest w with floor(w T / W) <= s
-    const long long w_first = div((P + 1) * W - 1, T), w_last = div((P + n) * W - 1, T);
+    auto holder = [&](int s) {
+        const unsigned long long x = (unsigned long long)(s + 1) * unsigned(W) - 1;
+        return x < (1ull << 32) ? int(unsigned(x) / unsigned(T)) : int(x / unsigned(T));
+    };
+    const int w_first = holder(P), w_last = holder(P + n - 1);
     if (w_first == w_last) return;  // one worker: written by the main kernel
     const int g = rr / a.Mq, r = rr - g * a.Mq;
     const int hb = g / a.HB, lh = g - hb * a.HB;
-    const long long each = (w_last - w_first + kInt4MergeWarps) / kInt4MergeWarps;
-    const long long from = w_first + warp * each, to = min(w_last + 1, from + each);
-    const bool before = div(w_first * T, W) < P;  // the first worker starts in an earlier request: its last slot
+    const int each = (w_last - w_first + kInt4MergeWarps) / kInt4MergeWarps;
+    const int from = w_first + warp * each, to = min(w_last + 1, from + each);
+    const bool before = int4_share(w_first, T, W) < P;  // the first worker starts in an earlier request: its last slot
 
     float m = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (long long w0 = from; w0 < to; w0 += kInt4MergeBatch) {
+    for (int w0 = from; w0 < to; w0 += kInt4MergeBatch) {
         float l2[kInt4MergeBatch], x[kInt4MergeBatch][V];
 #pragma unroll
         for (int k = 0; k < kInt4MergeBatch; ++k) {
-            const long long w = w0 + k;
+            const int w = w0 + k;
             l2[k] = -INFINITY;
             // a worker without a step (T < W) holds nothing
-            if (w >= to || (T < W && div(w * T, W) == div((w + 1) * T, W))) continue;
+            if (w >= to || (T < W && int4_share(w, T, W) == int4_share(w + 1, T, W))) continue;
             const int slot = w == w_first && before ? 1 : 0;
             const size_t prow = ((((size_t(hb) * W + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
             l2[k] = __ldg(a.lse_part + prow);
