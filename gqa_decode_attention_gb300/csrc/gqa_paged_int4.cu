@@ -13,13 +13,14 @@ namespace {
 constexpr int kInt4MaxRows = 128;  // query rows per KV head
 constexpr int kMaxDevices = 64;
 
-// What a shape runs as.
+// What a shape runs as, before the number of workers is known.
 struct Int4Plan {
     int B, Sq, Hq, Hkv, D, G, Mq;
     int NT;      // tiles of 8 query rows a consumer warp holds
     int RG, HB;  // consumer warps per head, heads per CTA
+    int rings, lanes;  // most rings of a CTA; groups of HB x RG warps on each
     int R;       // tokens of a TMA box: the largest power of two, at most 16, that divides the page size
-    int pitch, par_pitch, stage_bytes, stages, smem, threads, nhb;
+    int pitch, par_pitch, stage_bytes, nhb;
     bool param_tma;
     long long max_steps;
 };
@@ -30,95 +31,81 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     if (Sq < 1 || Hq < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
     if ((long long)(Hq / Hkv) * Sq > kInt4MaxRows) return GQA_ERR_UNSUPPORTED;
     if ((long long)pages_per_req * page_size > (1LL << 31) - 64) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
+    p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
+    if (p->max_steps >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
     p->B = B, p->Sq = Sq, p->Hq = Hq, p->Hkv = Hkv, p->D = D;
     p->G = Hq / Hkv;
     p->Mq = p->G * Sq;
     p->NT = p->Mq > 8 ? 2 : 1;
     p->RG = (p->Mq + 8 * p->NT - 1) / (8 * p->NT);
-    const int cap = p->NT == 1 ? kInt4MaxWarps : 4;
     int hb = 1;
-    while (hb < Hkv && 2 * hb * p->RG <= cap) hb *= 2;
+    while (hb < Hkv && 2 * hb * p->RG <= 8) hb *= 2;
     p->HB = hb;
     p->nhb = (Hkv + hb - 1) / hb;
+    const int groups = int4_consumers(p->NT) / (hb * p->RG);
+    p->rings = groups < kInt4MaxRings ? groups : kInt4MaxRings;
+    p->lanes = groups / p->rings;
     p->R = 16;
     while (page_size % p->R != 0) p->R /= 2;
     const int row = D / 2;
     p->pitch = (hb * p->R * row + 127) / 128 * 128;  // TMA writes to 128-byte boundaries
-    p->par_pitch = (hb * p->R * 8 + 127) / 128 * 128;
     p->param_tma = Hkv % 2 == 0 && hb > 1;           // a box's rows, and their stride, in whole 16 bytes
-    const int align = D == 128 ? 512 : 128;          // the swizzle repeats every 512 bytes
-    p->stage_bytes = ((kInt4Step / p->R) * (2 * p->pitch + p->par_pitch) + align - 1) / align * align;
-    // shared memory of an SM over the CTAs that registers allow (16 warps of 8
-    // rows, 12 of 16), less what the system keeps
-    const int warps = hb * p->RG, ctas = p->NT == 1 ? 16 / warps : warps <= 4 ? 12 / warps : 1;
-    p->stages = (228 * 1024 / ctas - 1024 - kInt4HeadBytes) / p->stage_bytes;
-    if (p->stages > kInt4MaxStages) p->stages = kInt4MaxStages;
-    if (p->stages < 2) p->stages = 2;
-    p->smem = p->stages * p->stage_bytes + kInt4HeadBytes;
-    p->threads = 32 * (hb * p->RG + 1);
-    p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
-    if (p->max_steps >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
+    p->par_pitch = p->param_tma ? (hb * p->R * 8 + 127) / 128 * 128 : hb * p->R * 8;
+    // 512: the period of the swizzle
+    p->stage_bytes = ((kInt4Step / p->R) * (2 * p->pitch + p->par_pitch) + 511) / 512 * 512;
     return GQA_OK;
 }
 
-// Instances: 8 query rows a warp and up to 8 warps; 16 rows a warp and up to 4
-// warps (three CTAs an SM); 16 rows and 5 to 8 warps (65 to 128 rows a head).
-int instance_of(const Int4Plan &p) { return p.NT == 1 ? 0 : p.HB * p.RG <= 4 ? 1 : 2; }
-
 const void *kernel_of(const Int4Plan &p) {
-    static const void *const kernels[2][3] = {
-        {reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 1, 8>), reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2, 4>),
-         reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2, 8>)},
-        {reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 1, 8>), reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2, 4>),
-         reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2, 8>)}};
-    return kernels[p.D == 128][instance_of(p)];
+    if (p.D == 64)
+        return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 1>)
+                         : reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2>);
+    return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 1>)
+                     : reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2>);
 }
 
-// Resident CTAs per SM of the plan's instance on `dev`, the current device;
-// the first query of an instance also raises its shared-memory limit there.
-int int4_occupancy(int dev, const Int4Plan &p) {
-    struct Entry {
-        int smem, threads, ctas;
-    };
+// Shared memory a CTA may have on `dev`, the current device; the first call
+// there raises the kernel's limit to it.  0 on an error.
+int int4_smem(int dev, const Int4Plan &p) {
     static std::mutex mu;
-    static Entry table[kMaxDevices][2][3][64];
-    static int used[kMaxDevices][2][3];
-    static bool raised[kMaxDevices][2][3];
+    static int most[kMaxDevices][2][2];
     std::lock_guard<std::mutex> lk(mu);
-    const int d = p.D == 128, n = instance_of(p);
-    Entry *t = table[dev][d][n];
-    for (int i = 0; i < used[dev][d][n]; ++i)
-        if (t[i].smem == p.smem && t[i].threads == p.threads) return t[i].ctas;
-    const void *kern = kernel_of(p);
-    if (!raised[dev][d][n]) {
-        int most = 0;
-        if (cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+    int &m = most[dev][p.D == 128][p.NT - 1];
+    if (m == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel_of(p), cudaFuncAttributeMaxDynamicSharedMemorySize, n) != cudaSuccess)
             return 0;
-        raised[dev][d][n] = true;
+        m = n;
     }
-    int ctas = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kern, p.threads, p.smem) != cudaSuccess) return 0;
-    if (used[dev][d][n] < 64) t[used[dev][d][n]++] = {p.smem, p.threads, ctas};
-    return ctas;
+    return m;
 }
 
-// Workers per head block: one resident CTA slot each, and no more than the
+// CTAs of one wave per head block (a CTA's registers fill an SM).
+int int4_ctas(const Int4Plan &p, int dev) {
+    const int n = host_sm_count(dev) / p.nhb;
+    return n < 1 ? 1 : n;
+}
+
+// Workers per head block: every ring of one wave, and no more than the
 // requests can have steps.
 int int4_workers(const Int4Plan &p, int requested, int dev) {
     long long W = requested;
     if (requested == 0) {
-        const long long occ = int4_occupancy(dev, p);
-        W = host_sm_count(dev) * (occ > 0 ? occ : 1) / p.nhb;
+        W = (long long)int4_ctas(p, dev) * p.rings;
         if (W > p.max_steps) W = p.max_steps;
     }
     if (W > 65535) W = 65535;
     return W < 1 ? 1 : int(W);
 }
 
+size_t int4_part_rows(const Int4Plan &p, int workers) {
+    return workers <= 1 ? 0 : size_t(p.nhb) * workers * 2 * p.HB * p.Mq;
+}
+
 size_t int4_workspace(const Int4Plan &p, int workers) {
-    if (workers <= 1) return 0;
-    const size_t rows = size_t(p.nhb) * workers * 2 * p.HB * p.Mq;
+    const size_t rows = int4_part_rows(p, workers);
+    if (rows == 0) return 0;
     return host_align256(rows * p.D * sizeof(float)) + host_align256(rows * sizeof(float)) +
            host_align256((size_t(p.B) + 1) * sizeof(int));
 }
@@ -165,7 +152,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     if (!host_current_device(&dev)) return GQA_ERR_CUDA;
     CUtensorMap k_map, v_map, p_map = {};
     const long long rows = (long long)num_pages * page_size;
-    if (int4_occupancy(dev, p) < 1 || !host_int4_tensor_map(&k_map, k_pool, rows, Hkv, D / 2, p.R, p.HB) ||
+    const int smem = int4_smem(dev, p);
+    if (smem == 0 || !host_int4_tensor_map(&k_map, k_pool, rows, Hkv, D / 2, p.R, p.HB) ||
         !host_int4_tensor_map(&v_map, v_pool, rows, Hkv, D / 2, p.R, p.HB) ||
         (p.param_tma && !host_int4_param_map(&p_map, kv_params, rows, Hkv, p.R, p.HB))) {
         cudaGetLastError();
@@ -196,7 +184,7 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     if (need > 0) {
-        const size_t part_rows = size_t(p.nhb) * workers * 2 * p.HB * p.Mq;
+        const size_t part_rows = int4_part_rows(p, workers);
         char *w = static_cast<char *>(ws);
         a.o_part = reinterpret_cast<float *>(w);
         w += host_align256(part_rows * D * sizeof(float));
@@ -215,7 +203,17 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.workers = workers;
     a.HB = p.HB;
     a.RG = p.RG;
-    a.stages = p.stages;
+    // One ring a CTA while the workers are fewer than the SMs; the rings share
+    // the CTA's memory.
+    const int ctas = int4_ctas(p, dev);
+    a.rings = workers >= ctas * p.rings ? p.rings : (workers + ctas - 1) / ctas;
+    a.rings_max = p.rings;
+    a.lanes = p.lanes;
+    const int boxes = (p.lanes - 1) * p.HB * p.RG * p.NT * (D / 4 + 6) * 128;  // what the lanes of a ring hand over
+    a.stages = ((smem - kInt4HeadBytes) / a.rings - boxes) / p.stage_bytes;
+    if (a.stages > kInt4MaxStages) a.stages = kInt4MaxStages;
+    a.stages -= a.stages % p.lanes;  // a stage serves one lane only
+    const int grid_y = (workers + a.rings - 1) / a.rings;
     a.box_rows = p.R;
     a.box_pitch = p.pitch;
     a.stage_bytes = p.stage_bytes;
@@ -234,13 +232,19 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     const bool timed = before != nullptr && after != nullptr;
     if (timed) cudaEventRecord(before, cs);
     void *args[] = {&k_map, &v_map, &p_map, &a};
-    cudaError_t e = launch(kernel_of(p), dim3(unsigned(p.nhb), unsigned(workers)), p.threads, p.smem, args, cs);
+    cudaError_t e = launch(kernel_of(p), dim3(unsigned(p.nhb), unsigned(grid_y)), int4_threads(p.NT),
+                           kInt4HeadBytes + a.rings * (a.stages * p.stage_bytes + boxes), args, cs);
     if (timed) cudaEventRecord(after, cs);
-    if (e == cudaSuccess && workers > 1) {
+    if (e == cudaSuccess && need > 0) {
+        // many partials a row: all warps of a CTA on one row
+        const bool split = workers > 16LL * B;
+        const int rows = Hkv * p.Mq, per = split ? 1 : int4_merge_warps(false);
+        const void *merge = split ? (D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64, true>)
+                                             : reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<128, true>))
+                                  : (D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64, false>)
+                                             : reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<128, false>));
         void *margs[] = {&a};
-        const void *merge = D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64>)
-                                    : reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<128>);
-        e = launch(merge, dim3(unsigned(Hkv * p.Mq), unsigned(B)), 32 * kInt4MergeWarps, 0, margs, cs);
+        e = launch(merge, dim3(unsigned((rows + per - 1) / per), unsigned(B)), 32 * int4_merge_warps(split), 0, margs, cs);
     }
     if (owned) cudaFreeAsync(ws, cs);
     if (e != cudaSuccess) {

@@ -37,14 +37,25 @@
 // and the loads run ahead across request borders.
 #pragma once
 
+#include <stddef.h>
+
 #include "gqa_common.cuh"
 #include "gqa_params.h"
 
 namespace gqa {
 
 constexpr int kInt4Step = 32;       // tokens a stage
-constexpr int kInt4MaxStages = 8;
-constexpr int kInt4MaxWarps = 8;    // consumer warps of a CTA
+constexpr int kInt4MaxStages = 8;   // of a ring
+constexpr int kInt4MaxRings = 4;    // of a CTA, one producer warp each
+// Consumer warps of a CTA that hold NT tiles of 8 query rows, and the
+// registers a thread of theirs and of the producers' warpgroup has: together
+// what the CTA was launched with (20 warps of 96, or 12 of 168).
+__host__ __device__ constexpr int int4_consumers(int nt) { return nt == 1 ? 16 : 8; }
+__host__ __device__ constexpr int int4_threads(int nt) { return 32 * (int4_consumers(nt) + 4); }
+__host__ __device__ constexpr int int4_consumer_regs(int nt) { return nt == 1 ? 112 : 216; }
+__host__ __device__ constexpr int int4_producer_regs(int nt) { return nt == 1 ? 32 : 72; }
+static_assert(16 * int4_consumer_regs(1) + 4 * int4_producer_regs(1) == 20 * 96, "registers");
+static_assert(8 * int4_consumer_regs(2) + 4 * int4_producer_regs(2) == 12 * 168, "registers");
 constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
 
 struct Int4Args {
@@ -58,6 +69,8 @@ struct Int4Args {
     int *step_prefix;         // [B + 1] first step of each request (several workers)
     int B, Sq, Hq, Hkv, G, Mq, page_size, pages_per_req, num_pages;
     int workers, HB, RG;      // workers per head block; heads of a CTA, warps (of 8 or 16 query rows) a head
+    int rings, rings_max;     // rings (workers) of a CTA, and how many its warps could serve
+    int lanes;                // groups of HB x RG warps that take turns at a ring's steps
     int stages, box_rows, box_pitch, stage_bytes;
     int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
     unsigned param_pitch;     // of a box's parameters in a stage
@@ -69,10 +82,27 @@ struct Int4Args {
     unsigned *err;
 };
 
-// Shared memory of a CTA: barriers, masks, schedule and flag, then the ring
-// (at constant addresses, and on the swizzle's 512-byte period).
-constexpr int kInt4HeadBytes = 512;
-static_assert(2 * kInt4MaxStages * 8 + kInt4MaxStages * 4 + 5 * 4 <= kInt4HeadBytes, "head");
+// Shared memory of a CTA: barriers, masks, schedules and flag of its rings (at
+// constant addresses), then the rings (on the swizzle's 512-byte period).
+struct Int4Head {
+    uint64_t full[kInt4MaxRings][kInt4MaxStages], empty[kInt4MaxRings][kInt4MaxStages];
+    uint64_t ready[kInt4MaxRings], taken[kInt4MaxRings];  // lanes: results handed to the first lane, and taken
+    uint32_t mask[kInt4MaxRings][kInt4MaxStages];  // tokens of a stage that are there
+    int begin[kInt4MaxRings], end[kInt4MaxRings];  // steps of the ring's share
+    int first[kInt4MaxRings], first_p[kInt4MaxRings];  // its first request, and that one's first step
+    int abort;
+};
+constexpr int kInt4HeadBytes = 1024;
+static_assert(sizeof(Int4Head) <= kInt4HeadBytes, "head");
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -203,40 +233,38 @@ __device__ __forceinline__ int int4_share(unsigned w, int T, int W) {
     return x < (1ull << 32) ? int(unsigned(x) / unsigned(W)) : int(x / unsigned(W));
 }
 
-template <int D, int NT, int WARPS>
-__global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(int4_threads(NT), 1)
     gqa_paged_int4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                           const __grid_constant__ CUtensorMap p_map, const Int4Args a) {
     constexpr int ROWB = D / 2;     // bytes of a row
     constexpr int KW = D / 32;      // K words a lane holds of a token
     constexpr int VW = D / 64;      // V words a lane holds of a token
     constexpr int DB = D / 16;      // output blocks: block j holds elements (D/8) gi + 2 j, + 2 j + 1
+    constexpr int CW = int4_consumers(NT);
     constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
     extern __shared__ __align__(1024) uint8_t smem4[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem4);
-    uint64_t *empty = full + kInt4MaxStages;
-    uint32_t *vmask = reinterpret_cast<uint32_t *>(empty + kInt4MaxStages);
-    int *sched = reinterpret_cast<int *>(vmask + kInt4MaxStages);  // begin, end, first request, its first step
-    volatile int *abort_flag = sched + 4;
-    int *warp_sum = reinterpret_cast<int *>(smem4 + kInt4HeadBytes);  // the ring is not in use yet
+    Int4Head *head = reinterpret_cast<Int4Head *>(smem4);
+    volatile int *abort_flag = &head->abort;
+    int *warp_sum = reinterpret_cast<int *>(smem4 + kInt4HeadBytes);  // the rings are not in use yet
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int warps = int(blockDim.x) >> 5;
     const int hb0 = blockIdx.x * a.HB;
     const int nh = min(a.HB, a.Hkv - hb0);
     const int cap = a.pages_per_req * a.page_size;
-    const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes;
 
     if (threadIdx.x == 0) {
-        for (int st = 0; st < a.stages; ++st) {
-            mbar_init(full + st, a.param_tma ? 1 : 33);  // the filling warp's expect, and its 32 lanes' parameter copies
-            mbar_init(empty + st, nh * a.RG);
+        for (int r = 0; r < a.rings; ++r) {
+            for (int st = 0; st < a.stages; ++st) {
+                mbar_init(&head->full[r][st], a.param_tma ? 1 : 33);  // the producer's expect (and its lanes' copies)
+                mbar_init(&head->empty[r][st], nh * a.RG);
+            }
+            mbar_init(&head->ready[r], max(1, (a.lanes - 1) * nh * a.RG));
+            mbar_init(&head->taken[r], nh * a.RG);
+            head->first[r] = a.B;
         }
-        sched[2] = a.B;
-        *abort_flag = 0;
+        head->abort = 0;
         fence_mbarrier_init();
-    }
-    if (threadIdx.x == 0) {
         prefetch_tmap(&k_map);
         prefetch_tmap(&v_map);
         if (a.param_tma) prefetch_tmap(&p_map);
@@ -250,7 +278,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
     // step (the last worker for those at the very end).
     bool bad = false;
     {
-        const int run = (a.B + int(blockDim.x) - 1) / int(blockDim.x);
+        const int run = (a.B + int4_threads(NT) - 1) / int4_threads(NT);
         const int b0 = min(a.B, int(threadIdx.x) * run), b1 = min(a.B, b0 + run);
         int mine = 0;
         for (int b = b0; b < b1; ++b) {
@@ -266,43 +294,63 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
         }
         if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        int T = 0, P = incl - mine;
-        for (int w = 0; w < warps; ++w) {
+        int T = 0, P0 = incl - mine;
+#pragma unroll
+        for (int w = 0; w < CW + 4; ++w) {
             const int s = warp_sum[w];
             T += s;
-            if (w < warp) P += s;
+            if (w < warp) P0 += s;
         }
-        const int begin = int4_share(blockIdx.y, T, a.workers), end = int4_share(blockIdx.y + 1, T, a.workers);
         const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
-        int hit = a.B, hit_p = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
-            const int n = (len + kInt4Step - 1) / kInt4Step;
-            if (record) a.step_prefix[b] = P;
-            if (hit == a.B && P + (n > 0 ? n : 1) > begin) hit = b, hit_p = P;
-            P += n;
+        int hit[kInt4MaxRings], hit_p[kInt4MaxRings];
+#pragma unroll
+        for (int r = 0; r < kInt4MaxRings; ++r) {
+            hit[r] = a.B;
+            hit_p[r] = 0;
+            if (r >= a.rings) continue;
+            const int w = r * int(gridDim.y) + int(blockIdx.y);
+            const int begin = int4_share(min(w, a.workers), T, a.workers);
+            int P = P0;
+            for (int b = b0; b < b1; ++b) {
+                const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
+                const int n = (len + kInt4Step - 1) / kInt4Step;
+                if (record && r == 0) a.step_prefix[b] = P;
+                if (hit[r] == a.B && P + (n > 0 ? n : 1) > begin) hit[r] = b, hit_p[r] = P;
+                P += n;
+            }
+            if (hit[r] < a.B) atomicMin(&head->first[r], hit[r]);
+            if (int(threadIdx.x) == r) {
+                head->begin[r] = begin;
+                head->end[r] = int4_share(min(w + 1, a.workers), T, a.workers);
+                head->first_p[r] = 0;
+            }
         }
         if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
-        if (hit < a.B) atomicMin(sched + 2, hit);
-        if (threadIdx.x == 0) sched[0] = begin, sched[1] = end, sched[3] = 0;
-        __syncthreads();  // also: every warp is done with warp_sum, which lies in the ring
-        if (hit < a.B && hit == sched[2]) sched[3] = hit_p;
+        __syncthreads();  // also: every warp is done with warp_sum, which lies in the rings
+#pragma unroll
+        for (int r = 0; r < kInt4MaxRings; ++r)
+            if (r < a.rings && hit[r] < a.B && hit[r] == head->first[r]) head->first_p[r] = hit_p[r];
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
         bad = false;
         fence_proxy_async_shared();  // warp_sum's place is written by TMA next
         __syncthreads();
     }
-    const int w_begin = sched[0], w_end = sched[1];
-    int seg_b = sched[2], seg_p = sched[3], seg_t = w_begin;
-    const bool last_worker = int(blockIdx.y) == a.workers - 1;
 
     const int R = a.box_rows;
     // Offsets in a stage: a token's row lies in box t / R, head h, row t % R.
     const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
     auto par_off = [&](int t, int h) { return 2 * v_off + uint32_t(t / R) * a.param_pitch + uint32_t((t % R) * a.HB + h) * 8; };
 
-    // =============================================================== producer
-    if (warp == warps - 1) {
+    // ============================================================== producers
+    if (warp >= CW) {
+        fewer_registers<int4_producer_regs(NT)>();
+        const int r = warp - CW;
+        if (r >= a.rings) return;
+        uint64_t *full = head->full[r], *empty = head->empty[r];
+        uint32_t *vmask = head->mask[r];
+        const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
+        const int w_end = head->end[r];
+        int seg_b = head->first[r], seg_p = head->first_p[r], seg_t = head->begin[r];
         const uint32_t box_bytes = uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
         const bool first = lane % R == 0;  // of a box
@@ -383,8 +431,20 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
     }
 
     // ============================================================== consumers
-    const int lh = warp / a.RG, rg = warp - lh * a.RG;
-    if (lh >= nh) return;
+    // The CW warps form groups of HB x RG, `lanes` groups to a ring.  Warps of an
+    // SM sub-partition (warp mod 4) run oldest first, and a ring is as fast as
+    // its slowest warp, so each group gets warps of every age.
+    more_registers<int4_consumer_regs(NT)>();
+    const int members = a.HB * a.RG, groups = a.rings_max * a.lanes;
+    const int member = warp / groups, group = (warp + warp / max(groups, 4)) % groups;
+    const int r = group / a.lanes, turn = group - r * a.lanes;
+    const int lh = member / a.RG, rg = member - lh * a.RG;
+    if (member >= members || r >= a.rings || lh >= nh) return;
+    const int w = r * int(gridDim.y) + int(blockIdx.y);  // worker
+    const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
+    const int w_begin = head->begin[r], w_end = head->end[r];
+    int seg_b = head->first[r], seg_p = head->first_p[r], seg_t = w_begin;
+    const bool last_worker = w == a.workers - 1;
     const int g = hb0 + lh;
     const int gi = lane >> 2, c = lane & 3;
     auto row_off = [&](int t) { return uint32_t(t / R) * a.box_pitch + uint32_t(lh * R + t % R) * ROWB; };
@@ -400,9 +460,11 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
     const int tok0 = tok_of<D>(gi);
     const uint32_t p_off = par_off(tok0, lh);
 
-    const uint32_t bars = smem_u32(full);  // full, empty, then the stages' token masks
+    const uint32_t full = smem_u32(head->full[r]), mask_at = smem_u32(head->mask[r]);
+    constexpr uint32_t kEmpty = offsetof(Int4Head, empty) - offsetof(Int4Head, full);
 
-    int st = 0;
+    int handed = 0;  // results handed between the lanes so far
+    int st = turn;  // the stages are a multiple of the lanes: a lane sees every round of its stages
     uint32_t phase = 0;
     bool failed = false;
     // Segment of the share: steps [seg_t, seg_next) of request seg_b.
@@ -481,14 +543,16 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
         // token (row 0 sees none past len - Sq)
         const int n_causal = a.Sq > 1 ? min(n_seg, n_seg - (max(len - a.Sq + 1, 0) / kInt4Step - (seg_t - seg_p))) : 0;
 
-        for (int left = n_seg; left > 0; --left) {
-            const bool ok = bar_wait_bounded(bars + 8 * st, phase, a.wait_limit_ns, abort_flag);
+        // this lane's steps of the segment: every lanes-th of the share's
+        const int skip = a.lanes == 1 ? 0 : (turn + a.lanes - (seg_t - w_begin) % a.lanes) % a.lanes;
+        for (int left = n_seg - skip; left > 0; left -= a.lanes) {
+            const bool ok = bar_wait_bounded(full + 8 * st, phase, a.wait_limit_ns, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
             }
             const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
-            const uint32_t mask = lds32(bars + 16 * kInt4MaxStages + 4 * st);
+            const uint32_t mask = lds32(mask_at + 4 * st);
             uint32_t kw[4][KW];  // token group j: tokens tok0 + 8 j
             uint2 par[4];
 #pragma unroll
@@ -638,8 +702,9 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
                     }
                 }
             __syncwarp();
-            if (lane == 0) bar_arrive(bars + 8 * (kInt4MaxStages + st));
-            if (++st == a.stages) st = 0, phase ^= 1;
+            if (lane == 0) bar_arrive(full + kEmpty + 8 * st);
+            st += a.lanes;
+            if (st >= a.stages) st -= a.stages, phase ^= 1;
 
             // ---- O^T += V^T . weights
 #pragma unroll
@@ -662,6 +727,66 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
         }
         if (failed) break;
 
+        // ---- lanes: the first one takes the others' results, which lie in
+        // shared memory behind the rings, thread for thread.  (Waits on
+        // barriers with a limit, so that a lane that gave up stops the others.)
+        if (a.lanes > 1 && n_seg > 0) {
+            constexpr int kWords = NT * (4 * DB + 6);
+            const uint32_t round = handed++ & 1;
+            float *box = reinterpret_cast<float *>(smem4 + kInt4HeadBytes + a.rings * a.stages * a.stage_bytes) +
+                         (r * (a.lanes - 1) * members + member) * kWords * 32 + lane;
+            const uint32_t ready = smem_u32(&head->ready[r]), taken = smem_u32(&head->taken[r]);
+            const bool wait = turn == 0 || handed > 1;
+            if (wait && !__all_sync(0xffffffffu, bar_wait_bounded(turn == 0 ? ready : taken, turn == 0 ? round : round ^ 1,
+                                                                  a.wait_limit_ns, abort_flag))) {
+                failed = true;
+                break;
+            }
+            if (turn > 0) {
+                box += (turn - 1) * members * kWords * 32;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float *p = box + nt * (4 * DB + 6) * 32;
+#pragma unroll
+                    for (int j = 0; j < DB; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[(4 * j + e) * 32] = o[nt][j][e];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        p[(4 * DB + e) * 32] = R_[nt][e];
+                        p[(4 * DB + 2 + e) * 32] = l[nt][e];
+                        p[(4 * DB + 4 + e) * 32] = z[nt][e];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(ready);
+            } else {
+                for (int k = 1; k < a.lanes; ++k, box += members * kWords * 32) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float *p = box + nt * (4 * DB + 6) * 32;
+                        float mine[2], other[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = p[(4 * DB + e) * 32], m = fmaxf(x, R_[nt][e]);
+                            mine[e] = fast_exp2(R_[nt][e] - m);
+                            other[e] = fast_exp2(x - m);
+                            R_[nt][e] = m;
+                            l[nt][e] = l[nt][e] * mine[e] + p[(4 * DB + 2 + e) * 32] * other[e];
+                            z[nt][e] = z[nt][e] * mine[e] + p[(4 * DB + 4 + e) * 32] * other[e];
+                        }
+#pragma unroll
+                        for (int j = 0; j < DB; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                o[nt][j][e] = o[nt][j][e] * mine[e & 1] + p[(4 * j + e) * 32] * other[e & 1];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(taken);
+            }
+        }
+
         // ---- epilogue of the segment: row 2 c + e of a tile, elements (D/8) gi .. + D/8 - 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -674,7 +799,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
                     Z += __shfl_xor_sync(0xffffffffu, Z, off);
                 }
                 const int r = (rg * NT + nt) * 8 + 2 * c + e;
-                if (r >= a.Mq) continue;
+                if (r >= a.Mq || turn > 0) continue;
                 const float f = L == 0.f ? 0.f : 1.f / L;  // NaN stays
                 const float lse2 = L == 0.f ? -INFINITY : R_[nt][e] + log2f(L);
                 float x[2 * DB];
@@ -684,7 +809,7 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
                     x[2 * j + 1] = fmaf(o[nt][j][2 + e], 1048576.f, Z) * f;
                 }
                 if (!complete) {
-                    const size_t prow = ((((size_t(blockIdx.x) * a.workers + blockIdx.y) * 2 + slot) * a.HB + lh) * a.Mq) + r;
+                    const size_t prow = ((((size_t(blockIdx.x) * a.workers + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
                     float *dst = a.o_part + prow * D + (D / 8) * gi;
 #pragma unroll
                     for (int j = 0; j < 2 * DB; j += 4)
@@ -714,20 +839,20 @@ __global__ void __launch_bounds__(32 * (WARPS + 1), NT == 1 || WARPS == 4 ? 2 : 
     }
 }
 
-// Merge of the partials of requests that several workers share.  CTA (row, b):
-// the workers that hold request b are dealt to its warps in runs, each warp
-// merges its run in order (8 partials in flight), and the warps' results are
-// merged in warp order: the same bits every time.
-constexpr int kInt4MergeWarps = 4;
+// Merge of the partials of requests that several workers share.  CTA (y, b): with SPLIT, one row, whose partials are dealt in runs to all warps and their
+// results merged in warp order -- few rows, many partials each; without, one
+// row a warp.  Each warp has 8 partials in flight and merges them in order:
+// the same bits every time.
 constexpr int kInt4MergeBatch = 8;
+__host__ __device__ constexpr int int4_merge_warps(bool split) { return split ? 16 : 8; }
 
-template <int D>
-__global__ void __launch_bounds__(32 * kInt4MergeWarps) gqa_paged_int4_merge_kernel(const Int4Args a) {
-    constexpr int V = D / 32;
-    __shared__ float sm_m[kInt4MergeWarps], sm_l[kInt4MergeWarps], sm_o[kInt4MergeWarps][D];
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_merge_kernel(const Int4Args a) {
+    constexpr int V = D / 32, NW = int4_merge_warps(SPLIT);
+    __shared__ float sm_m[NW], sm_l[NW], sm_o[SPLIT ? NW : 1][D];
     pdl_wait_primary();
-    const int b = blockIdx.y, rr = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, rr = SPLIT ? int(blockIdx.x) : int(blockIdx.x) * NW + warp;
     const int W = a.workers;
     const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P, T = a.step_prefix[a.B];
     if (n == 0) return;  // an empty request: written by the main kernel
@@ -738,24 +863,28 @@ __global__ void __launch_bounds__(32 * kInt4MergeWarps) gqa_paged_int4_merge_ker
     };
     const int w_first = holder(P), w_last = holder(P + n - 1);
     if (w_first == w_last) return;  // one worker: written by the main kernel
+    if (rr >= a.Hkv * a.Mq) return;
     const int g = rr / a.Mq, r = rr - g * a.Mq;
     const int hb = g / a.HB, lh = g - hb * a.HB;
-    const int each = (w_last - w_first + kInt4MergeWarps) / kInt4MergeWarps;
-    const int from = w_first + warp * each, to = min(w_last + 1, from + each);
+    const int parts = w_last - w_first + 1;
+    const int each = SPLIT ? (parts + NW - 1) / NW : parts;
+    const int from = SPLIT ? warp * each : 0, to = min(parts, from + each);
     const bool before = int4_share(w_first, T, W) < P;  // the first worker starts in an earlier request: its last slot
 
     float m = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int w0 = from; w0 < to; w0 += kInt4MergeBatch) {
+    for (int k0 = from; k0 < to; k0 += kInt4MergeBatch) {
         float l2[kInt4MergeBatch], x[kInt4MergeBatch][V];
 #pragma unroll
         for (int k = 0; k < kInt4MergeBatch; ++k) {
-            const int w = w0 + k;
+            const int part = k0 + k;
             l2[k] = -INFINITY;
+            if (part >= to) continue;
+            const int w = w_first + part;
             // a worker without a step (T < W) holds nothing
-            if (w >= to || (T < W && int4_share(w, T, W) == int4_share(w + 1, T, W))) continue;
-            const int slot = w == w_first && before ? 1 : 0;
+            if (T < W && int4_share(w, T, W) == int4_share(w + 1, T, W)) continue;
+            const int slot = part == 0 && before ? 1 : 0;
             const size_t prow = ((((size_t(hb) * W + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
             l2[k] = __ldg(a.lse_part + prow);
             if constexpr (V == 4) {
@@ -777,29 +906,35 @@ __global__ void __launch_bounds__(32 * kInt4MergeWarps) gqa_paged_int4_merge_ker
             m = mn;
         }
     }
-    if (lane == 0) sm_m[warp] = m, sm_l[warp] = L;
+    if constexpr (SPLIT) {
+        if (lane == 0) sm_m[warp] = m, sm_l[warp] = L;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = acc[v];
-    __syncthreads();
-    if (threadIdx.x >= D / 2) return;
-    float M = -INFINITY;
+        for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = acc[v];
+        __syncthreads();
+        if (warp > 0) return;
+        m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kInt4MergeWarps; ++w) M = fmaxf(M, sm_m[w]);
-    float S = 0.f, x0 = 0.f, x1 = 0.f;
+        for (int w = 0; w < NW; ++w) m = fmaxf(m, sm_m[w]);
+        L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kInt4MergeWarps; ++w) {
-        if (sm_l[w] == 0.f) continue;
-        const float f = fast_exp2(sm_m[w] - M);
-        S += f * sm_l[w];
-        x0 += f * sm_o[w][2 * threadIdx.x];
-        x1 += f * sm_o[w][2 * threadIdx.x + 1];
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (sm_l[w] == 0.f) continue;
+            const float f = fast_exp2(sm_m[w] - m);
+            L += f * sm_l[w];
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += f * sm_o[w][lane * V + v];
+        }
     }
-    const float inv = S == 0.f ? 0.f : 1.f / S;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     const int i = r / a.G, h = g * a.G + (r - i * a.G);
     const size_t row = (size_t(b) * a.Sq + i) * a.Hq + h;
-    *reinterpret_cast<uint32_t *>(a.out + row * D + 2 * threadIdx.x) = pack_bf16x2(x0 * inv, x1 * inv);
-    if (a.lse != nullptr && threadIdx.x == 0)
-        a.lse[(size_t(b) * a.Hq + h) * a.Sq + i] = S == 0.f ? -INFINITY : (M + log2f(S)) * 0.69314718055994530942f;
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+        *reinterpret_cast<uint32_t *>(a.out + row * D + lane * V + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+    if (a.lse != nullptr && lane == 0)
+        a.lse[(size_t(b) * a.Hq + h) * a.Sq + i] = L == 0.f ? -INFINITY : (m + log2f(L)) * 0.69314718055994530942f;
 }
 
 }  // namespace gqa

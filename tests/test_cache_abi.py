@@ -38,7 +38,7 @@ def test_int4_sizes_reject(lib):
     assert lib.gqa_decode_paged_int4_num_splits(2, 1, 8, 2, 96, 16, 4) == -2
     assert lib.gqa_decode_paged_int4_num_splits(2, 1, 6, 4, 128, 16, 4) == -1
     assert lib.gqa_decode_paged_int4_workspace_bytes(2, 1, 8, 2, 96, 16, 4, 3) == 0
-    assert lib.gqa_decode_paged_int4_workspace_bytes(2, 1, 8, 2, 128, 16, 4, 1) == 0
+    assert lib.gqa_decode_paged_int4_workspace_bytes(2, 1, 32, 8, 128, 16, 4, 1) == 0  # one worker writes all
     assert lib.gqa_decode_paged_int4_workspace_bytes(2, 1, 8, 2, 128, 16, 4, -1) == 0
 
 
