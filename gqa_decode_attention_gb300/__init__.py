@@ -484,16 +484,23 @@ def gqa_decode_paged_workspace_bytes(B, Sq, Hq, Hkv, D, kv_dtype, page_size, pag
 GQA_KV_INT4 = 3
 
 
-def _on_device_of(t: torch.Tensor, stream):
-    """(guard, stream pointer) of a call on t's device: the stream given, or that device's current one.  The guard is
-    entered around the call where another device is current."""
-    if not t.is_cuda:
+# A decode step runs these calls once a layer, so their checks are written to be cheap: one expression a tensor, the
+# message worked out only for a tensor that fails.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device_of(dev: int, stream):
+    """(guard, stream pointer) of a call on CUDA device `dev`: the stream given, or that device's current one.  The
+    guard is entered around the call where another device is current."""
+    if dev < 0:
         raise ValueError("expected CUDA tensors")
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    if s.device != t.device:
-        raise ValueError(f"stream on {s.device}, tensors on {t.device}")
-    guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-    return guard, s.cuda_stream
+    if stream is None:
+        s = _current_raw_stream(dev) if _current_raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on device {dev}")
+        s = stream.cuda_stream
+    return (None if dev == torch.cuda.current_device() else torch.cuda.device(dev)), s
 
 
 def _guarded(guard, fn, *args):
@@ -503,42 +510,58 @@ def _guarded(guard, fn, *args):
         return fn(*args)
 
 
-def _need_on(t: torch.Tensor, name: str, dtype, like: torch.Tensor, shape=None):
-    """As _need_shape, for an argument that must be there; shape None: any."""
-    if t.dtype != dtype or t.device != like.device or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name}: expected contiguous {dtype}{'' if shape is None else ' ' + str(tuple(shape))} on "
-                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _misfit(fn: str, name: str, t, dtype, dev: int, shape=None):
+    want = f"contiguous {dtype}{'' if shape is None else ' ' + str(list(shape))} on cuda:{dev}"
+    got = f"{t.dtype} {list(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+    return ValueError(f"{fn}: {name}: expected {want}, got {got}")
+
+
+def _fit(fn: str, name: str, t, dtype, dev: int, shape=None):
+    """A tensor the library reads or writes through a raw pointer: its type, device, layout and (unless None) shape."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise _misfit(fn, name, t, dtype, dev, shape)
 
 
 def _data(t):
     return None if t is None else t.data_ptr()
 
 
-def _cache(fn: str, k_pool, v_pool, kv_params, page_table, seq_lens, k_scales, v_scales):
+def _cache(fn: str, dev: int, k_pool, v_pool, kv_params, page_table, seq_lens, k_scales, v_scales):
     """Checks the cache's tensors against each other; returns (kv_dtype, num_pages, page_size, Hkv, D, B,
     pages_per_req, n_scales)."""
-    if k_pool.dim() != 4 or page_table.dim() != 2:
+    shape = k_pool.shape
+    if len(shape) != 4 or page_table.dim() != 2:
         raise ValueError(f"{fn}: pools [num_pages,page_size,Hkv,D or D/2], page_table 2-D")
-    num_pages, page_size, Hkv, width = k_pool.shape
-    kvd, D = (_kv_dtype(k_pool), width) if kv_params is None else (GQA_KV_INT4, 2 * width)
-    if kv_params is not None:
-        _need_on(k_pool, "k_pool", torch.uint8, k_pool)
-        _need_on(kv_params, "kv_params", torch.float16, k_pool, (num_pages, page_size, Hkv, 4))
-    _need_on(k_pool, "k_pool", k_pool.dtype, k_pool)
-    _need_on(v_pool, "v_pool", k_pool.dtype, k_pool, k_pool.shape)
-    _need_on(page_table, "page_table", torch.int32, k_pool)
+    num_pages, page_size, Hkv, D = shape
+    kind = k_pool.dtype
+    if kv_params is None:
+        kvd = _kv_dtype(k_pool)
+    else:
+        kvd, kind, D = GQA_KV_INT4, torch.uint8, 2 * D
+        _fit(fn, "kv_params", kv_params, torch.float16, dev, (num_pages, page_size, Hkv, 4))
+    _fit(fn, "k_pool", k_pool, kind, dev)
+    _fit(fn, "v_pool", v_pool, kind, dev, shape)
+    _fit(fn, "page_table", page_table, torch.int32, dev)
     B, pages_per_req = page_table.shape
-    _need_on(seq_lens, "seq_lens", torch.int32, k_pool, (B,))
+    _fit(fn, "seq_lens", seq_lens, torch.int32, dev, (B,))
     n_scales = 0
     if k_scales is not None or v_scales is not None:
         if k_scales is None or v_scales is None:
             raise ValueError(f"{fn}: k_scales and v_scales go together")
         n_scales = k_scales.numel()
-        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _need_on(t, n, torch.float32, k_pool)
+        _fit(fn, "k_scales", k_scales, torch.float32, dev)
+        _fit(fn, "v_scales", v_scales, torch.float32, dev)
         if v_scales.numel() != n_scales:
             raise ValueError(f"{fn}: k_scales and v_scales need the same number of values")
     return kvd, num_pages, page_size, Hkv, D, B, pages_per_req, n_scales
+
+
+def _new(shape, dtype, like, stream):
+    """An output the call allocates: safe to free while a given stream still writes it."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def gqa_decode_paged_int4(q, k_pool, v_pool, kv_params, page_table, seq_lens, out=None, lse=None, scale=None,
@@ -552,35 +575,33 @@ def gqa_decode_paged_int4(q, k_pool, v_pool, kv_params, page_table, seq_lens, ou
     Returns (out [B,Sq,Hq,D] bf16, lse [B,Hq,Sq] fp32 or None).
     """
     lib = _lib_handle or load_library()
-    guard, cs = _on_device_of(q, stream)
+    fn = "gqa_decode_paged_int4"
+    dev = q.get_device()
+    guard, cs = _on_device_of(dev, stream)
     if kv_params is None or q.dim() != 4:
-        raise ValueError("gqa_decode_paged_int4: q [B,Sq,Hq,D] and kv_params are needed")
-    _, num_pages, page_size, Hkv, D, B, ppr, _ = _cache("gqa_decode_paged_int4", k_pool, v_pool, kv_params,
-                                                        page_table, seq_lens, None, None)
+        raise ValueError(f"{fn}: q [B,Sq,Hq,D] and kv_params are needed")
+    _, num_pages, page_size, Hkv, D, B, ppr, _ = _cache(fn, dev, k_pool, v_pool, kv_params, page_table, seq_lens, None, None)
     _, Sq, Hq, _ = q.shape
-    _need_on(q, "q", torch.bfloat16, k_pool, (B, Sq, Hq, D))
+    _fit(fn, "q", q, torch.bfloat16, dev, (B, Sq, Hq, D))
     if out is None:
-        out = torch.empty_like(q)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _new((B, Sq, Hq, D), torch.bfloat16, q, stream)
     else:
-        _need_on(out, "out", torch.bfloat16, q, q.shape)
+        _fit(fn, "out", out, torch.bfloat16, dev, (B, Sq, Hq, D))
     if lse is not None:
-        _need_on(lse, "lse", torch.float32, q, (B, Hq, Sq))
+        _fit(fn, "lse", lse, torch.float32, dev, (B, Hq, Sq))
     elif with_lse:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-        if stream is not None:
-            lse.record_stream(stream)
+        lse = _new((B, Hq, Sq), torch.float32, q, stream)
     ws_bytes = 0
     if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != q.device:
-            raise ValueError(f"workspace: expected a contiguous tensor on {q.device}")
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(f"{fn}: workspace: expected a contiguous tensor on cuda:{dev}")
         ws_bytes = workspace.numel() * workspace.element_size()
     st = _guarded(guard, lib.gqa_decode_paged_int4, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
                   kv_params.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _data(lse), B, Sq,
                   Hq, Hkv, D, page_size, ppr, num_pages, _scale_arg(scale), int(num_splits), _data(workspace),
                   ws_bytes, cs)
-    _check(st, "gqa_decode_paged_int4")
+    if st:
+        raise GQAError(st, fn)
     return out, lse
 
 
@@ -596,11 +617,11 @@ def gqa_decode_paged_int4_workspace_bytes(B, Sq, Hq, Hkv, D, page_size, pages_pe
                                                                     int(num_splits)))
 
 
-def _heads_of(fn: str, t, name: str, T, heads, D, like):
+def _heads_of(fn: str, t, name: str, T, heads, D, dev):
     """Token stride of t [T, heads, D] bf16 whose heads are contiguous."""
-    if t.dtype != torch.bfloat16 or t.device != like.device or t.dim() != 3 or t.shape != (T, heads, D):
-        raise ValueError(f"{fn}: {name} must be bfloat16 [{T},{heads},{D}] on {like.device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != (T, heads, D):
+        raise ValueError(f"{fn}: {name} must be bfloat16 [{T},{heads},{D}] on cuda:{dev}, got {t.dtype} "
+                         f"{list(t.shape)} on {t.device}")
     s0, s1, s2 = t.stride()
     if T and (s2 != 1 or (heads > 1 and s1 != D)):
         raise ValueError(f"{fn}: the heads of a token of {name} must be contiguous")
@@ -621,38 +642,38 @@ def gqa_paged_append(k, v, k_pool, v_pool, page_table, seq_lens, cu_tokens=None,
     """
     lib = _lib_handle or load_library()
     fn = "gqa_paged_append"
-    guard, cs = _on_device_of(k, stream)
-    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, k_pool, v_pool, kv_params, page_table, seq_lens,
+    dev = k_pool.get_device()
+    guard, cs = _on_device_of(dev, stream)
+    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, dev, k_pool, v_pool, kv_params, page_table, seq_lens,
                                                                  k_scales, v_scales)
     T = k.shape[0]
-    k_stride = _heads_of(fn, k, "k", T, Hkv, D, k_pool)
-    v_stride = _heads_of(fn, v, "v", T, Hkv, D, k_pool)
+    k_stride = _heads_of(fn, k, "k", T, Hkv, D, dev)
+    v_stride = _heads_of(fn, v, "v", T, Hkv, D, dev)
     Hq = q_stride = 0
     if q is not None:
         Hq = q.shape[1] if q.dim() == 3 else 0
-        q_stride = _heads_of(fn, q, "q", T, Hq, D, k_pool)
+        q_stride = _heads_of(fn, q, "q", T, Hq, D, dev)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-            if stream is not None:
-                q_out.record_stream(stream)
+            q_out = _new((T, Hq, D), torch.bfloat16, q, stream)
         else:
-            _need_on(q_out, "q_out", torch.bfloat16, k_pool, (T, Hq, D))
+            _fit(fn, "q_out", q_out, torch.bfloat16, dev, (T, Hq, D))
     elif q_out is not None:
         raise ValueError(f"{fn}: q_out without q")
     if cu_tokens is not None:
-        _need_on(cu_tokens, "cu_tokens", torch.int32, k_pool, (B + 1,))
+        _fit(fn, "cu_tokens", cu_tokens, torch.int32, dev, (B + 1,))
     rot_dim = max_pos = 0
     if cos_sin is not None:
+        _fit(fn, "cos_sin", cos_sin, torch.float32, dev)
         if cos_sin.dim() != 2:
             raise ValueError(f"{fn}: cos_sin must be [max_pos, rot_dim]")
-        _need_on(cos_sin, "cos_sin", torch.float32, k_pool)
         max_pos, rot_dim = cos_sin.shape
     st = _guarded(guard, lib.gqa_paged_append, _data(q), q_stride, _data(q_out), k.data_ptr(), k_stride, v.data_ptr(),
-                  v_stride, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params), float(k_scale),
-                  float(v_scale), _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(),
-                  seq_lens.data_ptr(), _data(cu_tokens), _data(cos_sin), rot_dim, max_pos, int(bool(interleaved)), T,
-                  B, Hq, Hkv, D, page_size, ppr, num_pages, cs)
-    _check(st, fn)
+                  v_stride, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params), k_scale, v_scale,
+                  _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(), seq_lens.data_ptr(),
+                  _data(cu_tokens), _data(cos_sin), rot_dim, max_pos, 1 if interleaved else 0, T, B, Hq, Hkv, D,
+                  page_size, ppr, num_pages, cs)
+    if st:
+        raise GQAError(st, fn)
     return q_out
 
 
@@ -666,15 +687,16 @@ def gqa_paged_gather(k_pool, v_pool, page_table, seq_lens, k_out=None, v_out=Non
     """
     lib = _lib_handle or load_library()
     fn = "gqa_paged_gather"
-    guard, cs = _on_device_of(k_pool, stream)
-    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, k_pool, v_pool, kv_params, page_table, seq_lens,
+    dev = k_pool.get_device()
+    guard, cs = _on_device_of(dev, stream)
+    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, dev, k_pool, v_pool, kv_params, page_table, seq_lens,
                                                                  k_scales, v_scales)
     if (k_out is None) != (v_out is None):
         raise ValueError(f"{fn}: k_out and v_out go together")
     if k_out is None:
         if rows is None:
             raise ValueError(f"{fn}: k_out and v_out, or rows, are needed")
-        on = torch.cuda.current_stream(k_pool.device) if stream is None else stream
+        on = torch.cuda.current_stream(dev) if stream is None else stream
         with torch.cuda.stream(on):  # zeroed on the stream that writes them
             k_out, v_out = (torch.zeros((B, rows, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
                             for _ in range(2))
@@ -682,15 +704,15 @@ def gqa_paged_gather(k_pool, v_pool, page_table, seq_lens, k_out=None, v_out=Non
         if k_out.dim() != 4 or (rows is not None and rows != k_out.shape[1]):
             raise ValueError(f"{fn}: k_out must be [B,rows,Hkv,D]")
         rows = k_out.shape[1]
-        _need_on(k_out, "k_out", torch.bfloat16, k_pool, (B, rows, Hkv, D))
-        _need_on(v_out, "v_out", torch.bfloat16, k_pool, (B, rows, Hkv, D))
+        _fit(fn, "k_out", k_out, torch.bfloat16, dev, (B, rows, Hkv, D))
+        _fit(fn, "v_out", v_out, torch.bfloat16, dev, (B, rows, Hkv, D))
     if starts is not None:
-        _need_on(starts, "starts", torch.int32, k_pool, (B,))
-    st = _guarded(guard, lib.gqa_paged_gather, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params),
-                  float(k_scale), float(v_scale), _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(),
-                  seq_lens.data_ptr(), _data(starts), k_out.data_ptr(), v_out.data_ptr(), B, int(rows), Hkv, D,
-                  page_size, ppr, num_pages, cs)
-    _check(st, fn)
+        _fit(fn, "starts", starts, torch.int32, dev, (B,))
+    st = _guarded(guard, lib.gqa_paged_gather, kvd, k_pool.data_ptr(), v_pool.data_ptr(), _data(kv_params), k_scale,
+                  v_scale, _data(k_scales), _data(v_scales), n_scales, page_table.data_ptr(), seq_lens.data_ptr(),
+                  _data(starts), k_out.data_ptr(), v_out.data_ptr(), B, rows, Hkv, D, page_size, ppr, num_pages, cs)
+    if st:
+        raise GQAError(st, fn)
     return k_out, v_out
 
 

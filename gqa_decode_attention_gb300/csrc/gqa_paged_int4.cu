@@ -197,10 +197,15 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.Hkv = Hkv;
     a.G = p.G;
     a.Mq = p.Mq;
+    a.g_inv = (65536u + p.G - 1) / p.G;
     a.page_size = page_size;
     a.pages_per_req = pages_per_req;
     a.num_pages = num_pages;
     a.workers = workers;
+    int lg = 0;
+    while ((1LL << lg) < page_size) ++lg;
+    a.by_page.m = (1ull << (31 + lg)) / unsigned(page_size) + 1;
+    a.by_page.shift = 31 + lg;
     a.HB = p.HB;
     a.RG = p.RG;
     // One ring a CTA while the workers are fewer than the SMs; the rings share

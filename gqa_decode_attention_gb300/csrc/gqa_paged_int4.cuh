@@ -58,6 +58,14 @@ static_assert(16 * int4_consumer_regs(1) + 4 * int4_producer_regs(1) == 20 * 96,
 static_assert(8 * int4_consumer_regs(2) + 4 * int4_producer_regs(2) == 12 * 168, "registers");
 constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
 
+// x / d for x < 2^31, d of the host's choosing: m = floor(2^(31 + l) / d) + 1, l = ceil(log2 d).  (m d lies above
+// 2^(31 + l) by at most d <= 2^l, so x m / 2^(31 + l) is above x / d by less than 1 / d: the floor is right.)
+struct FastDiv {
+    unsigned long long m;
+    int shift;
+};
+__device__ __forceinline__ int fast_div(int x, const FastDiv &f) { return int((unsigned long long)unsigned(x) * f.m >> f.shift); }
+
 struct Int4Args {
     const __nv_bfloat16 *q;   // [B, Sq, Hq, D]
     const __half *params;     // [num_pages, page_size, Hkv, 4]
@@ -72,6 +80,8 @@ struct Int4Args {
     int rings, rings_max;     // rings (workers) of a CTA, and how many its warps could serve
     int lanes;                // groups of HB x RG warps that take turns at a ring's steps
     int stages, box_rows, box_pitch, stage_bytes;
+    FastDiv by_page;          // page_size
+    unsigned g_inv;           // ceil(2^16 / G): r / G = r * g_inv >> 16 for r < 128
     int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
     unsigned param_pitch;     // of a box's parameters in a stage
     unsigned par8, par16;     // as tok8, tok16, of the parameters
@@ -89,7 +99,7 @@ struct Int4Head {
     uint64_t ready[kInt4MaxRings], taken[kInt4MaxRings];  // lanes: results handed to the first lane, and taken
     uint32_t mask[kInt4MaxRings][kInt4MaxStages];  // tokens of a stage that are there
     int begin[kInt4MaxRings], end[kInt4MaxRings];  // steps of the ring's share
-    int first[kInt4MaxRings], first_p[kInt4MaxRings];  // its first request, and that one's first step
+    unsigned long long first[kInt4MaxRings];  // its first request (high half), and that one's first step
     int abort;
 };
 constexpr int kInt4HeadBytes = 1024;
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             }
             mbar_init(&head->ready[r], max(1, (a.lanes - 1) * nh * a.RG));
             mbar_init(&head->taken[r], nh * a.RG);
-            head->first[r] = a.B;
+            head->first[r] = (unsigned long long)a.B << 32;
         }
         head->abort = 0;
         fence_mbarrier_init();
@@ -273,65 +283,61 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 
     // ---- schedule.  Request b takes ceil(len_b / 32) steps; worker w takes
     // steps [w T / W, (w + 1) T / W) of the T steps of all requests in order.
-    // Each thread sums a run of requests, a scan over the CTA gives their first
-    // steps.  An empty request belongs to the worker whose range holds its
-    // step (the last worker for those at the very end).
+    // Each thread sums a run of requests (with few requests most warps have
+    // none and go on to the barriers), a scan gives their first steps, and
+    // whoever holds a share's first step writes it down.  An empty request
+    // belongs to the worker whose range holds its step (the last worker for
+    // those at the very end).
     bool bad = false;
     {
-        const int run = (a.B + int4_threads(NT) - 1) / int4_threads(NT);
+        constexpr int NTH = int4_threads(NT);
+        const int run = (a.B + NTH - 1) / NTH;
         const int b0 = min(a.B, int(threadIdx.x) * run), b1 = min(a.B, b0 + run);
-        int mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int len = __ldg(a.seq_lens + b);
-            bad |= len < 0 || len > cap;
-            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step;
-        }
-        int incl = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();
-        int T = 0, P0 = incl - mine;
-#pragma unroll
-        for (int w = 0; w < CW + 4; ++w) {
-            const int s = warp_sum[w];
-            T += s;
-            if (w < warp) P0 += s;
-        }
-        const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
-        int hit[kInt4MaxRings], hit_p[kInt4MaxRings];
-#pragma unroll
-        for (int r = 0; r < kInt4MaxRings; ++r) {
-            hit[r] = a.B;
-            hit_p[r] = 0;
-            if (r >= a.rings) continue;
-            const int w = r * int(gridDim.y) + int(blockIdx.y);
-            const int begin = int4_share(min(w, a.workers), T, a.workers);
-            int P = P0;
+        const int in_use = ((a.B + run - 1) / run + 31) / 32;  // warps with requests
+        int len0 = 0, mine = 0, incl = 0;
+        if (warp < in_use) {
             for (int b = b0; b < b1; ++b) {
-                const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
+                len0 = __ldg(a.seq_lens + b);
+                bad |= len0 < 0 || len0 > cap;
+                len0 = min(max(len0, 0), cap);
+                mine += (len0 + kInt4Step - 1) / kInt4Step;
+            }
+            incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            if (lane == 31) warp_sum[warp] = incl;
+        }
+        __syncthreads();
+        if (warp == 0 && lane < a.rings) {
+            int T = 0;
+            for (int w = 0; w < in_use; ++w) T += warp_sum[w];
+            const int w = lane * int(gridDim.y) + int(blockIdx.y);
+            head->begin[lane] = int4_share(min(w, a.workers), T, a.workers);
+            head->end[lane] = int4_share(min(w + 1, a.workers), T, a.workers);
+            if (lane == 0 && a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0) a.step_prefix[a.B] = T;
+        }
+        __syncthreads();
+        if (warp < in_use) {
+            int P = incl - mine;
+            for (int w = 0; w < warp; ++w) P += warp_sum[w];
+            const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
+            for (int b = b0; b < b1; ++b) {
+                const int len = run == 1 ? len0 : min(max(__ldg(a.seq_lens + b), 0), cap);
                 const int n = (len + kInt4Step - 1) / kInt4Step;
-                if (record && r == 0) a.step_prefix[b] = P;
-                if (hit[r] == a.B && P + (n > 0 ? n : 1) > begin) hit[r] = b, hit_p[r] = P;
+                if (record) a.step_prefix[b] = P;
+                for (int r = 0; r < a.rings; ++r) {
+                    const int begin = head->begin[r];
+                    if (P <= begin && P + max(n, 1) > begin)  // of several (empty ones first) the first counts
+                        atomicMin(&head->first[r], (unsigned long long)b << 32 | unsigned(P));
+                }
                 P += n;
             }
-            if (hit[r] < a.B) atomicMin(&head->first[r], hit[r]);
-            if (int(threadIdx.x) == r) {
-                head->begin[r] = begin;
-                head->end[r] = int4_share(min(w + 1, a.workers), T, a.workers);
-                head->first_p[r] = 0;
-            }
+            if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
+            bad = false;
         }
-        if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
-        __syncthreads();  // also: every warp is done with warp_sum, which lies in the rings
-#pragma unroll
-        for (int r = 0; r < kInt4MaxRings; ++r)
-            if (r < a.rings && hit[r] < a.B && hit[r] == head->first[r]) head->first_p[r] = hit_p[r];
-        if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
-        bad = false;
         fence_proxy_async_shared();  // warp_sum's place is written by TMA next
         __syncthreads();
     }
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
         const int w_end = head->end[r];
-        int seg_b = head->first[r], seg_p = head->first_p[r], seg_t = head->begin[r];
+        int seg_b = int(head->first[r] >> 32), seg_p = int(unsigned(head->first[r])), seg_t = head->begin[r];
         const uint32_t box_bytes = uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
         const bool first = lane % R == 0;  // of a box
@@ -364,17 +370,17 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             const int32_t *table = a.page_table + size_t(seg_b) * a.pages_per_req;
             const int t_end = min((seg_next - seg_p) * kInt4Step, len);
             int t = (seg_t - seg_p) * kInt4Step + lane;
-            int slot = t % a.page_size;
-            int page = t < t_end ? __ldg(table + t / a.page_size) : 0;
+            int at = fast_div(t, a.by_page);
+            int page = t < t_end ? __ldg(table + at) : 0;
             for (; t - lane < t_end; ++gs) {
                 const bool in = t < t_end;
                 const bool ok = in && page >= 0 && page < a.num_pages;
                 bad |= in && !ok;
-                const int row = ok ? page * a.page_size + slot : 0;
+                const int row = ok ? page * a.page_size + (t - at * a.page_size) : 0;
                 // the next step's page is on its way while this one is issued
                 t += kInt4Step;
-                slot = t % a.page_size;
-                if (t < t_end) page = __ldg(table + t / a.page_size);
+                at = fast_div(t, a.by_page);
+                if (t < t_end) page = __ldg(table + at);
                 const uint32_t valid = __ballot_sync(0xffffffffu, ok);
                 const bool box = ok && first;  // its first token's page holds all of a box
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
@@ -443,7 +449,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const int w = r * int(gridDim.y) + int(blockIdx.y);  // worker
     const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
     const int w_begin = head->begin[r], w_end = head->end[r];
-    int seg_b = head->first[r], seg_p = head->first_p[r], seg_t = w_begin;
+    int seg_b = int(head->first[r] >> 32), seg_p = int(unsigned(head->first[r])), seg_t = w_begin;
     const bool last_worker = w == a.workers - 1;
     const int g = hb0 + lh;
     const int gi = lane >> 2, c = lane & 3;
@@ -458,6 +464,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         vo[e] = v_off + (D == 128 ? r + swz(r, gi >> 1) + (gi & 1) * 8 : r + 4 * gi);
     }
     const int tok0 = tok_of<D>(gi);
+    auto row_of = [&](int r) { return int(unsigned(r) * a.g_inv >> 16); };  // query row i of the group's row r = i G + h
     const uint32_t p_off = par_off(tok0, lh);
 
     const uint32_t full = smem_u32(head->full[r]), mask_at = smem_u32(head->mask[r]);
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         for (int nt = 0; nt < NT; ++nt) {
             const int r = (rg * NT + nt) * 8 + gi;
             const bool real = r < a.Mq;
-            const int i = real ? r / a.G : 0;
+            const int i = real ? row_of(r) : 0;
             const __nv_bfloat16 *qrow =
                 a.q + ((size_t(b) * a.Sq + i) * a.Hq + g * a.G + (real ? r - i * a.G : 0)) * D + (D / 4) * c;
             float x[KW][8];
@@ -614,7 +621,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int r = (rg * NT + nt) * 8 + 2 * c + e;
-                            const bool seen = there && s0 + tok0 + 8 * j <= len - a.Sq + (r < a.Mq ? r / a.G : a.Sq);
+                            const bool seen = there && s0 + tok0 + 8 * j <= len - a.Sq + (r < a.Mq ? row_of(r) : a.Sq);
                             if (!seen) acc[nt][j >> 1][2 * (j & 1) + e] = -INFINITY;
                         }
                 }
@@ -800,13 +807,14 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 }
                 const int r = (rg * NT + nt) * 8 + 2 * c + e;
                 if (r >= a.Mq || turn > 0) continue;
-                const float f = L == 0.f ? 0.f : 1.f / L;  // NaN stays
-                const float lse2 = L == 0.f ? -INFINITY : R_[nt][e] + log2f(L);
+                const float f = L == 0.f ? 0.f : __fdividef(1.f, L);  // NaN stays
+                const float lse2 = L == 0.f ? -INFINITY : R_[nt][e] + __log2f(L);
+                const float f24 = f * 16777216.f, f20 = f * 1048576.f, zf = Z * f;
                 float x[2 * DB];
 #pragma unroll
                 for (int j = 0; j < DB; ++j) {
-                    x[2 * j] = fmaf(o[nt][j][e], 16777216.f, Z) * f;
-                    x[2 * j + 1] = fmaf(o[nt][j][2 + e], 1048576.f, Z) * f;
+                    x[2 * j] = fmaf(o[nt][j][e], f24, zf);
+                    x[2 * j + 1] = fmaf(o[nt][j][2 + e], f20, zf);
                 }
                 if (!complete) {
                     const size_t prow = ((((size_t(blockIdx.x) * a.workers + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
@@ -817,7 +825,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                     if (gi == 0) a.lse_part[prow] = lse2;
                     continue;
                 }
-                const int i = r / a.G, h = g * a.G + (r - i * a.G);
+                const int i = row_of(r), h = g * a.G + (r - i * a.G);
                 __nv_bfloat16 *dst = a.out + ((size_t(b) * a.Sq + i) * a.Hq + h) * D + (D / 8) * gi;
 #pragma unroll
                 for (int j = 0; j < 2 * DB; j += 8)
@@ -841,9 +849,10 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 
 // Merge of the partials of requests that several workers share.  CTA (y, b): with SPLIT, one row, whose partials are dealt in runs to all warps and their
 // results merged in warp order -- few rows, many partials each; without, one
-// row a warp.  Each warp has 8 partials in flight and merges them in order:
-// the same bits every time.
-constexpr int kInt4MergeBatch = 8;
+// row a warp.  A warp reads 32 partials' LSEs at once, one a lane, which gives
+// their weights, then adds them up in order, several in flight: the same bits
+// every time.
+constexpr int kInt4MergeBatch = 10;
 __host__ __device__ constexpr int int4_merge_warps(bool split) { return split ? 16 : 8; }
 
 template <int D, bool SPLIT>
@@ -874,36 +883,53 @@ __global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_m
     float m = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int k0 = from; k0 < to; k0 += kInt4MergeBatch) {
-        float l2[kInt4MergeBatch], x[kInt4MergeBatch][V];
+    for (int k0 = from; k0 < to; k0 += 32) {
+        // one partial a lane: its LSE gives the weights of the 32
+        const int part = k0 + lane, w = w_first + part;
+        float l2 = -INFINITY;
+        // a worker without a step (T < W) holds nothing
+        const bool there = part < to && !(T < W && int4_share(w, T, W) == int4_share(w + 1, T, W));
+        const size_t prow = ((((size_t(hb) * W + w) * 2 + (part == 0 && before ? 1 : 0)) * a.HB + lh) * a.Mq) + r;
+        if (there) l2 = __ldg(a.lse_part + prow);
+        float mn = l2;
 #pragma unroll
-        for (int k = 0; k < kInt4MergeBatch; ++k) {
-            const int part = k0 + k;
-            l2[k] = -INFINITY;
-            if (part >= to) continue;
-            const int w = w_first + part;
-            // a worker without a step (T < W) holds nothing
-            if (T < W && int4_share(w, T, W) == int4_share(w + 1, T, W)) continue;
-            const int slot = part == 0 && before ? 1 : 0;
-            const size_t prow = ((((size_t(hb) * W + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
-            l2[k] = __ldg(a.lse_part + prow);
-            if constexpr (V == 4) {
-                const float4 t = __ldg(reinterpret_cast<const float4 *>(a.o_part + prow * D) + lane);
-                x[k][0] = t.x, x[k][1] = t.y, x[k][2] = t.z, x[k][3] = t.w;
-            } else {
-                const float2 t = __ldg(reinterpret_cast<const float2 *>(a.o_part + prow * D) + lane);
-                x[k][0] = t.x, x[k][1] = t.y;
+        for (int off = 16; off > 0; off >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        mn = fmaxf(mn, m);
+        const float sc = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+        const float wgt = l2 == -INFINITY ? 0.f : fast_exp2(l2 - mn);
+        float sum = wgt;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        L = L * sc + sum;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= sc;
+        m = mn;
+        const size_t step = size_t(2) * a.HB * a.Mq * D;  // from a worker's partial to the next one's
+        const float *first = a.o_part + ((((size_t(hb) * W + w_first + k0) * 2) * a.HB + lh) * a.Mq + r) * D + lane * V;
+        const int n_here = min(32, to - k0);
+        for (int j0 = 0; j0 < n_here; j0 += kInt4MergeBatch) {
+            float x[kInt4MergeBatch][V];
+#pragma unroll
+            for (int j = 0; j < kInt4MergeBatch; ++j) {
+                const float f = __shfl_sync(0xffffffffu, wgt, (j0 + j) & 31);
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[j][v] = 0.f;
+                if (j0 + j >= n_here || f == 0.f) continue;  // a partial without weight may hold anything
+                const float *src = first + (j0 + j) * step + (k0 + j0 + j == 0 && before ? step / 2 : 0);
+                if constexpr (V == 4) {
+                    const float4 t = __ldg(reinterpret_cast<const float4 *>(src));
+                    x[j][0] = t.x, x[j][1] = t.y, x[j][2] = t.z, x[j][3] = t.w;
+                } else {
+                    const float2 t = __ldg(reinterpret_cast<const float2 *>(src));
+                    x[j][0] = t.x, x[j][1] = t.y;
+                }
             }
-        }
 #pragma unroll
-        for (int k = 0; k < kInt4MergeBatch; ++k) {
-            if (l2[k] == -INFINITY) continue;
-            const float mn = fmaxf(m, l2[k]);
-            const float sc = fast_exp2(m - mn), wgt = fast_exp2(l2[k] - mn);
+            for (int j = 0; j < kInt4MergeBatch; ++j) {
+                const float f = __shfl_sync(0xffffffffu, wgt, (j0 + j) & 31);
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = acc[v] * sc + wgt * x[k][v];
-            L = L * sc + wgt;
-            m = mn;
+                for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[j][v], acc[v]);
+            }
         }
     }
     if constexpr (SPLIT) {
