@@ -31,6 +31,8 @@ struct AppendArgs {
     const float *cos_sin;      // [max_pos, rot_dim]
     int rot_dim, max_pos, interleaved;
     int T, B, Hq, Hkv, page_size, pages_per_req, num_pages;
+    int lanes, heads_per_cta;  // heads of a token side by side in a CTA, and all that it walks over
+    int tokens;                // of a CTA
     unsigned *err;
 };
 
@@ -43,6 +45,7 @@ struct GatherArgs {
     const int32_t *page_table, *seq_lens, *starts;
     __nv_bfloat16 *k_out, *v_out;  // [B, rows, Hkv, D]
     int B, rows, Hkv, page_size, pages_per_req, num_pages;
+    int tokens;  // of a warp
     unsigned *err;
 };
 
@@ -68,11 +71,23 @@ __device__ __forceinline__ uint32_t e4m3x2_from_f32(float lo, float hi) {
     return r;
 }
 
+// Conversions between small integers and fp32 go through the mantissa (the
+// sum with 2^23, or 1.5 * 2^23 for signed values, rounds to the nearest even
+// integer and holds it in its low bits): the conversion instructions run at a
+// quarter of that rate and were 40 % of a 4-bit gather's time.
+constexpr float kMagic = 8388608.f, kMagicSigned = 12582912.f;
+
 // Symmetric int8 code of x * inv: nearest even, clamped to +-127, NaN as 0.
 __device__ __forceinline__ uint32_t int8_code(float x, float inv) {
-    float y = rintf(__fmul_rn(x, inv));
-    y = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
-    return uint32_t(int(y)) & 0xffu;
+    const float y = __fmul_rn(x, inv);
+    const float c = y == y ? fminf(fmaxf(y, -127.f), 127.f) : 0.f;
+    return __float_as_uint(c + kMagicSigned) & 0xffu;
+}
+
+// Code in 0..15 of (x - zero) * inv, nearest even.
+__device__ __forceinline__ uint32_t int4_code(float x, float zero, float inv) {
+    const float y = fminf(fmaxf(__fmul_rn(__fsub_rn(x, zero), inv), 0.f), 15.f);
+    return __float_as_uint(y + kMagic) & 15u;
 }
 
 constexpr float kF16Max = 65504.f;
@@ -86,29 +101,59 @@ __device__ __forceinline__ float int4_input(float x) { return x == x ? fminf(fma
 // One item: 16 elements of a token's head (two 16-byte pieces), which hold
 // whole rotation pairs: slot s of a head takes the pieces at 8 s and
 // rot / 2 + 8 s (pairs i, i + rot / 2), or the 16 neighbours at 16 s
-// (neighbouring pairs, and the elements past rot_dim).  Items of a token run
-// over its q, k and v heads; a CTA of 128 threads holds 128 U of them, U a
-// thread.  The threads of one head are neighbours in a warp, which is where a
-// 4-bit row's minimum and maximum are reduced.  The slot is the same for all
-// of a thread's items, so it loads its cosines and sines once.
+// (neighbouring pairs, and the elements past rot_dim).  A CTA holds a run of
+// tokens; `lanes` heads of a token lie side by side (the slots of a head on
+// neighbouring threads, which is where a 4-bit row's minimum and maximum are
+// reduced), and a thread walks over the token's heads in steps of `lanes`: its
+// slot and token stay, so it loads its cosines and sines once a token.
 //
-// All U items are loaded before the token's request, position and page are
-// looked up, so their latency overlaps that chain of dependent loads.
+// A token's request, position and page are a chain of dependent loads, some
+// microseconds long.  So a CTA looks up all of its tokens at once, a warp a
+// token, with the first heads' loads already in flight, and holds several
+// groups of tokens when there are enough for that (one group a CTA ran 24
+// heads of 64, 20K tokens, at 2 TB/s).
 //
 // The rotation is rounded after every product and sum (no fused multiply-add):
 // the codes of an 8-bit or 4-bit cache then do not depend on how a compiler
 // contracts the expression, and a plain fp32 computation of the same formula
 // gives the same bytes.
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
+constexpr int kAppendBatch = 3;  // heads a thread has in flight
+constexpr int kAppendTokens = 128;  // most tokens of a CTA
 
-template <int D, int KVT, int U>
-__global__ void __launch_bounds__(kAppendThreads) gqa_paged_append_kernel(const AppendArgs a) {
-    constexpr int SLOTS = D / 16;
-    const int t = blockIdx.x;
+struct AppendToken {
+    long long row;  // pool row; -1: no place for K and V; -2: skipped whole
+    int pos;
+};
+
+// The request that holds row t: the number of requests, from `lo` on, that end
+// at or before it.  Called by a whole warp with the same arguments.
+__device__ __forceinline__ int request_of(const int32_t *cu, int lo, int B, int t) {
     const int lane = threadIdx.x & 31;
-    const int items = (a.Hq + 2 * a.Hkv) * SLOTS;
-    const int item0 = blockIdx.y * (kAppendThreads * U) + threadIdx.x;
+    int n = B - lo;
+    while (n > 0) {
+        const int step = (n + 31) / 32;
+        const int p = (lane + 1) * step - 1;
+        const bool past = p < n && __ldg(cu + lo + p + 1) <= t;
+        const int c = __popc(__ballot_sync(0xffffffffu, past));
+        lo += c * step;
+        n = min(step - 1, n - c * step);
+    }
+    return lo;
+}
+
+template <int D, int KVT>
+__global__ void __launch_bounds__(kAppendThreads, 3) gqa_paged_append_kernel(const AppendArgs a) {
+    constexpr int SLOTS = D / 16;
+    __shared__ AppendToken tokens[kAppendTokens];
+    const int per_token = SLOTS * a.lanes;  // threads
+    const int side = kAppendThreads / per_token;  // tokens side by side
+    const int t0 = blockIdx.x * a.tokens, n_tok = min(a.tokens, a.T - t0);
+    const int mine = threadIdx.x / per_token;
     const int s = threadIdx.x % SLOTS;
+    const int heads = a.Hq + 2 * a.Hkv;
+    const int h_first = blockIdx.y * a.heads_per_cta + threadIdx.x % per_token / SLOTS;
+    const int h_end = min(heads, (int(blockIdx.y) + 1) * a.heads_per_cta);
     const bool rotated = 16 * s < a.rot_dim;
     const bool halves = rotated && !a.interleaved;
     const int off_a = halves ? 8 * s : 16 * s;
@@ -116,160 +161,174 @@ __global__ void __launch_bounds__(kAppendThreads) gqa_paged_append_kernel(const 
 
     pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
 
-    uint4 wa[U], wb[U];
+    uint4 wa[kAppendBatch], wb[kAppendBatch];
+    auto load = [&](int t, int h0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int item = item0 + u * kAppendThreads;
-        const int h = item / SLOTS;
-        const __nv_bfloat16 *src = h < a.Hq           ? a.q + (long long)t * a.q_stride + h * D
-                                   : h < a.Hq + a.Hkv ? a.k + (long long)t * a.k_stride + (h - a.Hq) * D
-                                                      : a.v + (long long)t * a.v_stride + (h - a.Hq - a.Hkv) * D;
-        wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
-        if (item < items) {
-            wa[u] = *reinterpret_cast<const uint4 *>(src + off_a);
-            wb[u] = *reinterpret_cast<const uint4 *>(src + off_b);
+        for (int u = 0; u < kAppendBatch; ++u) {
+            const int h = h0 + u * a.lanes;
+            const __nv_bfloat16 *src = h < a.Hq           ? a.q + (long long)t * a.q_stride + h * D
+                                       : h < a.Hq + a.Hkv ? a.k + (long long)t * a.k_stride + (h - a.Hq) * D
+                                                          : a.v + (long long)t * a.v_stride + (h - a.Hq - a.Hkv) * D;
+            wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
+            if (h < h_end && t < t0 + n_tok) {
+                wa[u] = *reinterpret_cast<const uint4 *>(src + off_a);
+                wb[u] = *reinterpret_cast<const uint4 *>(src + off_b);
+            }
         }
-    }
+    };
+    load(t0 + mine, h_first);
 
-    // the token's request: the number of requests that end at or before it
-    int b, first, count;
-    if (a.cu_tokens == nullptr) {
-        count = a.T / a.B;
-        b = t / count;
-        first = b * count;
-    } else {
-        int lo = 0, n = a.B;
-        while (n > 0) {
-            const int step = (n + 31) / 32;
-            const int p = (lane + 1) * step - 1;
-            const bool past = p < n && __ldg(a.cu_tokens + lo + p + 1) <= t;
-            const int c = __popc(__ballot_sync(0xffffffffu, past));
-            lo += c * step;
-            n = min(step - 1, n - c * step);
+    const int warp = threadIdx.x >> 5;
+    for (int i = warp, b = 0; i < n_tok; i += kAppendThreads / 32) {
+        const int t = t0 + i;
+        int start, count;
+        if (a.cu_tokens == nullptr) {
+            count = a.T / a.B;
+            b = t / count;
+            start = b * count;
+        } else {
+            b = request_of(a.cu_tokens, b, a.B, t);
+            start = b < a.B ? __ldg(a.cu_tokens + b) : 0;
+            count = b < a.B ? __ldg(a.cu_tokens + b + 1) - start : 0;
         }
-        b = lo;
-        if (b >= a.B) return;  // a row behind the last request
-        first = __ldg(a.cu_tokens + b);
-        count = __ldg(a.cu_tokens + b + 1) - first;
+        if ((threadIdx.x & 31) != 0) continue;
+        AppendToken tok = {-2, 0};
+        bool bad = false;
+        if (b < a.B) {  // else a row behind the last request
+            const long long pos = (long long)__ldg(a.seq_lens + b) - count + (t - start);
+            bad = t < start || pos < 0 || pos >= a.pages_per_req * a.page_size || (a.rot_dim > 0 && pos >= a.max_pos);
+            if (!bad) {
+                tok.pos = int(pos);
+                const int page = __ldg(a.page_table + (long long)b * a.pages_per_req + tok.pos / a.page_size);
+                bad = page < 0 || page >= a.num_pages;
+                tok.row = bad ? -1 : (long long)page * a.page_size + tok.pos % a.page_size;
+            }
+        }
+        tokens[i] = tok;
+        if (bad && blockIdx.y == 0) flag_error(a.err, kErrIndex);
     }
-    const int cap = a.pages_per_req * a.page_size;
-    const int len = __ldg(a.seq_lens + b);
-    const long long pos_ll = (long long)len - count + (t - first);
-    if (t < first || pos_ll < 0 || pos_ll >= cap || (a.rot_dim > 0 && pos_ll >= a.max_pos)) {
-        if (threadIdx.x == 0) flag_error(a.err, kErrIndex);
-        return;
-    }
-    const int pos = int(pos_ll);
-    const int page = __ldg(a.page_table + (long long)b * a.pages_per_req + pos / a.page_size);
-    float cs[8], sn[8];
-    if (rotated) {
-        const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (long long)pos * a.rot_dim + 8 * s);
-        const float4 *row2 = reinterpret_cast<const float4 *>(a.cos_sin + (long long)pos * a.rot_dim + a.rot_dim / 2 + 8 * s);
-        const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row2), s1 = __ldg(row2 + 1);
-        cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-        sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
-    }
-    const bool page_ok = page >= 0 && page < a.num_pages;
-    if (!page_ok && threadIdx.x == 0) flag_error(a.err, kErrIndex);
-    const long long row = page_ok ? (long long)page * a.page_size + pos % a.page_size : 0;
+    __syncthreads();
 
+    for (int base = 0; base < n_tok; base += side) {
+        const int t = t0 + base + mine;
+        const AppendToken tok = base + mine < n_tok ? tokens[base + mine] : AppendToken{-2, 0};
+        const bool there = tok.row >= -1;
+        if (base > 0) load(t, h_first);
+        float cs[8], sn[8];
+        if (rotated && there) {
+            const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (long long)tok.pos * a.rot_dim + 8 * s);
+            const float4 *row2 = reinterpret_cast<const float4 *>(a.cos_sin + (long long)tok.pos * a.rot_dim + a.rot_dim / 2 + 8 * s);
+            const float4 c0 = __ldg(row), c1 = __ldg(row + 1), s0 = __ldg(row2), s1 = __ldg(row2 + 1);
+            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+        } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int item = item0 + u * kAppendThreads;
-        const int h = item / SLOTS;
-        const bool is_q = h < a.Hq;
-        const bool is_v = h >= a.Hq + a.Hkv;
-        const int g = is_v ? h - a.Hq - a.Hkv : h - a.Hq;  // KV head
-        const bool store_kv = item < items && !is_q && page_ok;
-        float x[8], y[8];
-        unpack8(wa[u], x);
-        unpack8(wb[u], y);
-        if (rotated && !is_v) {
-            if (a.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-                    x[2 * i] = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(x1, sn[i]));
-                    x[2 * i + 1] = __fadd_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x0, sn[i]));
-                    y[2 * i] = __fsub_rn(__fmul_rn(y0, cs[i + 4]), __fmul_rn(y1, sn[i + 4]));
-                    y[2 * i + 1] = __fadd_rn(__fmul_rn(y1, cs[i + 4]), __fmul_rn(y0, sn[i + 4]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x0 = x[i], y0 = y[i];
-                    x[i] = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(y0, sn[i]));
-                    y[i] = __fadd_rn(__fmul_rn(y0, cs[i]), __fmul_rn(x0, sn[i]));
-                }
-            }
+            for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
         }
-        if (is_q) {
-            __nv_bfloat16 *dst = a.q_out + ((long long)t * a.Hq + h) * D;
-            *reinterpret_cast<uint4 *>(dst + off_a) = pack8(x);
-            *reinterpret_cast<uint4 *>(dst + off_b) = pack8(y);
-        }
-        uint8_t *pool = is_v ? a.v_pool : a.k_pool;
-        const long long head_row = row * a.Hkv + g;
-        if constexpr (KVT == GQA_KV_BF16) {
-            if (store_kv) {
-                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(pool) + head_row * D;
-                *reinterpret_cast<uint4 *>(dst + off_a) = pack8(x);
-                *reinterpret_cast<uint4 *>(dst + off_b) = pack8(y);
-            }
-        } else if constexpr (KVT == GQA_KV_INT4) {
-            // the row's range over the D / 16 threads of the head (every lane
-            // takes part: a warp can hold q heads beside k heads)
-            float mn = INFINITY, mx = -INFINITY;
+
+        // every thread makes the same number of rounds: 4-bit rows are reduced by shuffles
+        const int rounds = (a.heads_per_cta + a.lanes * kAppendBatch - 1) / (a.lanes * kAppendBatch);
+        for (int round = 0; round < rounds; ++round) {
+            const int h0 = h_first + round * kAppendBatch * a.lanes;
+            if (round > 0) load(t, h0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = int4_input(x[i]);
-                y[i] = int4_input(y[i]);
-                mn = fminf(mn, fminf(x[i], y[i]));
-                mx = fmaxf(mx, fmaxf(x[i], y[i]));
-            }
+            for (int u = 0; u < kAppendBatch; ++u) {
+                const int h = h0 + u * a.lanes;
+                const bool is_q = h < a.Hq;
+                const bool is_v = h >= a.Hq + a.Hkv;
+                const int g = is_v ? h - a.Hq - a.Hkv : h - a.Hq;  // KV head
+                const bool valid = h < h_end && there;
+                const bool store_kv = valid && !is_q && tok.row >= 0;
+                float x[8], y[8];
+                unpack8(wa[u], x);
+                unpack8(wb[u], y);
+                if (rotated && !is_v) {
+                    if (a.interleaved) {
 #pragma unroll
-            for (int o = 1; o < SLOTS; o *= 2) {
-                mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            }
-            const __half zero_h = __float2half_rn(mn);
-            const float zero = __half2float(zero_h);
-            const __half step_h = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(mx, zero), 1.f / 15.f), 0.f));
-            const float step = __half2float(step_h);
-            const float inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
-            uint32_t ca = 0, cb = 0;
+                        for (int i = 0; i < 4; ++i) {
+                            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+                            x[2 * i] = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(x1, sn[i]));
+                            x[2 * i + 1] = __fadd_rn(__fmul_rn(x1, cs[i]), __fmul_rn(x0, sn[i]));
+                            y[2 * i] = __fsub_rn(__fmul_rn(y0, cs[i + 4]), __fmul_rn(y1, sn[i + 4]));
+                            y[2 * i + 1] = __fadd_rn(__fmul_rn(y1, cs[i + 4]), __fmul_rn(y0, sn[i + 4]));
+                        }
+                    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float ux = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], zero), inv)), 0.f), 15.f);
-                const float uy = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(y[i], zero), inv)), 0.f), 15.f);
-                ca |= uint32_t(ux) << (4 * i);
-                cb |= uint32_t(uy) << (4 * i);
-            }
-            if (store_kv) {
-                uint8_t *dst = pool + head_row * (D / 2);
-                *reinterpret_cast<uint32_t *>(dst + off_a / 2) = ca;
-                *reinterpret_cast<uint32_t *>(dst + off_b / 2) = cb;
-                if (s == 0)
-                    *reinterpret_cast<__half2 *>(a.params + head_row * 4 + (is_v ? 2 : 0)) = __halves2half2(step_h, zero_h);
-            }
-        } else if (store_kv) {
-            const float *scales = is_v ? a.v_scales : a.k_scales;
-            const float inv = scales != nullptr ? __fdiv_rn(1.f, __ldg(scales + (a.n_scales > 1 ? g : 0)))
-                                                : (is_v ? a.v_inv : a.k_inv);
-            uint32_t c[4];
+                        for (int i = 0; i < 8; ++i) {
+                            const float x0 = x[i], y0 = y[i];
+                            x[i] = __fsub_rn(__fmul_rn(x0, cs[i]), __fmul_rn(y0, sn[i]));
+                            y[i] = __fadd_rn(__fmul_rn(y0, cs[i]), __fmul_rn(x0, sn[i]));
+                        }
+                    }
+                }
+                if (is_q && valid) {
+                    __nv_bfloat16 *dst = a.q_out + ((long long)t * a.Hq + h) * D;
+                    *reinterpret_cast<uint4 *>(dst + off_a) = pack8(x);
+                    *reinterpret_cast<uint4 *>(dst + off_b) = pack8(y);
+                }
+                uint8_t *pool = is_v ? a.v_pool : a.k_pool;
+                const long long head_row = tok.row * a.Hkv + g;
+                if constexpr (KVT == GQA_KV_BF16) {
+                    if (store_kv) {
+                        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(pool) + head_row * D;
+                        *reinterpret_cast<uint4 *>(dst + off_a) = pack8(x);
+                        *reinterpret_cast<uint4 *>(dst + off_b) = pack8(y);
+                    }
+                } else if constexpr (KVT == GQA_KV_INT4) {
+                    if (!__any_sync(0xffffffffu, store_kv)) continue;
+                    // the row's range over the D / 16 threads of the head (every lane
+                    // takes part: a warp can hold q heads beside k heads)
+                    float mn = INFINITY, mx = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float *p = j < 2 ? x + 4 * j : y + 4 * (j - 2);
-                if constexpr (KVT == GQA_KV_FP8_E4M3FN)
-                    c[j] = e4m3x2_from_f32(__fmul_rn(p[0], inv), __fmul_rn(p[1], inv)) |
-                           e4m3x2_from_f32(__fmul_rn(p[2], inv), __fmul_rn(p[3], inv)) << 16;
-                else
-                    c[j] = int8_code(p[0], inv) | int8_code(p[1], inv) << 8 | int8_code(p[2], inv) << 16 |
-                           int8_code(p[3], inv) << 24;
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = int4_input(x[i]);
+                        y[i] = int4_input(y[i]);
+                        mn = fminf(mn, fminf(x[i], y[i]));
+                        mx = fmaxf(mx, fmaxf(x[i], y[i]));
+                    }
+#pragma unroll
+                    for (int o = 1; o < SLOTS; o *= 2) {
+                        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    }
+                    const __half zero_h = __float2half_rn(mn);
+                    const float zero = __half2float(zero_h);
+                    const __half step_h = __float2half_rn(fmaxf(__fmul_rn(__fsub_rn(mx, zero), 1.f / 15.f), 0.f));
+                    const float step = __half2float(step_h);
+                    const float inv = step > 0.f ? __fdiv_rn(1.f, step) : 0.f;
+                    uint32_t ca = 0, cb = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        ca |= int4_code(x[i], zero, inv) << (4 * i);
+                        cb |= int4_code(y[i], zero, inv) << (4 * i);
+                    }
+                    if (store_kv) {
+                        uint8_t *dst = pool + head_row * (D / 2);
+                        *reinterpret_cast<uint32_t *>(dst + off_a / 2) = ca;
+                        *reinterpret_cast<uint32_t *>(dst + off_b / 2) = cb;
+                        if (s == 0)
+                            *reinterpret_cast<__half2 *>(a.params + head_row * 4 + (is_v ? 2 : 0)) = __halves2half2(step_h, zero_h);
+                    }
+                } else if (store_kv) {
+                    const float *scales = is_v ? a.v_scales : a.k_scales;
+                    const float inv = scales != nullptr ? __fdiv_rn(1.f, __ldg(scales + (a.n_scales > 1 ? g : 0)))
+                                                        : (is_v ? a.v_inv : a.k_inv);
+                    uint32_t c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float *p = j < 2 ? x + 4 * j : y + 4 * (j - 2);
+                        if constexpr (KVT == GQA_KV_FP8_E4M3FN)
+                            c[j] = e4m3x2_from_f32(__fmul_rn(p[0], inv), __fmul_rn(p[1], inv)) |
+                                   e4m3x2_from_f32(__fmul_rn(p[2], inv), __fmul_rn(p[3], inv)) << 16;
+                        else
+                            c[j] = int8_code(p[0], inv) | int8_code(p[1], inv) << 8 | int8_code(p[2], inv) << 16 |
+                                   int8_code(p[3], inv) << 24;
+                    }
+                    uint8_t *dst = pool + head_row * D;
+                    *reinterpret_cast<uint2 *>(dst + off_a) = make_uint2(c[0], c[1]);
+                    *reinterpret_cast<uint2 *>(dst + off_b) = make_uint2(c[2], c[3]);
+                }
             }
-            uint8_t *dst = pool + head_row * D;
-            *reinterpret_cast<uint2 *>(dst + off_a) = make_uint2(c[0], c[1]);
-            *reinterpret_cast<uint2 *>(dst + off_b) = make_uint2(c[2], c[3]);
         }
     }
 }
@@ -290,122 +349,176 @@ cudaError_t launch_pdl(void (*kern)(Args), const Args &a, dim3 grid, int threads
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+// With enough tokens a CTA walks over all heads of its tokens, with the number
+// of heads side by side (a power of two up to 16: 65K tokens of 80 heads of 128
+// took 227 us with 16, 237 with 32) that leaves the fewest places of a batch
+// empty, and of those the fewest batches; with few tokens (a decode step) the
+// heads are spread over the grid, one head a thread.
 template <int D, int KVT>
-cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream) {
-    constexpr int U = 4;
-    const int items = (a.Hq + 2 * a.Hkv) * (D / 16);
-    const int per = kAppendThreads * U;
-    return launch_pdl(gqa_paged_append_kernel<D, KVT, U>, a, dim3(unsigned(a.T), unsigned((items + per - 1) / per)),
-                      kAppendThreads, stream);
+cudaError_t launch_append(AppendArgs a, cudaStream_t stream) {
+    constexpr int SLOTS = D / 16;
+    const int heads = a.Hq + 2 * a.Hkv;
+    int lanes = 1;
+    long best = -1;
+    for (int n = 1; n <= 16; n *= 2) {
+        const long batches = (heads + n * kAppendBatch - 1) / (n * kAppendBatch);
+        const long cost = 16 * batches * kAppendBatch * n + batches * heads;
+        if (best < 0 || cost < best) best = cost, lanes = n;
+    }
+    a.lanes = lanes;
+    a.heads_per_cta = heads;
+    const int side = kAppendThreads / (SLOTS * lanes);
+    const long groups = (long(a.T) + side - 1) / side;
+    if (groups < 304) a.heads_per_cta = lanes;  // fewer than two CTAs an SM
+    // several groups of tokens a CTA where that leaves 16 CTAs an SM
+    long per = groups / (16 * 152);
+    if (per > kAppendTokens / side) per = kAppendTokens / side;
+    a.tokens = side * int(per < 1 ? 1 : per);
+    const long ctas = (long(a.T) + a.tokens - 1) / a.tokens;
+    return launch_pdl(gqa_paged_append_kernel<D, KVT>, a,
+                      dim3(unsigned(ctas), unsigned((heads + a.heads_per_cta - 1) / a.heads_per_cta)), kAppendThreads, stream);
 }
 
 // ------------------------------------------------------------------ gather
 //
-// A unit is 8 elements of K and the same 8 of V: one 16-byte store each.  The
-// units of a request are contiguous in the output, so a CTA takes a run of
-// them, neighbouring threads write neighbouring pieces, and a thread has the
-// loads of all its units in flight before it converts the first.
+// A warp takes a run of at most 32 tokens of one request; each lane looks up
+// one token's pool row.  A unit is 16 elements of a token's K and the same 16 of
+// V; neighbouring lanes take neighbouring units, so they read and write
+// neighbouring pieces, and a lane has the loads of a batch of units in flight
+// before it converts the first.
 constexpr int kGatherThreads = 256;
-constexpr int kGatherUnits = 4;
+// units of a lane in flight
+__host__ __device__ constexpr int gather_units(int kvt) { return kvt == GQA_KV_BF16 ? 2 : 4; }
+
+// Codes of 16 elements: 32 bytes of bf16, 16 of 8-bit codes, 8 of 4-bit codes.
+template <int KVT>
+struct GatherCodes {
+    uint32_t w[KVT == GQA_KV_BF16 ? 8 : KVT == GQA_KV_INT4 ? 2 : 4];
+};
 
 template <int KVT>
-__device__ __forceinline__ uint4 gather_load(const uint8_t *pool, long long elem) {
-    if constexpr (KVT == GQA_KV_BF16) return __ldg(reinterpret_cast<const uint4 *>(pool + elem * 2));
-    if constexpr (KVT == GQA_KV_INT4) return make_uint4(__ldg(reinterpret_cast<const unsigned int *>(pool + elem / 2)), 0, 0, 0);
-    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(pool + elem));
-    return make_uint4(x.x, x.y, 0, 0);
+__device__ __forceinline__ void gather_load(GatherCodes<KVT> &c, const uint8_t *pool, long long elem) {
+    if constexpr (KVT == GQA_KV_INT4) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(pool + elem / 2));
+        c.w[0] = x.x, c.w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < (KVT == GQA_KV_BF16 ? 2 : 1); ++i) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(pool + elem * (KVT == GQA_KV_BF16 ? 2 : 1)) + i);
+            c.w[4 * i] = x.x, c.w[4 * i + 1] = x.y, c.w[4 * i + 2] = x.z, c.w[4 * i + 3] = x.w;
+        }
+    }
 }
 
 // value = code * scale + zero in fp32 (the product is exact for 4-bit codes
-// and fp16 scales; 8-bit values round once here and once to bf16)
+// and fp16 scales; 8-bit values round once here and once to bf16); elements
+// 8 half .. 8 half + 7
 template <int KVT>
-__device__ __forceinline__ uint4 gather_value(const uint4 &w, float scale, float zero) {
-    if constexpr (KVT == GQA_KV_BF16) return w;
-    float x[8];
+__device__ __forceinline__ uint4 gather_value(const GatherCodes<KVT> &c, int half, float scale, float zero) {
+    if constexpr (KVT == GQA_KV_BF16) {
+        return make_uint4(c.w[4 * half], c.w[4 * half + 1], c.w[4 * half + 2], c.w[4 * half + 3]);
+    } else {
+        float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (KVT == GQA_KV_INT4) {
-            x[i] = __fadd_rn(__fmul_rn(float((w.x >> (4 * i)) & 15u), scale), zero);
-        } else {
-            const uint32_t word = i < 4 ? w.x : w.y;
-            if constexpr (KVT == GQA_KV_INT8) {
-                x[i] = __fmul_rn(float(int8_t(word >> (8 * (i & 3)))), scale);
-            } else if ((i & 1) == 0) {
-                const uint32_t h2 = e4m3x2_to_f16x2(uint16_t(word >> (8 * (i & 3))));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-                x[i] = __fmul_rn(f.x, scale);
-                x[i + 1] = __fmul_rn(f.y, scale);
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (KVT == GQA_KV_INT4) {
+                x[i] = fmaf(__uint_as_float((c.w[half] >> (4 * i) & 15u) | 0x4b000000u) - kMagic, scale, zero);
+            } else {
+                const uint32_t word = c.w[2 * half + i / 4];
+                if constexpr (KVT == GQA_KV_INT8) {
+                    const uint32_t byte = (word >> (8 * (i & 3)) & 0xffu) ^ 0x80u;  // code + 128
+                    x[i] = __fmul_rn(__uint_as_float(byte | 0x4b000000u) - (kMagic + 128.f), scale);
+                } else if ((i & 1) == 0) {
+                    const uint32_t h2 = e4m3x2_to_f16x2(uint16_t(word >> (8 * (i & 3))));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+                    x[i] = __fmul_rn(f.x, scale);
+                    x[i + 1] = __fmul_rn(f.y, scale);
+                }
             }
         }
+        return pack8(x);
     }
-    return pack8(x);
 }
 
 template <int D, int KVT>
 __global__ void __launch_bounds__(kGatherThreads) gqa_paged_gather_dense_kernel(const GatherArgs a) {
-    const int b = blockIdx.y;
-    const int upt = a.Hkv * (D / 8);  // units of a token
+    constexpr int SLOTS = D / 16, U = gather_units(KVT);
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
     pdl_wait_primary();
     const int cap = a.pages_per_req * a.page_size;
     const int len0 = __ldg(a.seq_lens + b), start0 = a.starts != nullptr ? __ldg(a.starts + b) : 0;
     const int len = min(max(len0, 0), cap), start = max(start0, 0);
     const int n = min(len - start, a.rows);
     if (threadIdx.x == 0 && blockIdx.x == 0 && (len != len0 || start != start0)) flag_error(a.err, kErrIndex);
-    const long long unit0 = (long long)blockIdx.x * (kGatherThreads * kGatherUnits);
-    if (n <= 0 || unit0 >= (long long)n * upt) return;
-    const int tok0 = int(unit0 / upt);
-    const int rem0 = int(unit0 - (long long)tok0 * upt);
-
-    uint4 kw[kGatherUnits], vw[kGatherUnits];
-    float ks[kGatherUnits], kz[kGatherUnits], vs[kGatherUnits], vz[kGatherUnits];
-    bool there[kGatherUnits];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kGatherUnits; ++i) {
-        const unsigned r = unsigned(rem0) + threadIdx.x + i * kGatherThreads;
-        const int j = tok0 + int(r / unsigned(upt));  // output row
-        const int u = int(r % unsigned(upt));
-        there[i] = j < n;
-        kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
-        ks[i] = kz[i] = vs[i] = vz[i] = 0.f;
-        if (!there[i]) continue;
-        const int pos = start + j;
+    // the warp's first output row
+    const long long j_first = ((long long)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5)) * a.tokens;
+    if (j_first >= n) return;
+    const int j0 = int(j_first), run = min(a.tokens, n - j0);
+    int row_l = -1;  // pool row of token `lane` of the run, -1 where the page is out of range
+    if (lane < run) {
+        const int pos = start + j0 + lane;
         const int page = __ldg(a.page_table + (long long)b * a.pages_per_req + pos / a.page_size);
-        if (page < 0 || page >= a.num_pages) {
-            bad = true;  // the row reads as zeros
-            continue;
-        }
-        const long long head_row = ((long long)page * a.page_size + pos % a.page_size) * a.Hkv + u / (D / 8);
-        const long long elem = head_row * D + 8 * (u % (D / 8));
-        kw[i] = gather_load<KVT>(a.k_pool, elem);
-        vw[i] = gather_load<KVT>(a.v_pool, elem);
-        if constexpr (KVT == GQA_KV_INT4) {
-            const uint2 p = __ldg(reinterpret_cast<const uint2 *>(a.params + head_row * 4));
-            const float2 pk = __half22float2(*reinterpret_cast<const __half2 *>(&p.x));
-            const float2 pv = __half22float2(*reinterpret_cast<const __half2 *>(&p.y));
-            ks[i] = pk.x, kz[i] = pk.y, vs[i] = pv.x, vz[i] = pv.y;
-        } else if constexpr (KVT != GQA_KV_BF16) {
-            const int si = a.n_scales > 1 ? u / (D / 8) : 0;
-            ks[i] = a.k_scales != nullptr ? __ldg(a.k_scales + si) : a.k_scale;
-            vs[i] = a.v_scales != nullptr ? __ldg(a.v_scales + si) : a.v_scale;
-        }
+        if (page >= 0 && page < a.num_pages)
+            row_l = page * a.page_size + pos % a.page_size;  // num_pages * page_size < 2^31
+        else
+            flag_error(a.err, kErrIndex);
     }
-    if (bad) flag_error(a.err, kErrIndex);
+    const unsigned upt = unsigned(a.Hkv) * SLOTS;  // units of a token
+    const unsigned units = unsigned(run) * upt;
+    for (unsigned u0 = 0; u0 < units; u0 += 32 * U) {
+        GatherCodes<KVT> k[U], v[U];
+        float ks[U], kz[U], vs[U], vz[U];
 #pragma unroll
-    for (int i = 0; i < kGatherUnits; ++i) {
-        if (!there[i]) continue;
-        const long long o = ((long long)b * a.rows * upt + unit0 + threadIdx.x + i * kGatherThreads) * 8;
-        *reinterpret_cast<uint4 *>(a.k_out + o) = gather_value<KVT>(kw[i], ks[i], kz[i]);
-        *reinterpret_cast<uint4 *>(a.v_out + o) = gather_value<KVT>(vw[i], vs[i], vz[i]);
+        for (int i = 0; i < U; ++i) {
+            const unsigned x = u0 + i * 32 + lane;
+            const unsigned j = x / upt, u = x - j * upt;  // token of the run, unit of the token
+            const int r = __shfl_sync(0xffffffffu, row_l, j & 31);
+            const long long row = x < units ? r : -1;
+            k[i] = v[i] = {};  // a row without a page reads as zeros
+            ks[i] = kz[i] = vs[i] = vz[i] = 0.f;
+            if (row < 0) continue;
+            const long long head_row = row * a.Hkv + u / SLOTS;
+            const long long elem = head_row * D + 16 * (u % SLOTS);
+            gather_load<KVT>(k[i], a.k_pool, elem);
+            gather_load<KVT>(v[i], a.v_pool, elem);
+            if constexpr (KVT == GQA_KV_INT4) {
+                const uint2 p = __ldg(reinterpret_cast<const uint2 *>(a.params + head_row * 4));
+                const float2 pk = __half22float2(*reinterpret_cast<const __half2 *>(&p.x));
+                const float2 pv = __half22float2(*reinterpret_cast<const __half2 *>(&p.y));
+                ks[i] = pk.x, kz[i] = pk.y, vs[i] = pv.x, vz[i] = pv.y;
+            } else if constexpr (KVT != GQA_KV_BF16) {
+                const int si = a.n_scales > 1 ? int(u / SLOTS) : 0;
+                ks[i] = a.k_scales != nullptr ? __ldg(a.k_scales + si) : a.k_scale;
+                vs[i] = a.v_scales != nullptr ? __ldg(a.v_scales + si) : a.v_scale;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const unsigned x = u0 + i * 32 + lane;
+            if (x >= units) continue;
+            const long long o = (((long long)b * a.rows + j0) * upt + x) * 16;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                *reinterpret_cast<uint4 *>(a.k_out + o + 8 * half) = gather_value<KVT>(k[i], half, ks[i], kz[i]);
+                *reinterpret_cast<uint4 *>(a.v_out + o + 8 * half) = gather_value<KVT>(v[i], half, vs[i], vz[i]);
+            }
+        }
     }
 }
 
 template <int D, int KVT>
-cudaError_t launch_gather(const GatherArgs &a, cudaStream_t stream) {
-    const long long units = (long long)a.rows * a.Hkv * (D / 8);
-    const long long per = kGatherThreads * kGatherUnits;
-    return launch_pdl(gqa_paged_gather_dense_kernel<D, KVT>, a, dim3(unsigned((units + per - 1) / per), unsigned(a.B)),
-                      kGatherThreads, stream);
+cudaError_t launch_gather(GatherArgs a, cudaStream_t stream) {
+    // Tokens of a warp: one batch of its lanes' units, fewer while that leaves
+    // less than 32 warps an SM.  (Runs of 32 tokens of 8 heads of 128, 2048 units
+    // a warp, took 145 us where runs of 2 took 110: a CTA should write one short
+    // piece of the output at a time.)
+    const long long all = (long long)a.rows * a.B / (32 * 152);
+    const int most = 32 * gather_units(KVT) / (a.Hkv * (D / 16));
+    a.tokens = most > 32 ? 32 : most < 1 ? 1 : most;
+    if (all < a.tokens) a.tokens = all < 1 ? 1 : int(all);
+    const int per = a.tokens * (kGatherThreads / 32);
+    return launch_pdl(gqa_paged_gather_dense_kernel<D, KVT>, a,
+                      dim3(unsigned((a.rows + per - 1) / per), unsigned(a.B)), kGatherThreads, stream);
 }
 
 // Checks shared by both entry points: pool type, scales, parameters.
@@ -458,8 +571,7 @@ extern "C" gqa_status gqa_paged_append(const void *q, long long q_stride, void *
     if (k_pool == nullptr || v_pool == nullptr || page_table == nullptr || seq_lens == nullptr ||
         (T > 0 && (k == nullptr || v == nullptr)))
         return GQA_ERR_INVALID_ARG;
-    const long long heads_max = 1 << 20;
-    if (Hkv > heads_max || (has_q && Hq > heads_max)) return GQA_ERR_UNSUPPORTED;
+    if (Hkv > (1 << 18) || (has_q && Hq > (1 << 18)) || T > (1 << 30)) return GQA_ERR_UNSUPPORTED;
     if (k_stride < (long long)Hkv * D || v_stride < (long long)Hkv * D || (has_q && q_stride < (long long)Hq * D))
         return GQA_ERR_INVALID_ARG;
     if (k_stride % 8 != 0 || v_stride % 8 != 0 || (has_q && q_stride % 8 != 0)) return GQA_ERR_ALIGNMENT;
@@ -522,7 +634,7 @@ extern "C" gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const v
     if (k_pool == nullptr || v_pool == nullptr || page_table == nullptr || seq_lens == nullptr ||
         (rows > 0 && (k_out == nullptr || v_out == nullptr)))
         return GQA_ERR_INVALID_ARG;
-    if (Hkv > (1 << 20) || (long long)rows * Hkv * (D / 8) >= (1LL << 40)) return GQA_ERR_UNSUPPORTED;
+    if (Hkv > (1 << 20) || rows > (1 << 30)) return GQA_ERR_UNSUPPORTED;
     if (!host_aligned(k_pool, 16) || !host_aligned(v_pool, 16) || !host_aligned(k_out, 16) ||
         !host_aligned(v_out, 16) || !host_aligned(page_table, 4) || !host_aligned(seq_lens, 4) ||
         !host_aligned(starts, 4))
