@@ -32,7 +32,7 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     if ((long long)(Hq / Hkv) * Sq > kInt4MaxRows) return GQA_ERR_UNSUPPORTED;
     if ((long long)pages_per_req * page_size > (1LL << 31) - 64) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
     p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
-    if (p->max_steps >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
+    if (p->max_steps + B >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
     p->B = B, p->Sq = Sq, p->Hq = Hq, p->Hkv = Hkv, p->D = D;
     p->G = Hq / Hkv;
     p->Mq = p->G * Sq;
@@ -44,6 +44,7 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     p->nhb = (Hkv + hb - 1) / hb;
     const int groups = int4_consumers(p->NT) / (hb * p->RG);
     p->rings = groups < kInt4MaxRings ? groups : kInt4MaxRings;
+    while (groups % p->rings != 0) --p->rings;
     p->lanes = groups / p->rings;
     p->R = 16;
     while (page_size % p->R != 0) p->R /= 2;

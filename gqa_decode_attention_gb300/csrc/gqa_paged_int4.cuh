@@ -49,13 +49,15 @@ constexpr int kInt4MaxStages = 8;   // of a ring
 constexpr int kInt4MaxRings = 4;    // of a CTA, one producer warp each
 // Consumer warps of a CTA that hold NT tiles of 8 query rows, and the
 // registers a thread of theirs and of the producers' warpgroup has: together
-// what the CTA was launched with (20 warps of 96, or 12 of 168).
+// what the CTA was launched with (20 warps of 96, or 12 of 168).  (12 warps of
+// 160 registers for 16 rows each were slower than 8 of 216.)
 __host__ __device__ constexpr int int4_consumers(int nt) { return nt == 1 ? 16 : 8; }
 __host__ __device__ constexpr int int4_threads(int nt) { return 32 * (int4_consumers(nt) + 4); }
 __host__ __device__ constexpr int int4_consumer_regs(int nt) { return nt == 1 ? 112 : 216; }
 __host__ __device__ constexpr int int4_producer_regs(int nt) { return nt == 1 ? 32 : 72; }
 static_assert(16 * int4_consumer_regs(1) + 4 * int4_producer_regs(1) == 20 * 96, "registers");
 static_assert(8 * int4_consumer_regs(2) + 4 * int4_producer_regs(2) == 12 * 168, "registers");
+constexpr int kInt4WarpRequests = 256;  // up to so many requests each warp works out the schedule for itself
 constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
 
 // x / d for x < 2^31, d of the host's choosing: m = floor(2^(31 + l) / d) + 1, l = ceil(log2 d).  (m d lies above
@@ -100,6 +102,7 @@ struct Int4Head {
     uint32_t mask[kInt4MaxRings][kInt4MaxStages];  // tokens of a stage that are there
     int begin[kInt4MaxRings], end[kInt4MaxRings];  // steps of the ring's share
     unsigned long long first[kInt4MaxRings];  // its first request (high half), and that one's first step
+    int warp_sum[20];
     int abort;
 };
 constexpr int kInt4HeadBytes = 1024;
@@ -124,6 +127,22 @@ __device__ __forceinline__ uint32_t prmt4(uint32_t a, uint32_t b, uint32_t sel) 
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
+}
+
+// Operands of a word's codes: of each half's lower byte (upper: its upper byte)
+// lo has the low code u, hi the high one times 16, as fp16 subnormals in units
+// of 2^-24.  The upper byte comes down by a permute that clears the rest, so
+// its high code is a difference, exact, on the FMA pipe: the ALU pipe, at half
+// the issue rate, is what these operands load most.
+__device__ __forceinline__ void code_pairs(uint32_t word, int upper, uint32_t &lo, uint32_t &hi) {
+    if (upper) {
+        const uint32_t b = prmt4(word, 0, 0x4341u);
+        lo = b & 0x000f000fu;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(lo));
+    } else {
+        lo = word & 0x000f000fu;
+        hi = word & 0x00f000f0u;
+    }
 }
 
 // Larger of two fp16 pairs, half by half (a NaN gives way to the other).
@@ -252,11 +271,10 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     constexpr int VW = D / 64;      // V words a lane holds of a token
     constexpr int DB = D / 16;      // output blocks: block j holds elements (D/8) gi + 2 j, + 2 j + 1
     constexpr int CW = int4_consumers(NT);
-    constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+    constexpr uint32_t M0 = 0x000f000fu, M = 0x00ff00ffu;
     extern __shared__ __align__(1024) uint8_t smem4[];
     Int4Head *head = reinterpret_cast<Int4Head *>(smem4);
     volatile int *abort_flag = &head->abort;
-    int *warp_sum = reinterpret_cast<int *>(smem4 + kInt4HeadBytes);  // the rings are not in use yet
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hb0 = blockIdx.x * a.HB;
@@ -281,66 +299,108 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     }
     pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
 
-    // ---- schedule.  Request b takes ceil(len_b / 32) steps; worker w takes
-    // steps [w T / W, (w + 1) T / W) of the T steps of all requests in order.
-    // Each thread sums a run of requests (with few requests most warps have
-    // none and go on to the barriers), a scan gives their first steps, and
-    // whoever holds a share's first step writes it down.  An empty request
-    // belongs to the worker whose range holds its step (the last worker for
-    // those at the very end).
+    // The CW consumer warps form groups of HB x RG, `lanes` groups to a ring;
+    // producer warp r serves ring r.  Warps of an SM sub-partition (warp mod 4)
+    // run oldest first, and a ring is as fast as its slowest warp, so the
+    // groups' warps are dealt so that each group has warps of every age.
+    const int members = a.HB * a.RG, groups = a.rings_max * a.lanes;
+    const int member = warp / groups;
+    const int group = (warp + (groups == 2 ? member >> 1 : groups == 4 ? member : 0)) % groups;
+    const int r = warp < CW ? group / a.lanes : warp - CW;
+
+    // ---- schedule.  Request b takes n_b = ceil(len_b / 32) steps and one more
+    // for what changing requests costs (queries, output); worker w takes places
+    // [w T / W, (w + 1) T / W) of the T places of all requests in order, b's
+    // steps first from P_b on.  An empty request belongs to whoever holds P_b.
     bool bad = false;
-    {
+    int w_begin, w_end, seg_b, seg_p;
+    if (a.B <= kInt4WarpRequests) {
+        // each warp for itself: a run of requests a lane, a scan, and the first
+        // lane with a request that holds the share's first step
+        const int run = (a.B + 31) / 32;
+        const int b0 = min(a.B, lane * run), b1 = min(a.B, b0 + run);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(a.seq_lens + b);
+            bad |= len < 0 || len > cap;
+            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + 1;
+        }
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        const int T = __shfl_sync(0xffffffffu, incl, 31);
+        const int w = r * int(gridDim.y) + int(blockIdx.y);
+        w_begin = int4_share(min(w, a.workers), T, a.workers);
+        w_end = int4_share(min(w + 1, a.workers), T, a.workers);
+        const bool record = a.step_prefix != nullptr && threadIdx.x < 32 && blockIdx.x == 0 && blockIdx.y == 0;
+        int P = incl - mine, hit = a.B, hit_p = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int n = run == 1 ? mine - 1 : (min(max(__ldg(a.seq_lens + b), 0), cap) + kInt4Step - 1) / kInt4Step;
+            if (record) a.step_prefix[b] = P;
+            if (hit == a.B && P + max(n, 1) > w_begin) hit = b, hit_p = P;
+            P += n + 1;
+        }
+        if (record && lane == 0) a.step_prefix[a.B] = T;
+        const unsigned found = __ballot_sync(0xffffffffu, hit < a.B);
+        const int src = found != 0 ? __ffs(found) - 1 : 0;
+        seg_b = __shfl_sync(0xffffffffu, hit, src);
+        seg_p = __shfl_sync(0xffffffffu, hit_p, src);
+        if (bad && threadIdx.x < 32 && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
+        bad = false;
+        __syncthreads();  // the barriers are set up
+    } else {
+        // the CTA together: a run of requests a thread
         constexpr int NTH = int4_threads(NT);
         const int run = (a.B + NTH - 1) / NTH;
         const int b0 = min(a.B, int(threadIdx.x) * run), b1 = min(a.B, b0 + run);
-        const int in_use = ((a.B + run - 1) / run + 31) / 32;  // warps with requests
-        int len0 = 0, mine = 0, incl = 0;
-        if (warp < in_use) {
-            for (int b = b0; b < b1; ++b) {
-                len0 = __ldg(a.seq_lens + b);
-                bad |= len0 < 0 || len0 > cap;
-                len0 = min(max(len0, 0), cap);
-                mine += (len0 + kInt4Step - 1) / kInt4Step;
-            }
-            incl = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += y;
-            }
-            if (lane == 31) warp_sum[warp] = incl;
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(a.seq_lens + b);
+            bad |= len < 0 || len > cap;
+            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + 1;
         }
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        if (lane == 31) head->warp_sum[warp] = incl;
         __syncthreads();
+        int T = 0, P = incl - mine;
+        for (int w = 0; w < CW + 4; ++w) {
+            T += head->warp_sum[w];
+            if (w < warp) P += head->warp_sum[w];
+        }
         if (warp == 0 && lane < a.rings) {
-            int T = 0;
-            for (int w = 0; w < in_use; ++w) T += warp_sum[w];
             const int w = lane * int(gridDim.y) + int(blockIdx.y);
             head->begin[lane] = int4_share(min(w, a.workers), T, a.workers);
             head->end[lane] = int4_share(min(w + 1, a.workers), T, a.workers);
-            if (lane == 0 && a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0) a.step_prefix[a.B] = T;
         }
         __syncthreads();
-        if (warp < in_use) {
-            int P = incl - mine;
-            for (int w = 0; w < warp; ++w) P += warp_sum[w];
-            const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
-            for (int b = b0; b < b1; ++b) {
-                const int len = run == 1 ? len0 : min(max(__ldg(a.seq_lens + b), 0), cap);
-                const int n = (len + kInt4Step - 1) / kInt4Step;
-                if (record) a.step_prefix[b] = P;
-                for (int r = 0; r < a.rings; ++r) {
-                    const int begin = head->begin[r];
-                    if (P <= begin && P + max(n, 1) > begin)  // of several (empty ones first) the first counts
-                        atomicMin(&head->first[r], (unsigned long long)b << 32 | unsigned(P));
-                }
-                P += n;
-            }
-            if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
-            bad = false;
+        const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
+        if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
+        for (int b = b0; b < b1; ++b) {
+            const int n = (min(max(__ldg(a.seq_lens + b), 0), cap) + kInt4Step - 1) / kInt4Step;
+            if (record) a.step_prefix[b] = P;
+            for (int k = 0; k < a.rings; ++k)
+                if (P + max(n, 1) > head->begin[k])  // of those the first counts
+                    atomicMin(&head->first[k], (unsigned long long)b << 32 | unsigned(P));
+            P += n + 1;
         }
-        fence_proxy_async_shared();  // warp_sum's place is written by TMA next
+        if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
+        bad = false;
         __syncthreads();
+        const int k = min(r, a.rings - 1);
+        w_begin = head->begin[k];
+        w_end = head->end[k];
+        seg_b = int(head->first[k] >> 32);
+        seg_p = int(unsigned(head->first[k]));
     }
+    int seg_t = max(w_begin, seg_p);  // past the place of the request before
 
     const int R = a.box_rows;
     // Offsets in a stage: a token's row lies in box t / R, head h, row t % R.
@@ -350,20 +410,17 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     // ============================================================== producers
     if (warp >= CW) {
         fewer_registers<int4_producer_regs(NT)>();
-        const int r = warp - CW;
         if (r >= a.rings) return;
         uint64_t *full = head->full[r], *empty = head->empty[r];
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
-        const int w_end = head->end[r];
-        int seg_b = int(head->first[r] >> 32), seg_p = int(unsigned(head->first[r])), seg_t = head->begin[r];
         const uint32_t box_bytes = uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
         const bool first = lane % R == 0;  // of a box
         int st = 0, gs = 0;
         uint32_t phase = 0;
         bool failed = false;
-        while (seg_t < w_end && !failed) {
+        while (seg_b < a.B && seg_t < w_end && !failed) {
             const int len = min(max(__ldg(a.seq_lens + seg_b), 0), cap);
             const int steps_b = (len + kInt4Step - 1) / kInt4Step;
             const int seg_next = min(w_end, seg_p + steps_b);
@@ -414,11 +471,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 }
                 if (++st == a.stages) st = 0, phase ^= 1;
             }
+            seg_t = seg_next;
             if (seg_next == seg_p + steps_b) {
-                seg_p = seg_next;
+                seg_t = seg_p = seg_next + 1;
                 ++seg_b;
             }
-            seg_t = seg_next;
         }
         if (bad) flag_error(a.err, kErrIndex);
         if (failed && lane == 0) {
@@ -437,20 +494,12 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     }
 
     // ============================================================== consumers
-    // The CW warps form groups of HB x RG, `lanes` groups to a ring.  Warps of an
-    // SM sub-partition (warp mod 4) run oldest first, and a ring is as fast as
-    // its slowest warp, so each group gets warps of every age.
     more_registers<int4_consumer_regs(NT)>();
-    const int members = a.HB * a.RG, groups = a.rings_max * a.lanes;
-    const int member = warp / groups, group = (warp + warp / max(groups, 4)) % groups;
-    const int r = group / a.lanes, turn = group - r * a.lanes;
+    const int turn = group - r * a.lanes;
     const int lh = member / a.RG, rg = member - lh * a.RG;
     if (member >= members || r >= a.rings || lh >= nh) return;
     const int w = r * int(gridDim.y) + int(blockIdx.y);  // worker
     const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
-    const int w_begin = head->begin[r], w_end = head->end[r];
-    int seg_b = int(head->first[r] >> 32), seg_p = int(unsigned(head->first[r])), seg_t = w_begin;
-    const bool last_worker = w == a.workers - 1;
     const int g = hb0 + lh;
     const int gi = lane >> 2, c = lane & 3;
     auto row_off = [&](int t) { return uint32_t(t / R) * a.box_pitch + uint32_t(lh * R + t % R) * ROWB; };
@@ -470,18 +519,35 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const uint32_t full = smem_u32(head->full[r]), mask_at = smem_u32(head->mask[r]);
     constexpr uint32_t kEmpty = offsetof(Int4Head, empty) - offsetof(Int4Head, full);
 
+    int done = 0;    // steps of the share before the segment
     int handed = 0;  // results handed between the lanes so far
     int st = turn;  // the stages are a multiple of the lanes: a lane sees every round of its stages
     uint32_t phase = 0;
     bool failed = false;
+    // Queries as they are in memory: lane gi has row gi (+ 8 a tile), its
+    // quarter c of the elements.  Loaded before the previous segment's results
+    // are written, so that the latency lies under that.
+    uint4 q_next[NT][KW];
+    auto load_queries = [&](int b) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = (rg * NT + nt) * 8 + gi;
+            const int i = row_of(row);
+            const __nv_bfloat16 *src = a.q + ((size_t(b) * a.Sq + i) * a.Hq + g * a.G + (row - i * a.G)) * D + (D / 4) * c;
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+                q_next[nt][w] = row < a.Mq && b < a.B ? __ldg(reinterpret_cast<const uint4 *>(src) + w) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load_queries(seg_b);
     // Segment of the share: steps [seg_t, seg_next) of request seg_b.
-    while (seg_b < a.B && (seg_t < w_end || (last_worker && seg_t == w_end))) {
+    while (seg_b < a.B && seg_t < w_end) {
         const int b = seg_b;
         const int len = min(max(__ldg(a.seq_lens + b), 0), cap);
         const int steps_b = (len + kInt4Step - 1) / kInt4Step;
         const int seg_next = min(w_end, seg_p + steps_b);
         const bool complete = seg_t == seg_p && seg_next == seg_p + steps_b;
-        const int slot = seg_t == w_begin ? 0 : 1;
+        const int slot = seg_t == seg_p ? 1 : 0;  // of a part: a request's first steps, or what follows
 
         // ---- queries.  Lane gi holds row gi (+ 8 a tile) at the elements of
         // its quarter c, times a power of two that brings the row's largest
@@ -492,17 +558,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         float o[NT][DB][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = (rg * NT + nt) * 8 + gi;
-            const bool real = r < a.Mq;
-            const int i = real ? row_of(r) : 0;
-            const __nv_bfloat16 *qrow =
-                a.q + ((size_t(b) * a.Sq + i) * a.Hq + g * a.G + (real ? r - i * a.G : 0)) * D + (D / 4) * c;
             float x[KW][8];
             float mx = 0.f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
-                const uint4 raw = real ? *reinterpret_cast<const uint4 *>(qrow + 8 * w) : make_uint4(0, 0, 0, 0);
-                const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+                const uint32_t rw[4] = {q_next[nt][w].x, q_next[nt][w].y, q_next[nt][w].z, q_next[nt][w].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     x[w][2 * j] = __uint_as_float(rw[j] << 16);
@@ -551,7 +611,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         const int n_causal = a.Sq > 1 ? min(n_seg, n_seg - (max(len - a.Sq + 1, 0) / kInt4Step - (seg_t - seg_p))) : 0;
 
         // this lane's steps of the segment: every lanes-th of the share's
-        const int skip = a.lanes == 1 ? 0 : (turn + a.lanes - (seg_t - w_begin) % a.lanes) % a.lanes;
+        const int skip = a.lanes == 1 ? 0 : (turn + a.lanes - done % a.lanes) % a.lanes;
         for (int left = n_seg - skip; left > 0; left -= a.lanes) {
             const bool ok = bar_wait_bounded(full + 8 * st, phase, a.wait_limit_ns, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -582,15 +642,17 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const uint32_t x0 = h ? kw[2 * t][w] >> 8 : kw[2 * t][w];
-                        const uint32_t x1 = h ? kw[2 * t + 1][w] >> 8 : kw[2 * t + 1][w];
+                        // codes 0, 4 and 1, 5 of the word, or 2, 6 and 3, 7
+                        uint32_t lo0, hi0, lo1, hi1;
+                        code_pairs(kw[2 * t][w], h, lo0, hi0);
+                        code_pairs(kw[2 * t + 1][w], h, lo1, hi1);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint32_t b0 = qf[nt][2 * w + h][0], b1 = qf[nt][2 * w + h][1];
                             if (w == 0 && h == 0)
-                                mma_f16_zero(acc[nt][t], x0 & M0, x1 & M0, x0 & M1, x1 & M1, b0, b1);
+                                mma_f16_zero(acc[nt][t], lo0, lo1, hi0, hi1, b0, b1);
                             else
-                                mma_f16_add(acc[nt][t], x0 & M0, x1 & M0, x0 & M1, x1 & M1, b0, b1);
+                                mma_f16_add(acc[nt][t], lo0, lo1, hi0, hi1, b0, b1);
                         }
                     }
 
@@ -723,16 +785,20 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         const uint32_t sel = h ? 0x7632u : 0x5410u;
                         const uint32_t x = prmt4(vw[4 * t][w], vw[4 * t + 1][w], sel);
                         const uint32_t y = prmt4(vw[4 * t + 2][w], vw[4 * t + 3][w], sel);
-                        const uint32_t x8 = x >> 8, y8 = y >> 8;
+                        // element 2 j: its codes; element 2 j + 1: whole bytes
+                        // (16 times its codes more than that), taken apart in the epilogue
+                        const uint32_t x8 = prmt4(x, 0, 0x4341u), y8 = prmt4(y, 0, 0x4341u);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             const int j = 4 * w + 2 * h;
-                            mma_f16_add(o[nt][j], x & M0, x & M1, y & M0, y & M1, wt[nt][2 * t], wt[nt][2 * t + 1]);
-                            mma_f16_add(o[nt][j + 1], x8 & M0, x8 & M1, y8 & M0, y8 & M1, wt[nt][2 * t], wt[nt][2 * t + 1]);
+                            mma_f16_add(o[nt][j], x & M0, x & M, y & M0, y & M, wt[nt][2 * t], wt[nt][2 * t + 1]);
+                            mma_f16_add(o[nt][j + 1], x8 & M0, x8, y8 & M0, y8, wt[nt][2 * t], wt[nt][2 * t + 1]);
                         }
                     }
         }
         if (failed) break;
+        load_queries(b + 1);
+        done += n_seg;
 
         // ---- lanes: the first one takes the others' results, which lie in
         // shared memory behind the rings, thread for thread.  (Waits on
@@ -814,7 +880,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                 for (int j = 0; j < DB; ++j) {
                     x[2 * j] = fmaf(o[nt][j][e], f24, zf);
-                    x[2 * j + 1] = fmaf(o[nt][j][2 + e], f20, zf);
+                    x[2 * j + 1] = fmaf(o[nt][j][2 + e] - o[nt][j][e], f20, zf);
                 }
                 if (!complete) {
                     const size_t prow = ((((size_t(blockIdx.x) * a.workers + w) * 2 + slot) * a.HB + lh) * a.Mq) + r;
@@ -835,11 +901,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 if (a.lse != nullptr && gi == 0)
                     a.lse[(size_t(b) * a.Hq + h) * a.Sq + i] = lse2 * 0.69314718055994530942f;
             }
+        seg_t = seg_next;
         if (seg_next == seg_p + steps_b) {
-            seg_p = seg_next;
+            seg_t = seg_p = seg_next + 1;
             ++seg_b;
         }
-        seg_t = seg_next;
     }
     if (failed && lane == 0) {
         flag_error(a.err, kErrTimeout);
@@ -852,18 +918,18 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 // row a warp.  A warp reads 32 partials' LSEs at once, one a lane, which gives
 // their weights, then adds them up in order, several in flight: the same bits
 // every time.
-constexpr int kInt4MergeBatch = 10;
+__host__ __device__ constexpr int int4_merge_batch(bool split) { return split ? 10 : 4; }  // partials in flight
 __host__ __device__ constexpr int int4_merge_warps(bool split) { return split ? 16 : 8; }
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_merge_kernel(const Int4Args a) {
-    constexpr int V = D / 32, NW = int4_merge_warps(SPLIT);
+__global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT), SPLIT ? 1 : 5) gqa_paged_int4_merge_kernel(const Int4Args a) {
+    constexpr int V = D / 32, NW = int4_merge_warps(SPLIT), BATCH = int4_merge_batch(SPLIT);
     __shared__ float sm_m[NW], sm_l[NW], sm_o[SPLIT ? NW : 1][D];
     pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y, rr = SPLIT ? int(blockIdx.x) : int(blockIdx.x) * NW + warp;
     const int W = a.workers;
-    const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P, T = a.step_prefix[a.B];
+    const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P - 1, T = a.step_prefix[a.B];
     if (n == 0) return;  // an empty request: written by the main kernel
     // worker of step s: the largest w with floor(w T / W) <= s
     auto holder = [&](int s) {
@@ -878,7 +944,6 @@ __global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_m
     const int parts = w_last - w_first + 1;
     const int each = SPLIT ? (parts + NW - 1) / NW : parts;
     const int from = SPLIT ? warp * each : 0, to = min(parts, from + each);
-    const bool before = int4_share(w_first, T, W) < P;  // the first worker starts in an earlier request: its last slot
 
     float m = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
@@ -889,7 +954,7 @@ __global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_m
         float l2 = -INFINITY;
         // a worker without a step (T < W) holds nothing
         const bool there = part < to && !(T < W && int4_share(w, T, W) == int4_share(w + 1, T, W));
-        const size_t prow = ((((size_t(hb) * W + w) * 2 + (part == 0 && before ? 1 : 0)) * a.HB + lh) * a.Mq) + r;
+        const size_t prow = ((((size_t(hb) * W + w) * 2 + (part == 0 ? 1 : 0)) * a.HB + lh) * a.Mq) + r;
         if (there) l2 = __ldg(a.lse_part + prow);
         float mn = l2;
 #pragma unroll
@@ -907,15 +972,15 @@ __global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_m
         const size_t step = size_t(2) * a.HB * a.Mq * D;  // from a worker's partial to the next one's
         const float *first = a.o_part + ((((size_t(hb) * W + w_first + k0) * 2) * a.HB + lh) * a.Mq + r) * D + lane * V;
         const int n_here = min(32, to - k0);
-        for (int j0 = 0; j0 < n_here; j0 += kInt4MergeBatch) {
-            float x[kInt4MergeBatch][V];
+        for (int j0 = 0; j0 < n_here; j0 += BATCH) {
+            float x[BATCH][V];
 #pragma unroll
-            for (int j = 0; j < kInt4MergeBatch; ++j) {
+            for (int j = 0; j < BATCH; ++j) {
                 const float f = __shfl_sync(0xffffffffu, wgt, (j0 + j) & 31);
 #pragma unroll
                 for (int v = 0; v < V; ++v) x[j][v] = 0.f;
                 if (j0 + j >= n_here || f == 0.f) continue;  // a partial without weight may hold anything
-                const float *src = first + (j0 + j) * step + (k0 + j0 + j == 0 && before ? step / 2 : 0);
+                const float *src = first + (j0 + j) * step + (k0 + j0 + j == 0 ? step / 2 : 0);
                 if constexpr (V == 4) {
                     const float4 t = __ldg(reinterpret_cast<const float4 *>(src));
                     x[j][0] = t.x, x[j][1] = t.y, x[j][2] = t.z, x[j][3] = t.w;
@@ -925,7 +990,7 @@ __global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT)) gqa_paged_int4_m
                 }
             }
 #pragma unroll
-            for (int j = 0; j < kInt4MergeBatch; ++j) {
+            for (int j = 0; j < BATCH; ++j) {
                 const float f = __shfl_sync(0xffffffffu, wgt, (j0 + j) & 31);
 #pragma unroll
                 for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[j][v], acc[v]);
