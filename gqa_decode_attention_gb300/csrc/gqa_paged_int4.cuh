@@ -32,7 +32,8 @@
 // head's rows back to back, and with the 64-byte swizzle (D = 128) and the
 // token order of `tok_of` every fragment read is free of bank conflicts.
 // Parameters come by TMA too, [token][head] (by cp.async where their rows are
-// not 16 bytes).  The warps never wait for
+// not 16 bytes); pages without a factor of 4 take K and V in 16-byte copies to
+// the same places, since a box ends at its page's end.  The warps never wait for
 // one another beyond the ring: each works out its segments from the lengths,
 // and the loads run ahead across request borders.
 #pragma once
@@ -76,8 +77,9 @@ struct Int4Args {
     float *lse;
     float *o_part;            // [head block, worker, 2 slots, HB, Mq, D] fp32, O / l
     float *lse_part;          // [head block, worker, 2 slots, HB, Mq] fp32, log2 domain
-    int *step_prefix;         // [B + 1] first step of each request (several workers)
+    int *step_prefix;         // [B + 2] first place of each request, their end, and the places shared out (several workers)
     int B, Sq, Hq, Hkv, G, Mq, page_size, pages_per_req, num_pages;
+    int change;               // steps' worth of time that a change of request costs (at least 1)
     int workers, HB, RG;      // workers per head block; heads of a CTA, warps (of 8 or 16 query rows) a head
     int rings, rings_max;     // rings (workers) of a CTA, and how many its warps could serve
     int lanes;                // groups of HB x RG warps that take turns at a ring's steps
@@ -85,6 +87,8 @@ struct Int4Args {
     FastDiv by_page;          // page_size
     unsigned g_inv;           // ceil(2^16 / G): r / G = r * g_inv >> 16 for r < 128
     int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
+    int row_copies;           // K and V in 16-byte copies instead of TMA boxes (page sizes without a factor of 4)
+    const uint8_t *k_pool, *v_pool;  // for those
     unsigned param_pitch;     // of a box's parameters in a stage
     unsigned par8, par16;     // as tok8, tok16, of the parameters
     unsigned tok8, tok16;     // bytes from a token's row in a stage to that of the token 8, 16 later (8, 16 keep the swizzle)
@@ -197,6 +201,9 @@ __device__ __forceinline__ void tma_load_2d(uint32_t smem_dst, const void *tmap,
 __device__ __forceinline__ void cp_async8(uint32_t smem_dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async16_to(uint32_t smem_dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
 // Arrives on the barrier (one of its expected arrivals) once every cp.async of
 // this thread has landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
@@ -256,6 +263,13 @@ __device__ __forceinline__ int tok_of(int g) {
     return D == 128 ? g ^ ((g >> 1) & 1) : g ^ (g >> 2);
 }
 
+// Byte of 16-byte unit `unit` in the row at offset `off` of a stage (which lies
+// on the swizzle's 512-byte period).
+template <int D>
+__device__ __forceinline__ uint32_t swizzle(uint32_t off, int unit) {
+    return D == 128 ? (uint32_t(unit) ^ ((off >> 7) & 3u)) << 4 : uint32_t(unit) << 4;
+}
+
 // First step of worker w's share of T steps over W workers: floor(w T / W).
 __device__ __forceinline__ int int4_share(unsigned w, int T, int W) {
     const unsigned long long x = (unsigned long long)w * unsigned(T);
@@ -293,8 +307,10 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         }
         head->abort = 0;
         fence_mbarrier_init();
-        prefetch_tmap(&k_map);
-        prefetch_tmap(&v_map);
+        if (!a.row_copies) {
+            prefetch_tmap(&k_map);
+            prefetch_tmap(&v_map);
+        }
         if (a.param_tma) prefetch_tmap(&p_map);
     }
     pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
@@ -308,12 +324,14 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const int group = (warp + (groups == 2 ? member >> 1 : groups == 4 ? member : 0)) % groups;
     const int r = warp < CW ? group / a.lanes : warp - CW;
 
-    // ---- schedule.  Request b takes n_b = ceil(len_b / 32) steps and one more
-    // for what changing requests costs (queries, output); worker w takes places
+    // ---- schedule.  Request b takes n_b = ceil(len_b / 32) steps and `change`
+    // more for what changing requests costs (queries, output); worker w takes places
     // [w T / W, (w + 1) T / W) of the T places of all requests in order, b's
     // steps first from P_b on.  An empty request belongs to whoever holds P_b.
     bool bad = false;
     int w_begin, w_end, seg_b, seg_p;
+    // no change follows the last request (an empty one keeps a place to be held)
+    const int trailing = a.change - (__ldg(a.seq_lens + a.B - 1) <= 0 ? 1 : 0);
     if (a.B <= kInt4WarpRequests) {
         // each warp for itself: a run of requests a lane, a scan, and the first
         // lane with a request that holds the share's first step
@@ -323,7 +341,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         for (int b = b0; b < b1; ++b) {
             const int len = __ldg(a.seq_lens + b);
             bad |= len < 0 || len > cap;
-            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + 1;
+            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + a.change;
         }
         int incl = mine;
 #pragma unroll
@@ -331,19 +349,19 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             const int y = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += y;
         }
-        const int T = __shfl_sync(0xffffffffu, incl, 31);
+        const int total = __shfl_sync(0xffffffffu, incl, 31), T = total - trailing;
         const int w = r * int(gridDim.y) + int(blockIdx.y);
         w_begin = int4_share(min(w, a.workers), T, a.workers);
         w_end = int4_share(min(w + 1, a.workers), T, a.workers);
         const bool record = a.step_prefix != nullptr && threadIdx.x < 32 && blockIdx.x == 0 && blockIdx.y == 0;
         int P = incl - mine, hit = a.B, hit_p = 0;
         for (int b = b0; b < b1; ++b) {
-            const int n = run == 1 ? mine - 1 : (min(max(__ldg(a.seq_lens + b), 0), cap) + kInt4Step - 1) / kInt4Step;
+            const int n = run == 1 ? mine - a.change : (min(max(__ldg(a.seq_lens + b), 0), cap) + kInt4Step - 1) / kInt4Step;
             if (record) a.step_prefix[b] = P;
             if (hit == a.B && P + max(n, 1) > w_begin) hit = b, hit_p = P;
-            P += n + 1;
+            P += n + a.change;
         }
-        if (record && lane == 0) a.step_prefix[a.B] = T;
+        if (record && lane == 0) a.step_prefix[a.B] = total, a.step_prefix[a.B + 1] = T;
         const unsigned found = __ballot_sync(0xffffffffu, hit < a.B);
         const int src = found != 0 ? __ffs(found) - 1 : 0;
         seg_b = __shfl_sync(0xffffffffu, hit, src);
@@ -360,7 +378,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         for (int b = b0; b < b1; ++b) {
             const int len = __ldg(a.seq_lens + b);
             bad |= len < 0 || len > cap;
-            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + 1;
+            mine += (min(max(len, 0), cap) + kInt4Step - 1) / kInt4Step + a.change;
         }
         int incl = mine;
 #pragma unroll
@@ -375,6 +393,8 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             T += head->warp_sum[w];
             if (w < warp) P += head->warp_sum[w];
         }
+        const int total = T;
+        T -= trailing;
         if (warp == 0 && lane < a.rings) {
             const int w = lane * int(gridDim.y) + int(blockIdx.y);
             head->begin[lane] = int4_share(min(w, a.workers), T, a.workers);
@@ -382,14 +402,14 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         }
         __syncthreads();
         const bool record = a.step_prefix != nullptr && blockIdx.x == 0 && blockIdx.y == 0;
-        if (record && threadIdx.x == 0) a.step_prefix[a.B] = T;
+        if (record && threadIdx.x == 0) a.step_prefix[a.B] = total, a.step_prefix[a.B + 1] = T;
         for (int b = b0; b < b1; ++b) {
             const int n = (min(max(__ldg(a.seq_lens + b), 0), cap) + kInt4Step - 1) / kInt4Step;
             if (record) a.step_prefix[b] = P;
             for (int k = 0; k < a.rings; ++k)
                 if (P + max(n, 1) > head->begin[k])  // of those the first counts
                     atomicMin(&head->first[k], (unsigned long long)b << 32 | unsigned(P));
-            P += n + 1;
+            P += n + a.change;
         }
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, kErrIndex);
         bad = false;
@@ -414,9 +434,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         uint64_t *full = head->full[r], *empty = head->empty[r];
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
-        const uint32_t box_bytes = uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
+        const uint32_t box_bytes = a.row_copies ? 0 : uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
-        const bool first = lane % R == 0;  // of a box
+        const bool first = lane % R == 0 && !a.row_copies;  // of a box
+        // 16-byte copies: a token's piece of the block's heads is 2^lc of them
+        const int lc = 31 - __clz(a.HB) + (D == 128 ? 2 : 1);
         int st = 0, gs = 0;
         uint32_t phase = 0;
         bool failed = false;
@@ -461,6 +483,20 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         tma_load_3d(base + box_at + v_off, &v_map, full + st, 0, row, hb0);
                         if (a.param_tma) tma_load_2d(base + par_at, &p_map, full + st, hb0 * 4, row);
                     }
+                    if (a.row_copies) {
+                        const size_t row_bytes = size_t(a.Hkv) * ROWB;
+                        for (int i = 0; i < 1 << lc; ++i) {
+                            const int x = i * 32 + lane, tok = x >> lc, u = x & ((1 << lc) - 1);
+                            const int h = u / (ROWB / 16);
+                            const int from = __shfl_sync(0xffffffffu, row, tok);
+                            if ((valid >> tok & 1u) == 0 || h >= nh) continue;
+                            const uint32_t off = uint32_t(tok / 16) * a.box_pitch + uint32_t(h * 16 + tok % 16) * ROWB;
+                            const uint32_t dst = base + off + swizzle<D>(off, u % (ROWB / 16));
+                            const size_t src = from * row_bytes + size_t(hb0) * ROWB + size_t(u) * 16;
+                            cp_async16_to(dst, a.k_pool + src);
+                            cp_async16_to(dst + v_off, a.v_pool + src);
+                        }
+                    }
                     if (!a.param_tma) {
                         if (ok) {
                             const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
@@ -473,7 +509,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             }
             seg_t = seg_next;
             if (seg_next == seg_p + steps_b) {
-                seg_t = seg_p = seg_next + 1;
+                seg_t = seg_p = seg_next + a.change;
                 ++seg_b;
             }
         }
@@ -503,14 +539,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const int g = hb0 + lh;
     const int gi = lane >> 2, c = lane & 3;
     auto row_off = [&](int t) { return uint32_t(t / R) * a.box_pitch + uint32_t(lh * R + t % R) * ROWB; };
-    auto swz = [&](uint32_t off, int unit) { return D == 128 ? (uint32_t(unit) ^ ((off >> 7) & 3u)) << 4 : uint32_t(unit) << 4; };
     const uint32_t k_row = row_off(tok_of<D>(gi));
-    const uint32_t k_off = D == 128 ? k_row + swz(k_row, c) : k_row + 8 * c;
+    const uint32_t k_off = D == 128 ? k_row + swizzle<D>(k_row, c) : k_row + 8 * c;
     uint32_t vo[2];  // tokens of MMA columns 2 c, 2 c + 1
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const uint32_t r = row_off(tok_of<D>(2 * c + e));
-        vo[e] = v_off + (D == 128 ? r + swz(r, gi >> 1) + (gi & 1) * 8 : r + 4 * gi);
+        vo[e] = v_off + (D == 128 ? r + swizzle<D>(r, gi >> 1) + (gi & 1) * 8 : r + 4 * gi);
     }
     const int tok0 = tok_of<D>(gi);
     auto row_of = [&](int r) { return int(unsigned(r) * a.g_inv >> 16); };  // query row i of the group's row r = i G + h
@@ -903,7 +938,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             }
         seg_t = seg_next;
         if (seg_next == seg_p + steps_b) {
-            seg_t = seg_p = seg_next + 1;
+            seg_t = seg_p = seg_next + a.change;
             ++seg_b;
         }
     }
@@ -918,18 +953,18 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 // row a warp.  A warp reads 32 partials' LSEs at once, one a lane, which gives
 // their weights, then adds them up in order, several in flight: the same bits
 // every time.
-__host__ __device__ constexpr int int4_merge_batch(bool split) { return split ? 10 : 4; }  // partials in flight
+__host__ __device__ constexpr int int4_merge_batch(bool split) { return split ? 8 : 4; }  // partials in flight
 __host__ __device__ constexpr int int4_merge_warps(bool split) { return split ? 16 : 8; }
 
 template <int D, bool SPLIT>
-__global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT), SPLIT ? 1 : 5) gqa_paged_int4_merge_kernel(const Int4Args a) {
+__global__ void __launch_bounds__(32 * int4_merge_warps(SPLIT), SPLIT ? 2 : 5) gqa_paged_int4_merge_kernel(const Int4Args a) {
     constexpr int V = D / 32, NW = int4_merge_warps(SPLIT), BATCH = int4_merge_batch(SPLIT);
     __shared__ float sm_m[NW], sm_l[NW], sm_o[SPLIT ? NW : 1][D];
     pdl_wait_primary();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.y, rr = SPLIT ? int(blockIdx.x) : int(blockIdx.x) * NW + warp;
     const int W = a.workers;
-    const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P - 1, T = a.step_prefix[a.B];
+    const int P = a.step_prefix[b], n = a.step_prefix[b + 1] - P - a.change, T = a.step_prefix[a.B + 1];
     if (n == 0) return;  // an empty request: written by the main kernel
     // worker of step s: the largest w with floor(w T / W) <= s
     auto holder = [&](int s) {

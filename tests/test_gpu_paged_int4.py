@@ -296,3 +296,85 @@ def test_other_streams_and_graphs(gq):
     graphs[0].replay()
     torch.cuda.synchronize()
     check({**ds[0], "lens": cs[0]["lens"].cpu()}, outs[0][0].cpu(), outs[0][1].cpu(), what="replayed with other lengths")
+
+
+@pytest.mark.parametrize("shape", [(2, 1, 8, 2, 128, 4, (300, 77)), (2, 2, 8, 8, 64, 12, (300, 5)), (1, 1, 8, 2, 128, 48, (1000,)),
+                                   (3, 1, 40, 10, 128, 2, (90, 33, 64)), (2, 3, 12, 3, 64, 4, (200, 1)), (2, 1, 2, 1, 128, 32, (1500, 900)),
+                                   (2, 1, 4, 2, 64, 6, (700, 31)), (1, 5, 10, 5, 64, 20, (444,))],
+                         ids=lambda s: "b%d_sq%d_h%dx%d_d%d_ps%d" % s[:6])
+@pytest.mark.parametrize("splits", [0, 1, 2, 700])
+def test_page_sizes_and_head_counts(gq, shape, splits):
+    d = make(*shape[:6], list(shape[6]), seed=100 + sum(shape[:6]))
+    out, lse = run(gq, d, num_splits=splits)
+    assert gq.gqa_device_status() == 0
+    check(d, out, lse, what=f"{shape} splits {splits}")
+
+
+@pytest.mark.parametrize("B", [255, 256, 257, 900])
+def test_many_requests(gq, B):
+    """Around and past the number of requests up to which each warp works out the schedule for itself; a third empty."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 70, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.33] = 0
+    lens[-1] = 0
+    d = make(B, 1, 8, 2, 64, 16, lens.tolist(), seed=B, ppr=5)
+    for splits in (0, 1, 7):
+        out, lse = run(gq, d, num_splits=splits)
+        assert gq.gqa_device_status() == 0
+        check(d, out, lse, what=f"splits {splits}")
+
+
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [0] * 300, [1] + [0] * 40, [0] * 40 + [1], [33] * 40, [0, 32] * 20])
+def test_empty_requests(gq, lens):
+    d = make(len(lens), 2, 8, 2, 64, 16, lens, seed=3, ppr=3)
+    for splits in (0, 1, 5):
+        out, lse = run(gq, d, num_splits=splits)
+        assert gq.gqa_device_status() == 0
+        check(d, out, lse, what=f"splits {splits}")
+
+
+def test_largest_batch(gq):
+    """65535 requests of 0 to 2 tokens, every result against 64 bits at once."""
+    B, Hq, Hkv, D = 65535, 2, 1, 64
+    g = torch.Generator(device="cuda").manual_seed(30)
+    q = torch.randn(B, 1, Hq, D, generator=g, device="cuda").to(torch.bfloat16)
+    k_pool, v_pool = (torch.randint(0, 256, (B, 2, Hkv, D // 2), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2))
+    params = (torch.rand(B, 2, Hkv, 4, generator=g, device="cuda") * torch.tensor([0.3, -4.0, 0.3, -4.0], device="cuda")).half()
+    table = torch.randperm(B, generator=g, device="cuda").view(B, 1).to(torch.int32)
+    lens = torch.randint(0, 3, (B,), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = gq.gqa_decode_paged_int4(q, k_pool, v_pool, params, table, lens)
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 0
+    at = table[:, 0].long()
+    k = ref.value_int4(k_pool[at], params[at][..., :2])[:, :, 0]
+    v = ref.value_int4(v_pool[at], params[at][..., 2:])[:, :, 0]
+    x = torch.einsum("bhd,btd->bht", q[:, 0].double(), k) / 8
+    x = x.masked_fill(torch.arange(2, device="cuda") >= lens[:, None, None], -math.inf)
+    some = lens > 0
+    want = torch.einsum("bht,btd->bhd", torch.softmax(x[some], -1), v[some])
+    assert torch.all(out[~some] == 0) and torch.all(torch.isneginf(lse[~some]))
+    # scores of at most sum |q| (15 * 0.3 + 4) / 8 and V of at most 8.5, by the bounds of cache_ref.int4_bounds
+    ds = (D + 8) * 2.0 ** -23 * 8.5 * q.double().abs().sum(-1).max() / 8
+    assert torch.all((out[some][:, 0].double() - want).abs() <= 2 * ds * 8.5 + 2.0 ** -11 * 4.5 + 2.0 ** -8 * want.abs())
+    assert torch.all((lse[some][..., 0].double() - torch.logsumexp(x[some], -1)).abs() <= ds + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("shape", [(3, 1, 32, 8, 128, 16), (2, 1, 8, 1, 64, 16), (2, 4, 16, 2, 128, 16), (2, 1, 6, 3, 64, 5)],
+                         ids=["rings", "lanes", "16rows", "copies"])
+def test_wait_that_runs_out(gq, shape):
+    """A first stage that is never loaded: the wait for it ends at its limit, the call reports it, and the next call on
+    the same stream is as it should be."""
+    B = shape[0]
+    d = make(*shape, [900] * B, seed=40)
+    want = run(gq, d, num_splits=3)
+    gq.gqa_set_wait_limit_ns(2_000_000)
+    gq.gqa_debug_set_fault_mode(1)
+    try:
+        run(gq, d, num_splits=3)
+        assert gq.gqa_device_status() == 6
+    finally:
+        gq.gqa_debug_set_fault_mode(0)
+        gq.gqa_set_wait_limit_ns(0)
+    again = run(gq, d, num_splits=3)
+    assert gq.gqa_device_status() == 0
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
