@@ -810,14 +810,18 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             st += a.lanes;
             if (st >= a.stages) st -= a.stages, phase ^= 1;
 
-            // ---- O^T += V^T . weights
+            // ---- O^T += V^T . weights, 32 tokens at a time.  The tensor cores
+            // cut off what does not fit their sums; codes are positive, so over
+            // a long walk the cuts would add up against the zeros' part, which
+            // cancels most of it.  The sum over the steps is rounded instead.
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int w = 0; w < VW; ++w)
 #pragma unroll
-                for (int w = 0; w < VW; ++w)
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t sel = h ? 0x7632u : 0x5410u;
+                    float sum[NT][2][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t sel = h ? 0x7632u : 0x5410u;
+                    for (int t = 0; t < 2; ++t) {
                         const uint32_t x = prmt4(vw[4 * t][w], vw[4 * t + 1][w], sel);
                         const uint32_t y = prmt4(vw[4 * t + 2][w], vw[4 * t + 3][w], sel);
                         // element 2 j: its codes; element 2 j + 1: whole bytes
@@ -825,11 +829,27 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         const uint32_t x8 = prmt4(x, 0, 0x4341u), y8 = prmt4(y, 0, 0x4341u);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const int j = 4 * w + 2 * h;
-                            mma_f16_add(o[nt][j], x & M0, x & M, y & M0, y & M, wt[nt][2 * t], wt[nt][2 * t + 1]);
-                            mma_f16_add(o[nt][j + 1], x8 & M0, x8, y8 & M0, y8, wt[nt][2 * t], wt[nt][2 * t + 1]);
+                            const uint32_t b0 = wt[nt][2 * t], b1 = wt[nt][2 * t + 1];
+                            if (t == 0) {
+                                mma_f16_zero(sum[nt][0], x & M0, x & M, y & M0, y & M, b0, b1);
+                                mma_f16_zero(sum[nt][1], x8 & M0, x8, y8 & M0, y8, b0, b1);
+                            } else {
+                                mma_f16_add(sum[nt][0], x & M0, x & M, y & M0, y & M, b0, b1);
+                                mma_f16_add(sum[nt][1], x8 & M0, x8, y8 & M0, y8, b0, b1);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                float(&acc_o)[4] = o[nt][4 * w + 2 * h + k];
+                                const float2 r2 = add2(make_float2(acc_o[e], acc_o[e + 1]), make_float2(sum[nt][k][e], sum[nt][k][e + 1]));
+                                acc_o[e] = r2.x, acc_o[e + 1] = r2.y;
+                            }
+                }
         }
         if (failed) break;
         load_queries(b + 1);
