@@ -64,21 +64,23 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     return GQA_OK;
 }
 
+template <int D, int NT>
+const void *kernel_for(bool copies) {
+    return copies ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<D, NT, true>)
+                  : reinterpret_cast<const void *>(gqa_paged_int4_kernel<D, NT, false>);
+}
 const void *kernel_of(const Int4Plan &p) {
-    if (p.D == 64)
-        return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 1>)
-                         : reinterpret_cast<const void *>(gqa_paged_int4_kernel<64, 2>);
-    return p.NT == 1 ? reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 1>)
-                     : reinterpret_cast<const void *>(gqa_paged_int4_kernel<128, 2>);
+    if (p.D == 64) return p.NT == 1 ? kernel_for<64, 1>(p.row_copies) : kernel_for<64, 2>(p.row_copies);
+    return p.NT == 1 ? kernel_for<128, 1>(p.row_copies) : kernel_for<128, 2>(p.row_copies);
 }
 
 // Shared memory a CTA may have on `dev`, the current device; the first call
 // there raises the kernel's limit to it.  0 on an error.
 int int4_smem(int dev, const Int4Plan &p) {
     static std::mutex mu;
-    static int most[kMaxDevices][2][2];
+    static int most[kMaxDevices][2][2][2];
     std::lock_guard<std::mutex> lk(mu);
-    int &m = most[dev][p.D == 128][p.NT - 1];
+    int &m = most[dev][p.D == 128][p.NT - 1][p.row_copies];
     if (m == 0) {
         int n = 0;
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
@@ -223,6 +225,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     const int ctas = int4_ctas(p, dev);
     a.rings = workers >= ctas * p.rings ? p.rings : (workers + ctas - 1) / ctas;
     a.rings_max = p.rings;
+    a.producers = p.row_copies ? kInt4MaxRings / a.rings : 1;
+    if (a.producers > 2) a.producers = 2;  // a warp copies 16 tokens at a time at most
     a.lanes = p.lanes;
     const int boxes = (p.lanes - 1) * p.HB * p.RG * p.NT * (D / 4 + 6) * 128;  // what the lanes of a ring hand over
     a.stages = ((smem - kInt4HeadBytes) / a.rings - boxes) / p.stage_bytes;
@@ -235,7 +239,6 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.tok8 = p.R == 16 ? 8 * (D / 2) : (8 / p.R) * p.pitch;
     a.tok16 = p.R == 16 ? p.pitch : (16 / p.R) * p.pitch;
     a.param_tma = p.param_tma;
-    a.row_copies = p.row_copies;
     a.k_pool = static_cast<const uint8_t *>(k_pool);
     a.v_pool = static_cast<const uint8_t *>(v_pool);
     a.param_pitch = p.par_pitch;

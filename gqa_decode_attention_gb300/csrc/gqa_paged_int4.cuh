@@ -51,13 +51,16 @@ constexpr int kInt4MaxRings = 4;    // of a CTA, one producer warp each
 // Consumer warps of a CTA that hold NT tiles of 8 query rows, and the
 // registers a thread of theirs and of the producers' warpgroup has: together
 // what the CTA was launched with (20 warps of 96, or 12 of 168).  (12 warps of
-// 160 registers for 16 rows each were slower than 8 of 216.)
+// 160 registers for 16 rows each were slower than 8 of 216.)  Producers that
+// copy rows themselves need more than those that start TMA: a spilled value
+// comes back behind all the copies under way.
 __host__ __device__ constexpr int int4_consumers(int nt) { return nt == 1 ? 16 : 8; }
 __host__ __device__ constexpr int int4_threads(int nt) { return 32 * (int4_consumers(nt) + 4); }
-__host__ __device__ constexpr int int4_consumer_regs(int nt) { return nt == 1 ? 112 : 216; }
-__host__ __device__ constexpr int int4_producer_regs(int nt) { return nt == 1 ? 32 : 72; }
-static_assert(16 * int4_consumer_regs(1) + 4 * int4_producer_regs(1) == 20 * 96, "registers");
-static_assert(8 * int4_consumer_regs(2) + 4 * int4_producer_regs(2) == 12 * 168, "registers");
+__host__ __device__ constexpr int int4_consumer_regs(int nt, bool copy) { return nt == 1 ? (copy ? 104 : 112) : 216; }
+__host__ __device__ constexpr int int4_producer_regs(int nt, bool copy) { return nt == 1 ? (copy ? 64 : 32) : 72; }
+static_assert(16 * int4_consumer_regs(1, false) + 4 * int4_producer_regs(1, false) == 20 * 96, "registers");
+static_assert(16 * int4_consumer_regs(1, true) + 4 * int4_producer_regs(1, true) == 20 * 96, "registers");
+static_assert(8 * int4_consumer_regs(2, true) + 4 * int4_producer_regs(2, true) == 12 * 168, "registers");
 constexpr int kInt4WarpRequests = 256;  // up to so many requests each warp works out the schedule for itself
 constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
 
@@ -87,8 +90,8 @@ struct Int4Args {
     FastDiv by_page;          // page_size
     unsigned g_inv;           // ceil(2^16 / G): r / G = r * g_inv >> 16 for r < 128
     int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
-    int row_copies;           // K and V in 16-byte copies instead of TMA boxes (page sizes without a factor of 4)
-    const uint8_t *k_pool, *v_pool;  // for those
+    int producers;            // warps that fill a ring
+    const uint8_t *k_pool, *v_pool;  // for 16-byte copies
     unsigned param_pitch;     // of a box's parameters in a stage
     unsigned par8, par16;     // as tok8, tok16, of the parameters
     unsigned tok8, tok16;     // bytes from a token's row in a stage to that of the token 8, 16 later (8, 16 keep the swizzle)
@@ -270,13 +273,15 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t off, int unit) {
     return D == 128 ? (uint32_t(unit) ^ ((off >> 7) & 3u)) << 4 : uint32_t(unit) << 4;
 }
 
-// First step of worker w's share of T steps over W workers: floor(w T / W).
+// First place of worker w's share of T places over W workers: floor(w T / W).
 __device__ __forceinline__ int int4_share(unsigned w, int T, int W) {
     const unsigned long long x = (unsigned long long)w * unsigned(T);
     return x < (1ull << 32) ? int(unsigned(x) / unsigned(W)) : int(x / unsigned(W));
 }
 
-template <int D, int NT>
+// COPY: K and V in 16-byte copies instead of TMA boxes (page sizes without a
+// factor of 4).
+template <int D, int NT, bool COPY>
 __global__ void __launch_bounds__(int4_threads(NT), 1)
     gqa_paged_int4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                           const __grid_constant__ CUtensorMap p_map, const Int4Args a) {
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     if (threadIdx.x == 0) {
         for (int r = 0; r < a.rings; ++r) {
             for (int st = 0; st < a.stages; ++st) {
-                mbar_init(&head->full[r][st], a.param_tma ? 1 : 33);  // the producer's expect (and its lanes' copies)
+                mbar_init(&head->full[r][st], a.param_tma ? 1 : 1 + 32 * a.producers);  // the expect, and lanes' copies
                 mbar_init(&head->empty[r][st], nh * a.RG);
             }
             mbar_init(&head->ready[r], max(1, (a.lanes - 1) * nh * a.RG));
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         }
         head->abort = 0;
         fence_mbarrier_init();
-        if (!a.row_copies) {
+        if constexpr (!COPY) {
             prefetch_tmap(&k_map);
             prefetch_tmap(&v_map);
         }
@@ -316,13 +321,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     pdl_wait_primary();  // inputs may be written by the previous kernel in the stream
 
     // The CW consumer warps form groups of HB x RG, `lanes` groups to a ring;
-    // producer warp r serves ring r.  Warps of an SM sub-partition (warp mod 4)
+    // producer warp p serves ring p mod rings.  Warps of an SM sub-partition (warp mod 4)
     // run oldest first, and a ring is as fast as its slowest warp, so the
     // groups' warps are dealt so that each group has warps of every age.
     const int members = a.HB * a.RG, groups = a.rings_max * a.lanes;
     const int member = warp / groups;
     const int group = (warp + (groups == 2 ? member >> 1 : groups == 4 ? member : 0)) % groups;
-    const int r = warp < CW ? group / a.lanes : warp - CW;
+    const int r = warp < CW ? group / a.lanes : (warp - CW) % a.rings;
 
     // ---- schedule.  Request b takes n_b = ceil(len_b / 32) steps and `change`
     // more for what changing requests costs (queries, output); worker w takes places
@@ -429,16 +434,25 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 
     // ============================================================== producers
     if (warp >= CW) {
-        fewer_registers<int4_producer_regs(NT)>();
-        if (r >= a.rings) return;
+        fewer_registers<int4_producer_regs(NT, COPY)>();
+        // 16-byte copies take a warp long, so all four share the rings' tokens
+        const int part = (warp - CW) / a.rings, parts = COPY ? a.producers : 1;
+        if (part >= parts) return;
         uint64_t *full = head->full[r], *empty = head->empty[r];
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
-        const uint32_t box_bytes = a.row_copies ? 0 : uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
+        const uint32_t box_bytes = COPY ? 0 : uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
-        const bool first = lane % R == 0 && !a.row_copies;  // of a box
-        // 16-byte copies: a token's piece of the block's heads is 2^lc of them
+        const bool first = lane % R == 0 && !COPY;  // of a box
+        // 16-byte copies: a token's piece of the block's heads is 2^lc of them;
+        // this lane always takes copy u of a token
         const int lc = 31 - __clz(a.HB) + (D == 128 ? 2 : 1);
+        const int u = lane & ((1 << lc) - 1);
+        const bool copies = u < nh * (ROWB / 16);
+        const uint32_t row_bytes = uint32_t(a.Hkv) * ROWB, copy_at = uint32_t(u / (ROWB / 16)) * 16 * ROWB;
+        const int per_part = kInt4Step / parts;
+        const uint8_t *k_src = a.k_pool + size_t(hb0) * ROWB + u * 16;
+        const uint8_t *v_src = a.v_pool + size_t(hb0) * ROWB + u * 16;
         int st = 0, gs = 0;
         uint32_t phase = 0;
         bool failed = false;
@@ -472,33 +486,31 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                     }
                 }
                 if (!(a.fault_mode == 1 && gs == 0)) {
-                    if (lane == 0) {
+                    if (lane == 0 && part == 0) {
                         vmask[st] = valid;
                         mbar_arrive_expect_tx(full + st, boxes * box_bytes);
                     }
                     __syncwarp();
                     const uint32_t base = ring + uint32_t(st) * a.stage_bytes;
-                    if (box) {
+                    if (!COPY && box) {
                         tma_load_3d(base + box_at, &k_map, full + st, 0, row, hb0);
                         tma_load_3d(base + box_at + v_off, &v_map, full + st, 0, row, hb0);
                         if (a.param_tma) tma_load_2d(base + par_at, &p_map, full + st, hb0 * 4, row);
                     }
-                    if (a.row_copies) {
-                        const size_t row_bytes = size_t(a.Hkv) * ROWB;
-                        for (int i = 0; i < 1 << lc; ++i) {
-                            const int x = i * 32 + lane, tok = x >> lc, u = x & ((1 << lc) - 1);
-                            const int h = u / (ROWB / 16);
-                            const int from = __shfl_sync(0xffffffffu, row, tok);
-                            if ((valid >> tok & 1u) == 0 || h >= nh) continue;
-                            const uint32_t off = uint32_t(tok / 16) * a.box_pitch + uint32_t(h * 16 + tok % 16) * ROWB;
+                    if constexpr (COPY) {
+#pragma unroll 4
+                        for (int tok = part * per_part + (lane >> lc); tok < (part + 1) * per_part; tok += 32 >> lc) {
+                            const uint32_t from = __shfl_sync(0xffffffffu, row, tok);
+                            if ((valid >> tok & 1u) == 0 || !copies) continue;
+                            const uint32_t off = (tok & 16 ? a.box_pitch : 0) + copy_at + uint32_t(tok & 15) * ROWB;
                             const uint32_t dst = base + off + swizzle<D>(off, u % (ROWB / 16));
-                            const size_t src = from * row_bytes + size_t(hb0) * ROWB + size_t(u) * 16;
-                            cp_async16_to(dst, a.k_pool + src);
-                            cp_async16_to(dst + v_off, a.v_pool + src);
+                            const unsigned long long src = (unsigned long long)from * row_bytes;
+                            cp_async16_to(dst, k_src + src);
+                            cp_async16_to(dst + v_off, v_src + src);
                         }
                     }
-                    if (!a.param_tma) {
-                        if (ok) {
+                    if (COPY || !a.param_tma) {
+                        if (ok && part == parts - 1) {
                             const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
                             for (int h = 0; h < nh; ++h) cp_async8(base + par_at + h * 8, src + h * 4);
                         }
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     }
 
     // ============================================================== consumers
-    more_registers<int4_consumer_regs(NT)>();
+    more_registers<int4_consumer_regs(NT, COPY)>();
     const int turn = group - r * a.lanes;
     const int lh = member / a.RG, rg = member - lh * a.RG;
     if (member >= members || r >= a.rings || lh >= nh) return;
