@@ -533,17 +533,24 @@ def _cache(fn: str, dev: int, k_pool, v_pool, kv_params, page_table, seq_lens, k
     if len(shape) != 4 or page_table.dim() != 2:
         raise ValueError(f"{fn}: pools [num_pages,page_size,Hkv,D or D/2], page_table 2-D")
     num_pages, page_size, Hkv, D = shape
+    B, pages_per_req = page_table.shape
     kind = k_pool.dtype
     if kv_params is None:
         kvd = _kv_dtype(k_pool)
     else:
-        kvd, kind, D = GQA_KV_INT4, torch.uint8, 2 * D
+        kvd, D = GQA_KV_INT4, 2 * D
+        if kind is not torch.uint8:
+            raise _misfit(fn, "k_pool", k_pool, torch.uint8, dev)
         _fit(fn, "kv_params", kv_params, torch.float16, dev, (num_pages, page_size, Hkv, 4))
-    _fit(fn, "k_pool", k_pool, kind, dev)
-    _fit(fn, "v_pool", v_pool, kind, dev, shape)
-    _fit(fn, "page_table", page_table, torch.int32, dev)
-    B, pages_per_req = page_table.shape
-    _fit(fn, "seq_lens", seq_lens, torch.int32, dev, (B,))
+    if not (v_pool.dtype is kind and page_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
+            and v_pool.shape == shape and seq_lens.shape == (B,)
+            and k_pool.get_device() == dev and v_pool.get_device() == dev and page_table.get_device() == dev
+            and seq_lens.get_device() == dev and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and page_table.is_contiguous() and seq_lens.is_contiguous()):
+        _fit(fn, "k_pool", k_pool, kind, dev)
+        _fit(fn, "v_pool", v_pool, kind, dev, shape)
+        _fit(fn, "page_table", page_table, torch.int32, dev)
+        _fit(fn, "seq_lens", seq_lens, torch.int32, dev, (B,))
     n_scales = 0
     if k_scales is not None or v_scales is not None:
         if k_scales is None or v_scales is None:
