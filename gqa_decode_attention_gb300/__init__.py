@@ -563,11 +563,15 @@ def _cache(fn: str, dev: int, k_pool, v_pool, kv_params, page_table, seq_lens, k
     return kvd, num_pages, page_size, Hkv, D, B, pages_per_req, n_scales
 
 
-def _new(shape, dtype, like, stream):
-    """An output the call allocates: safe to free while a given stream still writes it."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape, dtype, like, stream, make=torch.empty):
+    """An output the call allocates.  With a stream given it comes from that stream's memory -- the current stream's may
+    still be in use by work queued there, which the kernel would not wait for -- and it may be freed while the current
+    stream still reads it."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
     return t
 
 
@@ -703,10 +707,7 @@ def gqa_paged_gather(k_pool, v_pool, page_table, seq_lens, k_out=None, v_out=Non
     if k_out is None:
         if rows is None:
             raise ValueError(f"{fn}: k_out and v_out, or rows, are needed")
-        on = torch.cuda.current_stream(dev) if stream is None else stream
-        with torch.cuda.stream(on):  # zeroed on the stream that writes them
-            k_out, v_out = (torch.zeros((B, rows, Hkv, D), dtype=torch.bfloat16, device=k_pool.device)
-                            for _ in range(2))
+        k_out, v_out = (_new((B, rows, Hkv, D), torch.bfloat16, k_pool, stream, torch.zeros) for _ in range(2))
     else:
         if k_out.dim() != 4 or (rows is not None and rows != k_out.shape[1]):
             raise ValueError(f"{fn}: k_out must be [B,rows,Hkv,D]")

@@ -21,13 +21,24 @@
 //    two tokens of one element: a byte permute merges two tokens' halves, then
 //    the same masks apply.
 //  - The running maximum is a lazy reference: the row's maximum is only
-//    reduced over the warp (and O rescaled) when some weight would pass 2^9,
+//    reduced over the warp (and O rescaled) when some weight would pass 2^15,
 //    which after the first steps of a walk is rare; a step otherwise costs one vote.
 //
-// Layout.  As in the other paged kernels a CTA takes a block of KV heads and
-// one worker's share of all requests' steps (here of 32 tokens), one warp per
-// head (and per 16 query rows), over a ring of shared-memory stages that the
-// warps fill in turns.  K and V come by TMA as boxes of (row bytes) x (up to 16
+// What is rounded.  q (bf16) is exact in fp16 after a power of two that is
+// taken from the row's largest element, down to 2^-27 of that.  The codes are
+// exact.  p vs is rounded to fp16, half a step of which is 2^-11, an eighth of
+// the bf16 output's; everything that is summed is summed in fp32.
+//
+// Layout.  As in the other paged kernels a CTA takes a block of KV heads and a
+// worker's share of all requests' steps (here of 32 tokens).  One CTA fills an
+// SM: 16 consumer warps for 8 query rows each, or 8 for 16 rows, one per head
+// (and per group of rows), and four producer warps with few registers, one for
+// each of up to four rings of shared-memory stages; a ring is a worker.  (Of
+// the ways tried on 32 requests of 16K to 32K tokens, 64 heads over 8 of 128:
+// several CTAs an SM whose consumers start the loads in turns 177 us, a
+// producer warp in each 155, this 145.)  Where heads and row groups are fewer than the warps, `lanes`
+// groups take turns at a ring's steps and join their results in shared memory.
+// K and V come by TMA as boxes of (row bytes) x (up to 16
 // tokens of one page) x (heads of the block): shared memory then holds each
 // head's rows back to back, and with the 64-byte swizzle (D = 128) and the
 // token order of `tok_of` every fragment read is free of bank conflicts.
@@ -36,6 +47,14 @@
 // the same places, since a box ends at its page's end.  The warps never wait for
 // one another beyond the ring: each works out its segments from the lengths,
 // and the loads run ahead across request borders.
+//
+// Measured on GB300 (main and merge kernel): the 32 requests above, 814 MB,
+// 145 us, 5.6 TB/s, 83 % of the copy peak -- bound by HBM and by SMs whose path
+// to memory is slower, which the shares do not know of; one request of 128K tokens 43 us,
+// of which the start is 6 and the merge 5; 256 requests of up to 1K tokens
+// 47 us, bound by the consumers' instructions and the changes of request; 16
+// requests of 4 x 4 rows a head and up to 8K tokens 35 us, where 16 rows a warp
+// make a step 1.2 us long.
 #pragma once
 
 #include <stddef.h>
@@ -63,6 +82,11 @@ static_assert(16 * int4_consumer_regs(1, true) + 4 * int4_producer_regs(1, true)
 static_assert(8 * int4_consumer_regs(2, true) + 4 * int4_producer_regs(2, true) == 12 * 168, "registers");
 constexpr int kInt4WarpRequests = 256;  // up to so many requests each warp works out the schedule for itself
 constexpr float kInt4NoRef = -3e38f;  // reference of a row that has seen nothing
+// log2 of a row's largest weight when its reference is set.  Weights are fp16:
+// at 2^7 what is rounded to nothing lies 2^-32 below the largest (at 1 it lay
+// 2^-25 below, which over millions of tokens can be seen), and up to 2^15,
+// where the reference moves, a step's largest may be 2^8 times the first one's.
+constexpr float kInt4Top = 7.f;
 
 // x / d for x < 2^31, d of the host's choosing: m = floor(2^(31 + l) / d) + 1, l = ceil(log2 d).  (m d lies above
 // 2^(31 + l) by at most d <= 2^l, so x m / 2^(31 + l) is above x / d by less than 1 / d: the floor is right.)
@@ -158,10 +182,16 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
     asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// Whether a half of x, which is not negative, is above 2^9 (a NaN is not).
-__device__ __forceinline__ bool above_512(uint32_t x) {
+// Whether a half of x, which is not negative, is above 2^15 (a NaN is not).
+__device__ __forceinline__ bool above_2_15(uint32_t x) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-    return fmaxf(f.x, f.y) > 512.f;
+    return fmaxf(f.x, f.y) > 32768.f;
+}
+// Larger of x and y; a NaN stays one.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
 }
 
 // d = A(16x16 f16) * B(16x8 f16), starting from zero
@@ -598,7 +628,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 
         // ---- queries.  Lane gi holds row gi (+ 8 a tile) at the elements of
         // its quarter c, times a power of two that brings the row's largest
-        // element near 2^14 (bf16 values stay exact in fp16 down to 2^-28 of
+        // element near 2^14 (bf16 values stay exact in fp16 down to 2^-27 of
         // it).  The second code of a half is 16 u, so its q is q / 16.
         uint32_t qf[NT][2 * KW][2];
         float A[NT][2], qs[NT][2], R_[NT][2], l[NT][2], z[NT][2];
@@ -709,7 +739,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             for (int j = 0; j < 4; ++j) {
                 const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].x));
                 const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].y));
-                vs[j] = fmaxf(v2.x, 5.9604644775390625e-8f);  // fp16's smallest: a weight of 0 would hide its score
+                vs[j] = max_nan(v2.x, 5.9604644775390625e-8f);  // fp16's smallest: a weight of 0 would hide its score
                 vz[j] = v2.y;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -724,14 +754,17 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool there = (mask >> (tok0 + 8 * j)) & 1u;
-                    if (!there) vs[j] = vz[j] = 0.f;  // the slot may hold anything
+                    // a weight of 0 does not hide a NaN or infinity of V from the
+                    // rows that do not see its token: those that do get it by the score
+                    const bool odd = there && !(fmaxf(vs[j], fabsf(vz[j])) <= 65504.f && vs[j] == vs[j] && vz[j] == vz[j]);
+                    if (!there || odd) vs[j] = vz[j] = 0.f;  // a slot that is not there may hold anything
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int r = (rg * NT + nt) * 8 + 2 * c + e;
                             const bool seen = there && s0 + tok0 + 8 * j <= len - a.Sq + (r < a.Mq ? row_of(r) : a.Sq);
-                            if (!seen) acc[nt][j >> 1][2 * (j & 1) + e] = -INFINITY;
+                            if (!seen || odd) acc[nt][j >> 1][2 * (j & 1) + e] = seen ? NAN : -INFINITY;
                         }
                 }
             }
@@ -759,9 +792,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 }
             };
             weigh();
-            if (__any_sync(0xffffffffu, above_512(top))) {
-                // Move the references up to the step's largest score + log2(V
-                // scale): the largest weight of the row is then 1.
+            if (__any_sync(0xffffffffu, above_2_15(top))) {
+                // Move references up to the step's largest score + log2(V scale)
+                // - kInt4Top: the row's largest weight is then 2^kInt4Top.  Only of
+                // rows past the limit themselves (by more than the roundings of
+                // the test above), so that no row's bits depend on another row.
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float corr[2];
@@ -771,12 +806,12 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float y = acc[nt][j >> 1][2 * (j & 1) + e];
-                            if (vs[j] > 0.f) m = fmaxf(m, fmaf(y, A[nt][e], log2f(vs[j])));
+                            if (vs[j] > 0.f && vs[j] <= 65504.f) m = fmaxf(m, fmaf(y, A[nt][e], log2f(vs[j]) - kInt4Top));
                         }
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        m = fmaxf(m, R_[nt][e]);
+                        m = m > R_[nt][e] + (15.f - kInt4Top + 0.00390625f) ? m : R_[nt][e];
                         corr[e] = fast_exp2(R_[nt][e] - m);
                         R_[nt][e] = m;
                         l[nt][e] *= corr[e];
@@ -980,11 +1015,12 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     }
 }
 
-// Merge of the partials of requests that several workers share.  CTA (y, b): with SPLIT, one row, whose partials are dealt in runs to all warps and their
-// results merged in warp order -- few rows, many partials each; without, one
-// row a warp.  A warp reads 32 partials' LSEs at once, one a lane, which gives
-// their weights, then adds them up in order, several in flight: the same bits
-// every time.
+// Merge of the partials of requests that several workers share.  CTA (x, b):
+// with SPLIT, row x of request b, whose partials are dealt in runs to all warps
+// and their results merged in warp order -- few rows, many partials each;
+// without, one row a warp.  A warp reads 32 partials' LSEs at once, one a lane,
+// which gives their weights, then adds them up in order, several in flight: the
+// same bits every time.  A few us, most of them the launch.
 __host__ __device__ constexpr int int4_merge_batch(bool split) { return split ? 8 : 4; }  // partials in flight
 __host__ __device__ constexpr int int4_merge_warps(bool split) { return split ? 16 : 8; }
 

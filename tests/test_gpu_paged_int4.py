@@ -222,6 +222,30 @@ def test_nan_rows_stay_their_own(gq):
     assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse.permute(0, 2, 1)[~hit], clean[1].permute(0, 2, 1)[~hit])
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("which", [0, 1, 2, 3])
+def test_parameters_that_are_not_finite(gq, value, which):
+    """A token's K scale or zero, or V scale or zero, NaN or infinite (a scale below zero has no meaning): the rows that
+    see it have no finite result, the rows and heads that do not keep every bit."""
+    if which % 2 == 0 and value < 0:
+        value = float("nan")
+    d = make(2, 3, 16, 2, 128, 16, [300, 500], seed=21)
+    clean = run(gq, d, num_splits=3)
+    bad = {**d, "params": d["params"].clone()}
+    at = lambda b, t: int(ref.slots(d["table"][b], 16, [t])[0])  # noqa: E731
+    flat = bad["params"].view(-1, 2, 4)
+    flat[at(0, 299), 1, which] = value  # seen by the last row of request 0 only
+    flat[at(1, 498), 0, which] = value  # by the last two of request 1
+    flat[at(1, 100), 1, which] = value  # by all
+    out, lse = run(gq, bad, num_splits=3)
+    hit = torch.zeros(2, 3, 16, dtype=torch.bool)
+    hit[0, 2, 8:] = hit[1, 1:, :8] = hit[1, :, 8:] = True
+    assert torch.equal(out[~hit], clean[0][~hit])
+    assert torch.equal(lse.permute(0, 2, 1)[~hit], clean[1].permute(0, 2, 1)[~hit])
+    if which >= 2 or value != value:  # a K parameter of infinity may give scores of -inf alone, which weigh nothing
+        assert not torch.any(torch.isfinite(out[hit]).all(-1))
+
+
 def test_codes_beyond_four_gib(gq):
     """Pools of more than 4 GiB each, the request's pages at their far end."""
     num_pages, ps, Hkv, D = 540_000, 16, 8, 128
@@ -296,6 +320,29 @@ def test_other_streams_and_graphs(gq):
     graphs[0].replay()
     torch.cuda.synchronize()
     check({**ds[0], "lens": cs[0]["lens"].cpu()}, outs[0][0].cpu(), outs[0][1].cpu(), what="replayed with other lengths")
+
+
+def test_allocated_outputs_of_a_given_stream(gq):
+    """Outputs that a call on another stream allocates do not take memory that work queued on the current stream still
+    reads."""
+    d = make(64, 1, 32, 8, 128, 16, [40] * 64, seed=22)
+    c = {n: t.cuda() for n, t in d.items()}
+    args = (c["q"], c["k_pool"], c["v_pool"], c["params"], c["table"], c["lens"])
+    want = gq.gqa_decode_paged_int4(*args)
+    side = torch.cuda.Stream()
+    busy = torch.zeros(256 << 20, dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x = torch.full_like(c["q"], 3.0)
+        y = torch.empty_like(x)
+        for _ in range(20):
+            busy.add_(1.0)
+        y.copy_(x)
+        del x  # its memory may be handed out again, behind the copy on this stream
+        got = gq.gqa_decode_paged_int4(*args, stream=side)
+        torch.cuda.synchronize()
+        assert torch.all(y == 3.0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.parametrize("shape", [(2, 1, 8, 2, 128, 4, (300, 77)), (2, 2, 8, 8, 64, 12, (300, 5)), (1, 1, 8, 2, 128, 48, (1000,)),
