@@ -13,6 +13,8 @@ namespace {
 constexpr int kInt4MaxRows = 128;  // query rows per KV head
 constexpr int kMaxDevices = 64;
 
+constexpr int kInt4MaxLanes = 8;
+
 // What a shape runs as, before the number of workers is known.
 struct Int4Plan {
     int B, Sq, Hq, Hkv, D, G, Mq;
@@ -32,7 +34,7 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     if (st != GQA_OK) return st;
     if (Sq < 1 || Hq < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
     if ((long long)(Hq / Hkv) * Sq > kInt4MaxRows) return GQA_ERR_UNSUPPORTED;
-    if ((long long)pages_per_req * page_size > (1LL << 31) - 64) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
+    if ((long long)pages_per_req * page_size > (1LL << 31) - 256) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
     p->G = Hq / Hkv;
     p->Mq = p->G * Sq;
     p->NT = p->Mq > 8 ? 2 : 1;
@@ -97,24 +99,55 @@ int int4_ctas(const Int4Plan &p, int dev) {
     return n < 1 ? 1 : n;
 }
 
-// Workers per head block: every ring of one wave, and no more than the
-// requests can have steps.
-int int4_workers(const Int4Plan &p, int requested, int dev) {
-    long long W = requested;
-    if (requested == 0) {
-        W = (long long)int4_ctas(p, dev) * p.rings;
-        if (W > p.max_steps) W = p.max_steps;
-    }
+// How the requests' steps are shared out.
+struct Int4Split {
+    int workers;  // per head block
+    bool whole;   // a worker takes whole requests: one launch, no workspace
+    int rings, lanes;  // as in the plan; whole requests may take other ones
+};
+
+// The automatic choice (requested = 0).  Equal shares of all steps, for every
+// ring of one wave and no more than the requests can have steps, keep every SM
+// busy whatever the lengths are, but cost a second launch for the merge and the
+// workspace.  Short requests are better off whole: one launch, no workspace, all
+// warps of a CTA on one request's steps in turns (measured, us a call without /
+// with the host's part, shares against whole: one request of 512 tokens, 8 heads
+// over 2 of 64, 9.8 / 34 against 8.9 / 30; 40 of 256 tokens, 32 heads over 8 of
+// 128, 15.3 / 39 against 13.9 / 35, of 512 17.1 / 39.7 against 20.6 / 40.9).  The
+// estimates below are fitted to such measurements; a request's length is known
+// only as the page table's width, taken as filled to 0.7 on average where the
+// lengths even out.  A requested number is a number of shares, unless it is that
+// of the automatic choice: the same number gives the same bits.
+Int4Split int4_split(const Int4Plan &p, int requested, int dev) {
+    const long long ctas = int4_ctas(p, dev);
+    long long W = ctas * p.rings;
+    if (W > p.max_steps) W = p.max_steps;
     if (W > 65535) W = 65535;
-    return W < 1 ? 1 : int(W);
+    if (W < 1) W = 1;
+    const int groups = int4_consumers(p.NT) / (p.HB * p.RG);
+    const long long steps = p.max_steps / p.B;  // of a request, at most
+    // whole requests: as many rings as requests come to a CTA, the other groups in turns on each
+    const long long each = (p.B + ctas - 1) / ctas;
+    int rings = 1, lanes = 1;
+    while (rings < each && 2 * rings <= groups && rings < kInt4MaxRings) rings *= 2;
+    while (lanes < steps && 2 * lanes * rings <= groups && lanes < kInt4MaxLanes) lanes *= 2;
+    double turns = double((steps + lanes - 1) / lanes) * (p.D == 64 ? 1.3 : 1.7);  // us
+    if (p.row_copies && turns < 0.7 * steps) turns = 0.7 * steps;  // what its producers take
+    const double whole = 5 + double((each + rings - 1) / rings) * (turns + 0.2 * (lanes - 1) + 1);
+    const double shares = 11.5 + 0.7 * 2.3 / groups * double(p.max_steps + (long long)p.B * p.change) / double(ctas);
+    if (whole < shares || W == 1) {
+        const int workers = int(p.B < ctas * rings ? p.B : ctas * rings);
+        if (requested == 0 || requested == workers) return {workers, true, rings, lanes};
+    }
+    return {int(requested == 0 ? W : requested < 65535 ? requested : 65535), false, p.rings, p.lanes};
 }
 
-size_t int4_part_rows(const Int4Plan &p, int workers) {
-    return workers <= 1 ? 0 : size_t(p.nhb) * workers * 2 * p.HB * p.Mq;
+size_t int4_part_rows(const Int4Plan &p, const Int4Split &s) {
+    return s.whole || s.workers <= 1 ? 0 : size_t(p.nhb) * s.workers * 2 * p.HB * p.Mq;
 }
 
-size_t int4_workspace(const Int4Plan &p, int workers) {
-    const size_t rows = int4_part_rows(p, workers);
+size_t int4_workspace(const Int4Plan &p, const Int4Split &s) {
+    const size_t rows = int4_part_rows(p, s);
     if (rows == 0) return 0;
     return host_align256(rows * p.D * sizeof(float)) + host_align256(rows * sizeof(float)) +
            host_align256((size_t(p.B) + 2) * sizeof(int));
@@ -170,9 +203,10 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
         cudaGetLastError();
         return GQA_ERR_CUDA;
     }
-    const int workers = int4_workers(p, num_splits, dev);
+    const Int4Split split = int4_split(p, num_splits, dev);
+    const int workers = split.workers;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const size_t need = int4_workspace(p, workers);
+    const size_t need = int4_workspace(p, split);
     void *ws = workspace;
     bool owned = false;
     if (need > 0) {
@@ -195,7 +229,7 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     if (need > 0) {
-        const size_t part_rows = int4_part_rows(p, workers);
+        const size_t part_rows = int4_part_rows(p, split);
         char *w = static_cast<char *>(ws);
         a.o_part = reinterpret_cast<float *>(w);
         w += host_align256(part_rows * D * sizeof(float));
@@ -214,6 +248,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.num_pages = num_pages;
     a.workers = workers;
     a.change = p.change;
+    a.whole = split.whole;
+    a.next_b = split.whole ? workers : 1;
     int lg = 0;
     while ((1LL << lg) < page_size) ++lg;
     a.by_page.m = (1ull << (31 + lg)) / unsigned(page_size) + 1;
@@ -223,15 +259,16 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     // One ring a CTA while the workers are fewer than the SMs; the rings share
     // the CTA's memory.
     const int ctas = int4_ctas(p, dev);
-    a.rings = workers >= ctas * p.rings ? p.rings : (workers + ctas - 1) / ctas;
-    a.rings_max = p.rings;
-    a.producers = p.row_copies ? kInt4MaxRings / a.rings : 1;
-    if (a.producers > 2) a.producers = 2;  // a warp copies 16 tokens at a time at most
-    a.lanes = p.lanes;
-    const int boxes = (p.lanes - 1) * p.HB * p.RG * p.NT * (D / 4 + 6) * 128;  // what the lanes of a ring hand over
+    a.rings = workers >= ctas * split.rings ? split.rings : (workers + ctas - 1) / ctas;
+    a.rings_max = split.rings;
+    a.lanes = split.lanes;
+    const int boxes = (a.lanes - 1) * p.HB * p.RG * p.NT * (D / 4 + 6) * 128;  // what the lanes of a ring hand over
     a.stages = ((smem - kInt4HeadBytes) / a.rings - boxes) / p.stage_bytes;
     if (a.stages > kInt4MaxStages) a.stages = kInt4MaxStages;
-    a.stages -= a.stages % p.lanes;  // a stage serves one lane only
+    a.stages -= a.stages % a.lanes;  // a stage serves one lane only
+    a.producers = kInt4MaxRings / a.rings;
+    if (p.row_copies && a.producers > 2) a.producers = 2;  // a warp copies 16 tokens at a time at most
+    while (!p.row_copies && a.stages % a.producers != 0) a.producers /= 2;  // a stage has one producer
     const int grid_y = (workers + a.rings - 1) / a.rings;
     a.box_rows = p.R;
     a.box_pitch = p.pitch;
@@ -258,14 +295,14 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     if (timed) cudaEventRecord(after, cs);
     if (e == cudaSuccess && need > 0) {
         // many partials a row: all warps of a CTA on one row
-        const bool split = workers > 16LL * B;
-        const int rows = Hkv * p.Mq, per = split ? 1 : int4_merge_warps(false);
-        const void *merge = split ? (D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64, true>)
+        const bool wide = workers > 16LL * B;
+        const int rows = Hkv * p.Mq, per = wide ? 1 : int4_merge_warps(false);
+        const void *merge = wide ? (D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64, true>)
                                              : reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<128, true>))
                                   : (D == 64 ? reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<64, false>)
                                              : reinterpret_cast<const void *>(gqa_paged_int4_merge_kernel<128, false>));
         void *margs[] = {&a};
-        e = launch(merge, dim3(unsigned((rows + per - 1) / per), unsigned(B)), 32 * int4_merge_warps(split), 0, margs, cs);
+        e = launch(merge, dim3(unsigned((rows + per - 1) / per), unsigned(B)), 32 * int4_merge_warps(wide), 0, margs, cs);
     }
     if (owned) cudaFreeAsync(ws, cs);
     if (e != cudaSuccess) {
@@ -282,7 +319,7 @@ extern "C" int gqa_decode_paged_int4_num_splits(int B, int Sq, int Hq, int Hkv, 
     if (st != GQA_OK) return -int(st);
     int dev = 0;
     if (!host_current_device(&dev)) return -int(GQA_ERR_CUDA);
-    return int4_workers(p, 0, dev);
+    return int4_split(p, 0, dev).workers;
 }
 
 extern "C" size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size,
@@ -290,6 +327,6 @@ extern "C" size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, i
     Int4Plan p;
     if (plan_int4(B, Sq, Hq, Hkv, D, page_size, pages_per_req, 1, &p) != GQA_OK || num_splits < 0) return 0;
     int dev = 0;
-    if (num_splits == 0 && !host_current_device(&dev)) return 0;
-    return int4_workspace(p, int4_workers(p, num_splits, dev));
+    if (!host_current_device(&dev)) return 0;
+    return int4_workspace(p, int4_split(p, num_splits, dev));
 }

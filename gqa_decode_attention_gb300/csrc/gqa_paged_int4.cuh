@@ -65,7 +65,7 @@
 namespace gqa {
 
 constexpr int kInt4Step = 32;       // tokens a stage
-constexpr int kInt4MaxStages = 8;   // of a ring
+constexpr int kInt4MaxStages = 16;  // of a ring
 constexpr int kInt4MaxRings = 4;    // of a CTA, one producer warp each
 // Consumer warps of a CTA that hold NT tiles of 8 query rows, and the
 // registers a thread of theirs and of the producers' warpgroup has: together
@@ -107,6 +107,8 @@ struct Int4Args {
     int *step_prefix;         // [B + 2] first place of each request, their end, and the places shared out (several workers)
     int B, Sq, Hq, Hkv, G, Mq, page_size, pages_per_req, num_pages;
     int change;               // steps' worth of time that a change of request costs (at least 1)
+    int whole;                // 1: worker w takes the whole requests w, w + workers, ...; 0: an equal share of all steps
+    int next_b;               // from a worker's request to its next one: workers if whole, else 1
     int workers, HB, RG;      // workers per head block; heads of a CTA, warps (of 8 or 16 query rows) a head
     int rings, rings_max;     // rings (workers) of a CTA, and how many its warps could serve
     int lanes;                // groups of HB x RG warps that take turns at a ring's steps
@@ -114,7 +116,7 @@ struct Int4Args {
     FastDiv by_page;          // page_size
     unsigned g_inv;           // ceil(2^16 / G): r / G = r * g_inv >> 16 for r < 128
     int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
-    int producers;            // warps that fill a ring
+    int producers;            // warps that fill a ring: in turns (TMA), or a part of each step's tokens each (16-byte copies)
     const uint8_t *k_pool, *v_pool;  // for 16-byte copies
     unsigned param_pitch;     // of a box's parameters in a stage
     unsigned par8, par16;     // as tok8, tok16, of the parameters
@@ -136,8 +138,8 @@ struct Int4Head {
     int warp_sum[20];
     int abort;
 };
-constexpr int kInt4HeadBytes = 1024;
-static_assert(sizeof(Int4Head) <= kInt4HeadBytes, "head");
+constexpr int kInt4HeadBytes = 2048;
+static_assert(sizeof(Int4Head) <= kInt4HeadBytes && kInt4MaxStages <= 32, "head");
 
 template <int REGS>
 __device__ __forceinline__ void more_registers() {
@@ -330,18 +332,18 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const int nh = min(a.HB, a.Hkv - hb0);
     const int cap = a.pages_per_req * a.page_size;
 
-    if (threadIdx.x == 0) {
-        for (int r = 0; r < a.rings; ++r) {
-            for (int st = 0; st < a.stages; ++st) {
-                mbar_init(&head->full[r][st], a.param_tma ? 1 : 1 + 32 * a.producers);  // the expect, and lanes' copies
-                mbar_init(&head->empty[r][st], nh * a.RG);
-            }
-            mbar_init(&head->ready[r], max(1, (a.lanes - 1) * nh * a.RG));
-            mbar_init(&head->taken[r], nh * a.RG);
-            head->first[r] = (unsigned long long)a.B << 32;
+    if (warp < a.rings && lane < a.stages) {  // a ring a warp, a stage a lane
+        mbar_init(&head->full[warp][lane], a.param_tma ? 1 : 1 + 32 * (COPY ? a.producers : 1));  // the expect, and lanes' copies
+        mbar_init(&head->empty[warp][lane], nh * a.RG);
+        if (lane == 0) {
+            mbar_init(&head->ready[warp], max(1, (a.lanes - 1) * nh * a.RG));
+            mbar_init(&head->taken[warp], nh * a.RG);
+            head->first[warp] = (unsigned long long)a.B << 32;
         }
-        head->abort = 0;
         fence_mbarrier_init();
+    }
+    if (threadIdx.x == 0) {
+        head->abort = 0;
         if constexpr (!COPY) {
             prefetch_tmap(&k_map);
             prefetch_tmap(&v_map);
@@ -367,7 +369,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     int w_begin, w_end, seg_b, seg_p;
     // no change follows the last request (an empty one keeps a place to be held)
     const int trailing = a.change - (__ldg(a.seq_lens + a.B - 1) <= 0 ? 1 : 0);
-    if (a.B <= kInt4WarpRequests) {
+    if (a.whole) {
+        const int w = r * int(gridDim.y) + int(blockIdx.y);
+        w_begin = seg_p = 0;  // counted over the worker's own requests
+        w_end = 0x7fffffff;
+        seg_b = w < a.workers ? w : a.B;
+        __syncthreads();  // the barriers are set up
+    } else if (a.B <= kInt4WarpRequests) {
         // each warp for itself: a run of requests a lane, a scan, and the first
         // lane with a request that holds the share's first step
         const int run = (a.B + 31) / 32;
@@ -465,9 +473,12 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     // ============================================================== producers
     if (warp >= CW) {
         fewer_registers<int4_producer_regs(NT, COPY)>();
-        // 16-byte copies take a warp long, so all four share the rings' tokens
-        const int part = (warp - CW) / a.rings, parts = COPY ? a.producers : 1;
+        // One warp starts a step's TMA every 0.65 us, so a ring's warps take turns
+        // (one request of 1K tokens, 8 lanes on one ring: 27 -> 12 us); of
+        // 16-byte copies each takes a part of every step's tokens.
+        const int part = (warp - CW) / a.rings, parts = a.producers;
         if (part >= parts) return;
+        const int every = COPY ? 1 : a.producers;  // takes every so many steps, and stages
         uint64_t *full = head->full[r], *empty = head->empty[r];
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
@@ -483,40 +494,41 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         const int per_part = kInt4Step / parts;
         const uint8_t *k_src = a.k_pool + size_t(hb0) * ROWB + u * 16;
         const uint8_t *v_src = a.v_pool + size_t(hb0) * ROWB + u * 16;
-        int st = 0, gs = 0;
-        uint32_t phase = 0;
+        int st = COPY ? 0 : part, round = 0;  // stage of this warp's next step, and times it was used
+        int ahead = st;  // from the segment's first step to that one
         bool failed = false;
         while (seg_b < a.B && seg_t < w_end && !failed) {
-            const int len = min(max(__ldg(a.seq_lens + seg_b), 0), cap);
+            const int len0 = __ldg(a.seq_lens + seg_b), len = min(max(len0, 0), cap);
+            bad |= len0 != len;
             const int steps_b = (len + kInt4Step - 1) / kInt4Step;
             const int seg_next = min(w_end, seg_p + steps_b);
             const int32_t *table = a.page_table + size_t(seg_b) * a.pages_per_req;
             const int t_end = min((seg_next - seg_p) * kInt4Step, len);
-            int t = (seg_t - seg_p) * kInt4Step + lane;
+            int t = (seg_t - seg_p + ahead) * kInt4Step + lane;
             int at = fast_div(t, a.by_page);
             int page = t < t_end ? __ldg(table + at) : 0;
-            for (; t - lane < t_end; ++gs) {
+            while (t - lane < t_end) {
                 const bool in = t < t_end;
                 const bool ok = in && page >= 0 && page < a.num_pages;
                 bad |= in && !ok;
                 const int row = ok ? page * a.page_size + (t - at * a.page_size) : 0;
                 // the next step's page is on its way while this one is issued
-                t += kInt4Step;
+                t += kInt4Step * every;
                 at = fast_div(t, a.by_page);
                 if (t < t_end) page = __ldg(table + at);
                 const uint32_t valid = __ballot_sync(0xffffffffu, ok);
                 const bool box = ok && first;  // its first token's page holds all of a box
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-                if (gs >= a.stages) {
+                if (round > 0) {
                     bool free = true;
-                    if (lane == 0) free = mbar_wait_bounded(empty + st, phase ^ 1, a.wait_limit_ns, abort_flag);
+                    if (lane == 0) free = mbar_wait_bounded(empty + st, (round - 1) & 1, a.wait_limit_ns, abort_flag);
                     if (!__shfl_sync(0xffffffffu, free, 0)) {
                         failed = true;
                         break;
                     }
                 }
-                if (!(a.fault_mode == 1 && gs == 0)) {
-                    if (lane == 0 && part == 0) {
+                if (!(a.fault_mode == 1 && round == 0 && st == 0)) {
+                    if (lane == 0 && (!COPY || part == 0)) {
                         vmask[st] = valid;
                         mbar_arrive_expect_tx(full + st, boxes * box_bytes);
                     }
@@ -540,19 +552,21 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         }
                     }
                     if (COPY || !a.param_tma) {
-                        if (ok && part == parts - 1) {
+                        if (ok && (!COPY || part == parts - 1)) {
                             const __half *src = a.params + (size_t(row) * a.Hkv + hb0) * 4;
                             for (int h = 0; h < nh; ++h) cp_async8(base + par_at + h * 8, src + h * 4);
                         }
                         cp_async_arrive(full + st);
                     }
                 }
-                if (++st == a.stages) st = 0, phase ^= 1;
+                st += every;
+                if (st >= a.stages) st -= a.stages, ++round;
             }
+            if (!COPY) ahead = (t - lane) / kInt4Step - (seg_next - seg_p);
             seg_t = seg_next;
             if (seg_next == seg_p + steps_b) {
                 seg_t = seg_p = seg_next + a.change;
-                ++seg_b;
+                seg_b += a.next_b;
             }
         }
         if (bad) flag_error(a.err, kErrIndex);
@@ -562,10 +576,10 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         }
         // Every copy must land before the CTA's shared memory is released;
         // after an abort some may not have been waited for.
-        for (int i = 0; i < a.stages && i < gs; ++i) {
-            const int last = i + ((gs - 1 - i) / a.stages) * a.stages;  // last step issued into stage i
-            if (a.fault_mode == 1 && last == 0) continue;
-            if (lane == 0 && !mbar_wait_bounded(full + i, (last / a.stages) & 1, a.wait_limit_ns, nullptr))
+        for (int i = COPY ? 0 : part; i < a.stages; i += every) {
+            const int last = round - (i < st ? 0 : 1);  // the last round in which stage i was filled
+            if (last < 0 || (a.fault_mode == 1 && last == 0 && i == 0)) continue;
+            if (lane == 0 && !mbar_wait_bounded(full + i, last & 1, a.wait_limit_ns, nullptr))
                 flag_error(a.err, kErrTimeout);
         }
         return;
@@ -899,7 +913,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 }
         }
         if (failed) break;
-        load_queries(b + 1);
+        load_queries(b + a.next_b);
         done += n_seg;
 
         // ---- lanes: the first one takes the others' results, which lie in
@@ -1006,7 +1020,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         seg_t = seg_next;
         if (seg_next == seg_p + steps_b) {
             seg_t = seg_p = seg_next + a.change;
-            ++seg_b;
+            seg_b += a.next_b;
         }
     }
     if (failed && lane == 0) {

@@ -406,9 +406,10 @@ size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, i
  *   result that is not finite; other rows are not touched by either, and what
  *   the pools hold in slots past a request's length is never used.
  * Limits: D in {64, 128}; (Hq / Hkv) * Sq <= 128; pages_per_req * page_size
- *   <= 2^31 - 64, and B times it (rounded up to 32) < 2^36; the rest as
+ *   <= 2^31 - 256, and B times it (rounded up to 32) < 2^36; the rest as
  *   gqa_decode_paged.  kv_params 16-byte aligned.
- * num_splits = workers per block of KV heads (0 = automatic); workspace as
+ * num_splits = workers per block of KV heads (0 = automatic; short requests then
+ *   go to one worker each, in one launch without a workspace); workspace as
  *   gqa_decode_paged_ex (NULL = library pool; otherwise 256-byte aligned,
  *   gqa_decode_paged_int4_workspace_bytes, not in use by other work in
  *   flight).  The same split count gives the same bits.

@@ -380,6 +380,33 @@ def test_empty_requests(gq, lens):
         check(d, out, lse, what=f"splits {splits}")
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 8, 2, 64, 16, 500), (3, 1, 32, 8, 128, 16, 130), (2, 4, 32, 8, 128, 32, 64), (7, 2, 16, 1, 64, 8, 250),
+                                   (170, 1, 16, 8, 128, 16, 90), (400, 1, 8, 2, 64, 16, 100), (700, 1, 3, 1, 64, 16, 70), (320, 3, 8, 2, 128, 16, 40),
+                                   (1300, 1, 4, 2, 64, 5, 33), (5, 1, 8, 8, 64, 5, 96), (900, 1, 2, 1, 128, 4, 32)],
+                         ids=lambda s: "b%d_sq%d_h%dx%d_d%d_ps%d_kv%d" % s)
+def test_short_requests_whole(gq, shape):
+    """Short requests, which the automatic choice leaves to one worker each: no workspace, as many requests as CTAs and
+    more, and several of them after one another on a worker; the same bits at any number of requests around them."""
+    B, Sq, Hq, Hkv, D, ps, hi = shape
+    g = torch.Generator().manual_seed(sum(shape))
+    lens = torch.randint(0, hi + 1, (B,), generator=g)
+    lens[B // 2] = hi
+    lens[torch.rand(B, generator=g) < 0.1] = 0
+    d = make(B, Sq, Hq, Hkv, D, ps, lens.tolist(), seed=B, ppr=-(-hi // ps))
+    ppr = d["table"].shape[1]
+    assert gq.gqa_decode_paged_int4_workspace_bytes(B, Sq, Hq, Hkv, D, ps, ppr) == 0
+    out, lse = run(gq, d)
+    assert gq.gqa_device_status() == 0
+    check(d, out, lse)
+    n = gq.gqa_decode_paged_int4_num_splits(B, Sq, Hq, Hkv, D, ps, ppr)
+    again = run(gq, d, num_splits=n)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    bad = {**d, "lens": d["lens"].clone()}
+    bad["lens"][B - 1] = ppr * ps + 1
+    run(gq, bad)
+    assert gq.gqa_device_status() == 7
+
+
 def test_largest_batch(gq):
     """65535 requests of 0 to 2 tokens, every result against 64 bits at once."""
     B, Hq, Hkv, D = 65535, 2, 1, 64
@@ -423,5 +450,25 @@ def test_wait_that_runs_out(gq, shape):
         gq.gqa_debug_set_fault_mode(0)
         gq.gqa_set_wait_limit_ns(0)
     again = run(gq, d, num_splits=3)
+    assert gq.gqa_device_status() == 0
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+
+
+@pytest.mark.parametrize("shape", [(3, 1, 8, 2, 64, 16), (2, 4, 16, 2, 128, 16), (160, 1, 16, 8, 128, 16), (2, 1, 6, 3, 64, 5)],
+                         ids=["lanes", "16rows", "rings", "copies"])
+def test_wait_that_runs_out_on_whole_requests(gq, shape):
+    B = shape[0]
+    d = make(*shape, [90] * B, seed=41)
+    assert gq.gqa_decode_paged_int4_workspace_bytes(*shape, d["table"].shape[1]) == 0
+    want = run(gq, d)
+    gq.gqa_set_wait_limit_ns(2_000_000)
+    gq.gqa_debug_set_fault_mode(1)
+    try:
+        run(gq, d)
+        assert gq.gqa_device_status() == 6
+    finally:
+        gq.gqa_debug_set_fault_mode(0)
+        gq.gqa_set_wait_limit_ns(0)
+    again = run(gq, d)
     assert gq.gqa_device_status() == 0
     assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
