@@ -21,10 +21,12 @@ struct Int4Plan {
     int NT;      // tiles of 8 query rows a consumer warp holds
     int RG, HB;  // consumer warps per head, heads per CTA
     int rings, lanes;  // most rings of a CTA; groups of HB x RG warps on each
-    int R;       // tokens of a TMA box: the largest power of two, at most 16, that divides the page size
+    int R;       // tokens of a TMA box: the largest power of two, at most a step, that divides the page size
     bool row_copies;  // no TMA for K and V: below R = 4 the boxes are too many (96 a step with pages of 5: 2.7 us)
     int pitch, par_pitch, stage_bytes, nhb;
     bool param_tma;
+    int param_rows;  // of a box of the parameters' map if its rows are 32 bytes, 0 if tokens
+    int param_heads;
     long long max_steps;
     int change;  // places that a change of request takes in the schedule
 };
@@ -53,14 +55,21 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     p->rings = groups < kInt4MaxRings ? groups : kInt4MaxRings;
     while (groups % p->rings != 0) --p->rings;
     p->lanes = groups / p->rings;
-    p->R = 16;
+    // A warp takes 110 to 130 cycles to start a box, which bounds large caches of one small head (126 requests, 79838
+    // steps of one head of 64: 112 us with boxes of 16 and parameters by cp.async, 108 with parameters by TMA, 91 with 32).
+    p->R = kInt4Step;
     while (page_size % p->R != 0) p->R /= 2;
     p->row_copies = p->R < 4;
     if (p->row_copies) p->R = 16;  // the places of whole boxes
     const int row = D / 2;
     p->pitch = (hb * p->R * row + 127) / 128 * 128;  // TMA writes to 128-byte boundaries
-    p->param_tma = Hkv % 2 == 0 && hb > 1 && !p->row_copies;           // a box's rows, and their stride, in whole 16 bytes
-    p->par_pitch = p->param_tma ? (hb * p->R * 8 + 127) / 128 * 128 : hb * p->R * 8;
+    // Parameters by TMA where a token's are whole 16 bytes, or where a CTA has all heads, so that a box's are one
+    // piece, seen as rows of 32 bytes (R * Hkv * 8 bytes, R a multiple of 4).
+    const bool even = Hkv % 2 == 0 && hb > 1;
+    p->param_tma = !p->row_copies && (even || p->nhb == 1);
+    p->param_rows = p->param_tma && !even ? p->R * Hkv / 4 : 0;
+    p->param_heads = p->param_rows > 0 ? Hkv : hb;
+    p->par_pitch = p->param_tma ? (p->param_heads * p->R * 8 + 127) / 128 * 128 : hb * p->R * 8;
     // 512: the period of the swizzle
     p->stage_bytes = ((kInt4Step / p->R) * (2 * p->pitch + p->par_pitch) + 511) / 512 * 512;
     return GQA_OK;
@@ -116,7 +125,7 @@ struct Int4Split {
 // 128, 15.3 / 39 against 13.9 / 35, of 512 17.1 / 39.7 against 20.6 / 40.9).  The
 // estimates below are fitted to such measurements; a request's length is known
 // only as the page table's width, taken as filled to 0.7 on average where the
-// lengths even out.  A requested number is a number of shares, unless it is that
+// lengths even out; past 40 us uneven lengths cost more than a merge.  A requested number is a number of shares, unless it is that
 // of the automatic choice: the same number gives the same bits.
 Int4Split int4_split(const Int4Plan &p, int requested, int dev) {
     const long long ctas = int4_ctas(p, dev);
@@ -135,7 +144,7 @@ Int4Split int4_split(const Int4Plan &p, int requested, int dev) {
     if (p.row_copies && turns < 0.7 * steps) turns = 0.7 * steps;  // what its producers take
     const double whole = 5 + double((each + rings - 1) / rings) * (turns + 0.2 * (lanes - 1) + 1);
     const double shares = 11.5 + 0.7 * 2.3 / groups * double(p.max_steps + (long long)p.B * p.change) / double(ctas);
-    if (whole < shares || W == 1) {
+    if ((whole < shares && whole < 40) || W == 1) {
         const int workers = int(p.B < ctas * rings ? p.B : ctas * rings);
         if (requested == 0 || requested == workers) return {workers, true, rings, lanes};
     }
@@ -199,7 +208,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     if (smem == 0 ||
         (!p.row_copies && (!host_int4_tensor_map(&k_map, k_pool, rows, Hkv, D / 2, p.R, p.HB) ||
                            !host_int4_tensor_map(&v_map, v_pool, rows, Hkv, D / 2, p.R, p.HB))) ||
-        (p.param_tma && !host_int4_param_map(&p_map, kv_params, rows, Hkv, p.R, p.HB))) {
+        (p.param_tma && !(p.param_rows > 0 ? host_int4_param_map(&p_map, kv_params, rows / 4 * Hkv, 4, p.param_rows, 4)
+                                         : host_int4_param_map(&p_map, kv_params, rows, Hkv, p.R, p.HB)))) {
         cudaGetLastError();
         return GQA_ERR_CUDA;
     }
@@ -274,14 +284,17 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     a.box_rows = p.R;
     a.box_pitch = p.pitch;
     a.stage_bytes = p.stage_bytes;
-    a.tok8 = p.R == 16 ? 8 * (D / 2) : (8 / p.R) * p.pitch;
-    a.tok16 = p.R == 16 ? p.pitch : (16 / p.R) * p.pitch;
+    a.tok8 = p.R >= 16 ? 8 * (D / 2) : (8 / p.R) * p.pitch;
+    a.tok16 = p.R == 32 ? 16 * (D / 2) : p.R == 16 ? p.pitch : (16 / p.R) * p.pitch;
     a.param_tma = p.param_tma;
+    a.param_shift = p.param_rows > 0 ? 2 : 0;
+    a.param_mul = p.param_rows > 0 ? Hkv : 1;
+    a.param_heads = p.param_heads;
     a.k_pool = static_cast<const uint8_t *>(k_pool);
     a.v_pool = static_cast<const uint8_t *>(v_pool);
     a.param_pitch = p.par_pitch;
-    a.par8 = p.R == 16 ? 8 * p.HB * 8 : (8 / p.R) * p.par_pitch;
-    a.par16 = p.R == 16 ? p.par_pitch : (16 / p.R) * p.par_pitch;
+    a.par8 = p.R >= 16 ? 8 * p.param_heads * 8 : (8 / p.R) * p.par_pitch;
+    a.par16 = p.R == 32 ? 16 * p.param_heads * 8 : p.R == 16 ? p.par_pitch : (16 / p.R) * p.par_pitch;
     a.alpha = host_resolve_scale(scale, D) * 1.4426950408889634f;
     a.wait_limit_ns = host_wait_limit_ns();
     a.fault_mode = host_fault_mode();

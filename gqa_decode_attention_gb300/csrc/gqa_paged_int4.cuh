@@ -44,7 +44,7 @@
 // head's rows back to back, and with the 64-byte swizzle (D = 128) and the
 // token order of `tok_of` every fragment read is free of bank conflicts.
 // Parameters come by TMA too, [token][head] (by cp.async where their rows are
-// not 16 bytes); pages without a factor of 4 take K and V in 16-byte copies to
+// not 16 bytes and the CTA has not all heads); pages without a factor of 4 take K and V in 16-byte copies to
 // the same places, since a box ends at its page's end.  The warps never wait for
 // one another beyond the ring: each works out its segments from the lengths,
 // and the loads run ahead across request borders.  Short requests are not
@@ -117,7 +117,9 @@ struct Int4Args {
     int stages, box_rows, box_pitch, stage_bytes;
     FastDiv by_page;          // page_size
     unsigned g_inv;           // ceil(2^16 / G): r / G = r * g_inv >> 16 for r < 128
-    int param_tma;            // parameters by TMA (Hkv even, several heads a CTA), else by 8-byte cp.async
+    int param_tma;            // parameters by 2-D TMA, else by 8-byte cp.async
+    int param_heads;          // heads between a token's parameters and the next one's in a stage
+    int param_shift, param_mul;  // a box's row of the parameters' map: (first row >> shift) * mul
     int producers;            // warps that fill a ring: in turns (TMA), or a part of each step's tokens each (16-byte copies)
     const uint8_t *k_pool, *v_pool;  // for 16-byte copies
     unsigned param_pitch;     // of a box's parameters in a stage
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     const int R = a.box_rows;
     // Offsets in a stage: a token's row lies in box t / R, head h, row t % R.
     const uint32_t v_off = uint32_t(kInt4Step / R) * a.box_pitch;
-    auto par_off = [&](int t, int h) { return 2 * v_off + uint32_t(t / R) * a.param_pitch + uint32_t((t % R) * a.HB + h) * 8; };
+    auto par_off = [&](int t, int h) { return 2 * v_off + uint32_t(t / R) * a.param_pitch + uint32_t((t % R) * a.param_heads + h) * 8; };
 
     // ============================================================== producers
     if (warp >= CW) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
         uint64_t *full = head->full[r], *empty = head->empty[r];
         uint32_t *vmask = head->mask[r];
         const uint32_t ring = smem_u32(smem4) + kInt4HeadBytes + uint32_t(r * a.stages) * a.stage_bytes;
-        const uint32_t box_bytes = COPY ? 0 : uint32_t(a.HB) * R * (2 * ROWB + (a.param_tma ? 8 : 0));
+        const uint32_t box_bytes = COPY ? 0 : uint32_t(R) * (a.HB * 2 * ROWB + (a.param_tma ? a.param_heads * 8 : 0));
         const uint32_t box_at = uint32_t(lane / R) * a.box_pitch, par_at = par_off(lane, 0);
         const bool first = lane % R == 0 && !COPY;  // of a box
         // 16-byte copies: a token's piece of the block's heads is 2^lc of them;
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                     if (!COPY && box) {
                         tma_load_3d(base + box_at, &k_map, full + st, 0, row, hb0);
                         tma_load_3d(base + box_at + v_off, &v_map, full + st, 0, row, hb0);
-                        if (a.param_tma) tma_load_2d(base + par_at, &p_map, full + st, hb0 * 4, row);
+                        if (a.param_tma) tma_load_2d(base + par_at, &p_map, full + st, hb0 * 4, (row >> a.param_shift) * a.param_mul);
                     }
                     if constexpr (COPY) {
 #pragma unroll 4
