@@ -39,7 +39,7 @@
 // several CTAs an SM whose consumers start the loads in turns 177 us, a
 // producer warp in each 155, this 145.)  Where heads and row groups are fewer than the warps, `lanes`
 // groups take turns at a ring's steps and join their results in shared memory.
-// K and V come by TMA as boxes of (row bytes) x (up to 16
+// K and V come by TMA as boxes of (row bytes) x (up to 32
 // tokens of one page) x (heads of the block): shared memory then holds each
 // head's rows back to back, and with the 64-byte swizzle (D = 128) and the
 // token order of `tok_of` every fragment read is free of bank conflicts.
