@@ -277,7 +277,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
     if (a.stages > kInt4MaxStages) a.stages = kInt4MaxStages;
     a.stages -= a.stages % a.lanes;  // a stage serves one lane only
     a.producers = kInt4MaxRings / a.rings;
-    if (p.row_copies && a.producers > 2) a.producers = 2;  // a warp copies 16 tokens at a time at most
+    // 16-byte copies: a warp's turn is 32 pieces, 32 / (HB * D / 32) tokens, of its part of the step's 32
+    while (p.row_copies && a.producers > p.HB * (D / 32)) a.producers /= 2;
     // TMA: a stage has one producer, and one keeps up with a lane, which takes longer than 0.65 us a step
     while (!p.row_copies && (a.stages % a.producers != 0 || a.producers > a.lanes)) a.producers /= 2;
     const int grid_y = (workers + a.rings - 1) / a.rings;
