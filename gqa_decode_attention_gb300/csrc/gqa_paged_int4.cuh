@@ -34,17 +34,18 @@
 // SM: 16 consumer warps for 8 query rows each, or 8 for 16 rows, one per head
 // (and per group of rows), and four producer warps with few registers, one for
 // each of up to four rings of shared-memory stages, or in turns on fewer; a ring
-// is a worker.  (Of
-// the ways tried on 32 requests of 16K to 32K tokens, 64 heads over 8 of 128:
-// several CTAs an SM whose consumers start the loads in turns 177 us, a
-// producer warp in each 155, this 145.)  Where heads and row groups are fewer than the warps, `lanes`
-// groups take turns at a ring's steps and join their results in shared memory.
-// K and V come by TMA as boxes of (row bytes) x (up to 32
-// tokens of one page) x (heads of the block): shared memory then holds each
-// head's rows back to back, and with the 64-byte swizzle (D = 128) and the
-// token order of `tok_of` every fragment read is free of bank conflicts.
-// Parameters come by TMA too, [token][head] (by cp.async where their rows are
-// not 16 bytes and the CTA has not all heads); pages without a factor of 4 take K and V in 16-byte copies to
+// is a worker.  (Of the ways tried on 32 requests of 16K to 32K tokens, 64 heads
+// over 8 of 128: several CTAs an SM whose consumers start the loads in turns
+// 177 us, a producer warp in each 155, this 145.)  Where heads and row groups are
+// fewer than the warps, `lanes` groups take turns at a ring's steps and join
+// their results in shared memory.
+//
+// K and V come by TMA as boxes of (row bytes) x (up to 32 tokens of one page) x
+// (heads of the block): shared memory then holds each head's rows back to back,
+// and with the 64-byte swizzle (D = 128) and the token order of `tok_of` every
+// fragment read is free of bank conflicts.  Parameters come by TMA too,
+// [token][head] (by cp.async where their rows are not 16 bytes and the CTA has
+// not all heads); pages without a factor of 4 take K and V in 16-byte copies to
 // the same places, since a box ends at its page's end.  The warps never wait for
 // one another beyond the ring: each works out its segments from the lengths,
 // and the loads run ahead across request borders.  Short requests are not
@@ -52,11 +53,11 @@
 //
 // Measured on GB300 (main and merge kernel): the 32 requests above, 814 MB,
 // 145 us, 5.6 TB/s, 83 % of the copy peak -- bound by HBM and by SMs whose path
-// to memory is slower, which the shares do not know of; one request of 128K tokens 43 us,
-// of which the start is 6 and the merge 5; 256 requests of up to 1K tokens
-// 47 us, bound by the consumers' instructions and the changes of request; 16
-// requests of 4 x 4 rows a head and up to 8K tokens 36 us, where 16 rows a warp
-// make a step 1.2 us long; 40 whole requests of 256 tokens 14 us.
+// to memory is slower, which the shares do not know of; one request of 128K
+// tokens 43 us, of which the start is 6 and the merge 5; 256 requests of up to
+// 1K tokens 46 us, bound by the consumers' instructions and the changes of
+// request; 16 requests of 4 x 4 rows a head and up to 8K tokens 36 us, where 16
+// rows a warp make a step 1.2 us long; 40 whole requests of 256 tokens 14 us.
 #pragma once
 
 #include <stddef.h>
