@@ -14,10 +14,11 @@ constexpr int kInt4MaxRows = 128;  // query rows per KV head
 constexpr int kMaxDevices = 64;
 
 constexpr int kInt4MaxLanes = 8;
+constexpr int kInt4MaxShortRows = 32;  // of a KV head, with 8 rows a warp in short requests
 
 // What a shape runs as, before the number of workers is known.
 struct Int4Plan {
-    int B, Sq, Hq, Hkv, D, G, Mq;
+    int B, Sq, Hq, Hkv, D, G, Mq, page_size;
     int NT;      // tiles of 8 query rows a consumer warp holds
     int RG, HB;  // consumer warps per head, heads per CTA
     int rings, lanes;  // most rings of a CTA; groups of HB x RG warps on each
@@ -31,22 +32,14 @@ struct Int4Plan {
     int change;  // places that a change of request takes in the schedule
 };
 
-gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int pages_per_req, int num_pages, Int4Plan *p) {
-    gqa_status st = host_check_pages(B, Hkv, D, page_size, pages_per_req, num_pages);
-    if (st != GQA_OK) return st;
-    if (Sq < 1 || Hq < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
-    if ((long long)(Hq / Hkv) * Sq > kInt4MaxRows) return GQA_ERR_UNSUPPORTED;
-    if ((long long)pages_per_req * page_size > (1LL << 31) - 256) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
-    p->G = Hq / Hkv;
-    p->Mq = p->G * Sq;
-    p->NT = p->Mq > 8 ? 2 : 1;
+// The plan's layout with NT tiles of 8 query rows a warp.
+void int4_layout(Int4Plan *p, int nt) {
+    const int Hkv = p->Hkv, page_size = p->page_size;
+    p->NT = nt;
     // Measured (us a call): 256 requests of up to 1K tokens, 8 rows a warp, 47.6 with 1, 46.5 with 2, 48.6 with 4; 16
     // requests of up to 8K tokens, 16 rows a warp, 41.9 with 1, 35.3 with 4, 33.9 with 6, 34.6 with 12.
-    p->change = p->NT == 1 ? 2 : 6;
-    p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
-    if (p->max_steps + (long long)B * p->change >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
-    p->B = B, p->Sq = Sq, p->Hq = Hq, p->Hkv = Hkv, p->D = D;
-    p->RG = (p->Mq + 8 * p->NT - 1) / (8 * p->NT);
+    p->change = nt == 1 ? 2 : 6;
+    p->RG = (p->Mq + 8 * nt - 1) / (8 * nt);
     int hb = 1;
     while (hb < Hkv && 2 * hb * p->RG <= 8) hb *= 2;
     p->HB = hb;
@@ -61,7 +54,7 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     while (page_size % p->R != 0) p->R /= 2;
     p->row_copies = p->R < 4;
     if (p->row_copies) p->R = 16;  // the places of whole boxes
-    const int row = D / 2;
+    const int row = p->D / 2;
     p->pitch = (hb * p->R * row + 127) / 128 * 128;  // TMA writes to 128-byte boundaries
     // Parameters by TMA where a token's are whole 16 bytes, or where a CTA has all heads, so that a box's are one
     // piece, seen as rows of 32 bytes (R * Hkv * 8 bytes, R a multiple of 4).
@@ -72,6 +65,20 @@ gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int p
     p->par_pitch = p->param_tma ? (p->param_heads * p->R * 8 + 127) / 128 * 128 : hb * p->R * 8;
     // 512: the period of the swizzle
     p->stage_bytes = ((kInt4Step / p->R) * (2 * p->pitch + p->par_pitch) + 511) / 512 * 512;
+}
+
+gqa_status plan_int4(int B, int Sq, int Hq, int Hkv, int D, int page_size, int pages_per_req, int num_pages, Int4Plan *p) {
+    gqa_status st = host_check_pages(B, Hkv, D, page_size, pages_per_req, num_pages);
+    if (st != GQA_OK) return st;
+    if (Sq < 1 || Hq < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
+    if ((long long)(Hq / Hkv) * Sq > kInt4MaxRows) return GQA_ERR_UNSUPPORTED;
+    if ((long long)pages_per_req * page_size > (1LL << 31) - 256) return GQA_ERR_UNSUPPORTED;  // token indexes step past the end
+    p->B = B, p->Sq = Sq, p->Hq = Hq, p->Hkv = Hkv, p->D = D, p->page_size = page_size;
+    p->G = Hq / Hkv;
+    p->Mq = p->G * Sq;
+    p->max_steps = (long long)B * (((long long)pages_per_req * page_size + kInt4Step - 1) / kInt4Step);
+    int4_layout(p, p->Mq > 8 ? 2 : 1);
+    if (p->max_steps + (long long)B * p->change >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;  // the schedule counts steps in 32 bits
     return GQA_OK;
 }
 
@@ -129,7 +136,7 @@ struct Int4Split {
 // of up to 6K tokens, 32 rows a head of 64: 196 against 103 us).  A requested
 // number is a number of shares, unless it is that of the automatic choice: the
 // same number gives the same bits.
-Int4Split int4_split(const Int4Plan &p, int requested, int dev) {
+Int4Split int4_auto(const Int4Plan &p, int dev, double *us) {
     const long long ctas = int4_ctas(p, dev);
     long long W = ctas * p.rings;
     if (W > p.max_steps) W = p.max_steps;
@@ -142,15 +149,35 @@ Int4Split int4_split(const Int4Plan &p, int requested, int dev) {
     int rings = 1, lanes = 1;
     while (rings < each && 2 * rings <= groups && rings < kInt4MaxRings) rings *= 2;
     while (lanes < steps && 2 * lanes * rings <= groups && lanes < kInt4MaxLanes) lanes *= 2;
-    double turns = double((steps + lanes - 1) / lanes) * (p.D == 64 ? 1.3 : 1.7);  // us
+    double turns = double((steps + lanes - 1) / lanes) * (p.D == 64 ? 1.3 : 1.7);
     if (p.row_copies && turns < 0.7 * steps) turns = 0.7 * steps;  // what its producers take
-    const double whole = 5 + double((each + rings - 1) / rings) * (turns + 0.2 * (lanes - 1) + 1);
+    const double whole = (p.NT == 1 ? 5 : 8) + double((each + rings - 1) / rings) * (turns + 0.2 * (lanes - 1) + 1);
     const double shares = 11.5 + 0.7 * 2.3 / groups * double(p.max_steps + (long long)p.B * p.change) / double(ctas);
-    if ((whole < shares && whole < 40) || W == 1) {
-        const int workers = int(p.B < ctas * rings ? p.B : ctas * rings);
-        if (requested == 0 || requested == workers) return {workers, true, rings, lanes};
+    *us = whole < shares ? whole : shares;
+    if ((whole < shares && whole < 40) || W == 1) return {int(p.B < ctas * rings ? p.B : ctas * rings), true, rings, lanes};
+    return {int(W), false, p.rings, p.lanes};
+}
+
+// More than 8 rows a head: 16 of them a warp turn a step's codes into operands
+// once for all, 8 of them start and end a request sooner.  Long walks are 8 to
+// 10 % faster with 16, short whole requests 20 to 30 % with 8 (22 requests of 11
+// tokens, 15 rows a head of 128, 7.6 against 6.1 us).
+Int4Split int4_split(Int4Plan *p, int requested, int dev) {
+    Int4Plan best = *p;
+    double us;
+    Int4Split s = int4_auto(best, dev, &us);
+    if (p->NT == 2 && p->Mq <= kInt4MaxShortRows) {
+        Int4Plan p1 = *p;
+        int4_layout(&p1, 1);
+        double us1;
+        const Int4Split s1 = int4_auto(p1, dev, &us1);
+        if (s1.whole && us1 < us) best = p1, s = s1;
     }
-    return {int(requested == 0 ? W : requested < 65535 ? requested : 65535), false, p.rings, p.lanes};
+    if (requested == 0 || (s.whole && requested == s.workers)) {
+        *p = best;
+        return s;
+    }
+    return {requested < 65535 ? requested : 65535, false, p->rings, p->lanes};
 }
 
 size_t int4_part_rows(const Int4Plan &p, const Int4Split &s) {
@@ -204,6 +231,8 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
         return GQA_ERR_ALIGNMENT;
     int dev = 0;
     if (!host_current_device(&dev)) return GQA_ERR_CUDA;
+    const Int4Split split = int4_split(&p, num_splits, dev);
+    const int workers = split.workers;
     CUtensorMap k_map = {}, v_map = {}, p_map = {};
     const long long rows = (long long)num_pages * page_size;
     const int smem = int4_smem(dev, p);
@@ -215,8 +244,6 @@ extern "C" gqa_status gqa_decode_paged_int4(const void *q, const void *k_pool, c
         cudaGetLastError();
         return GQA_ERR_CUDA;
     }
-    const Int4Split split = int4_split(p, num_splits, dev);
-    const int workers = split.workers;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const size_t need = int4_workspace(p, split);
     void *ws = workspace;
@@ -336,7 +363,7 @@ extern "C" int gqa_decode_paged_int4_num_splits(int B, int Sq, int Hq, int Hkv, 
     if (st != GQA_OK) return -int(st);
     int dev = 0;
     if (!host_current_device(&dev)) return -int(GQA_ERR_CUDA);
-    return int4_split(p, 0, dev).workers;
+    return int4_split(&p, 0, dev).workers;
 }
 
 extern "C" size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, int page_size,
@@ -345,5 +372,6 @@ extern "C" size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, i
     if (plan_int4(B, Sq, Hq, Hkv, D, page_size, pages_per_req, 1, &p) != GQA_OK || num_splits < 0) return 0;
     int dev = 0;
     if (!host_current_device(&dev)) return 0;
-    return int4_workspace(p, int4_split(p, num_splits, dev));
+    const Int4Split split = int4_split(&p, num_splits, dev);
+    return int4_workspace(p, split);
 }

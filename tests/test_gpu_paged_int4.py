@@ -382,7 +382,8 @@ def test_empty_requests(gq, lens):
 
 @pytest.mark.parametrize("shape", [(1, 1, 8, 2, 64, 16, 500), (3, 1, 32, 8, 128, 16, 130), (2, 4, 32, 8, 128, 32, 64), (7, 2, 16, 1, 64, 8, 250),
                                    (170, 1, 16, 8, 128, 16, 90), (400, 1, 8, 2, 64, 16, 100), (700, 1, 3, 1, 64, 16, 70), (320, 3, 8, 2, 128, 16, 40),
-                                   (1300, 1, 4, 2, 64, 5, 33), (5, 1, 8, 8, 64, 5, 96), (900, 1, 2, 1, 128, 4, 32)],
+                                   (1300, 1, 4, 2, 64, 5, 33), (5, 1, 8, 8, 64, 5, 96), (900, 1, 2, 1, 128, 4, 32),
+                                   (4, 5, 8, 2, 128, 16, 60), (3, 1, 30, 1, 64, 16, 90), (200, 2, 24, 3, 128, 8, 30), (6, 8, 16, 4, 64, 3, 50)],
                          ids=lambda s: "b%d_sq%d_h%dx%d_d%d_ps%d_kv%d" % s)
 def test_short_requests_whole(gq, shape):
     """Short requests, which the automatic choice leaves to one worker each: no workspace, as many requests as CTAs and
