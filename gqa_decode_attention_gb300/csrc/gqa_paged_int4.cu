@@ -161,7 +161,8 @@ Int4Split int4_auto(const Int4Plan &p, int dev, double *us) {
 // More than 8 rows a head: 16 of them a warp turn a step's codes into operands
 // once for all, 8 of them start and end a request sooner.  Long walks are 8 to
 // 10 % faster with 16, short whole requests 20 to 30 % with 8 (22 requests of 11
-// tokens, 15 rows a head of 128, 7.6 against 6.1 us).
+// tokens, 15 rows a head of 128, 7.6 against 6.1 us), and shares of up to three
+// steps an SM 3 to 8 %.
 Int4Split int4_split(Int4Plan *p, int requested, int dev) {
     Int4Plan best = *p;
     double us;
@@ -171,9 +172,9 @@ Int4Split int4_split(Int4Plan *p, int requested, int dev) {
         int4_layout(&p1, 1);
         double us1;
         const Int4Split s1 = int4_auto(p1, dev, &us1);
-        if (s1.whole && us1 < us) best = p1, s = s1;
+        if (s1.whole ? us1 < us : !s.whole && p->max_steps < 3LL * int4_ctas(*p, dev)) best = p1, s = s1;
     }
-    if (requested == 0 || (s.whole && requested == s.workers)) {
+    if (requested == 0 || requested == s.workers) {
         *p = best;
         return s;
     }
