@@ -469,7 +469,8 @@ size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int
  * Device-checked (GQA_ERR_DEVICE_INDEX in the device error word): a token
  *   whose position is outside the request's pages or past max_pos is skipped
  *   whole; one whose page id is out of range gets its q_out row only.  Two
- *   tokens sent to the same slot leave one of the two, unspecified which.
+ *   tokens sent to the same slot leave pieces of either there, and nothing else
+ *   is touched.
  * ------------------------------------------------------------------------ */
 gqa_status gqa_paged_append(const void *q, long long q_stride, void *q_out, const void *k, long long k_stride,
                             const void *v, long long v_stride, int kv_dtype, void *k_pool, void *v_pool,

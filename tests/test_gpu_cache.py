@@ -418,3 +418,20 @@ def test_on_a_given_stream(gq):
     assert same(got, want) and same(a["k_pool"], b["k_pool"])
     k2, v2 = gq.gqa_paged_gather(a["k_pool"], a["v_pool"], a["table"], a["lens"], rows=60, k_scale=0.5, v_scale=0.5)
     assert same(k, k2) and same(v, v2)
+
+
+def test_same_slot_of_two_requests(gq):
+    """Two tokens sent to one slot: whatever lies there after comes from either of them, and no other slot changes."""
+    g = torch.Generator().manual_seed(27)
+    k, v = (torch.randn(2, 2, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    k_pool, v_pool = (torch.randn(4, 8, 2, 64, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    before = k_pool.clone(), v_pool.clone()
+    table = torch.tensor([[2], [2]], dtype=torch.int32).cuda()
+    lens = torch.tensor([5, 5], dtype=torch.int32).cuda()
+    gq.gqa_paged_append(k, v, k_pool, v_pool, table, lens)
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 0
+    for pool, old, x in ((k_pool, before[0], k), (v_pool, before[1], v)):
+        assert torch.all((pool[2, 4] == x[0]) | (pool[2, 4] == x[1]))
+        pool[2, 4] = old[2, 4]
+        assert torch.equal(pool, old)

@@ -153,6 +153,18 @@ def test_bad_pages_and_lengths_are_flagged(gq):
     check(d, out, lse)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_requests_that_share_pages(gq, splits):
+    """Requests with the same pages (a common prefix), one of them with the same page more than once."""
+    d = make(4, 1, 16, 4, 128, 16, [200, 200, 200, 200], seed=23)
+    d["table"][1] = d["table"][0]
+    d["table"][2, :9] = d["table"][0, :9]
+    d["table"][3] = d["table"][3, 2]
+    out, lse = run(gq, d, num_splits=splits)
+    assert gq.gqa_device_status() == 0
+    check(d, out, lse)
+
+
 def test_all_pages_bad(gq):
     d = make(1, 2, 8, 2, 64, 16, [100], seed=9)
     d["table"][:] = -1
