@@ -4,9 +4,10 @@
 // Mathematics.  With codes u in 0..15 and a token's own scale and zero,
 // K^_t = u_t ks_t + kz_t and V^_t = v_t vs_t + vz_t, a row's scores and output are
 //   s_t = scale (ks_t sum_d q_d u_td + kz_t sum_d q_d)
-//   O_d = (sum_t p_t vs_t v_td + sum_t p_t vz_t) / sum_t p_t,  p_t = e^(s_t).
-// So the tensor cores multiply plain codes: q.u, and (p vs).v; scale and zero
-// of K enter the scores, those of V the weights and one extra sum a row.
+//   O_d = (sum_t p_t vs_t (v_td - 8) + sum_t p_t (vz_t + 8 vs_t)) / sum_t p_t,  p_t = e^(s_t).
+// So the tensor cores multiply plain codes: q.u, and (p vs).v, whose sums start
+// at -8 sum p vs; scale and zero of K enter the scores, those of V the weights
+// and one extra sum a row.
 //
 // What bounds it.  A token costs 2 (D/2 + 4) bytes per KV head, a quarter of a
 // bf16 cache, so the walk must turn codes into operands at four times the
@@ -27,7 +28,11 @@
 // What is rounded.  q (bf16) is exact in fp16 after a power of two that is
 // taken from the row's largest element, down to 2^-27 of that.  The codes are
 // exact.  p vs is rounded to fp16, half a step of which is 2^-11, an eighth of
-// the bf16 output's; everything that is summed is summed in fp32.
+// the bf16 output's.  That rounding counts by what a weight is multiplied with:
+// the code's distance from the middle, which is of the size of V's spread
+// (against the code itself, three times that, the output's error against 64
+// bits was 1.7e-3 to 1.79e-3 where its own rounding is 1.64e-3 to 1.67e-3).
+// Everything that is summed is summed in fp32.
 //
 // Layout.  As in the other paged kernels a CTA takes a block of KV heads and a
 // worker's share of all requests' steps (here of 32 tokens).  One CTA fills an
@@ -210,6 +215,15 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// d = A * B + c
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
 __device__ __forceinline__ void mma_f16_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -328,6 +342,7 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
     constexpr int DB = D / 16;      // output blocks: block j holds elements (D/8) gi + 2 j, + 2 j + 1
     constexpr int CW = int4_consumers(NT);
     constexpr uint32_t M0 = 0x000f000fu, M = 0x00ff00ffu;
+    constexpr uint32_t kMinus8 = 0x80088008u, kMinus136 = 0x80888088u;  // in units of 2^-24, as the codes
     extern __shared__ __align__(1024) uint8_t smem4[];
     Int4Head *head = reinterpret_cast<Int4Head *>(smem4);
     volatile int *abort_flag = &head->abort;
@@ -787,6 +802,8 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         }
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) vz[j] = fmaf(8.f, vs[j], vz[j]);  // the value of V's middle code
             // Weights of V as fp16 pairs (rows 2 c, 2 c + 1), the step's sums of
             // p and p vz, and the largest weight.
             uint32_t wt[NT][4], top = 0;
@@ -857,6 +874,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) wt[nt][j] = movmatrix_trans(wt[nt][j]);
             }
+            // what the sums start from: every code 8 less, every whole byte 8 + 16 x 8
+            float middle[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_zero(middle[nt], kMinus8, kMinus136, kMinus8, kMinus136, wt[nt][0], wt[nt][1]);
+                mma_f16_add(middle[nt], kMinus8, kMinus136, kMinus8, kMinus136, wt[nt][2], wt[nt][3]);
+            }
 
             uint32_t vw[8][VW];  // token pair j: tokens of columns 2 c, 2 c + 1, 8 j later
 #pragma unroll
@@ -876,10 +900,10 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             st += a.lanes;
             if (st >= a.stages) st -= a.stages, phase ^= 1;
 
-            // ---- O^T += V^T . weights, 32 tokens at a time.  The tensor cores
-            // cut off what does not fit their sums; codes are positive, so over
-            // a long walk the cuts would add up against the zeros' part, which
-            // cancels most of it.  The sum over the steps is rounded instead.
+            // ---- O^T += (V - 8)^T . weights, 32 tokens at a time.  The tensor
+            // cores cut off what does not fit their sums, always towards zero,
+            // so over a long walk the cuts would add up.  The sum over the
+            // steps is rounded instead.
 #pragma unroll
             for (int w = 0; w < VW; ++w)
 #pragma unroll
@@ -897,8 +921,8 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                         for (int nt = 0; nt < NT; ++nt) {
                             const uint32_t b0 = wt[nt][2 * t], b1 = wt[nt][2 * t + 1];
                             if (t == 0) {
-                                mma_f16_zero(sum[nt][0], x & M0, x & M, y & M0, y & M, b0, b1);
-                                mma_f16_zero(sum[nt][1], x8 & M0, x8, y8 & M0, y8, b0, b1);
+                                mma_f16_from(sum[nt][0], middle[nt], x & M0, x & M, y & M0, y & M, b0, b1);
+                                mma_f16_from(sum[nt][1], middle[nt], x8 & M0, x8, y8 & M0, y8, b0, b1);
                             } else {
                                 mma_f16_add(sum[nt][0], x & M0, x & M, y & M0, y & M, b0, b1);
                                 mma_f16_add(sum[nt][1], x8 & M0, x8, y8 & M0, y8, b0, b1);

@@ -485,3 +485,40 @@ def test_wait_that_runs_out_on_whole_requests(gq, shape):
     again = run(gq, d)
     assert gq.gqa_device_status() == 0
     assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+
+
+def test_weight_roundings_cancel_in_a_flat_value(gq):
+    """V's codes all 8 with a zero of -8 scales: every element is 0 whatever the weights are.  A weight's fp16 rounding
+    (2^-11) counts by the code's distance from 8, here 0; what is left are fp32 sums, within 2^-17 of the largest
+    magnitude that they could hold, 15 scales and the zero."""
+    for shape in ((3, 1, 32, 8, 128, 16, [4, 9, 300]), (2, 4, 16, 2, 64, 16, [70, 7])):
+        d = make(*shape[:6], shape[6], seed=41)
+        p = d["params"]
+        d["v_pool"].fill_(0x88)
+        p[..., 3] = -8 * p[..., 2]
+        for splits in (0, 1, 4):
+            out, lse = run(gq, d, num_splits=splits)
+            for b, n in enumerate(shape[6]):
+                at = ref.slots(d["table"][b], shape[5], range(n))
+                top = float(p.flatten(0, 1)[at][..., 2].double().max())
+                assert float(out[b].double().abs().max()) <= 2.0 ** -17 * 23 * top, (shape, splits, b)
+
+
+def test_error_is_the_outputs_rounding(gq):
+    """Root mean square error against 64 bits on N(0, 1) entries, beside that of the 64-bit result rounded to bf16.  A
+    weight's rounding is at most 2^-11, 2^-11 / sqrt(3) in the mean square; a row of 128 normal values spans at most 7.5
+    of its deviations, so that a code's distance from 8 is in the mean square at most 1.25 deviations (codes spread
+    as the values do, their middle off by up to 0.75).  Against an output of one deviation's scale that is 1.25 x
+    2.82e-4 = 3.53e-4 beside the rounding's 1.6e-3 or more: at most sqrt(1 + 0.22^2) = 1.024 of it."""
+    d = make(4, 1, 32, 8, 128, 16, [300, 900, 2000, 500], seed=42)
+    out, _ = run(gq, d)
+    want = torch.zeros(out.shape, dtype=torch.float64)
+    for b in range(4):
+        n = int(d["lens"][b])
+        at = ref.slots(d["table"][b], 16, range(n))
+        p = d["params"].flatten(0, 1)[at]
+        want[b, 0], _ = ref.attend(d["q"][b, 0], ref.value_int4(d["k_pool"].flatten(0, 1)[at], p[..., :2]),
+                                   ref.value_int4(d["v_pool"].flatten(0, 1)[at], p[..., 2:]), n)
+    own = float((out.double() - want).square().mean().sqrt())
+    rounding = float((want.to(torch.bfloat16).double() - want).square().mean().sqrt())
+    assert own <= 1.03 * rounding, (own, rounding)
