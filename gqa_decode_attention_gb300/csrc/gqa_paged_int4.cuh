@@ -776,12 +776,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
                 vs[j] = max_nan(v2.x, 5.9604644775390625e-8f);  // fp16's smallest: a weight of 0 would hide its score
                 vz[j] = v2.y;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &y = acc[nt][j >> 1][2 * (j & 1) + e];
-                        y = fmaf(y, k2.x, k2.y * qs[nt][e]);
-                    }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float *y = &acc[nt][j >> 1][2 * (j & 1)];
+                    // rounded here, so that a score less itself is 0 at any size
+                    const float2 x = mul2(make_float2(fmaf(y[0], k2.x, k2.y * qs[nt][0]), fmaf(y[1], k2.x, k2.y * qs[nt][1])),
+                                          make_float2(A[nt][0], A[nt][1]));
+                    y[0] = x.x, y[1] = x.y;
+                }
             }
             if (mask != 0xffffffffu || left <= n_causal) {  // tokens that are not there, or not seen by all rows
                 const int s0 = (seg_next - seg_p - left) * kInt4Step;  // the step's first token
@@ -816,9 +817,11 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float p[2];
+                        const float2 d = add2(make_float2(acc[nt][j >> 1][2 * (j & 1)], acc[nt][j >> 1][2 * (j & 1) + 1]),
+                                              make_float2(-R_[nt][0], -R_[nt][1]));
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            p[e] = fast_exp2(fmaf(acc[nt][j >> 1][2 * (j & 1) + e], A[nt][e], -R_[nt][e]));
+                            p[e] = fast_exp2(e == 0 ? d.x : d.y);
                             sp[nt][e] += p[e];
                             sz[nt][e] = fmaf(p[e], vz[j], sz[nt][e]);
                         }
@@ -842,7 +845,12 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float y = acc[nt][j >> 1][2 * (j & 1) + e];
-                            if (vs[j] > 0.f && vs[j] <= 65504.f) m = fmaxf(m, fmaf(y, A[nt][e], log2f(vs[j]) - kInt4Top));
+                            if (!(vs[j] > 0.f && vs[j] <= 65504.f)) continue;
+                            const float top_j = log2f(vs[j]) - kInt4Top;
+                            float m_j = y + top_j;
+                            // a score of 2^28 has steps of 32: rounded down, the weight could pass fp16
+                            if (y - m_j > 8.f - top_j) m_j = __fadd_ru(y, top_j);
+                            m = fmaxf(m, m_j);
                         }
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));

@@ -522,3 +522,33 @@ def test_error_is_the_outputs_rounding(gq):
     own = float((out.double() - want).square().mean().sqrt())
     rounding = float((want.to(torch.bfloat16).double() - want).square().mean().sqrt())
     assert own <= 1.03 * rounding, (own, rounding)
+
+
+@pytest.mark.parametrize("e,gain", [(18, 1.0), (21, 2.0 ** -9), (22, 2.0 ** -9), (23, 2.0 ** -9), (24, 1.0), (27, 1.0), (60, 1.0), (115, 1.0)])
+def test_large_scores(gq, e, gain):
+    """Scores of 2^e to 2^(e + 7) leave the weight to one token, however far below the next one is in fp32's steps.  The
+    LSE is the largest score within (D + 8) 2^-23 of the magnitudes summed, the output that token's V, rounded to bf16
+    (2^-8 of itself; the weight's rounding 2^-11 of 8 scales, fp32 sums 2^-17 of 15 scales and the zero).  (At 2^28 fp32
+    has steps of 32, while an fp16 weight has room for 2^15 above 1: small V scales are where they could leave it.)"""
+    D, n = 128, 200
+    d = make(1, 1, 4, 2, D, 16, [n], seed=45, v_gain=gain)
+    d["q"] = torch.randint(1, 4, d["q"].shape, generator=torch.Generator().manual_seed(46)).float().to(torch.bfloat16) * 2.0 ** e
+    scale = 1.0
+    out, lse = run(gq, d, scale=scale, num_splits=3)
+    assert gq.gqa_device_status() == 0
+    at = ref.slots(d["table"][0], 16, range(n))
+    p = d["params"].flatten(0, 1)[at]
+    k, v = ref.value_int4(d["k_pool"].flatten(0, 1)[at], p[..., :2]), ref.value_int4(d["v_pool"].flatten(0, 1)[at], p[..., 2:])
+    mag = float((15 * p[..., 0].double() + p[..., 1].double().abs()).max())
+    for h in range(4):
+        q = d["q"][0, 0, h].double()
+        s = k[:, h // 2] @ q * scale
+        best = int(s.argmax())
+        bound = (D + 8) * 2.0 ** -23 * mag * float(q.sum()) * scale
+        second = float(s.sort().values[-2])
+        assert float(s[best]) - second > 4 * bound  # the data: one token stands alone
+        assert abs(float(lse[0, h, 0]) - float(s[best])) <= bound
+        want = v[best, h // 2]
+        vs = float(p[best, h // 2, 2])
+        v_mag = 15 * vs + abs(float(p[best, h // 2, 3]))
+        assert torch.all((out[0, 0, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 8 * vs + 2.0 ** -17 * v_mag)
