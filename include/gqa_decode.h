@@ -402,7 +402,8 @@ size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, i
  *   taken as 2^-24, which changes an element by less than 1e-6.
  * q, out, lse, page_table, seq_lens, scale, causal rows, empty rows (out = 0,
  *   lse = -inf) and device checks as gqa_decode_paged.  A row whose scores are
- *   NaN gives NaN, a row that sees a token with a NaN or infinite parameter a
+ *   NaN gives NaN, and so does one with an infinite query element or whose
+ *   largest one times scale passes 2^117; a row that sees a token with a NaN or infinite parameter a
  *   result that is not finite; other rows are not touched by either, and what
  *   the pools hold in slots past a request's length is never used.
  * Limits: D in {64, 128}; (Hq / Hkv) * Sq <= 128; pages_per_req * page_size

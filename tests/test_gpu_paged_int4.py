@@ -552,3 +552,26 @@ def test_large_scores(gq, e, gain):
         vs = float(p[best, h // 2, 2])
         v_mag = 15 * vs + abs(float(p[best, h // 2, 3]))
         assert torch.all((out[0, 0, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 8 * vs + 2.0 ** -17 * v_mag)
+
+
+def test_queries_past_the_range_give_nan(gq):
+    """A row with an infinite query element, or one whose scale times its largest element passes 2^117, is NaN where it
+    sees a token and empty where it does not; finite rows up to there are right.  (All K values are below 0 or all
+    above, so that no score is NaN by itself.)"""
+    for sign in (1.0, -1.0):
+        d = make(2, 2, 8, 2, 128, 16, [300, 1], seed=44)
+        d["params"][..., 0] = 0.25
+        d["params"][..., 1] = 0.5 if sign > 0 else -4.5
+        d["q"] = d["q"].abs()
+        clean = run(gq, d, num_splits=3)
+        bad = {**d, "q": d["q"].clone()}
+        bad["q"][0, 0, 3, 17] = float("inf")
+        bad["q"][0, 1, 4, 9] = -float("inf")
+        bad["q"][0, 1, 6, 9] = 3e38
+        bad["q"][1, :, 2, 64] = float("inf")  # the first row of request 1 sees nothing
+        out, lse = run(gq, bad, num_splits=3)
+        hit = torch.zeros(2, 2, 8, dtype=torch.bool)
+        hit[0, 0, 3] = hit[0, 1, 4] = hit[0, 1, 6] = hit[1, 1, 2] = True
+        lse, was = lse.permute(0, 2, 1), clean[1].permute(0, 2, 1)
+        assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+        assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], was[~hit])
