@@ -199,6 +199,12 @@ __device__ __forceinline__ bool above_2_15(uint32_t x) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
     return fmaxf(f.x, f.y) > 32768.f;
 }
+// x + 0 x + 0 y, half by half: x where both are finite, else NaN.
+__device__ __forceinline__ uint32_t nan_unless_finite(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tfma.rn.f16x2 t, %1, %3, %1;\n\tfma.rn.f16x2 %0, %2, %3, t;\n\t}" : "=r"(r) : "r"(x), "r"(y), "r"(0u));
+    return r;
+}
 // Larger of x and y; a NaN stays one.
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
@@ -775,7 +781,9 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             float vs[4], vz[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].x));
+                // a token with a NaN or infinite parameter has a score of NaN, so that no weight of 0 hides it
+                const uint32_t pk = nan_unless_finite(par[j].x, par[j].y);
+                const float2 k2 = __half22float2(*reinterpret_cast<const __half2 *>(&pk));
                 const float2 v2 = __half22float2(*reinterpret_cast<const __half2 *>(&par[j].y));
                 vs[j] = max_nan(v2.x, 5.9604644775390625e-8f);  // fp16's smallest: a weight of 0 would hide its score
                 vz[j] = v2.y;
@@ -793,17 +801,17 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const bool there = (mask >> (tok0 + 8 * j)) & 1u;
-                    // a weight of 0 does not hide a NaN or infinity of V from the
-                    // rows that do not see its token: those that do get it by the score
-                    const bool odd = there && !(fmaxf(vs[j], fabsf(vz[j])) <= 65504.f && vs[j] == vs[j] && vz[j] == vz[j]);
-                    if (!there || odd) vs[j] = vz[j] = 0.f;  // a slot that is not there may hold anything
+                    // a slot that is not there may hold anything; a NaN or infinity of V would pass a weight of
+                    // 0 in the rows that do not see its token, and those that do have it by the score
+                    const bool odd = !(fmaxf(vs[j], fabsf(vz[j])) <= 65504.f && vs[j] == vs[j] && vz[j] == vz[j]);
+                    if (!there || odd) vs[j] = vz[j] = 0.f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int r = (rg * NT + nt) * 8 + 2 * c + e;
                             const bool seen = there && s0 + tok0 + 8 * j <= len - a.Sq + (r < a.Mq ? row_of(r) : a.Sq);
-                            if (!seen || odd) acc[nt][j >> 1][2 * (j & 1) + e] = seen ? NAN : -INFINITY;
+                            if (!seen) acc[nt][j >> 1][2 * (j & 1) + e] = -INFINITY;
                         }
                 }
             }

@@ -401,11 +401,12 @@ size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, i
  *   Scales are >= 0; a V scale below 2^-24 (the smallest fp16 value: 0) is
  *   taken as 2^-24, which changes an element by less than 1e-6.
  * q, out, lse, page_table, seq_lens, scale, causal rows, empty rows (out = 0,
- *   lse = -inf) and device checks as gqa_decode_paged.  A row whose scores are
- *   NaN gives NaN, and so does one with an infinite query element or whose
- *   largest one times scale passes 2^117; a row that sees a token with a NaN or infinite parameter a
- *   result that is not finite; other rows are not touched by either, and what
- *   the pools hold in slots past a request's length is never used.
+ *   lse = -inf) and device checks as gqa_decode_paged.  A row is
+ *   NaN, its LSE too, where its scores are NaN, where a query element of it is
+ *   infinite or, times scale, 2^117 or more (scores may then leave fp32's range),
+ *   and where a token that it sees has a NaN or infinite parameter, whatever
+ *   that token would weigh.  Other rows are not touched by that, and what the
+ *   pools hold in slots past a request's length is never used.
  * Limits: D in {64, 128}; (Hq / Hkv) * Sq <= 128; pages_per_req * page_size
  *   <= 2^31 - 256, and B times it (rounded up to 32) < 2^36; the rest as
  *   gqa_decode_paged.  kv_params 16-byte aligned.

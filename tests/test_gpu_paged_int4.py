@@ -575,3 +575,30 @@ def test_queries_past_the_range_give_nan(gq):
         lse, was = lse.permute(0, 2, 1), clean[1].permute(0, 2, 1)
         assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
         assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], was[~hit])
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("which", [0, 1, 2, 3])
+def test_parameters_that_are_not_finite_give_nan(gq, which, value, splits):
+    """A row that sees a token with a NaN or infinite parameter is NaN, its LSE too, whatever that token weighs: the
+    query sums are positive and the token's K is -30, hundreds of nats below the others, unless its own K parameter is the
+    one.  Early in the request (a step that all rows see whole) and in its last step; any number of workers."""
+    d = make(2, 3, 16, 2, 128, 16, [900, 500], seed=43)
+    d["q"] = d["q"].abs()
+    at = lambda b, t: int(ref.slots(d["table"][b], 16, [t])[0])  # noqa: E731
+    flat = d["params"].view(-1, 2, 4)
+    places = [(0, 100, 0), (1, 499, 1)]  # seen by all rows of request 0; by the last one of request 1
+    for b, t, g in places:
+        flat[at(b, t), g, :2] = torch.tensor([0.0, -30.0]).half()
+    clean = run(gq, d, num_splits=splits)
+    assert torch.isfinite(clean[0]).all() and torch.isfinite(clean[1]).all()
+    for b, t, g in places:
+        flat[at(b, t), g, which] = value
+    out, lse = run(gq, d, num_splits=splits)
+    assert gq.gqa_device_status() == 0
+    hit = torch.zeros(2, 3, 16, dtype=torch.bool)
+    hit[0, :, :8] = hit[1, 2, 8:] = True
+    lse, was = lse.permute(0, 2, 1), clean[1].permute(0, 2, 1)
+    assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], was[~hit])
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
