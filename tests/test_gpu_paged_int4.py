@@ -602,3 +602,19 @@ def test_parameters_that_are_not_finite_give_nan(gq, which, value, splits):
     lse, was = lse.permute(0, 2, 1), clean[1].permute(0, 2, 1)
     assert torch.equal(out[~hit], clean[0][~hit]) and torch.equal(lse[~hit], was[~hit])
     assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 24, 1, 64, 16, (3001,)), (2, 1, 20, 1, 128, 5, (900, 33)), (2, 1, 24, 1, 128, 16, (5000, 2047)),
+                                   (1, 6, 3, 1, 64, 8, (2500,))],
+                         ids=lambda s: "b%d_sq%d_h%dx%d_d%d_ps%d" % s[:6])
+def test_five_groups_on_one_ring(gq, shape):
+    """One KV head of 17 to 24 rows, 8 rows a warp: three warps a group, five groups that take turns at one ring of 15
+    stages, and one warp without work; shares of all steps (there is a workspace)."""
+    d = make(*shape[:6], list(shape[6]), seed=200 + sum(shape[:6]))
+    assert gq.gqa_decode_paged_int4_workspace_bytes(*shape[:6], d["table"].shape[1]) > 0
+    first = run(gq, d)
+    assert gq.gqa_device_status() == 0
+    check(d, *first, what=str(shape))
+    for _ in range(3):
+        again = run(gq, d)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
