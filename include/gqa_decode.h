@@ -454,10 +454,11 @@ size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int
  *   GQA_KV_FP8_E4M3FN  e4m3(x * (1 / scale)), saturated at +-448, NaN kept
  *   GQA_KV_INT8        nearest even of x * (1 / scale), clamped to +-127, NaN as 0
  *   GQA_KV_INT4        per token and head (x clamped to the fp16 range, NaN as
- *                      0): zero = fp16(min x), scale = fp16((max x - zero) / 15),
- *                      code = nearest even of (x - zero) * (1 / scale), clamped to 0..15
- *                      (all 0 when the scale is 0), into kv_params as for
- *                      gqa_decode_paged_int4.
+ *                      0): zero = fp16(min x), scale = fp16((max x - zero) * c15) with
+ *                      c15 = fp32(1 / 15) (a product, which is not the quotient by 15 for
+ *                      some rows), code = nearest even of (x - zero) * (1 / scale), clamped
+ *                      to 0..15 (all 0 when the scale is 0), every step in fp32, into
+ *                      kv_params as for gqa_decode_paged_int4.
  * 8-bit pools take host scales k_scale, v_scale (finite, > 0) or, with
  * k_scales and v_scales non-NULL, n_scales (1 or Hkv) device scales each.
  *

@@ -435,3 +435,23 @@ def test_same_slot_of_two_requests(gq):
         assert torch.all((pool[2, 4] == x[0]) | (pool[2, 4] == x[1]))
         pool[2, 4] = old[2, 4]
         assert torch.equal(pool, old)
+
+
+def test_four_bit_scale_is_a_product(gq):
+    """The scale is fp16 of (max - zero) times fp32's 1/15, which differs from fp16 of the quotient for some rows."""
+    pairs = [(0.271484375, -0.00099945068359375), (0.55859375, -0.0010223388671875), (0.322265625, -0.00102996826171875),
+             (1.1328125, -0.001068115234375)]
+    x = torch.zeros(4, 1, 64, dtype=torch.bfloat16)
+    for i, (high, low) in enumerate(pairs):
+        x[i, 0, 5], x[i, 0, 40] = high, low
+    high, low = torch.tensor(pairs).T
+    assert torch.equal(x[:, 0].float().amax(-1), high) and torch.equal(low.half().float(), low)
+    scale = ((high - low) * (torch.tensor(1.0) / 15)).half()
+    assert torch.all(scale != ((high - low) / 15).half())
+    pool = torch.zeros(1, 16, 1, 32, dtype=torch.uint8, device="cuda")
+    params = torch.zeros(1, 16, 1, 4, dtype=torch.float16, device="cuda")
+    gq.gqa_paged_append(x.cuda(), x.cuda(), pool, pool.clone(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                        torch.tensor([4], dtype=torch.int32, device="cuda"), kv_params=params)
+    want = torch.stack([scale, low.half(), scale, low.half()], -1)
+    assert gq.gqa_device_status() == 0
+    assert same(params[0, :4, 0], want)
