@@ -470,10 +470,10 @@ size_t gqa_decode_paged_int4_workspace_bytes(int B, int Sq, int Hq, int Hkv, int
  * Limits: D in {64, 128}; rot_dim a multiple of 16, at most D; T >= 0; page
  *   limits as gqa_decode_paged.
  * Device-checked (GQA_ERR_DEVICE_INDEX in the device error word): a token
- *   whose position is outside the request's pages or past max_pos is skipped
- *   whole; one whose page id is out of range gets its q_out row only.  Two
- *   tokens sent to the same slot leave pieces of either there, and nothing else
- *   is touched.
+ *   whose position is outside the request's pages or past max_pos, or whose row
+ *   lies before cu_tokens[0], is skipped whole; one whose page id is out of
+ *   range gets its q_out row only.  Two tokens sent to the same slot leave
+ *   pieces of either there, and nothing else is touched.
  * ------------------------------------------------------------------------ */
 gqa_status gqa_paged_append(const void *q, long long q_stride, void *q_out, const void *k, long long k_stride,
                             const void *v, long long v_stride, int kv_dtype, void *k_pool, void *v_pool,

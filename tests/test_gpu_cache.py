@@ -455,3 +455,19 @@ def test_four_bit_scale_is_a_product(gq):
     want = torch.stack([scale, low.half(), scale, low.half()], -1)
     assert gq.gqa_device_status() == 0
     assert same(params[0, :4, 0], want)
+
+
+def test_rows_before_the_first_request(gq):
+    """Rows before cu_tokens[0] belong to nobody: skipped whole and flagged, as the header says; the others go where
+    they belong."""
+    d = case("bf16", 2, [3, 2], [4, 0], 4, 2, 64, 16, seed=33)
+    d["qkv"] = torch.cat([torch.ones(2, *d["qkv"].shape[1:], dtype=torch.bfloat16), d["qkv"]])
+    table = ref.rope_table(32, 64)
+    q, k_pool, v_pool, _ = appended({**d, "qkv": d["qkv"][2:]}, 64, False, table)
+    c = cuda({**d, "cu": d["cu"] + 2})
+    q_out = torch.full((7, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    append(gq, d, c, table.cuda(), False, q_out=q_out)
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 7
+    assert same(c["k_pool"], k_pool) and same(c["v_pool"], v_pool)
+    assert torch.all(q_out[:2] == 3.0) and same(q_out[2:], q)
