@@ -689,11 +689,9 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // exponent of mx, kept where 2^-ex and 2^ex are normal; a row of only
-            // zeros stays as it is
-            int ex = int(__float_as_uint(mx) >> 23) - 127 - 14;
+            // exponent of mx, kept where 2^-ex and 2^ex are normal
             const bool inf = mx > 3.4e38f;
-            ex = mx == 0.f || inf ? 0 : max(ex, -100);
+            const int ex = inf ? 0 : max(int(__float_as_uint(mx) >> 23) - 127 - 14, -100);
             const float down = __uint_as_float(uint32_t(127 - ex) << 23);
             float sum = 0.f;
 #pragma unroll
@@ -711,11 +709,13 @@ __global__ void __launch_bounds__(int4_threads(NT), 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             // score in the log2 domain = A (ks acc + kz qs), acc = 2^-24 sum q u
-            // (a factor past fp32's range or an infinite query: every score NaN by
-            // the zeros' part, since scores of -inf alone would look like no token)
+            // (an infinite query, or scale * mx past 2^103: every score NaN by the
+            // zeros' part.  Up to there the least of all scores, D = 128 elements
+            // of a K of -65504, lies above -2^127.6; scores below kInt4NoRef would
+            // look like no token.)
             const float factor = a.alpha * __uint_as_float(uint32_t(127 + ex) << 23) * 16777216.f;
             const float row_a = fmaxf(factor, 1e-37f);
-            const float row_qs = inf || factor > 3.4e38f ? NAN : sum * (1.f / 16777216.f);
+            const float row_qs = inf || factor > 1.4982e34f ? NAN : sum * (1.f / 16777216.f);  // log2(e) 2^113
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // rows of this lane's scores: 2 c + e
                 A[nt][e] = __shfl_sync(0xffffffffu, row_a, 4 * (2 * c + e));

@@ -403,7 +403,7 @@ size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, i
  * q, out, lse, page_table, seq_lens, scale, causal rows, empty rows (out = 0,
  *   lse = -inf) and device checks as gqa_decode_paged.  A row is
  *   NaN, its LSE too, where its scores are NaN, where a query element of it is
- *   infinite or, times scale, 2^117 or more (scores may then leave fp32's range),
+ *   infinite or, times scale, past 2^103 (up to 2^104 it may still be right),
  *   and where a token that it sees has a NaN or infinite parameter, whatever
  *   that token would weigh.  Other rows are not touched by that, and what the
  *   pools hold in slots past a request's length is never used.

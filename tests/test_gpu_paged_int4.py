@@ -524,7 +524,7 @@ def test_error_is_the_outputs_rounding(gq):
     assert own <= 1.03 * rounding, (own, rounding)
 
 
-@pytest.mark.parametrize("e,gain", [(18, 1.0), (21, 2.0 ** -9), (22, 2.0 ** -9), (23, 2.0 ** -9), (24, 1.0), (27, 1.0), (60, 1.0), (115, 1.0)])
+@pytest.mark.parametrize("e,gain", [(18, 1.0), (21, 2.0 ** -9), (22, 2.0 ** -9), (23, 2.0 ** -9), (24, 1.0), (27, 1.0), (60, 1.0), (101, 1.0)])
 def test_large_scores(gq, e, gain):
     """Scores of 2^e to 2^(e + 7) leave the weight to one token, however far below the next one is in fp32's steps.  The
     LSE is the largest score within (D + 8) 2^-23 of the magnitudes summed, the output that token's V, rounded to bf16
@@ -555,7 +555,7 @@ def test_large_scores(gq, e, gain):
 
 
 def test_queries_past_the_range_give_nan(gq):
-    """A row with an infinite query element, or one whose scale times its largest element passes 2^117, is NaN where it
+    """A row with an infinite query element, or one whose scale times its largest element passes 2^104, is NaN where it
     sees a token and empty where it does not; finite rows up to there are right.  (All K values are below 0 or all
     above, so that no score is NaN by itself.)"""
     for sign in (1.0, -1.0):
@@ -618,3 +618,38 @@ def test_five_groups_on_one_ring(gq, shape):
     for _ in range(3):
         again = run(gq, d)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_least_scores(gq, D):
+    """All K at fp16's lowest value and queries as large as they may be: scores near fp32's lowest are scores, past the
+    limit NaN, never a row without tokens.  Queries of zero take any scale.  (Workers' results are joined by their LSEs,
+    which at -65504 x 64 and below have steps of 0.25 and more: how many of the 100 equal tokens a worker had is lost in
+    them, by any factor from there on, so that several workers give some mean of the tokens.)"""
+    d = make(1, 1, 8, 2, D, 16, [100], seed=47)
+    d["params"][..., 0] = 0.0
+    d["params"][..., 1] = -65504.0
+    at = ref.slots(d["table"][0], 16, range(100))
+    each = ref.value_int4(d["v_pool"].flatten(0, 1)[at], d["params"].flatten(0, 1)[at][..., 2:])
+    v = each.mean(0)  # equal weights
+    tops = [2.0 ** 60, 1.5 * 2.0 ** 103, 2.0 ** 104, 2.0 ** 120, 2.0 ** 127, 0.0, 1.0, 2.0 ** 102]
+    d["q"] = torch.tensor(tops).view(1, 1, 8, 1).expand(1, 1, 8, D).to(torch.bfloat16).contiguous()
+    for splits in (0, 3):
+        out, lse = run(gq, d, scale=1.0, num_splits=splits)
+        for h, x in enumerate(tops):
+            if x >= 2.0 ** 104:
+                assert torch.isnan(out[0, 0, h]).all() and torch.isnan(lse[0, h, 0]), h
+                continue
+            s = -65504.0 * D * x + math.log(100)
+            # 64 fp32 terms and their scale; V: 15 scales and the zero as in check()
+            assert abs(float(lse[0, h, 0]) - s) <= (D + 8) * 2.0 ** -23 * abs(s) + 2.0 ** -17, h
+            want = v[h // 4]
+            if splits > 1 and x > 0:
+                low, high = each[:, h // 4].amin(0), each[:, h // 4].amax(0)
+                want = torch.minimum(torch.maximum(out[0, 0, h].double(), low), high)
+            assert torch.all((out[0, 0, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 3 + 2.0 ** -17 * 10), h
+    d["q"].zero_()
+    for scale in (2.0 ** 60, 2.0 ** 120):
+        out, lse = run(gq, d, scale=scale)
+        assert torch.all((lse.double() - math.log(100)).abs() <= 2.0 ** -17)
+        assert torch.all((out[0, 0].double().view(2, 4, D) - v[:, None]).abs() <= 2.0 ** -8 * v.abs()[:, None] + 2.0 ** -11 * 3 + 2.0 ** -17 * 10)
