@@ -8,8 +8,8 @@
 // 16-byte pieces.  Measured on GB300: 37K prompt tokens of 64/8 heads of 128
 // into an FP8 cache 226 us, 96 % of the copy peak; one decode step of 32 such
 // requests 3.3 us; 103K tokens of 8 heads of 128 gathered from a 4-bit cache
-// 111 us -- four fifths of its bytes are writes, and a plain fill of the same
-// size takes 108 us.
+// 110 us -- four fifths of its bytes are writes, and a plain fill of the same
+// size takes 109 to 113 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

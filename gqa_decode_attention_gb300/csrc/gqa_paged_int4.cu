@@ -160,9 +160,13 @@ Int4Split int4_auto(const Int4Plan &p, int dev, double *us) {
 
 // More than 8 rows a head: 16 of them a warp turn a step's codes into operands
 // once for all, 8 of them start and end a request sooner.  Long walks are 8 to
-// 10 % faster with 16, short whole requests 20 to 30 % with 8 (22 requests of 11
-// tokens, 15 rows a head of 128, 7.6 against 6.1 us), and shares of up to three
-// steps an SM 3 to 8 %.
+// 10 % faster with 16, short whole requests 6 to 21 % with 8 (22 requests of 11
+// tokens, 15 rows a head of 128, 6.7 against 5.3 us).  Shares of up to three steps
+// an SM, measured both ways on 112 shapes: most are 3 to 14 % faster with 8 (one
+// request of 1K tokens, 16 rows for each of 8 heads of 128, 14.2 against 12.3 us);
+// up to 3 % slower are 16 rows for each of 4 heads of 128, four requests of 2K
+// tokens and 8 heads, and one request with 24 rows on one head (at 8K tokens, d 64,
+// 7 %: 11.7 against 12.5).
 Int4Split int4_split(Int4Plan *p, int requested, int dev) {
     Int4Plan best = *p;
     double us;

@@ -41,7 +41,7 @@
 // each of up to four rings of shared-memory stages, or in turns on fewer; a ring
 // is a worker.  (Of the ways tried on 32 requests of 16K to 32K tokens, 64 heads
 // over 8 of 128: several CTAs an SM whose consumers start the loads in turns
-// 177 us, a producer warp in each 155, this 145.)  Where heads and row groups are
+// 177 us, a producer warp in each 155, this 143.)  Where heads and row groups are
 // fewer than the warps, `lanes` groups take turns at a ring's steps and join
 // their results in shared memory.
 //
@@ -57,12 +57,13 @@
 // shared out: a ring takes whole ones, one launch without partial results.
 //
 // Measured on GB300 (main and merge kernel): the 32 requests above, 814 MB,
-// 145 us, 5.6 TB/s, 83 % of the copy peak -- bound by HBM and by SMs whose path
-// to memory is slower, which the shares do not know of; one request of 128K
-// tokens 43 us, of which the start is 6 and the merge 5; 256 requests of up to
-// 1K tokens 46 us, bound by the consumers' instructions and the changes of
-// request; 16 requests of 4 x 4 rows a head and up to 8K tokens 36 us, where 16
-// rows a warp make a step 1.2 us long; 40 whole requests of 256 tokens 14 us.
+// 141-146 us by box, 82 to 85 % of the copy peak -- bound by HBM and by SMs
+// whose path to memory is slower, which the shares do not know of; one request of
+// 128K tokens 44 us, of which the start is 6 and the merge 5; 256 requests of up
+// to 1K tokens 47 us, where the consumers fill half of the issue slots (ALU pipe 41
+// %, tensor pipe 22 %), wait the rest of the time and change requests; 16 requests of 4 x 4 rows a head
+// and up to 8K tokens 37 us, where 16 rows a warp make a step 1.2 us long; 40
+// whole requests of 256 tokens 14 us.
 #pragma once
 
 #include <stddef.h>
@@ -77,8 +78,7 @@ constexpr int kInt4MaxStages = 16;  // of a ring
 constexpr int kInt4MaxRings = 4;    // of a CTA; as many producer warps
 // Consumer warps of a CTA that hold NT tiles of 8 query rows, and the
 // registers a thread of theirs and of the producers' warpgroup has: together
-// what the CTA was launched with (20 warps of 96, or 12 of 168).  (12 warps of
-// 160 registers for 16 rows each were slower than 8 of 216.)  Producers that
+// what the CTA was launched with (20 warps of 96, or 12 of 168).  Producers that
 // copy rows themselves need more than those that start TMA: a spilled value
 // comes back behind all the copies under way.
 __host__ __device__ constexpr int int4_consumers(int nt) { return nt == 1 ? 16 : 8; }

@@ -407,6 +407,10 @@ size_t gqa_decode_paged_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D, i
  *   and where a token that it sees has a NaN or infinite parameter, whatever
  *   that token would weigh.  Other rows are not touched by that, and what the
  *   pools hold in slots past a request's length is never used.
+ * Rounding: a weight times its token's V scale is rounded to fp16 (2^-11) and
+ *   counts by the code's distance from 8, at most 2^-11 of 8 scales; query
+ *   elements below 2^-27 of their row's largest lose bits, 2^-35 of it at
+ *   most; all sums are fp32.
  * Limits: D in {64, 128}; (Hq / Hkv) * Sq <= 128; pages_per_req * page_size
  *   <= 2^31 - 256, and B times it (rounded up to 32) < 2^36; the rest as
  *   gqa_decode_paged.  kv_params 16-byte aligned.
