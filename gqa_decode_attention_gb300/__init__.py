@@ -39,6 +39,7 @@ EXPORTS = [
     "gqa_decode_paged_num_splits", "gqa_decode_paged_workspace_bytes", "gqa_decode_paged_dev_scales",
     "gqa_decode_paged_int4", "gqa_decode_paged_int4_num_splits", "gqa_decode_paged_int4_workspace_bytes",
     "gqa_paged_append", "gqa_paged_gather",
+    "gqa_prefill", "gqa_prefill_workspace_bytes", "gqa_prefill_paged", "gqa_prefill_paged_workspace_bytes", "gqa_merge",
     "gqa_paged_gather_fp8", "gqa_fp8_e4m3fn_to_f32", "gqa_device_status", "gqa_set_wait_limit_ns",
     "gqa_debug_set_fault_mode", "gqa_debug_set_kernel_events", "gqa_debug_read_stream",
     "gqa_decode_paged_engine", "gqa_debug_set_paged_engine",
@@ -115,6 +116,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                      + [i] * 11 + [vp])
     lib.gqa_paged_gather.restype = st
     lib.gqa_paged_gather.argtypes = [i, vp, vp, vp, f, f, vp, vp, i, vp, vp, vp, vp, vp] + [i] * 7 + [vp]
+    lib.gqa_prefill.restype = st
+    lib.gqa_prefill.argtypes = [vp, ll, vp, ll, vp, ll, vp, vp, vp, vp] + [i] * 8 + [f, vp, sz, vp]
+    lib.gqa_prefill_workspace_bytes.restype = sz
+    lib.gqa_prefill_workspace_bytes.argtypes = [i] * 6
+    lib.gqa_prefill_paged.restype = st
+    lib.gqa_prefill_paged.argtypes = [vp, ll, i, vp, vp, vp, f, f, vp, vp, i, vp, vp, vp, vp, vp] + [i] * 9 + [f, vp, sz, vp]
+    lib.gqa_prefill_paged_workspace_bytes.restype = sz
+    lib.gqa_prefill_paged_workspace_bytes.argtypes = [i] * 5
+    lib.gqa_merge.restype = st
+    lib.gqa_merge.argtypes = [vp, vp, i, vp, vp, ll, i, vp]
     lib.gqa_paged_gather_fp8.restype = st
     lib.gqa_paged_gather_fp8.argtypes = [vp, vp, vp, vp] + [i] * 7 + [vp]
     lib.gqa_fp8_e4m3fn_to_f32.restype = st
@@ -722,6 +733,151 @@ def gqa_paged_gather(k_pool, v_pool, page_table, seq_lens, k_out=None, v_out=Non
     if st:
         raise GQAError(st, fn)
     return k_out, v_out
+
+
+# ---------------------------------------------------------------------------
+# prompts: packed, over the paged cache, in parts
+# ---------------------------------------------------------------------------
+def _outputs(fn, q, T, Hq, Dv, out, lse, with_lse, stream, dev):
+    if out is None:
+        out = _new((T, Hq, Dv), torch.bfloat16, q, stream)
+    else:
+        _fit(fn, "out", out, torch.bfloat16, dev, (T, Hq, Dv))
+    if lse is not None:
+        _fit(fn, "lse", lse, torch.float32, dev, (T, Hq))
+    elif with_lse:
+        lse = _new((T, Hq), torch.float32, q, stream)
+    return out, lse
+
+
+def _workspace(fn, workspace, dev):
+    if workspace is None:
+        return 0
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"{fn}: workspace: expected a contiguous tensor on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
+
+
+def gqa_prefill(q, k, v, cu_q=None, cu_k=None, out=None, lse=None, causal=True, scale=None, workspace=None, stream=None,
+                with_lse=True):
+    """Attention over whole prompts packed one after the other.
+
+    q [Tq,Hq,Dqk], k [Tk,Hkv,Dqk], v [Tk,Hkv,Dv] bf16 on CUDA with free token strides (slices of a fused projection);
+    (Dqk, Dv) one of (64, 64), (128, 128), (192, 128).  cu_q int32 [B+1]: sequence b owns rows cu_q[b] .. cu_q[b+1]-1
+    (None: all rows are one sequence); cu_k the same for the keys (None: cu_q, or all keys).  causal: row i of n over L
+    keys sees the keys j <= L - n + i.  workspace: optional CUDA uint8 tensor of gqa_prefill_workspace_bytes.
+    Returns (out [Tq,Hq,Dv] bf16, lse [Tq,Hq] fp32 or None); rows of no sequence are left as they were.
+    """
+    lib = _lib_handle or load_library()
+    fn = "gqa_prefill"
+    dev = q.get_device()
+    guard, cs = _on_device_of(dev, stream)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"{fn}: q, k and v must be [tokens,heads,head size]")
+    Tq, Hq, Dqk = q.shape
+    Tk, Hkv, _ = k.shape
+    Dv = v.shape[2]
+    q_stride = _heads_of(fn, q, "q", Tq, Hq, Dqk, dev)
+    k_stride = _heads_of(fn, k, "k", Tk, Hkv, Dqk, dev)
+    v_stride = _heads_of(fn, v, "v", Tk, Hkv, Dv, dev)
+    B = 1
+    if cu_q is not None:
+        B = cu_q.numel() - 1
+        _fit(fn, "cu_q", cu_q, torch.int32, dev, (B + 1,))
+    if cu_k is not None:
+        if cu_q is None:
+            B = cu_k.numel() - 1
+        _fit(fn, "cu_k", cu_k, torch.int32, dev, (B + 1,))
+    out, lse = _outputs(fn, q, Tq, Hq, Dv, out, lse, with_lse, stream, dev)
+    ws_bytes = _workspace(fn, workspace, dev)
+    st = _guarded(guard, lib.gqa_prefill, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                  _data(cu_q), _data(cu_k), out.data_ptr(), _data(lse), Tq, Tk, B, Hq, Hkv, Dqk, Dv,
+                  1 if causal else 0, _scale_arg(scale), _data(workspace), ws_bytes, cs)
+    if st:
+        raise GQAError(st, fn)
+    return out, lse
+
+
+def gqa_prefill_workspace_bytes(Tq, B, Hq, Hkv, Dqk, Dv) -> int:
+    return int(load_library().gqa_prefill_workspace_bytes(Tq, B, Hq, Hkv, Dqk, Dv))
+
+
+def gqa_prefill_paged(q, k_pool, v_pool, page_table, seq_lens, cu_tokens=None, out=None, lse=None, causal=True,
+                      scale=None, kv_params=None, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None, workspace=None,
+                      stream=None, with_lse=True):
+    """Attention of new tokens over the paged cache that holds them, any number of tokens a request.
+
+    q [T,Hq,D] bf16 with a free token stride; cu_tokens int32 [B+1]: request b owns rows cu_tokens[b] ..
+    cu_tokens[b+1]-1 (None: T / B each); seq_lens int32 [B] counts the new tokens too.  causal: row i of n sees the
+    tokens j <= seq_lens[b] - n + i; else all of them.  Pools, kv_params and scales as gqa_paged_gather.  workspace:
+    optional CUDA uint8 tensor of gqa_prefill_paged_workspace_bytes.
+    Returns (out [T,Hq,D] bf16, lse [T,Hq] fp32 or None); rows of no request are left as they were.
+    """
+    lib = _lib_handle or load_library()
+    fn = "gqa_prefill_paged"
+    dev = q.get_device()
+    guard, cs = _on_device_of(dev, stream)
+    kvd, num_pages, page_size, Hkv, D, B, ppr, n_scales = _cache(fn, dev, k_pool, v_pool, kv_params, page_table, seq_lens,
+                                                                 k_scales, v_scales)
+    if q.dim() != 3:
+        raise ValueError(f"{fn}: q must be [tokens,heads,head size]")
+    T, Hq, _ = q.shape
+    q_stride = _heads_of(fn, q, "q", T, Hq, D, dev)
+    if cu_tokens is not None:
+        _fit(fn, "cu_tokens", cu_tokens, torch.int32, dev, (B + 1,))
+    out, lse = _outputs(fn, q, T, Hq, D, out, lse, with_lse, stream, dev)
+    ws_bytes = _workspace(fn, workspace, dev)
+    st = _guarded(guard, lib.gqa_prefill_paged, q.data_ptr(), q_stride, kvd, k_pool.data_ptr(), v_pool.data_ptr(),
+                  _data(kv_params), k_scale, v_scale, _data(k_scales), _data(v_scales), n_scales,
+                  page_table.data_ptr(), seq_lens.data_ptr(), _data(cu_tokens), out.data_ptr(), _data(lse), T, B, Hq,
+                  Hkv, D, page_size, ppr, num_pages, 1 if causal else 0, _scale_arg(scale), _data(workspace), ws_bytes,
+                  cs)
+    if st:
+        raise GQAError(st, fn)
+    return out, lse
+
+
+def gqa_prefill_paged_workspace_bytes(T, B, Hq, Hkv, D) -> int:
+    return int(load_library().gqa_prefill_paged_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+GQA_MERGE_MAX_PARTS = 8
+
+
+def gqa_merge(outs, lses, out=None, lse=None, stream=None, with_lse=True):
+    """Attentions over parts of the keys made one: outs, a list of up to 8 bf16 tensors [...,D], and lses, of fp32
+    tensors [...], are what attention over each part gives (rows in the same order, as gqa_prefill, gqa_prefill_paged
+    and single-token decode calls return them).
+
+    Returns (out [...,D] bf16, lse [...] fp32 or None); out and lse may be one of the parts'.
+    """
+    lib = _lib_handle or load_library()
+    fn = "gqa_merge"
+    n = len(outs)
+    if n < 1 or n != len(lses) or n > GQA_MERGE_MAX_PARTS:
+        raise ValueError(f"{fn}: one to {GQA_MERGE_MAX_PARTS} outs, and as many lses")
+    shape = outs[0].shape
+    if len(shape) < 1:
+        raise ValueError(f"{fn}: outs must be [...,D]")
+    dev = outs[0].get_device()
+    guard, cs = _on_device_of(dev, stream)
+    for o, s in zip(outs, lses):
+        _fit(fn, "outs", o, torch.bfloat16, dev, shape)
+        _fit(fn, "lses", s, torch.float32, dev, shape[:-1])
+    if out is None:
+        out = _new(shape, torch.bfloat16, outs[0], stream)
+    else:
+        _fit(fn, "out", out, torch.bfloat16, dev, shape)
+    if lse is not None:
+        _fit(fn, "lse", lse, torch.float32, dev, shape[:-1])
+    elif with_lse:
+        lse = _new(shape[:-1], torch.float32, outs[0], stream)
+    ptrs = ctypes.c_void_p * n
+    st = _guarded(guard, lib.gqa_merge, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[s.data_ptr() for s in lses]), n,
+                  out.data_ptr(), _data(lse), lses[0].numel(), shape[-1], cs)
+    if st:
+        raise GQAError(st, fn)
+    return out, lse
 
 
 def gqa_paged_gather_fp8(pool, page_table, topk_idx, out=None, stream=None):

@@ -524,22 +524,6 @@ cudaError_t launch_gather(GatherArgs a, cudaStream_t stream) {
                       dim3(unsigned((a.rows + per - 1) / per), unsigned(a.B)), kGatherThreads, stream);
 }
 
-// Checks shared by both entry points: pool type, scales, parameters.
-gqa_status check_cache(int kv_dtype, const void *params, float k_scale, float v_scale, const float *k_scales,
-                       const float *v_scales, int n_scales, int Hkv) {
-    if (kv_dtype < GQA_KV_BF16 || kv_dtype > GQA_KV_INT4) return GQA_ERR_INVALID_ARG;
-    if ((kv_dtype == GQA_KV_INT4) != (params != nullptr)) return GQA_ERR_INVALID_ARG;
-    const bool kv8 = kv_dtype == GQA_KV_FP8_E4M3FN || kv_dtype == GQA_KV_INT8;
-    if (k_scales != nullptr || v_scales != nullptr) {
-        if (!kv8 || k_scales == nullptr || v_scales == nullptr || (n_scales != 1 && n_scales != Hkv))
-            return GQA_ERR_INVALID_ARG;
-        if (!host_aligned(k_scales, 4) || !host_aligned(v_scales, 4)) return GQA_ERR_ALIGNMENT;
-    } else if (kv8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale))) {
-        return GQA_ERR_INVALID_ARG;
-    }
-    return host_aligned(params, 8) ? GQA_OK : GQA_ERR_ALIGNMENT;
-}
-
 }  // namespace
 }  // namespace gqa
 
@@ -567,7 +551,7 @@ extern "C" gqa_status gqa_paged_append(const void *q, long long q_stride, void *
     if (cu_tokens == nullptr && T % B != 0) return GQA_ERR_INVALID_ARG;
     if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0) return GQA_ERR_INVALID_ARG;
     if (rot_dim > 0 && (cos_sin == nullptr || max_pos < 1)) return GQA_ERR_INVALID_ARG;
-    st = check_cache(kv_dtype, kv_params, k_scale, v_scale, k_scales, v_scales, n_scales, Hkv);
+    st = host_check_cache(kv_dtype, kv_params, k_scale, v_scale, k_scales, v_scales, n_scales, Hkv);
     if (st != GQA_OK) return st;
     const bool kv8 = kv_dtype == GQA_KV_FP8_E4M3FN || kv_dtype == GQA_KV_INT8;
     if (kv8 && k_scales == nullptr && (!(k_scale > 0.f) || !(v_scale > 0.f))) return GQA_ERR_INVALID_ARG;
@@ -632,7 +616,7 @@ extern "C" gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const v
     gqa_status st = host_check_pages(B, Hkv, D, page_size, pages_per_req, num_pages);
     if (st != GQA_OK) return st;
     if (rows < 0) return GQA_ERR_INVALID_ARG;
-    st = check_cache(kv_dtype, kv_params, k_scale, v_scale, k_scales, v_scales, n_scales, Hkv);
+    st = host_check_cache(kv_dtype, kv_params, k_scale, v_scale, k_scales, v_scales, n_scales, Hkv);
     if (st != GQA_OK) return st;
     if (k_pool == nullptr || v_pool == nullptr || page_table == nullptr || seq_lens == nullptr ||
         (rows > 0 && (k_out == nullptr || v_out == nullptr)))

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cmath>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -46,6 +47,22 @@ inline gqa_status host_check_pages(int B, int Hkv, int D, int page_size, int pag
         return GQA_ERR_UNSUPPORTED;
     if (B > 65535) return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
+}
+
+// A cache's type with its parameters and scales, as append, gather and the prompt attention take them.
+inline gqa_status host_check_cache(int kv_dtype, const void *params, float k_scale, float v_scale, const float *k_scales,
+                                   const float *v_scales, int n_scales, int Hkv) {
+    if (kv_dtype < GQA_KV_BF16 || kv_dtype > GQA_KV_INT4) return GQA_ERR_INVALID_ARG;
+    if ((kv_dtype == GQA_KV_INT4) != (params != nullptr)) return GQA_ERR_INVALID_ARG;
+    const bool kv8 = kv_dtype == GQA_KV_FP8_E4M3FN || kv_dtype == GQA_KV_INT8;
+    if (k_scales != nullptr || v_scales != nullptr) {
+        if (!kv8 || k_scales == nullptr || v_scales == nullptr || (n_scales != 1 && n_scales != Hkv))
+            return GQA_ERR_INVALID_ARG;
+        if (!host_aligned(k_scales, 4) || !host_aligned(v_scales, 4)) return GQA_ERR_ALIGNMENT;
+    } else if (kv8 && (!std::isfinite(k_scale) || !std::isfinite(v_scale))) {
+        return GQA_ERR_INVALID_ARG;
+    }
+    return host_aligned(params, 8) ? GQA_OK : GQA_ERR_ALIGNMENT;
 }
 
 }  // namespace gqa

@@ -510,6 +510,104 @@ gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const void *v_pool
                             int page_size, int pages_per_req, int num_pages, gqa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Attention over whole prompts, packed one after the other.
+ *
+ * Sequence b owns the rows cu_q[b] .. cu_q[b+1]-1 of q and the rows
+ * cu_k[b] .. cu_k[b+1]-1 of k and v (n_b queries over L_b keys).  For its query
+ * row i, query head h and KV head g = h // (Hq/Hkv), with the visible keys
+ * j <= L_b - n_b + i (causal != 0: bottom-right alignment, as in gqa_decode)
+ * or all L_b of them (causal == 0):
+ *   s_j = scale * q[i,h,:] . k[j,g,:],  lse[i,h] = ln sum_j exp(s_j),
+ *   out[i,h,:] = sum_j exp(s_j - lse) v[j,g,:].
+ * A row that sees no key gives out = 0 and lse = -inf.  Rows of out and lse
+ * that belong to no sequence are left as they were.  What k and v hold in keys
+ * that a row does not see never reaches it, NaN and infinities included; an
+ * element of v that is not finite makes that element of every row that sees it
+ * infinite or NaN.
+ *
+ * q : device bf16 [Tq, Hq, Dqk]; k [Tk, Hkv, Dqk]; v [Tk, Hkv, Dv]; heads
+ *   contiguous, tokens q_stride, k_stride, v_stride elements apart (multiples
+ *   of 8, at least heads * head size, so that slices of a fused projection need
+ *   no copy).  out : device bf16 [Tq, Hq, Dv].  lse : device fp32 [Tq, Hq] or NULL.
+ * cu_q, cu_k : device int32 [B + 1], not decreasing.  cu_q NULL: Tq / B rows
+ *   each.  cu_k NULL: cu_q's offsets for the keys too, or Tk / B keys each when
+ *   cu_q is NULL.
+ * (Dqk, Dv): (64, 64), (128, 128), (192, 128).  scale <= 0 or NaN selects
+ *   1 / sqrt(Dqk).
+ * Rounding: weights are rounded to bf16 (2^-8 of each at most, relative to a
+ *   reference within 2^8 of the row's largest); their sum is not; sums are fp32.
+ * Limits: Tq, Tk >= 0; B <= 65535; Hq / Hkv <= 4096; Tq * Hq < 2^31.
+ * Workspace: NULL = library pool, allocated stream-ordered; otherwise device
+ *   memory of at least gqa_prefill_workspace_bytes, 256-byte aligned, not in
+ *   use by other work in flight (two graphs that may run at once need one each).
+ * Device-checked (GQA_ERR_DEVICE_INDEX in the device error word): offsets
+ *   outside [0, Tq] or [0, Tk], or decreasing, are clamped.
+ * The same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+gqa_status gqa_prefill(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                       long long v_stride, const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse, int Tq,
+                       int Tk, int B, int Hq, int Hkv, int Dqk, int Dv, int causal, float scale, void *workspace,
+                       size_t workspace_bytes, gqa_stream_t stream);
+
+/* Workspace bytes of gqa_prefill on the current device (0 on invalid arguments). */
+size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int Dv);
+
+/* ------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache that holds them: a chunk of a
+ * prompt, draft tokens to check, or the one token of a decode step, in any mix.
+ *
+ * gqa_prefill's operation with the keys in a paged cache: request b has the
+ * query rows cu_tokens[b] .. cu_tokens[b+1]-1 (NULL: T / B each) and L_b =
+ * seq_lens[b] keys, which count the new tokens too (what gqa_paged_append,
+ * called before it, takes); token t lies at page page_table[b, t / page_size],
+ * slot t % page_size.  causal == 0 lets every row see all L_b keys (a prefix that
+ * several requests share, for gqa_merge).
+ *
+ * q : device bf16 [T, Hq, D], heads contiguous, tokens q_stride elements apart;
+ * out bf16 [T, Hq, D]; lse fp32 [T, Hq] or NULL.
+ * Pools, kv_params, scales, page_table, kv_dtype: as gqa_paged_gather (8-bit
+ *   pools take finite host scales, or n_scales = 1 or Hkv device scales, read by
+ *   the kernel); pools 16-byte, kv_params 8-byte aligned.
+ * Limits: D in {64, 128}; page limits as gqa_decode_paged; pages_per_req *
+ *   page_size <= 2^31 - 256; the rest, and the workspace, as gqa_prefill.
+ * Rounding: bf16 pools as gqa_prefill; codes enter the products as fp16 values
+ *   and weights are rounded to fp16 (2^-11, and by at most 2^-25 of the largest
+ *   where they are small); see gqa_decode_paged_int4 for what 4-bit codes stand for.
+ * Device-checked (GQA_ERR_DEVICE_INDEX): offsets as gqa_prefill; a seq_lens[b]
+ *   outside [0, pages_per_req * page_size] is clamped; a token whose page id is
+ *   out of range reads as zeros.
+ * What the pools hold in slots past a request's length is never used.
+ * ------------------------------------------------------------------------ */
+gqa_status gqa_prefill_paged(const void *q, long long q_stride, int kv_dtype, const void *k_pool, const void *v_pool,
+                             const void *kv_params, float k_scale, float v_scale, const float *k_scales,
+                             const float *v_scales, int n_scales, const int32_t *page_table,
+                             const int32_t *seq_lens, const int32_t *cu_tokens, void *out, float *lse, int T, int B,
+                             int Hq, int Hkv, int D, int page_size, int pages_per_req, int num_pages, int causal,
+                             float scale, void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/* Workspace bytes of gqa_prefill_paged on the current device (0 on invalid arguments). */
+size_t gqa_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+
+/* ------------------------------------------------------------------------
+ * Attentions over parts of the keys made one: outs[p] and lses[p], p < n, are
+ * what attention over part p alone gives, and the result is what attention over
+ * all parts would give:
+ *   lse[r] = ln sum_p exp(lses[p][r]),  out[r,:] = sum_p exp(lses[p][r] - lse[r]) outs[p][r,:].
+ * A part with lses[p][r] = -inf (no visible key) has no share, whatever outs[p]
+ * holds in that row; a row without any share gives out = 0 and lse = -inf.  An
+ * LSE of NaN or +inf makes its row NaN.
+ *
+ * outs : host array of n device pointers, bf16 [rows, D]; lses : host array of n
+ *   device pointers, fp32 [rows].  out bf16 [rows, D], lse fp32 [rows] or NULL;
+ *   both may be one of the parts'.
+ * Limits: 1 <= n <= 8; D a multiple of 8, at most 256; 0 <= rows < 2^31.  outs and out
+ *   16-byte aligned.
+ * ------------------------------------------------------------------------ */
+#define GQA_MERGE_MAX_PARTS 8
+gqa_status gqa_merge(const void *const *outs, const float *const *lses, int n, void *out, float *lse, long long rows,
+                     int D, gqa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Test hooks.  They run the paged kernel's own index mapping and FP8
  * conversion in isolation so those can be checked bit for bit.
  * ------------------------------------------------------------------------ */
