@@ -36,6 +36,11 @@ bool host_int4_tensor_map(CUtensorMap *map, const void *base, long long rows, in
 // rows of heads * 4, boxes of (box_heads * 4, box_rows).
 bool host_int4_param_map(CUtensorMap *map, const void *base, long long rows, int heads, int box_rows, int box_heads);
 
+// TMA descriptor of bf16 [rows, heads, D] (rows row_stride elements apart), boxes of 64 elements x box_heads heads x
+// box_rows rows with the 128-byte swizzle.  Rows and heads past the end read as zeros.
+bool host_rows_tensor_map(CUtensorMap *map, const void *base, long long rows, int heads, int D, long long row_stride,
+                          int box_rows, int box_heads);
+
 inline bool host_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline size_t host_align256(size_t x) { return (x + 255) & ~size_t(255); }
 

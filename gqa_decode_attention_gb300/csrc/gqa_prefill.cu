@@ -1,144 +1,136 @@
 // gqa_prefill.cu -- attention over packed prompts and of new tokens over the
 // paged cache: kernel, and the C entry points.
+#include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "gqa_common.cuh"
 #include "gqa_host.h"
-#include "gqa_prefill.h"
+#include "gqa_prefill_kernel.cuh"
 
 namespace gqa {
 namespace {
 
-// First and one past the last row of sequence b, clamped into [0, total].
-__device__ __forceinline__ void prefill_range(const int32_t *cu, int per, int b, int total, unsigned *err, int *from,
-                                              int *to) {
-    if (cu == nullptr) {
-        *from = b * per, *to = (b + 1) * per;
-        return;
-    }
-    const int f = cu[b], t = cu[b + 1];
-    *from = min(max(f, 0), total);
-    *to = min(max(t, *from), total);
-    if (*from != f || *to != t) flag_error(err, kErrIndex);
+constexpr int kMaxDevices = 64;
+constexpr int kMaxWorkers = kPlanThreads;
+
+// Tiles of a shape: query heads of a KV head side by side, as many tokens as fit.
+void prefill_tiles(PrefillArgs *a) {
+    const int blocks = (a->G + kPreTile - 1) / kPreTile;
+    a->g_tile = (a->G + blocks - 1) / blocks;
+    a->tok_tile = kPreTile / a->g_tile;
+    a->head_blocks = a->Hkv * blocks;
+    a->max_items = a->Tq / (2 * a->tok_tile) + a->B;
 }
 
-template <int N>
-__device__ __forceinline__ void load_bf16(float (&x)[N], const __nv_bfloat16 *p) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + i));
-        x[i] = f.x, x[i + 1] = f.y;
+// Lays the plan and the partial results out in `base` (null: only counts); returns the bytes.
+size_t prefill_workspace(PrefillArgs *a, int Dv, bool parts, char *base) {
+    size_t at = 0;
+    auto take = [&](auto **p, size_t n) {
+        *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + at);
+        at += host_align256(n * sizeof(**p));
+    };
+    take(&a->plan, 1);
+    take(&a->items, size_t(a->max_items));
+    take(&a->unsorted, size_t(a->max_items));
+    take(&a->tile_prefix, size_t(a->B) + 1);
+    take(&a->cost_prefix, size_t(a->max_items) + 1);
+    take(&a->cuts, size_t(a->workers) + 1);
+    if (parts) {
+        take(&a->o_part, size_t(2) * a->workers * 2 * kPreTile * Dv);
+        take(&a->lse_part, size_t(2) * a->workers * 2 * kPreTile);
     }
+    return at;
 }
 
-// Elements d .. d + N - 1 of key `row` (of a pool) and KV head g.
-template <int KVT, int D, int N>
-__device__ __forceinline__ void load_codes(float (&x)[N], const uint8_t *pool, const __half *params, int which,
-                                           long long row, int Hkv, int g, int d) {
-    const long long head = row * Hkv + g;
-    if constexpr (KVT == GQA_KV_BF16) {
-        load_bf16(x, reinterpret_cast<const __nv_bfloat16 *>(pool) + head * D + d);
-    } else if constexpr (KVT == GQA_KV_INT4) {
-        const float scale = __half2float(params[head * 4 + 2 * which]);
-        const float zero = __half2float(params[head * 4 + 2 * which + 1]);
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const int c = pool[head * (D / 2) + (d + i) / 2];
-            x[i] = float(c & 15) * scale + zero, x[i + 1] = float(c >> 4) * scale + zero;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint8_t c = pool[head * D + d + i];
-            if constexpr (KVT == GQA_KV_INT8) {
-                x[i] = float(int8_t(c));
-            } else {
-                const uint32_t h = e4m3x2_to_f16x2(c);
-                x[i] = __half2float(*reinterpret_cast<const __half *>(&h));
+int prefill_workers(int dev) { return std::max(1, std::min(host_sm_count(dev), kMaxWorkers)); }
+
+cudaError_t launch_after(const void *kern, dim3 grid, int threads, int smem, void **args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // Programmatic dependent launch: starts while the kernel before it ends, and waits for it before it reads.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
+}
+
+template <int DQK, int DV, int SRC>
+gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t workspace_bytes, int dev, cudaStream_t cs) {
+    using C = PrefillCfg<DQK, DV, SRC>;
+    const void *kern = reinterpret_cast<const void *>(gqa_prefill_kernel<DQK, DV, SRC>);
+    static std::mutex mu;
+    static bool raised[kMaxDevices];
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!raised[dev]) {
+            // The kernel's warps share its registers out anew, which waits for ever if they are fewer than counted on.
+            cudaFuncAttributes at;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
+                cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * C::THREADS < C::REGS) {
+                cudaGetLastError();
+                return GQA_ERR_CUDA;
             }
+            raised[dev] = true;
         }
     }
-}
-
-// One warp a (query row, head): the keys one after the other, the head size over the lanes.
-template <int KVT, int D, int DV>
-__global__ void __launch_bounds__(128) gqa_prefill_kernel(const PrefillArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (unit >= (long long)a.Tq * a.Hq) return;
-    const int t = int(unit / a.Hq), h = int(unit % a.Hq), g = h / a.G;
-    int from = 0, to = 0, b = 0;
-    if (a.cu_q == nullptr) {
-        b = t / a.per_q;
-        prefill_range(nullptr, a.per_q, b, a.Tq, a.err, &from, &to);
+    a.workers = prefill_workers(dev);
+    // Items of fewer steps than a part of one has at least are not divided, and need neither partial results nor a merge.
+    a.may_split = (keys + kPreKeys - 1) / kPreKeys >= kPreMinSplit + kPreSnap;
+    CUtensorMap q_map, k_map, v_map;
+    bool maps = host_rows_tensor_map(&q_map, a.q, a.Tq, a.Hq, DQK, a.q_stride, a.tok_tile, a.g_tile);
+    if (SRC == kPreDense) {
+        // (without keys nothing is loaded through the maps)
+        const bool none = a.Tk == 0;
+        maps = maps && host_rows_tensor_map(&k_map, none ? a.q : a.k, none ? 1 : a.Tk, a.Hkv, DQK, a.k_stride, kPreKeys, 1) &&
+               host_rows_tensor_map(&v_map, none ? a.q : a.v, none ? 1 : a.Tk, a.Hkv, DV, a.v_stride, kPreKeys, 1);
+    } else if (SRC == kPrePages) {
+        const long long rows = (long long)a.num_pages * a.page_size;
+        maps = maps && host_rows_tensor_map(&k_map, a.k_pool, rows, a.Hkv, DQK, (long long)a.Hkv * DQK, a.box_rows, 1) &&
+               host_rows_tensor_map(&v_map, a.v_pool, rows, a.Hkv, DV, (long long)a.Hkv * DV, a.box_rows, 1);
+    }
+    if (!maps) return GQA_ERR_CUDA;
+    const size_t need = prefill_workspace(&a, DV, a.may_split, nullptr);
+    void *ws = workspace;
+    bool owned = false;
+    if (ws != nullptr) {
+        if (workspace_bytes < prefill_workspace(&a, DV, true, nullptr)) return GQA_ERR_NO_MEMORY;
+        if (!host_aligned(ws, 256)) return GQA_ERR_ALIGNMENT;
     } else {
-        b = a.B;
-        for (int x = a.B - 1; x >= 0; --x) {
-            int f, e;
-            prefill_range(a.cu_q, 0, x, a.Tq, a.err, &f, &e);
-            if (t >= f && t < e) b = x, from = f, to = e;
+        if (host_pool_alloc(&ws, need, dev, cs) != cudaSuccess) {
+            cudaGetLastError();
+            return GQA_ERR_NO_MEMORY;
         }
-        if (b == a.B) return;
+        owned = true;
     }
-    int kf = 0, kt = 0;
-    if constexpr (KVT == kPreDense) {
-        prefill_range(a.cu_k, a.per_k, b, a.Tk, a.err, &kf, &kt);
-    } else {
-        const int cap = a.pages_per_req * a.page_size;
-        kt = min(max(a.seq_lens[b], 0), cap);
-        if (kt != a.seq_lens[b]) flag_error(a.err, kErrIndex);
+    prefill_workspace(&a, DV, a.may_split, static_cast<char *>(ws));
+    constexpr bool paged = SRC != kPreDense;
+    gqa_prefill_plan_kernel<paged><<<1, kPlanThreads, 0, cs>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        cudaEvent_t before, after;
+        host_kernel_events(&before, &after);
+        const bool timed = before != nullptr && after != nullptr;
+        if (timed) cudaEventRecord(before, cs);
+        void *args[] = {&q_map, &k_map, &v_map, &a};
+        e = launch_after(kern, dim3(unsigned(a.workers)), C::THREADS, C::SMEM, args, cs);
+        if (timed) cudaEventRecord(after, cs);
     }
-    const int L = kt - kf;
-    const int seen = a.causal ? min(max(L - (to - from) + (t - from) + 1, 0), L) : L;
-    constexpr int N = D / 32, NV = DV / 32;
-    float q[N], o[NV] = {}, m = -INFINITY, l = 0.f;
-    load_bf16(q, a.q + t * a.q_stride + h * D + lane * N);
-    float alpha = a.alpha, vs = a.v_scale;
-    if (a.k_scales != nullptr) {
-        alpha *= a.k_scales[a.n_scales > 1 ? g : 0];
-        vs = a.v_scales[a.n_scales > 1 ? g : 0];
+    if (e == cudaSuccess && a.may_split && a.workers > 1) {
+        void *args[] = {&a};
+        e = launch_after(reinterpret_cast<const void *>(gqa_prefill_merge_kernel<DV>),
+                         dim3(unsigned(a.workers - 1), 2 * kPreTile / kPreMergeRows), kPreMergeThreads, 0, args, cs);
     }
-    for (int j = 0; j < seen; ++j) {
-        float k[N] = {}, v[NV] = {};
-        if constexpr (KVT == kPreDense) {
-            load_bf16(k, a.k + (long long)(kf + j) * a.k_stride + g * D + lane * N);
-            load_bf16(v, a.v + (long long)(kf + j) * a.v_stride + g * DV + lane * NV);
-        } else {
-            const int page = a.page_table[(long long)b * a.pages_per_req + j / a.page_size];
-            if (page < 0 || page >= a.num_pages) {
-                flag_error(a.err, kErrIndex);
-            } else {
-                const long long row = (long long)page * a.page_size + j % a.page_size;
-                load_codes<KVT, D>(k, a.k_pool, a.params, 0, row, a.Hkv, g, lane * N);
-                load_codes<KVT, D>(v, a.v_pool, a.params, 1, row, a.Hkv, g, lane * NV);
-            }
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s += q[i] * k[i];
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= alpha;
-        const float m2 = fmaxf(m, s);
-        const float use = m2 == -INFINITY ? 0.f : m2;
-        const float f = exp2f(m - use), p = exp2f(s - use);
-        m = m2;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) o[i] = o[i] * f + p * v[i];
+    if (owned) cudaFreeAsync(ws, cs);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GQA_ERR_CUDA;
     }
-    const float inv = l == 0.f ? 0.f : vs / l;
-    __nv_bfloat16 *dst = a.out + (long long)unit * DV + lane * NV;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) dst[i] = __float2bfloat16(l == 0.f ? 0.f : o[i] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[unit] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-}
-
-template <int KVT, int D, int DV>
-gqa_status launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
-    const long long units = (long long)a.Tq * a.Hq;
-    gqa_prefill_kernel<KVT, D, DV><<<unsigned((units + 3) / 4), 128, 0, stream>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
     return GQA_OK;
 }
 
@@ -147,6 +139,10 @@ gqa_status check_prefill(int Tq, int B, int Hq, int Hkv, int Dqk, int Dv) {
     if (Tq < 0 || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0) return GQA_ERR_INVALID_ARG;
     if (!((Dqk == 64 && Dv == 64) || (Dqk == 128 && Dv == 128) || (Dqk == 192 && Dv == 128))) return GQA_ERR_UNSUPPORTED;
     if (B > 65535 || Hq / Hkv > 4096 || (long long)Tq * Hq >= (1LL << 31)) return GQA_ERR_UNSUPPORTED;
+    PrefillArgs a = {};
+    a.Tq = Tq, a.B = B, a.Hkv = Hkv, a.G = Hq / Hkv;
+    prefill_tiles(&a);
+    if ((long long)a.max_items * a.head_blocks >= (1LL << 31) - kMaxWorkers) return GQA_ERR_UNSUPPORTED;  // pieces count in 32 bits
     return GQA_OK;
 }
 
@@ -156,8 +152,13 @@ gqa_status check_prefill(int Tq, int B, int Hq, int Hkv, int Dqk, int Dv) {
 using namespace gqa;
 
 extern "C" size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int Dv) {
-    (void)Tq, (void)B, (void)Hq, (void)Hkv, (void)Dqk, (void)Dv;
-    return 0;
+    int dev = 0;
+    if (check_prefill(Tq, B, Hq, Hkv, Dqk, Dv) != GQA_OK || !host_current_device(&dev)) return 0;
+    PrefillArgs a = {};
+    a.Tq = Tq, a.B = B, a.Hkv = Hkv, a.G = Hq / Hkv;
+    prefill_tiles(&a);
+    a.workers = prefill_workers(dev);
+    return prefill_workspace(&a, Dv, true, nullptr);
 }
 
 extern "C" size_t gqa_prefill_paged_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
@@ -170,6 +171,7 @@ extern "C" gqa_status gqa_prefill(const void *q, long long q_stride, const void 
                                   void *workspace, size_t workspace_bytes, gqa_stream_t stream) {
     gqa_status st = check_prefill(Tq, B, Hq, Hkv, Dqk, Dv);
     if (st != GQA_OK) return st;
+    if (Tk > (1LL << 31) - 256) return GQA_ERR_UNSUPPORTED;  // key indexes step past the end
     if (Tk < 0 || (cu_q == nullptr && Tq % B != 0) || (cu_q == nullptr && cu_k == nullptr && Tk % B != 0))
         return GQA_ERR_INVALID_ARG;
     if (Tq > 0 && (q == nullptr || out == nullptr || (Tk > 0 && (k == nullptr || v == nullptr)))) return GQA_ERR_INVALID_ARG;
@@ -201,9 +203,10 @@ extern "C" gqa_status gqa_prefill(const void *q, long long q_stride, const void 
     a.fault_mode = host_fault_mode();
     a.err = host_error_word(dev);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (Dqk == 64) return launch_prefill<kPreDense, 64, 64>(a, cs);
-    if (Dqk == 128) return launch_prefill<kPreDense, 128, 128>(a, cs);
-    return launch_prefill<kPreDense, 192, 128>(a, cs);
+    prefill_tiles(&a);
+    if (Dqk == 64) return launch_prefill<64, 64, kPreDense>(a, Tk, workspace, workspace_bytes, dev, cs);
+    if (Dqk == 128) return launch_prefill<128, 128, kPreDense>(a, Tk, workspace, workspace_bytes, dev, cs);
+    return launch_prefill<192, 128, kPreDense>(a, Tk, workspace, workspace_bytes, dev, cs);
 }
 
 extern "C" gqa_status gqa_prefill_paged(const void *q, long long q_stride, int kv_dtype, const void *k_pool,
@@ -257,13 +260,18 @@ extern "C" gqa_status gqa_prefill_paged(const void *q, long long q_stride, int k
     a.fault_mode = host_fault_mode();
     a.err = host_error_word(dev);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-#define GQA_PREFILL_KVT(KVT) \
-    (D == 64 ? launch_prefill<KVT, 64, 64>(a, cs) : launch_prefill<KVT, 128, 128>(a, cs))
+    prefill_tiles(&a);
+    const long long keys = (long long)pages_per_req * page_size;
+    a.box_rows = kPreKeys;
+    while (page_size % a.box_rows != 0) a.box_rows /= 2;
+#define GQA_PREFILL_SOURCE(SRC)                                                                     \
+    (D == 64 ? launch_prefill<64, 64, SRC>(a, keys, workspace, workspace_bytes, dev, cs)            \
+             : launch_prefill<128, 128, SRC>(a, keys, workspace, workspace_bytes, dev, cs))
     switch (kv_dtype) {
-        case GQA_KV_BF16: return GQA_PREFILL_KVT(GQA_KV_BF16);
-        case GQA_KV_FP8_E4M3FN: return GQA_PREFILL_KVT(GQA_KV_FP8_E4M3FN);
-        case GQA_KV_INT8: return GQA_PREFILL_KVT(GQA_KV_INT8);
-        default: return GQA_PREFILL_KVT(GQA_KV_INT4);
+        case GQA_KV_BF16: return a.box_rows >= 8 ? GQA_PREFILL_SOURCE(kPrePages) : GQA_PREFILL_SOURCE(kPreCopy);
+        case GQA_KV_FP8_E4M3FN: return GQA_PREFILL_SOURCE(kPreFp8);
+        case GQA_KV_INT8: return GQA_PREFILL_SOURCE(kPreInt8);
+        default: return GQA_PREFILL_SOURCE(kPreInt4);
     }
-#undef GQA_PREFILL_KVT
+#undef GQA_PREFILL_SOURCE
 }

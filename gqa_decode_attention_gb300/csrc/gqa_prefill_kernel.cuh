@@ -1,0 +1,683 @@
+// gqa_prefill_kernel.cuh -- prompt attention on the fifth-generation tensor cores (tcgen05 + TMEM).
+//
+//   s_j = scale q.k_j over the keys that a row sees,  out = sum_j exp(s_j - lse) v_j
+//
+// One persistent CTA an SM walks its pieces of the plan (gqa_prefill_plan.cuh).  A tile is 128 query rows: tok_tile
+// consecutive tokens x g_tile query heads of one KV head (TMA lays them out so), so that one token of a grouped model still
+// fills rows, and K and V are read once for all of them.  Steps of 128 keys:
+//   S_t = Q_t K^T  (128 x 128, K = Dqk)   P_t = exp2(alpha S_t - reference)   O_t += P_t V  (128 x Dv, K = 128)
+// with two tiles t = 0, 1 in TMEM (S 128 columns and O Dv columns each; P_t overwrites S_t as 16-bit values and is the A
+// operand of the second product).  The tensor core works on one tile's products while the other tile's softmax runs: the
+// issue order is P_t V of a step, then Q_t K^T of tile t's next step, then the same for the other tile.  An item with rows for
+// one tile only gives its steps to the two row groups in turns and joins their (reference, sum, O) at the end.
+//
+// Roles: warps 0-3 and 4-7 softmax of tile 0 and 1, a thread a row; warp 8 issues the products; warp 9 loads Q and K, warp
+// 10 V, by TMA; warp 11 clears, in steps past what some row sees, the V rows that no row may see (0 x NaN is NaN) and
+// elements of V that are not finite, which rows that see them get back at the end; such steps land on a barrier of their own
+// and warp 11 hands them on.
+// Pools that TMA cannot bring as they are wanted (codes; bf16 pages of odd sizes) have four more warps that copy or convert
+// K and V through registers (gqa_prefill_load.cuh); warp 9 then loads Q only.  Codes enter the products as fp16: FP8 and int8
+// codes as they are (exact), 4-bit codes of K as they are, with scale and zero applied to the scores, those of V as values.
+// Q is converted to fp16 in place, each row times a power of two (exact but for elements 2^-28 below the row's largest).
+// Tensor products run in the order of their issue, so S_t of a step being there says that O_t of the step before is too.
+#pragma once
+
+#include "gqa_prefill_load.cuh"
+#include "gqa_umma.cuh"
+
+namespace gqa {
+
+constexpr float kPreRescaleLog2 = 8.f;  // a row's reference moves when its maximum grows past it by 2^8
+
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// Adds to a row's result (bf16 out, or fp32 part) the elements of V's rows key0 .. key1 - 1 that are not finite: the
+// products had zeros there.  (What is added is the value without its scale and weight: infinite or NaN all the same.)
+template <int DV, int SRC, typename T>
+__device__ __noinline__ void prefill_add_not_finite(const PrefillArgs &a, int req, int k_row, int g, int key0, int key1, T *dst) {
+    for (int key = key0; key < key1; ++key) {
+        long long head;
+        if constexpr (SRC != kPreDense) {
+            const int row = prefill_pool_row(a, req, key);
+            if (row < 0) continue;
+            head = (long long)row * a.Hkv + g;
+        }
+        for (int d = 0; d < DV; ++d) {
+            float x;
+            if constexpr (SRC == kPreDense) {
+                x = __bfloat162float(a.v[(long long)(k_row + key) * a.v_stride + g * DV + d]);
+            } else if constexpr (SRC == kPreFp8) {
+                x = (a.v_pool[head * DV + d] & 0x7f) == 0x7f ? NAN : 0.f;
+            } else if constexpr (SRC == kPreInt4) {
+                x = __half2float(a.params[head * 4 + 2]) + __half2float(a.params[head * 4 + 3]);
+            } else if constexpr (SRC == kPreInt8) {
+                x = 0.f;
+            } else {
+                x = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.v_pool)[head * DV + d]);
+            }
+            if (!isfinite(x)) dst[d] = T(float(dst[d]) + (SRC == kPreInt4 ? NAN : x));
+        }
+    }
+}
+
+// The row's 8 elements of one 16-byte unit as fp16, times `scale`; the order that 4-bit codes come in for those.
+template <int SRC>
+__device__ __forceinline__ uint4 prefill_q_unit(uint4 x, float scale) {
+    float f[8];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16) * scale;
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * scale;
+    }
+    if constexpr (SRC == kPreInt4)
+        return make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+    return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+}
+
+template <int DQK, int DV, int SRC>
+__global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
+    gqa_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PrefillArgs a) {
+    using C = PrefillCfg<DQK, DV, SRC>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float2 *stat = reinterpret_cast<float2 *>(smem + C::STAT_OFF);
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // [1] a piece's rows have landed
+    uint64_t *q_empty = q_full + 1;     // [1] ... and its last score product is done
+    uint64_t *k_full = q_empty + 1;     // [KST]
+    uint64_t *k_empty = k_full + C::KST;
+    uint64_t *v_full = k_empty + C::KST;  // [VST]
+    uint64_t *v_empty = v_full + C::VST;
+    uint64_t *v_raw = v_empty + C::VST;  // [VST] V of a step past what some row sees, not cleared yet
+    uint64_t *s_full = v_raw + C::VST;     // [2] a tile's scores are there
+    uint64_t *p_full = s_full + 2;         // [2] a tile's weights are
+    uint64_t *o_full = p_full + 2;         // [2] a tile's last product of the piece is done
+    uint64_t *q_ready = o_full + 2;        // [2] a tile's rows are fp16
+    uint64_t *stat_full = q_ready + 2;      // [1] row group 1's references and sums are in `stat`
+    uint64_t *stat_free = stat_full + 1;   // [1] ... and joined, its O too
+    uint64_t *fin = stat_free + 1;         // [1] every product is done
+    uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(fin + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
+    volatile int *bad_v = abort_flag + 1;  // elements of V that are not finite were cleared, in this piece or an earlier one
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t limit = a.wait_limit_ns;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        constexpr int loaders = C::TMA ? 1 : 128;
+        for (int s = 0; s < C::KST; ++s) mbar_init(&k_full[s], loaders), mbar_init(&k_empty[s], 1);
+        for (int s = 0; s < C::VST; ++s) mbar_init(&v_full[s], loaders), mbar_init(&v_empty[s], 1), mbar_init(&v_raw[s], 1);
+        for (int t = 0; t < 2; ++t) mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 128), mbar_init(&o_full[t], 1), mbar_init(&q_ready[t], 128);
+        mbar_init(stat_full, 128);
+        mbar_init(stat_free, 128);
+        mbar_init(fin, 1);
+        *abort_flag = 0;
+        *bad_v = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 8) tmem_alloc(tmem_base_s, C::TMEM_COLS);
+    if (threadIdx.x == 288) {
+        prefetch_tmap(&tm_q);
+        if constexpr (C::TMA) prefetch_tmap(&tm_k), prefetch_tmap(&tm_v);
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tbase = *tmem_base_s;
+    pdl_wait_primary();  // the plan, and whatever wrote the inputs
+
+    bool ok = true;
+    if (!C::TMA && warp >= 12) {
+        if constexpr (!C::TMA) {
+            regs_dec<C::LOAD_REGS>();
+            ok = prefill_load<DQK, DV, SRC>(a, smem, k_full, k_empty, v_full, v_empty, abort_flag, bad_v);
+        }
+        if (!ok && lane == 0) {
+            flag_error(a.err, kErrTimeout);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        regs_dec<C::OTHER_REGS>();
+        PrefillWalk walk(a, blockIdx.x);
+        PrefillPiece p;
+        if (warp == 8) {
+            // -------------------------------------------------------- products
+            if (lane == 0) {
+                constexpr uint32_t fmt = C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u;
+                constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreKeys, false, false) & fmt;
+                constexpr uint32_t idesc_pv = idesc_bf16_f32(kPreTile, DV, false, true) & fmt;
+                const uint32_t q_addr = smem_u32(smem + C::Q_OFF), k_addr = smem_u32(smem + C::K_OFF),
+                               v_addr = smem_u32(smem + C::V_OFF);
+                int n_piece = 0, k_at = 0, v_at = 0;  // steps used before this piece
+                uint32_t p_phase = 0;
+                while (ok && walk.next(&p)) {
+                    if (p.units == 0) continue;
+                    if constexpr (C::F16)
+                        ok = mbar_wait_bounded(&q_ready[0], n_piece & 1, limit, abort_flag) &&
+                             mbar_wait_bounded(&q_ready[1], n_piece & 1, limit, abort_flag);
+                    else
+                        ok = mbar_wait_bounded(q_full, n_piece & 1, limit, abort_flag);
+                    ++n_piece;
+                    auto qk = [&](int u) {
+                        const int t = u & 1, j = k_at + (p.two ? u >> 1 : u), st = j % C::KST;
+                        if (!p.two || t == 0) {
+                            ok = mbar_wait_bounded(&k_full[st], (j / C::KST) & 1, limit, abort_flag);
+                            if (!ok) return;
+                        }
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kk = 0; kk < DQK / 16; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kPreTile * 128) + (kk & 3) * 32;
+                            umma_bf16(tbase + C::S_COL + t * kPreKeys, smem_desc_sw128(q_addr + t * C::Q_BYTES + off, 16, 1024),
+                                      smem_desc_sw128(k_addr + st * C::K_BYTES + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&s_full[t]);
+                        if (!p.two || t == 1) umma_commit(&k_empty[st]);
+                        if (u == p.units - 1) umma_commit(q_empty);
+                    };
+                    if (ok) qk(0);
+                    if (ok && p.units > 1) qk(1);
+                    for (int u = 0; ok && u < p.units; ++u) {
+                        const int t = u & 1, j = v_at + (p.two ? u >> 1 : u), st = j % C::VST;
+                        if (!p.two || t == 0) {
+                            ok = mbar_wait_bounded(&v_full[st], (j / C::VST) & 1, limit, abort_flag);
+                            if (!ok) break;
+                        }
+                        ok = mbar_wait_bounded(&p_full[t], p_phase >> t & 1, limit, abort_flag);
+                        p_phase ^= 1u << t;
+                        if (!ok) break;
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int kg = 0; kg < kPreKeys / 16; ++kg)
+                            umma_bf16_ta(tbase + C::O_COL + t * DV, tbase + C::S_COL + t * kPreKeys + kg * 8,
+                                         smem_desc_sw128(v_addr + st * C::V_BYTES + kg * 2048, kPreKeys * 128, 1024), idesc_pv,
+                                         (u > 1 || kg > 0) ? 1u : 0u);
+                        if (!p.two || t == 1) umma_commit(&v_empty[st]);
+                        if (u + 2 >= p.units) umma_commit(&o_full[t]);
+                        if (u + 2 < p.units) qk(u + 2);
+                    }
+                    k_at += p.s1 - p.s0;
+                    v_at += p.s1 - p.s0;
+                }
+                if (!ok) {
+                    flag_error(a.err, kErrTimeout);
+                    *abort_flag = 1;
+                }
+                umma_commit(fin);
+                mbar_wait_bounded(fin, 0, limit, nullptr);
+            }
+        } else if (warp == 9 || (C::TMA && warp == 10)) {
+            // -------------------------------------------------------- loads: Q and K, or V
+            const bool is_k = warp == 9;
+            const int stages = is_k ? C::KST : C::VST, chunks = is_k ? C::QC : C::VC;
+            const int stage_bytes = is_k ? C::K_BYTES : C::V_BYTES;
+            uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+            uint8_t *ring = smem + (is_k ? C::K_OFF : C::V_OFF);
+            const CUtensorMap *map = is_k ? &tm_k : &tm_v;
+            int n_piece = 0, at = 0;
+            uint32_t raw_next = 0, raw_last = 0;  // a bit a stage: parity of its next uncleared step, whether its last was one
+            while (ok && walk.next(&p)) {
+                if (p.units == 0) continue;
+                if (is_k) {
+                    ok = n_piece == 0 || mbar_wait_bounded(q_empty, (n_piece - 1) & 1, limit, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    ++n_piece;
+                    if (lane == 0) {
+                        const int tiles = p.units > 1 ? 2 : 1;
+                        mbar_arrive_expect_tx(q_full, tiles * C::QC * a.g_tile * a.tok_tile * 128);
+                        for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                            for (int c = 0; c < C::QC; ++c)
+                                tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + c * (kPreTile * 128), &tm_q, q_full, c * 64,
+                                            p.g * a.G + p.hb * a.g_tile, p.item.q_row + (p.two ? t * a.tok_tile : 0));
+                    }
+                    __syncwarp();
+                }
+                for (int step = p.s0; C::TMA && ok && step < p.s1; ++step, ++at) {
+                    const int st = at % stages;
+                    int row = 0;  // of this lane's box
+                    bool there = false;
+                    if constexpr (SRC == kPrePages) {
+                        const int key = step * kPreKeys + lane * a.box_rows;
+                        there = lane * a.box_rows < kPreKeys && key < p.item.L;
+                        if (there) row = prefill_pool_row(a, p.item.req, key);
+                        if (row < 0) row = a.num_pages * a.page_size;  // past the end: zeros
+                    }
+                    ok = at < stages || mbar_wait_bounded(&empty[st], (at / stages - 1) & 1, limit, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (a.fault_mode == 1 && is_k && at == 0) continue;  // test hook: this stage never fills
+                    uint8_t *dst = ring + st * stage_bytes;
+                    uint64_t *bar = &full[st];
+                    raw_last &= ~(1u << st);
+                    if (!is_k && p.masked(step)) {
+                        bar = &v_raw[st];
+                        raw_last |= 1u << st;
+                        raw_next ^= 1u << st;
+                    }
+                    if constexpr (SRC == kPreDense) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar, stage_bytes);
+                            for (int c = 0; c < chunks; ++c)
+                                tma_load_3d(dst + c * (kPreKeys * 128), map, bar, c * 64, p.g, p.item.k_row + step * kPreKeys);
+                        }
+                    } else {
+                        const int boxes = __popc(__ballot_sync(0xffffffffu, there));
+                        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * chunks * a.box_rows * 128);
+                        __syncwarp();
+                        if (there)
+                            for (int c = 0; c < chunks; ++c)
+                                tma_load_3d(dst + c * (kPreKeys * 128) + lane * a.box_rows * 128, map, bar, c * 64, p.g, row);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok && lane == 0) {
+                flag_error(a.err, kErrTimeout);
+                *abort_flag = 1;
+            }
+            if (lane == 0 && (!ok || *abort_flag)) {
+                // copies in flight land before the CTA goes
+                for (int i = max(0, at - stages); i < at; ++i) {
+                    const int st = i % stages;
+                    if (a.fault_mode == 1 && is_k && i == 0) continue;
+                    if (raw_last >> st & 1) mbar_wait_bounded(&v_raw[st], raw_next >> st & 1 ^ 1, limit, nullptr);
+                    else mbar_wait_bounded(&full[st], (i / stages) & 1, limit, nullptr);
+                }
+                if (is_k && n_piece > 0) mbar_wait_bounded(q_full, (n_piece - 1) & 1, limit, nullptr);
+            }
+        } else if (C::TMA) {
+            // -------------------------------------------------------- V rows that no row may see
+            int at = 0;
+            uint32_t raw_phase = 0;
+            while (ok && walk.next(&p)) {
+                if (p.units == 0) continue;
+                for (int step = p.s0; ok && step < p.s1; ++step) {
+                    const int st = (at + step - p.s0) % C::VST;
+                    if (!p.masked(step)) continue;
+                    ok = mbar_wait_bounded(&v_raw[st], raw_phase >> st & 1, limit, abort_flag);
+                    raw_phase ^= 1u << st;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    bool found = false;
+                    uint8_t *tile = smem + C::V_OFF + st * C::V_BYTES;
+                    const int from = max(0, p.first_limit - step * kPreKeys), gone = p.item.L - step * kPreKeys;
+                    // a quarter warp a 128-byte row piece; the swizzle permutes 16-byte units within it
+                    for (int i = from * 8 + lane; i < kPreKeys * 8; i += 32) {
+                        const int key = i >> 3;
+#pragma unroll
+                        for (int c = 0; c < C::VC; ++c) {
+                            uint4 *x = reinterpret_cast<uint4 *>(tile + c * (kPreKeys * 128) + i * 16);
+                            if (key >= gone) {
+                                *x = make_uint4(0, 0, 0, 0);
+                            } else {
+                                uint4 y = *x;
+                                if (not_finite2<C::F16>(y.x) || not_finite2<C::F16>(y.y) || not_finite2<C::F16>(y.z) ||
+                                    not_finite2<C::F16>(y.w)) {
+                                    found = true;
+                                    *x = make_uint4(finite2<C::F16>(y.x), finite2<C::F16>(y.y), finite2<C::F16>(y.z),
+                                                    finite2<C::F16>(y.w));
+                                }
+                            }
+                        }
+                    }
+                    if (found) *bad_v = 1;
+                    fence_proxy_async_shared();
+                    __threadfence_block();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&v_full[st]);
+                }
+                at += p.s1 - p.s0;
+            }
+            if (!ok && lane == 0) {
+                flag_error(a.err, kErrTimeout);
+                *abort_flag = 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue: a thread a row
+        regs_inc<C::SOFT_REGS>();
+        const int t = warp >> 2;
+        const int row = threadIdx.x & 127;
+        const int tok_in = row / a.g_tile, head_in = row - tok_in * a.g_tile;
+        const uint32_t lane_base = tbase + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t s_at = lane_base + C::S_COL + t * kPreKeys;
+        PrefillWalk walk(a, blockIdx.x);
+        PrefillPiece p;
+        uint32_t s_phase = 0, o_phase = 0, stat_phase = 0, q_phase = 0;
+        int par_at = 0;  // steps before this piece
+        while (ok && walk.next(&p)) {
+            const int tok = tok_in + (p.two ? t * a.tok_tile : 0);
+            const bool real = tok_in < a.tok_tile && tok < p.item.n_tok && p.hb * a.g_tile + head_in < a.G;
+            const int seen = !real ? 0 : a.causal ? min(max(p.item.limit0 + tok, 0), p.item.L) : p.item.L;
+            const bool idle = !__any_sync(0xffffffffu, real);  // nothing in this warp's rows: it only keeps step
+            const int all_see = __reduce_min_sync(0xffffffffu, real ? seen : 0x7fffffff);
+            const int n_units = p.units == 0 ? 0 : p.units_of(t);
+            float alpha = a.alpha, v_scale = a.v_scale;
+            if constexpr (C::F16) {
+                if (a.k_scales != nullptr) {
+                    alpha *= a.k_scales[a.n_scales > 1 ? p.g : 0];
+                    v_scale = a.v_scales[a.n_scales > 1 ? p.g : 0];
+                }
+            }
+            float q_sum = 0.f;  // of the row as the product takes it
+            if constexpr (C::F16) {
+                if (p.units > 0) {
+                    ok = mbar_wait_bounded(q_full, q_phase, limit, abort_flag);
+                    q_phase ^= 1;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (!idle && n_units > 0) {
+                        uint8_t *q = smem + C::Q_OFF + t * C::Q_BYTES + row * 128;
+                        auto unit = [&](int u) {
+                            return reinterpret_cast<uint4 *>(q + (u >> 3) * (kPreTile * 128) + (((u & 7) ^ (row & 7)) << 4));
+                        };
+                        uint32_t top = 0;  // of the magnitudes' bits, two 16-bit halves
+#pragma unroll 4
+                        for (int u = 0; u < DQK / 8; ++u) {
+                            const uint4 x = *unit(u);
+                            top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu)),
+                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+                        }
+                        const int e = int(max(top & 0xffffu, top >> 16) >> 7);  // exponent field of the largest
+                        // the largest comes to [2^14, 2^15); rows of zeros, infinities and NaN stay as they are, and rows
+                        // below 2^-113 end lower
+                        const int up = e == 0xff ? 0 : min(141 - e, 127);
+                        const float two_up = __int_as_float((up + 127) << 23);
+                        const float flip = alpha < 0.f ? -two_up : two_up;  // a negative scale goes into Q: the maximum wants a positive one
+#pragma unroll 4
+                        for (int u = 0; u < DQK / 8; ++u) {
+                            const uint4 x = prefill_q_unit<SRC>(*unit(u), flip);
+                            if constexpr (C::K_PARAMS) {
+                                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                                    q_sum += f.x + f.y;
+                                }
+                            }
+                            *unit(u) = x;
+                        }
+                        alpha = ldexpf(fabsf(alpha), -up);
+                        fence_proxy_async_shared();
+                    }
+                    mbar_arrive(&q_ready[t]);
+                }
+            }
+            if (alpha < 1e-37f) alpha = 1e-37f;  // a scale of zero must not make NaN of a masked score
+            float m_ref = -INFINITY, l = 0.f;  // reference (log2 domain), sum of the weights
+            for (int i = 0; i < n_units; ++i) {
+                ok = mbar_wait_bounded(&s_full[t], s_phase, limit, abort_flag);
+                s_phase ^= 1;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (!idle) {
+                    tc_fence_after_sync();
+                    uint32_t sr[kPreKeys / 32][32];
+#pragma unroll
+                    for (int h = 0; h < kPreKeys / 32; ++h) tmem_ld32(s_at + h * 32, sr[h]);
+                    tmem_wait_ld();
+                    const int step = p.step_of(p.two ? 2 * i : 2 * i + t), key0 = step * kPreKeys;
+                    if constexpr (C::K_PARAMS) {
+                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF) +
+                                            (par_at + step - p.s0) % C::PST * (kPreKeys / 2);
+                        const float2 qs2 = make_float2(q_sum, q_sum);
+#pragma unroll
+                        for (int c = 0; c < kPreKeys; c += 2) {
+                            const float4 y = par[c / 2];
+                            const float2 x = fma2(make_float2(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1])),
+                                                  make_float2(y.x, y.y), mul2(qs2, make_float2(y.z, y.w)));
+                            sr[c >> 5][c & 31] = __float_as_uint(x.x);
+                            sr[c >> 5][(c & 31) + 1] = __float_as_uint(x.y);
+                        }
+                    }
+                    if (key0 + kPreKeys > all_see) {
+                        const int left = seen - key0;
+#pragma unroll
+                        for (int h = 0; h < kPreKeys / 32; ++h)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (h * 32 + c >= left) sr[h][c] = __float_as_uint(-INFINITY);
+                    }
+                    // the maximum over four chains of three-input maxima (exact); scores stay raw, the scale enters through
+                    // the maximum (exact: it is not negative) and one fma a weight
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < kPreKeys / 32; ++h)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2)
+                            m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(sr[h][c]), __uint_as_float(sr[h][c + 1]));
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * alpha;
+                    const bool renew = mx > m_ref + kPreRescaleLog2;
+                    const bool rescale = renew && i > 0 && m_ref != -INFINITY;
+                    if (__any_sync(0xffffffffu, rescale)) {
+                        const float corr = rescale ? fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+                        for (int c = 0; c < DV / 32; ++c) {
+                            uint32_t ov[32];
+                            tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 o2 = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                                                       make_float2(corr, corr));
+                                ov[e] = __float_as_uint(o2.x);
+                                ov[e + 1] = __float_as_uint(o2.y);
+                            }
+                            tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                        }
+                        l *= corr;
+                    }
+                    if (renew) m_ref = mx;
+                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                    // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in
+                    // fp32 before they are rounded for the product
+                    const float2 al2 = make_float2(alpha, alpha), nm2 = make_float2(-m_use, -m_use);
+                    float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c2 = 0; c2 < 32; ++c2) {
+                            const int c = half * 64 + 2 * c2;
+                            const float2 x = fma2(make_float2(__uint_as_float(sr[c >> 5][c & 31]),
+                                                              __uint_as_float(sr[c >> 5][(c & 31) + 1])), al2, nm2);
+                            const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            sum2[c2 & 1] = add2(sum2[c2 & 1], w);
+                            pk[c2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                        }
+                        tmem_st32(s_at + half * 32, pk);
+                    }
+                    tmem_wait_st();
+                    l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
+                    tc_fence_before_sync();
+                }
+                mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            par_at += p.s1 - p.s0;
+
+            // ---- epilogue: row group t's own rows, or (one tile) group 0 for both
+            const bool join = !p.two && p.units > 1;
+            if (n_units > 0) {
+                ok = mbar_wait_bounded(&o_full[t], o_phase, limit, abort_flag);
+                o_phase ^= 1;
+            }
+            if (join && t == 0) {  // group 1 hands its part over once its own O is there
+                ok = ok && mbar_wait_bounded(stat_full, stat_phase, limit, abort_flag);
+                stat_phase ^= 1;
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (join && t == 1) {
+                stat[row] = make_float2(m_ref, l);
+                tc_fence_before_sync();
+                mbar_arrive(stat_full);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(stat_free, stat_phase, limit, abort_flag));
+                stat_phase ^= 1;
+                if (!ok) break;
+            }
+            if (p.two || t == 0) {
+                float f0 = 1.f, f1 = 0.f;
+                if (join) {
+                    const float2 other = stat[row];
+                    const float m = fmaxf(m_ref, other.x), use = m == -INFINITY ? 0.f : m;
+                    f0 = fast_exp2(m_ref - use);
+                    f1 = fast_exp2(other.x - use);
+                    l = l * f0 + other.y * f1;
+                    m_ref = m;
+                }
+                if (!idle) {
+                    const bool any = real && l != 0.f;  // a row that sees no key is zeros (a sum of NaN is not zero)
+                    const float inv = any ? v_scale / l : 0.f;
+                    const float lse2 = any ? m_ref + log2f(l) : -INFINITY;
+                    const bool fix = n_units > 0 && p.s1 * kPreKeys > p.first_limit && *bad_v != 0;
+                    const long long out_row = (long long)(p.item.q_row + tok) * a.Hq + p.g * a.G + p.hb * a.g_tile + head_in;
+                    const int part_row = (p.slot * 2 + (p.two ? t : 0)) * kPreTile + row;
+#pragma unroll 1
+                    for (int c = 0; c < DV / 32; ++c) {
+                        float o[32];
+                        if (n_units > 0) {
+                            uint32_t ov[32];
+                            tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                            if (join) {
+                                uint32_t ow[32];
+                                tmem_ld32(lane_base + C::O_COL + DV + c * 32, ow);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = (__uint_as_float(ov[e]) * f0 + __uint_as_float(ow[e]) * f1) * inv;
+                            } else {
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(ov[e]) * inv;
+                            }
+                        }
+                        if (!any) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        }
+                        if (!real) continue;
+                        if constexpr (SRC == kPreInt4) {  // back from the order that 4-bit codes come in
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                const float x1 = o[e + 1], x2 = o[e + 2], x3 = o[e + 3], x4 = o[e + 4], x5 = o[e + 5], x6 = o[e + 6];
+                                o[e + 1] = x2, o[e + 2] = x4, o[e + 3] = x6, o[e + 4] = x1, o[e + 5] = x3, o[e + 6] = x5;
+                            }
+                        }
+                        if (p.slot < 0) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * DV + c * 32);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                                    pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(a.o_part + (long long)part_row * DV + c * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    if (fix && any) {
+                        const int key0 = max(p.first_limit, p.s0 * kPreKeys), key1 = min(seen, p.s1 * kPreKeys);
+                        if (p.slot < 0)
+                            prefill_add_not_finite<DV, SRC>(a, p.item.req, p.item.k_row, p.g, key0, key1, a.out + out_row * DV);
+                        else
+                            prefill_add_not_finite<DV, SRC>(a, p.item.req, p.item.k_row, p.g, key0, key1,
+                                                            a.o_part + (long long)part_row * DV);
+                    }
+                    if (real) {
+                        if (p.slot >= 0) a.lse_part[part_row] = lse2;
+                        else if (a.lse != nullptr) a.lse[out_row] = lse2 * 0.69314718055994530942f;
+                    }
+                }
+                if (join) {
+                    tc_fence_before_sync();
+                    mbar_arrive(stat_free);
+                }
+            }
+            tc_fence_before_sync();  // O is read before the next piece's first weights are handed over
+        }
+        if (!ok) {
+            flag_error(a.err, kErrTimeout);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+    }
+
+    // every product is done (the issuer waited for it) and every TMEM access made
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after_sync();
+        tmem_dealloc(tbase, C::TMEM_COLS);
+    }
+}
+
+// Joins the partial results of items whose steps several workers hold.  CTA (w, r): if worker w's share begins within an item
+// and is the first to do so there, rows r * kPreMergeRows .. of that item: the part that worker w - 1 ended with, then
+// those of w and the workers after it, in their order.
+constexpr int kPreMergeRows = 16;
+constexpr int kPreMergeThreads = 256;
+
+template <int DV>
+__global__ void __launch_bounds__(kPreMergeThreads) gqa_prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
+    pdl_wait_primary();
+    const int w = blockIdx.x + 1;
+    const int2 cut = a.cuts[w];
+    if (cut.y == 0) return;
+    const int2 prev = a.cuts[w - 1];
+    if (prev.x == cut.x && prev.y > 0) return;  // joined from the first cut of the item
+    int last = w;  // the last worker with a cut in the item
+    while (last + 1 < a.workers && a.cuts[last + 1].x == cut.x && a.cuts[last + 1].y > 0) ++last;
+    const PrefillItem it = a.items[cut.x / a.head_blocks];
+    const int h = cut.x % a.head_blocks, per = a.head_blocks / a.Hkv;
+    const int rows = (it.n_tok > a.tok_tile ? 2 : 1) * kPreTile;
+    constexpr int LANES = DV / 4;  // threads of a row
+    for (int r = blockIdx.y * kPreMergeRows + threadIdx.x / LANES; r < min(rows, int(blockIdx.y + 1) * kPreMergeRows);
+         r += kPreMergeThreads / LANES) {
+        const int tile = r / kPreTile, in = r % kPreTile;
+        const int tok = tile * a.tok_tile + in / a.g_tile, head = (h % per) * a.g_tile + in % a.g_tile;
+        if (in / a.g_tile >= a.tok_tile || tok >= it.n_tok || head >= a.G) continue;
+        const int d = threadIdx.x % LANES * 4;
+        float top = -INFINITY;
+        auto none = [&](int x) {  // an empty share between two cuts at one place
+            return x >= w && a.cuts[x].x == a.cuts[x + 1].x && a.cuts[x].y == a.cuts[x + 1].y;
+        };
+        for (int x = w - 1; x <= last; ++x) {
+            if (none(x)) continue;
+            const int slot = x == w - 1 ? 2 * x + 1 : 2 * x;
+            top = fmaxf(top, a.lse_part[slot * 2 * kPreTile + r]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+        float total = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = w - 1; x <= last; ++x) {
+            if (none(x)) continue;
+            const int at = (x == w - 1 ? 2 * x + 1 : 2 * x) * 2 * kPreTile + r;
+            const float lse = a.lse_part[at], f = exp2f(lse - ref);
+            if (lse == -INFINITY) continue;
+            total += f;
+            const float4 y = *reinterpret_cast<const float4 *>(a.o_part + (long long)at * DV + d);
+            o.x += f * y.x, o.y += f * y.y, o.z += f * y.z, o.w += f * y.w;
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const long long row = (long long)(it.q_row + tok) * a.Hq + h / per * a.G + head;
+        *reinterpret_cast<uint2 *>(a.out + row * DV + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (a.lse != nullptr && d == 0) a.lse[row] = total == 0.f ? -INFINITY : (ref + log2f(total)) * 0.69314718055994530942f;
+    }
+}
+
+}  // namespace gqa
