@@ -69,10 +69,10 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!raised[dev]) {
-            // The kernel's warps share its registers out anew, which waits for ever if they are fewer than counted on.
+            // The kernel's warps share its registers out anew, which goes wrong if they are not as many as counted on.
             cudaFuncAttributes at;
             if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess ||
-                cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * C::THREADS < C::REGS) {
+                cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs != C::LAUNCH_REGS) {
                 cudaGetLastError();
                 return GQA_ERR_CUDA;
             }

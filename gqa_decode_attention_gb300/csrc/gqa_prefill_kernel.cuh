@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
     bool ok = true;
     if (!C::TMA && warp >= 12) {
         if constexpr (!C::TMA) {
-            regs_dec<C::LOAD_REGS>();
+            set_registers<C::LAUNCH_REGS, C::LOAD_REGS>();
             ok = prefill_load<DQK, DV, SRC>(a, smem, k_full, k_empty, v_full, v_empty, abort_flag, bad_v);
         }
         if (!ok && lane == 0) {
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         }
         __syncwarp();
     } else if (warp >= 8) {
-        regs_dec<C::OTHER_REGS>();
+        set_registers<C::LAUNCH_REGS, C::OTHER_REGS>();
         PrefillWalk walk(a, blockIdx.x);
         PrefillPiece p;
         if (warp == 8) {
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue: a thread a row
-        regs_inc<C::SOFT_REGS>();
+        set_registers<C::LAUNCH_REGS, C::SOFT_REGS>();
         const int t = warp >> 2;
         const int row = threadIdx.x & 127;
         const int tok_in = row / a.g_tile, head_in = row - tok_in * a.g_tile;
@@ -424,40 +424,64 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 if (!ok) break;
                 if (!idle) {
                     tc_fence_after_sync();
-                    uint32_t sr[kPreKeys / 32][32];
-#pragma unroll
-                    for (int h = 0; h < kPreKeys / 32; ++h) tmem_ld32(s_at + h * 32, sr[h]);
-                    tmem_wait_ld();
                     const int step = p.step_of(p.two ? 2 * i : 2 * i + t), key0 = step * kPreKeys;
-                    if constexpr (C::K_PARAMS) {
-                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF) +
-                                            (par_at + step - p.s0) % C::PST * (kPreKeys / 2);
-                        const float2 qs2 = make_float2(q_sum, q_sum);
+                    const bool masked = key0 + kPreKeys > all_see;
+                    const int left = seen - key0;
+                    // With registers for a row's 128 scores they are read once, else a second time for the weights.
+                    constexpr int BUFS = C::TMA ? 4 : 2;
+                    uint32_t sr[BUFS][32];
+                    // Scores h * 32 .. of the row as they go into the maximum; raw, the scale enters through the maximum (exact:
+                    // it is positive) and one fma a weight.
+                    auto hide = [&](uint32_t (&x)[32], int h) {
 #pragma unroll
-                        for (int c = 0; c < kPreKeys; c += 2) {
-                            const float4 y = par[c / 2];
-                            const float2 x = fma2(make_float2(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[c >> 5][(c & 31) + 1])),
-                                                  make_float2(y.x, y.y), mul2(qs2, make_float2(y.z, y.w)));
-                            sr[c >> 5][c & 31] = __float_as_uint(x.x);
-                            sr[c >> 5][(c & 31) + 1] = __float_as_uint(x.y);
-                        }
-                    }
-                    if (key0 + kPreKeys > all_see) {
-                        const int left = seen - key0;
-#pragma unroll
-                        for (int h = 0; h < kPreKeys / 32; ++h)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (h * 32 + c >= left) sr[h][c] = __float_as_uint(-INFINITY);
-                    }
-                    // the maximum over four chains of three-input maxima (exact); scores stay raw, the scale enters through
-                    // the maximum (exact: it is not negative) and one fma a weight
+                        for (int c = 0; c < 32; ++c)
+                            if (h * 32 + c >= left) x[c] = __float_as_uint(-INFINITY);
+                    };
+                    // the maximum over four chains of three-input maxima (exact)
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if constexpr (BUFS == 4) {
 #pragma unroll
-                    for (int h = 0; h < kPreKeys / 32; ++h)
+                        for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
+                        tmem_wait_ld();
+                    } else {
+                        tmem_ld32(s_at, sr[0]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t (&x)[32] = sr[h % BUFS];
+                        if constexpr (BUFS == 2) {
+                            tmem_wait_ld();
+                            // (scores that go back with their parameters applied are read again after the last is written)
+                            if (h < 3 || !C::K_PARAMS) tmem_ld32(s_at + (h + 1) % 4 * 32, sr[(h + 1) % 2]);
+                        }
+                        if constexpr (C::K_PARAMS) {
+                            const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512) + h * 8;
+                            const float2 qs2 = make_float2(q_sum, q_sum);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const uint4 y = par[c / 4];
+                                const uint32_t w[4] = {y.x, y.y, y.z, y.w};  // scales of two keys, zeros of two keys, twice
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e]));
+                                    const float2 kz = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e + 1]));
+                                    const float2 z = fma2(make_float2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), ks,
+                                                          mul2(qs2, kz));
+                                    x[c + 2 * e] = __float_as_uint(z.x);
+                                    x[c + 2 * e + 1] = __float_as_uint(z.y);
+                                }
+                            }
+                        }
+                        if (masked) hide(x, h);
 #pragma unroll
                         for (int c = 0; c < 32; c += 2)
-                            m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(sr[h][c]), __uint_as_float(sr[h][c + 1]));
+                            m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        if constexpr (C::K_PARAMS) tmem_st32(s_at + h * 32, x);
+                    }
+                    if constexpr (C::K_PARAMS) {
+                        tmem_wait_st();
+                        tmem_ld32(s_at, sr[0]);
+                    }
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * alpha;
                     const bool renew = mx > m_ref + kPreRescaleLog2;
                     const bool rescale = renew && i > 0 && m_ref != -INFINITY;
@@ -486,18 +510,22 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const float2 al2 = make_float2(alpha, alpha), nm2 = make_float2(-m_use, -m_use);
                     float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int c2 = 0; c2 < 32; ++c2) {
-                            const int c = half * 64 + 2 * c2;
-                            const float2 x = fma2(make_float2(__uint_as_float(sr[c >> 5][c & 31]),
-                                                              __uint_as_float(sr[c >> 5][(c & 31) + 1])), al2, nm2);
-                            const float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                            sum2[c2 & 1] = add2(sum2[c2 & 1], w);
-                            pk[c2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t (&x)[32] = sr[h % BUFS];
+                        if constexpr (BUFS == 2) {
+                            tmem_wait_ld();
+                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) % 2]);
+                            if (masked && !C::K_PARAMS) hide(x, h);
                         }
-                        tmem_st32(s_at + half * 32, pk);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), al2, nm2);
+                            const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], w);
+                            pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                        }
+                        tmem_st16(s_at + h * 16, pk);  // (columns whose scores have been read)
                     }
                     tmem_wait_st();
                     l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);

@@ -2,6 +2,8 @@
 // registers: pools of codes, converted to fp16, and bf16 pools whose pages are no multiple of 8 tokens.
 #pragma once
 
+#include <type_traits>
+
 #include "gqa_prefill_plan.cuh"
 
 namespace gqa {
@@ -15,8 +17,8 @@ struct PrefillCfg {
     static constexpr int Q_BYTES = QC * kPreTile * 128;
     static constexpr int K_BYTES = QC * kPreKeys * 128;
     static constexpr int V_BYTES = VC * kPreKeys * 128;
-    static constexpr int KST = DQK == 192 || (DQK == 128 && K_PARAMS) ? 2 : DQK == 128 ? 3 : 5;
-    static constexpr int VST = DQK == 192 ? 1 : DQK == 128 ? 2 : 5;
+    static constexpr int KST = DQK == 192 || (DQK == 128 && F16) ? 2 : DQK == 128 ? 3 : F16 ? 4 : 5;
+    static constexpr int VST = DQK == 192 ? 1 : DQK == 128 ? 2 : F16 ? 4 : 5;
     // A key's parameters are read until its step's weights are out: when a stage of K is free for the KST-th step after it,
     // the weights of the second step before that one are (one tile an item; of the first with two).
     static constexpr int PST = KST + 2;
@@ -24,27 +26,30 @@ struct PrefillCfg {
     static constexpr int K_OFF = 2 * Q_BYTES;
     static constexpr int V_OFF = K_OFF + KST * K_BYTES;
     static constexpr int STAT_OFF = V_OFF + VST * V_BYTES;  // [128] float2: what row group 1 hands over
-    static constexpr int PAR_OFF = STAT_OFF + 1024;         // [PST][64] float4: scales, zeros of two keys
-    static constexpr int BAR_OFF = PAR_OFF + (K_PARAMS ? PST * 1024 : 0);
+    static constexpr int PAR_OFF = STAT_OFF + 1024;         // [PST][64] uint2: fp16 scales of two keys, their zeros
+    static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * 512 : 0);  // codes of K and of V on their way
+    static constexpr int RAW_BYTES = !F16 ? 0 : kPreKeys * DV / (SRC == kPreInt4 ? 2 : 1);
+    static constexpr int BAR_OFF = RAW_OFF + 2 * RAW_BYTES;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     // Registers by warp group, shared out anew from the launch's 168 or 128 a thread (softmax, the group of warp 8, loaders).
     static constexpr int THREADS = TMA ? 384 : 512;
     static constexpr int SOFT_REGS = TMA ? 224 : 176, OTHER_REGS = TMA ? 56 : 64, LOAD_REGS = 96;
     static constexpr int REGS = 256 * SOFT_REGS + 128 * OTHER_REGS + (TMA ? 0 : 128 * LOAD_REGS);
-    static_assert(REGS <= 65536, "registers");
+    static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
+    static_assert(REGS <= LAUNCH_REGS * THREADS, "registers");
     static constexpr uint32_t S_COL = 0, O_COL = 2 * kPreKeys;
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(O_COL + 2 * DV <= TMEM_COLS, "TMEM");
 };
 
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// The warp group's registers a thread from here on; FROM is what it was launched with.  (Giving registers back with a
+// number above the present one, or asking for more with one below, is undefined.)
+template <int FROM, int N>
+__device__ __forceinline__ void set_registers() {
+    static_assert(N % 8 == 0 && N >= 24 && N <= 256, "registers");
+    if constexpr (N > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Any of the two 16-bit halves infinite or NaN.
@@ -185,44 +190,65 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
         hand_on(0);
         cp_async_wait_all();
     } else {
-        // Codes: a step's pieces of K are in registers while V's are converted and the other way round.
+        // Codes: a step's pieces of K are on their way while V's are converted and the other way round.  They wait in shared
+        // memory, each thread's where nobody else looks, so that a thread only waits for its own copies.  (In registers they
+        // came through L1, which beside this much shared memory is smaller than what should be on its way: a mixed step of 32
+        // requests over an FP8 cache took 2836 us.)
         constexpr int PER = SRC == kPreInt4 ? 2 : 4;        // pieces of a 64-element chunk
         constexpr int ROWS = 32 / PER;                      // rows of a warp's load
         constexpr int N = 32 / ROWS * C::VC;                // loads of a lane
         constexpr int ROW_BYTES = SRC == kPreInt4 ? DV / 2 : DV;
         const int in_chunk = lane & (PER - 1), in_rows = lane / PER;
-        uint4 kc[N], vc[N];
+        const uint32_t raw = smem_u32(smem + C::RAW_OFF) + (threadIdx.x & 127) * 16;
+        const int row_bytes = a.Hkv * ROW_BYTES;
         uint2 par = {}, next_par = {};
         int row = -1, next_row = -1;
+        // Page ids two steps ahead, rows one step ahead: nothing waits for a load that it has just asked for.
+        int page = 0;
+        const int *table = nullptr;
+        auto look_ahead = [&](int step) {
+            const int key = step * kPreKeys + lw * 32 + lane;
+            if (key < p.item.L) page = table[key / a.page_size];
+        };
         auto look_up = [&](int step) {
             const int key = step * kPreKeys + lw * 32 + lane;
-            next_row = key < p.item.L ? prefill_pool_row(a, p.item.req, key) : -1;
+            next_row = -1;
+            if (key < p.item.L && step < p.s1) {
+                if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrIndex);
+                else next_row = page * a.page_size + key % a.page_size;
+            }
             if constexpr (SRC == kPreInt4) {
                 next_par = make_uint2(0, 0);
                 if (next_row >= 0) next_par = __ldg(reinterpret_cast<const uint2 *>(a.params) + (long long)next_row * a.Hkv + p.g);
             }
         };
-        auto load = [&](uint4 (&c)[N], const uint8_t *pool, int r) {
+        auto load = [&](bool is_v, const uint8_t *pool, int r) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
+            for (int i = 0; i < N; i += C::VC) {
                 const int from = __shfl_sync(0xffffffffu, r, i / C::VC * ROWS + in_rows);
-                c[i] = make_uint4(0, 0, 0, 0);
-                if (from >= 0)
-                    c[i] = __ldg(reinterpret_cast<const uint4 *>(pool + ((long long)from * a.Hkv + p.g) * ROW_BYTES +
-                                                                 (i % C::VC * PER + in_chunk) * 16));
+                const uint8_t *src = pool + (long long)max(from, 0) * row_bytes;
+#pragma unroll
+                for (int x = 0; x < C::VC; ++x)
+                    cp_async16_or_zero(raw + (is_v ? C::RAW_BYTES : 0) + (i + x) * 2048, src + x * PER * 16, from >= 0);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
         // first_clean: keys of the step from here on may hold what some row must not see
-        auto store = [&](const uint4 (&c)[N], uint8_t *tile, bool is_v, int first_clean) {
+        auto store = [&](auto is_v_t, auto clean_t, uint8_t *tile, int first_clean) {
+            constexpr bool is_v = decltype(is_v_t)::value, clean = decltype(clean_t)::value;
             bool found = false;
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the other one's newest copies
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int in = i / C::VC * ROWS + in_rows, k = lw * 32 + in;
                 uint8_t *dst = tile + i % C::VC * CHUNK + k * 128;
-                const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(raw + (is_v ? C::RAW_BYTES : 0) + i * 2048));
                 __half2 vs = {}, vz = {};
                 if constexpr (SRC == kPreInt4) {
-                    if (is_v) {
+                    if constexpr (is_v) {
                         const uint32_t x = __shfl_sync(0xffffffffu, par.y, in);
                         const __half2 y = *reinterpret_cast<const __half2 *>(&x);
                         vs = __low2half2(y), vz = __high2half2(y);
@@ -235,7 +261,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                     for (int e = 0; e < 4; ++e) {
                         if constexpr (SRC == kPreInt4) {
                             __half2 x = widen_int4(w[u], e);
-                            if (is_v) {
+                            if constexpr (is_v) {
                                 // values past fp16's largest are it; a parameter that is not finite is NaN already
                                 const __half2 big(__half_raw{0x7bff}, __half_raw{0x7bff});
                                 x = __hmin2_nan(__hmax2_nan(__hfma2(x, vs, vz), __hneg2(big)), big);
@@ -245,11 +271,13 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                             o[e] = widen_pair<SRC>(w[2 * u + (e >> 1)], e & 1);
                         }
                     }
-                    if (SRC != kPreInt8 && is_v && k >= first_clean) {
+                    if constexpr (clean) {
+                        if (k >= first_clean) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            found |= not_finite2<true>(o[e]);
-                            o[e] = finite2<true>(o[e]);
+                            for (int e = 0; e < 4; ++e) {
+                                found |= not_finite2<true>(o[e]);
+                                o[e] = finite2<true>(o[e]);
+                            }
                         }
                     }
                     *reinterpret_cast<uint4 *>(dst + (((in_chunk * (8 / PER) + u) ^ (k & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -259,46 +287,52 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
         };
         while (ok && walk.next(&p)) {
             if (p.units == 0) continue;
+            const uint8_t *k_pool = a.k_pool + p.g * ROW_BYTES + in_chunk * 16, *v_pool = a.v_pool + p.g * ROW_BYTES + in_chunk * 16;
+            table = a.page_table + (long long)p.item.req * a.pages_per_req;
+            look_ahead(p.s0);
             look_up(p.s0);
             row = next_row, par = next_par;
-            load(kc, a.k_pool, row);
-            load(vc, a.v_pool, row);
+            look_ahead(p.s0 + 1);
+            load(false, k_pool, row);
+            load(true, v_pool, row);
             for (int step = p.s0; step < p.s1; ++step, ++at) {
-                const bool more = step + 1 < p.s1;
-                if (more) look_up(step + 1);
+                look_up(step + 1);
+                look_ahead(step + 2);
                 if constexpr (SRC == kPreInt4) {
-                    const bool fine = (par.x & 0x7c00u) != 0x7c00u && (par.x & 0x7c000000u) != 0x7c000000u;
+                    if ((par.x & 0x7c00u) == 0x7c00u || (par.x & 0x7c000000u) == 0x7c000000u) par.x = 0x7fff7fffu;
                     if ((par.y & 0x7c00u) == 0x7c00u || (par.y & 0x7c000000u) == 0x7c000000u) par.y = 0x7fff7fffu;
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.x));
-                    const float scale = fine ? f.x : NAN, zero = f.y;
-                    const float scale1 = __shfl_down_sync(0xffffffffu, scale, 1), zero1 = __shfl_down_sync(0xffffffffu, zero, 1);
+                    const uint32_t of_next = __shfl_down_sync(0xffffffffu, par.x, 1);
                     // (the ring of parameters is free when the stage of K is, see PST)
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if ((lane & 1) == 0)
-                        reinterpret_cast<float4 *>(smem + C::PAR_OFF)[at % C::PST * (kPreKeys / 2) + (lw * 32 + lane) / 2] =
-                            make_float4(scale, scale1, zero, zero1);
+                        reinterpret_cast<uint2 *>(smem + C::PAR_OFF)[at % C::PST * (kPreKeys / 2) + (lw * 32 + lane) / 2] =
+                            make_uint2(__byte_perm(par.x, of_next, 0x5410), __byte_perm(par.x, of_next, 0x7632));
                 } else {
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
-                store(kc, smem + C::K_OFF + at % C::KST * C::K_BYTES, false, 0);
+                store(std::false_type(), std::false_type(), smem + C::K_OFF + at % C::KST * C::K_BYTES, 0);
                 fence_proxy_async_shared();
                 if (!(a.fault_mode == 1 && at == 0)) mbar_arrive(&k_full[at % C::KST]);  // test hook: the first stage never fills
-                if (more) load(kc, a.k_pool, next_row);
+                load(false, k_pool, next_row);
                 ok = at < C::VST || mbar_wait_bounded(&v_empty[at % C::VST], (at / C::VST - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                store(vc, smem + C::V_OFF + at % C::VST * C::V_BYTES, true, p.first_limit - step * kPreKeys);
+                if (SRC != kPreInt8 && p.masked(step))
+                    store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, p.first_limit - step * kPreKeys);
+                else
+                    store(std::true_type(), std::false_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, 0);
                 fence_proxy_async_shared();
                 __threadfence_block();
                 mbar_arrive(&v_full[at % C::VST]);
-                if (more) load(vc, a.v_pool, next_row);
+                load(true, v_pool, next_row);
                 row = next_row, par = next_par;
             }
         }
+        cp_async_wait_all();
     }
     return ok;
 }
