@@ -66,6 +66,33 @@ __device__ __noinline__ void prefill_add_not_finite(const PrefillArgs &a, int re
     }
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Shared-memory matrix descriptors of 128-byte-swizzled operands (smem_desc_sw128) in two words: the low one moves by
+// offset / 16, the high one is the same for all (1024 bytes between groups of 8 rows).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | lbo >> 4 << 16; }
+constexpr uint32_t kDescHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+
+// D[tmem] (+)= A[smem] B[smem], and with A in tensor memory.
+template <bool ADD>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "n"(int(ADD))
+        : "memory");
+}
+template <bool ADD>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "n"(int(ADD))
+        : "memory");
+}
+
 // The row's 8 elements of one 16-byte unit as fp16, times `scale`; the order that 4-bit codes come in for those.
 template <int SRC>
 __device__ __forceinline__ uint4 prefill_q_unit(uint4 x, float scale) {
@@ -151,70 +178,81 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         PrefillPiece p;
         if (warp == 8) {
             // -------------------------------------------------------- products
-            if (lane == 0) {
-                constexpr uint32_t fmt = C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u;
-                constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreKeys, false, false) & fmt;
-                constexpr uint32_t idesc_pv = idesc_bf16_f32(kPreTile, DV, false, true) & fmt;
-                const uint32_t q_addr = smem_u32(smem + C::Q_OFF), k_addr = smem_u32(smem + C::K_OFF),
-                               v_addr = smem_u32(smem + C::V_OFF);
-                int n_piece = 0, k_at = 0, v_at = 0;  // steps used before this piece
-                uint32_t p_phase = 0;
-                while (ok && walk.next(&p)) {
-                    if (p.units == 0) continue;
-                    if constexpr (C::F16)
-                        ok = mbar_wait_bounded(&q_ready[0], n_piece & 1, limit, abort_flag) &&
-                             mbar_wait_bounded(&q_ready[1], n_piece & 1, limit, abort_flag);
-                    else
-                        ok = mbar_wait_bounded(q_full, n_piece & 1, limit, abort_flag);
-                    ++n_piece;
-                    auto qk = [&](int u) {
-                        const int t = u & 1, j = k_at + (p.two ? u >> 1 : u), st = j % C::KST;
-                        if (!p.two || t == 0) {
-                            ok = mbar_wait_bounded(&k_full[st], (j / C::KST) & 1, limit, abort_flag);
-                            if (!ok) return;
-                        }
-                        tc_fence_after_sync();
+            // The whole warp walks, one elected lane issues: what an instruction takes is the same in every lane, and its
+            // descriptors are a base and a constant, so that the issue keeps up with 64 cycles a product while the softmax
+            // warps of this scheduler are busy.
+            constexpr uint32_t fmt = C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u;
+            constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreKeys, false, false) & fmt;
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(kPreTile, DV, false, true) & fmt;
+            const uint32_t q_desc = desc_lo(smem_u32(smem + C::Q_OFF), 16), k_desc = desc_lo(smem_u32(smem + C::K_OFF), 16);
+            const uint32_t v_desc = desc_lo(smem_u32(smem + C::V_OFF), kPreKeys * 128);
+            const bool me = elect_one();
+            int n_piece = 0, at = 0;  // steps used before this piece
+            uint32_t p_phase = 0;
+            while (ok && walk.next(&p)) {
+                if (p.units == 0) continue;
+                if constexpr (C::F16)
+                    ok = mbar_wait_bounded(&q_ready[0], n_piece & 1, limit, abort_flag) &&
+                         mbar_wait_bounded(&q_ready[1], n_piece & 1, limit, abort_flag);
+                else
+                    ok = mbar_wait_bounded(q_full, n_piece & 1, limit, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                ++n_piece;
+                auto qk = [&](int u) {
+                    const int t = u & 1, j = at + (p.two ? u >> 1 : u), st = j % C::KST;
+                    if (!p.two || t == 0) {
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&k_full[st], (j / C::KST) & 1, limit, abort_flag));
+                        if (!ok) return;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t d = tbase + C::S_COL + t * kPreKeys;
+                    const uint32_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + st * (C::K_BYTES >> 4);
+                    const bool last_use = !p.two || t == 1, last = u == p.units - 1;
+                    if (me) {
 #pragma unroll
                         for (int kk = 0; kk < DQK / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kPreTile * 128) + (kk & 3) * 32;
-                            umma_bf16(tbase + C::S_COL + t * kPreKeys, smem_desc_sw128(q_addr + t * C::Q_BYTES + off, 16, 1024),
-                                      smem_desc_sw128(k_addr + st * C::K_BYTES + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+                            const uint32_t off = (kk >> 2) * (kPreTile * 128 >> 4) + (kk & 3) * 2;
+                            if (kk == 0) umma_ss<false>(d, qd, kd, idesc_qk);
+                            else umma_ss<true>(d, qd + off, kd + off, idesc_qk);
                         }
                         umma_commit(&s_full[t]);
-                        if (!p.two || t == 1) umma_commit(&k_empty[st]);
-                        if (u == p.units - 1) umma_commit(q_empty);
-                    };
-                    if (ok) qk(0);
-                    if (ok && p.units > 1) qk(1);
-                    for (int u = 0; ok && u < p.units; ++u) {
-                        const int t = u & 1, j = v_at + (p.two ? u >> 1 : u), st = j % C::VST;
-                        if (!p.two || t == 0) {
-                            ok = mbar_wait_bounded(&v_full[st], (j / C::VST) & 1, limit, abort_flag);
-                            if (!ok) break;
-                        }
-                        ok = mbar_wait_bounded(&p_full[t], p_phase >> t & 1, limit, abort_flag);
-                        p_phase ^= 1u << t;
-                        if (!ok) break;
-                        tc_fence_after_sync();
-#pragma unroll
-                        for (int kg = 0; kg < kPreKeys / 16; ++kg)
-                            umma_bf16_ta(tbase + C::O_COL + t * DV, tbase + C::S_COL + t * kPreKeys + kg * 8,
-                                         smem_desc_sw128(v_addr + st * C::V_BYTES + kg * 2048, kPreKeys * 128, 1024), idesc_pv,
-                                         (u > 1 || kg > 0) ? 1u : 0u);
-                        if (!p.two || t == 1) umma_commit(&v_empty[st]);
-                        if (u + 2 >= p.units) umma_commit(&o_full[t]);
-                        if (u + 2 < p.units) qk(u + 2);
+                        if (last_use) umma_commit(&k_empty[st]);
+                        if (last) umma_commit(q_empty);
                     }
-                    k_at += p.s1 - p.s0;
-                    v_at += p.s1 - p.s0;
+                    __syncwarp();
+                };
+                if (ok) qk(0);
+                if (ok && p.units > 1) qk(1);
+                for (int u = 0; ok && u < p.units; ++u) {
+                    const int t = u & 1, j = at + (p.two ? u >> 1 : u), st = j % C::VST;
+                    if (!p.two || t == 0) ok = mbar_wait_bounded(&v_full[st], (j / C::VST) & 1, limit, abort_flag);
+                    ok = ok && mbar_wait_bounded(&p_full[t], p_phase >> t & 1, limit, abort_flag);
+                    p_phase ^= 1u << t;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t d = tbase + C::O_COL + t * DV, w = tbase + C::S_COL + t * kPreKeys;
+                    const uint32_t vd = v_desc + st * (C::V_BYTES >> 4);
+                    const bool last_use = !p.two || t == 1, last = u + 2 >= p.units;
+                    if (me) {
+                        if (u > 1) umma_ts<true>(d, w, vd, idesc_pv);
+                        else umma_ts<false>(d, w, vd, idesc_pv);
+#pragma unroll
+                        for (int kg = 1; kg < kPreKeys / 16; ++kg) umma_ts<true>(d, w + kg * 8, vd + kg * (2048 >> 4), idesc_pv);
+                        if (last_use) umma_commit(&v_empty[st]);
+                        if (last) umma_commit(&o_full[t]);
+                    }
+                    __syncwarp();
+                    if (!last) qk(u + 2);
                 }
-                if (!ok) {
-                    flag_error(a.err, kErrTimeout);
-                    *abort_flag = 1;
-                }
-                umma_commit(fin);
-                mbar_wait_bounded(fin, 0, limit, nullptr);
+                at += p.s1 - p.s0;
             }
+            if (!ok && me) {
+                flag_error(a.err, kErrTimeout);
+                *abort_flag = 1;
+            }
+            if (me) umma_commit(fin);
+            mbar_wait_bounded(fin, 0, limit, nullptr);
         } else if (warp == 9 || (C::TMA && warp == 10)) {
             // -------------------------------------------------------- loads: Q and K, or V
             const bool is_k = warp == 9;
