@@ -35,6 +35,7 @@ size_t prefill_workspace(PrefillArgs *a, int Dv, bool parts, char *base) {
     take(&a->unsorted, size_t(a->max_items));
     take(&a->tile_prefix, size_t(a->B) + 1);
     take(&a->cost_prefix, size_t(a->max_items) + 1);
+    take(&a->joins, size_t(a->workers));
     take(&a->cuts, size_t(a->workers) + 1);
     if (parts) {
         take(&a->o_part, size_t(2) * a->workers * 2 * kPreTile * Dv);
@@ -110,7 +111,8 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     }
     prefill_workspace(&a, DV, a.may_split, static_cast<char *>(ws));
     constexpr bool paged = SRC != kPreDense;
-    gqa_prefill_plan_kernel<paged><<<1, kPlanThreads, 0, cs>>>(a);
+    if (a.B <= kPlanThreads && a.max_items <= kPlanThreads) gqa_prefill_plan_kernel<paged, true><<<1, kPlanThreads, 0, cs>>>(a);
+    else gqa_prefill_plan_kernel<paged, false><<<1, kPlanThreads, 0, cs>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
         cudaEvent_t before, after;

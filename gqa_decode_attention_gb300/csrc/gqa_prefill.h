@@ -42,7 +42,7 @@ struct PrefillPlan {
     int n_items;
     int rounds;     // whole items: worker w takes, in round r, number r * W + w, or r * W + W - 1 - w in odd rounds
     int total;      // items x head blocks
-    int overflow;
+    int n_joins;    // items with partial results
 };
 
 struct PrefillArgs {
@@ -85,9 +85,11 @@ struct PrefillArgs {
     int max_items;
     PrefillPlan *plan;
     PrefillItem *items;      // [max_items], longest first
+    // where the planning CTA's shared memory does not hold them
     PrefillItem *unsorted;   // [max_items]
     int *tile_prefix;        // [B + 1]
     long long *cost_prefix;  // [max_items + 1]
+    int2 *joins;             // [workers]: of a divided item, the first and last worker whose share begins within it
     int2 *cuts;              // [workers + 1]: where a worker's share of the divided part begins (number, step)
     float *o_part;           // [2 workers][2 * kPreTile][Dv]
     float *lse_part;         // [2 workers][2 * kPreTile], log2 domain

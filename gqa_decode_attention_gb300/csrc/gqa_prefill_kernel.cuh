@@ -93,6 +93,28 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint
         : "memory");
 }
 
+// Lanes without bit d keep word a and get the partner's a for b; lanes with it the other way round.
+__device__ __forceinline__ void swap_words(uint32_t &a, uint32_t &b, int d, bool up) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, d);
+    a = up ? got : a;
+    b = up ? b : got;
+}
+
+// Lane q of four gets piece q (words 4 q ..) of each of the four lanes.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[16], int lane) {
+    const bool up1 = (lane & 1) != 0, up2 = (lane & 2) != 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        swap_words(x[w], x[4 + w], 1, up1);
+        swap_words(x[8 + w], x[12 + w], 1, up1);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        swap_words(x[w], x[8 + w], 2, up2);
+        swap_words(x[4 + w], x[12 + w], 2, up2);
+    }
+}
+
 // The row's 8 elements of one 16-byte unit as fp16, times `scale`; the order that 4-bit codes come in for those.
 template <int SRC>
 __device__ __forceinline__ uint4 prefill_q_unit(uint4 x, float scale) {
@@ -178,37 +200,36 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         PrefillPiece p;
         if (warp == 8) {
             // -------------------------------------------------------- products
-            // The whole warp walks, one elected lane issues: what an instruction takes is the same in every lane, and its
-            // descriptors are a base and a constant, so that the issue keeps up with 64 cycles a product while the softmax
-            // warps of this scheduler are busy.
+            // One lane; descriptors are a base and a constant and ring places are counted, so that the next product is issued
+            // before the one under way ends (rebuilding descriptors took 134 cycles a product beside two softmax warps, where
+            // the tensor core takes 64).
             constexpr uint32_t fmt = C::F16 ? ~((1u << 7) | (1u << 10)) : ~0u;
             constexpr uint32_t idesc_qk = idesc_bf16_f32(kPreTile, kPreKeys, false, false) & fmt;
             constexpr uint32_t idesc_pv = idesc_bf16_f32(kPreTile, DV, false, true) & fmt;
-            const uint32_t q_desc = desc_lo(smem_u32(smem + C::Q_OFF), 16), k_desc = desc_lo(smem_u32(smem + C::K_OFF), 16);
-            const uint32_t v_desc = desc_lo(smem_u32(smem + C::V_OFF), kPreKeys * 128);
-            const bool me = elect_one();
-            int n_piece = 0, at = 0;  // steps used before this piece
-            uint32_t p_phase = 0;
-            while (ok && walk.next(&p)) {
-                if (p.units == 0) continue;
-                if constexpr (C::F16)
-                    ok = mbar_wait_bounded(&q_ready[0], n_piece & 1, limit, abort_flag) &&
-                         mbar_wait_bounded(&q_ready[1], n_piece & 1, limit, abort_flag);
-                else
-                    ok = mbar_wait_bounded(q_full, n_piece & 1, limit, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                ++n_piece;
-                auto qk = [&](int u) {
-                    const int t = u & 1, j = at + (p.two ? u >> 1 : u), st = j % C::KST;
-                    if (!p.two || t == 0) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&k_full[st], (j / C::KST) & 1, limit, abort_flag));
-                        if (!ok) return;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t d = tbase + C::S_COL + t * kPreKeys;
-                    const uint32_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + st * (C::K_BYTES >> 4);
-                    const bool last_use = !p.two || t == 1, last = u == p.units - 1;
-                    if (me) {
+            if (elect_one()) {
+                const uint32_t q_desc = desc_lo(smem_u32(smem + C::Q_OFF), 16), k_desc = desc_lo(smem_u32(smem + C::K_OFF), 16);
+                const uint32_t v_desc = desc_lo(smem_u32(smem + C::V_OFF), kPreKeys * 128);
+                uint32_t q_phase = 0, p_phase = 0, k_phase = 0, v_phase = 0;
+                int ks = 0, vs = 0;  // stages in turn
+                while (ok && walk.next(&p)) {
+                    if (p.units == 0) continue;
+                    if constexpr (C::F16)
+                        ok = mbar_wait_bounded(&q_ready[0], q_phase, limit, abort_flag) &&
+                             mbar_wait_bounded(&q_ready[1], q_phase, limit, abort_flag);
+                    else
+                        ok = mbar_wait_bounded(q_full, q_phase, limit, abort_flag);
+                    q_phase ^= 1;
+                    const int units = p.units;
+                    const bool two = p.two;
+                    auto qk = [&](int u) {
+                        const uint32_t t = u & 1;
+                        if (!two || t == 0) {
+                            ok = mbar_wait_bounded(&k_full[ks], k_phase, limit, abort_flag);
+                            if (!ok) return;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t d = tbase + C::S_COL + t * kPreKeys;
+                        const uint32_t qd = q_desc + t * (C::Q_BYTES >> 4), kd = k_desc + ks * (C::K_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < DQK / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * (kPreTile * 128 >> 4) + (kk & 3) * 2;
@@ -216,43 +237,42 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             else umma_ss<true>(d, qd + off, kd + off, idesc_qk);
                         }
                         umma_commit(&s_full[t]);
-                        if (last_use) umma_commit(&k_empty[st]);
-                        if (last) umma_commit(q_empty);
-                    }
-                    __syncwarp();
-                };
-                if (ok) qk(0);
-                if (ok && p.units > 1) qk(1);
-                for (int u = 0; ok && u < p.units; ++u) {
-                    const int t = u & 1, j = at + (p.two ? u >> 1 : u), st = j % C::VST;
-                    if (!p.two || t == 0) ok = mbar_wait_bounded(&v_full[st], (j / C::VST) & 1, limit, abort_flag);
-                    ok = ok && mbar_wait_bounded(&p_full[t], p_phase >> t & 1, limit, abort_flag);
-                    p_phase ^= 1u << t;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint32_t d = tbase + C::O_COL + t * DV, w = tbase + C::S_COL + t * kPreKeys;
-                    const uint32_t vd = v_desc + st * (C::V_BYTES >> 4);
-                    const bool last_use = !p.two || t == 1, last = u + 2 >= p.units;
-                    if (me) {
+                        if (!two || t == 1) {
+                            umma_commit(&k_empty[ks]);
+                            if (++ks == C::KST) ks = 0, k_phase ^= 1;
+                        }
+                        if (u == units - 1) umma_commit(q_empty);
+                    };
+                    if (ok) qk(0);
+                    if (ok && units > 1) qk(1);
+                    for (int u = 0; ok && u < units; ++u) {
+                        const uint32_t t = u & 1;
+                        if (!two || t == 0) ok = mbar_wait_bounded(&v_full[vs], v_phase, limit, abort_flag);
+                        ok = ok && mbar_wait_bounded(&p_full[t], p_phase >> t & 1, limit, abort_flag);
+                        p_phase ^= 1u << t;
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t d = tbase + C::O_COL + t * DV, w = tbase + C::S_COL + t * kPreKeys;
+                        const uint32_t vd = v_desc + vs * (C::V_BYTES >> 4);
                         if (u > 1) umma_ts<true>(d, w, vd, idesc_pv);
                         else umma_ts<false>(d, w, vd, idesc_pv);
 #pragma unroll
                         for (int kg = 1; kg < kPreKeys / 16; ++kg) umma_ts<true>(d, w + kg * 8, vd + kg * (2048 >> 4), idesc_pv);
-                        if (last_use) umma_commit(&v_empty[st]);
-                        if (last) umma_commit(&o_full[t]);
+                        if (!two || t == 1) {
+                            umma_commit(&v_empty[vs]);
+                            if (++vs == C::VST) vs = 0, v_phase ^= 1;
+                        }
+                        if (u + 2 >= units) umma_commit(&o_full[t]);
+                        else qk(u + 2);
                     }
-                    __syncwarp();
-                    if (!last) qk(u + 2);
                 }
-                at += p.s1 - p.s0;
+                if (!ok) {
+                    flag_error(a.err, kErrTimeout);
+                    *abort_flag = 1;
+                }
+                umma_commit(fin);
+                mbar_wait_bounded(fin, 0, limit, nullptr);
             }
-            if (!ok && me) {
-                flag_error(a.err, kErrTimeout);
-                *abort_flag = 1;
-            }
-            if (me) umma_commit(fin);
-            mbar_wait_bounded(fin, 0, limit, nullptr);
         } else if (warp == 9 || (C::TMA && warp == 10)) {
             // -------------------------------------------------------- loads: Q and K, or V
             const bool is_k = warp == 9;
@@ -465,33 +485,11 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const int step = p.step_of(p.two ? 2 * i : 2 * i + t), key0 = step * kPreKeys;
                     const bool masked = key0 + kPreKeys > all_see;
                     const int left = seen - key0;
-                    // With registers for a row's 128 scores they are read once, else a second time for the weights.
-                    constexpr int BUFS = C::TMA ? 4 : 2;
-                    uint32_t sr[BUFS][32];
-                    // Scores h * 32 .. of the row as they go into the maximum; raw, the scale enters through the maximum (exact:
-                    // it is positive) and one fma a weight.
-                    auto hide = [&](uint32_t (&x)[32], int h) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (h * 32 + c >= left) x[c] = __float_as_uint(-INFINITY);
-                    };
-                    // the maximum over four chains of three-input maxima (exact)
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if constexpr (BUFS == 4) {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
-                        tmem_wait_ld();
-                    } else {
-                        tmem_ld32(s_at, sr[0]);
-                    }
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t (&x)[32] = sr[h % BUFS];
-                        if constexpr (BUFS == 2) {
-                            tmem_wait_ld();
-                            // (scores that go back with their parameters applied are read again after the last is written)
-                            if (h < 3 || !C::K_PARAMS) tmem_ld32(s_at + (h + 1) % 4 * 32, sr[(h + 1) % 2]);
-                        }
+                    float m4[4];
+                    uint32_t pk[kPreKeys / 2];
+                    // Scores h * 32 .. of the row as they go into the maximum: 4-bit keys' parameters applied, -inf for keys that the
+                    // row does not see.  The scale enters through the maximum (exact: it is positive) and one fma a weight.
+                    auto finish = [&](uint32_t (&x)[32], int h) {
                         if constexpr (C::K_PARAMS) {
                             const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512) + h * 8;
                             const float2 qs2 = make_float2(q_sum, q_sum);
@@ -510,61 +508,103 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 }
                             }
                         }
-                        if (masked) hide(x, h);
+                        if (masked) {
+                            const int n = left - h * 32;
+                            const uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(see & 1u << c)) x[c] = __float_as_uint(-INFINITY);
+                        }
+                    };
+                    auto maximum = [&](const uint32_t (&x)[32]) {  // four chains of three-input maxima (exact)
 #pragma unroll
                         for (int c = 0; c < 32; c += 2)
                             m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                        if constexpr (C::K_PARAMS) tmem_st32(s_at + h * 32, x);
-                    }
-                    if constexpr (C::K_PARAMS) {
-                        tmem_wait_st();
-                        tmem_ld32(s_at, sr[0]);
-                    }
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * alpha;
-                    const bool renew = mx > m_ref + kPreRescaleLog2;
-                    const bool rescale = renew && i > 0 && m_ref != -INFINITY;
-                    if (__any_sync(0xffffffffu, rescale)) {
-                        const float corr = rescale ? fast_exp2(m_ref - mx) : 1.f;
-#pragma unroll 1
-                        for (int c = 0; c < DV / 32; ++c) {
-                            uint32_t ov[32];
-                            tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 o2 = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
-                                                       make_float2(corr, corr));
-                                ov[e] = __float_as_uint(o2.x);
-                                ov[e + 1] = __float_as_uint(o2.y);
-                            }
-                            tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
-                        }
-                        l *= corr;
-                    }
-                    if (renew) m_ref = mx;
-                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                    // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in
-                    // fp32 before they are rounded for the product
-                    const float2 al2 = make_float2(alpha, alpha), nm2 = make_float2(-m_use, -m_use);
-                    float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t (&x)[32] = sr[h % BUFS];
-                        if constexpr (BUFS == 2) {
-                            tmem_wait_ld();
-                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) % 2]);
-                            if (masked && !C::K_PARAMS) hide(x, h);
-                        }
-                        uint32_t pk[16];
+                    };
+                    float2 sum2[2];
+                    // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in fp32
+                    // before they are rounded for the product
+                    const float2 al2 = make_float2(alpha, alpha);
+                    auto weigh = [&](const uint32_t (&x)[32], int h, float2 nm2) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), al2, nm2);
                             const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                             sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], w);
-                            pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                            pk[h * 16 + c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                         }
-                        tmem_st16(s_at + h * 16, pk);  // (columns whose scores have been read)
+                    };
+                    // A row's reference follows its maximum when that passes it by 2^8; O and the sum then change with it.
+                    auto follow = [&]() {
+                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * alpha;
+                        const bool renew = mx > m_ref + kPreRescaleLog2;
+                        const bool rescale = renew && i > 0 && m_ref != -INFINITY;
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            const float corr = rescale ? fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+                            for (int c = 0; c < DV / 32; ++c) {
+                                uint32_t ov[32];
+                                tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 o2 = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                                                           make_float2(corr, corr));
+                                    ov[e] = __float_as_uint(o2.x);
+                                    ov[e + 1] = __float_as_uint(o2.y);
+                                }
+                                tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                            }
+                            l *= corr;
+                        }
+                        if (renew) m_ref = mx;
+                        return renew;
+                    };
+                    if constexpr (C::TMA) {
+                        // a row's scores in registers: the maximum, then the weights
+                        uint32_t sr[4][32];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
+                        tmem_wait_ld();
+                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            finish(sr[h], h);
+                            maximum(sr[h]);
+                        }
+                        follow();
+                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            weigh(sr[h], h, make_float2(-m_use, -m_use));
+                        }
+                    } else {
+                        // Registers for half of them: maximum and weights in one pass with the reference as it is, once more in the
+                        // few steps whose maximum passes it.
+#pragma unroll 1
+                        for (bool again = true; again;) {
+                            const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                            const float2 nm2 = make_float2(-m_use, -m_use);
+                            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+                            sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+                            uint32_t sr[2][32];
+                            tmem_ld32(s_at, sr[0]);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                tmem_wait_ld();
+                                if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) & 1]);
+                                finish(sr[h & 1], h);
+                                maximum(sr[h & 1]);
+                                weigh(sr[h & 1], h, nm2);
+                            }
+                            again = __any_sync(0xffffffffu, follow());
+                        }
                     }
+                    // All of them at the end: a store holds its registers for some 180 cycles, which stores between the pieces
+                    // of one loop would wait for.
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
                     tmem_wait_st();
                     l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
                     tc_fence_before_sync();
@@ -612,6 +652,16 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const bool fix = n_units > 0 && p.s1 * kPreKeys > p.first_limit && *bad_v != 0;
                     const long long out_row = (long long)(p.item.q_row + tok) * a.Hq + p.g * a.G + p.hb * a.g_tile + head_in;
                     const int part_row = (p.slot * 2 + (p.two ? t : 0)) * kPreTile + row;
+                    // A row's 64 bytes go out by four lanes (a 16-byte piece each; a lane alone would touch 32 rows an
+                    // instruction): lanes of a quad exchange pieces, and lane q writes piece q of the quad's rows in turn.
+                    const long long mine = p.slot < 0 ? out_row * DV * 2 : (long long)part_row * DV * 4;
+                    char *rows[4];
+                    const unsigned there = __ballot_sync(0xffffffffu, real) >> (lane & ~3);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        rows[r] = (p.slot < 0 ? reinterpret_cast<char *>(a.out) : reinterpret_cast<char *>(a.o_part)) +
+                                  __shfl_sync(0xffffffffu, mine, (lane & ~3) + r) + (lane & 3) * 16;
+                    }
 #pragma unroll 1
                     for (int c = 0; c < DV / 32; ++c) {
                         float o[32];
@@ -635,7 +685,6 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = 0.f;
                         }
-                        if (!real) continue;
                         if constexpr (SRC == kPreInt4) {  // back from the order that 4-bit codes come in
 #pragma unroll
                             for (int e = 0; e < 32; e += 8) {
@@ -644,17 +693,30 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             }
                         }
                         if (p.slot < 0) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(a.out + out_row * DV + c * 32);
+                            uint32_t x[16];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                                    pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                            for (int e = 0; e < 16; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+                            quad_transpose(x, lane);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (there >> r & 1)
+                                    *reinterpret_cast<uint4 *>(rows[r] + c * 64) = make_uint4(x[4 * r], x[4 * r + 1], x[4 * r + 2], x[4 * r + 3]);
                         } else {
-                            float4 *dst = reinterpret_cast<float4 *>(a.o_part + (long long)part_row * DV + c * 32);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            for (int half = 0; half < 2; ++half) {
+                                uint32_t x[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[half * 16 + e]);
+                                quad_transpose(x, lane);
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    if (there >> r & 1)
+                                        *reinterpret_cast<uint4 *>(rows[r] + c * 128 + half * 64) =
+                                            make_uint4(x[4 * r], x[4 * r + 1], x[4 * r + 2], x[4 * r + 3]);
+                            }
                         }
                     }
+                    __syncwarp();  // a row's elements were written by its quad
                     if (fix && any) {
                         const int key0 = max(p.first_limit, p.s0 * kPreKeys), key1 = min(seen, p.s1 * kPreKeys);
                         if (p.slot < 0)
@@ -691,58 +753,86 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
     }
 }
 
-// Joins the partial results of items whose steps several workers hold.  CTA (w, r): if worker w's share begins within an item
-// and is the first to do so there, rows r * kPreMergeRows .. of that item: the part that worker w - 1 ended with, then
-// those of w and the workers after it, in their order.
-constexpr int kPreMergeRows = 16;
-constexpr int kPreMergeThreads = 256;
+// Joins the partial results of items whose steps several workers hold: CTA (j, b) rows 32 b .. of the j-th of them.  The
+// weights of all its rows and parts first, then the rows' pieces, 16 bytes a thread, in the parts' order.
+constexpr int kPreMergeRows = 32, kPreMergeThreads = 256, kPreMergeParts = 64;  // parts whose weights are held at a time
 
 template <int DV>
 __global__ void __launch_bounds__(kPreMergeThreads) gqa_prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
+    __shared__ float weight[kPreMergeParts][kPreMergeRows];
+    __shared__ int place[kPreMergeParts];  // first row of a part's results, -1 for a share without steps
+    __shared__ float top_s[kPreMergeRows];
     pdl_wait_primary();
-    const int w = blockIdx.x + 1;
-    const int2 cut = a.cuts[w];
-    if (cut.y == 0) return;
-    const int2 prev = a.cuts[w - 1];
-    if (prev.x == cut.x && prev.y > 0) return;  // joined from the first cut of the item
-    int last = w;  // the last worker with a cut in the item
-    while (last + 1 < a.workers && a.cuts[last + 1].x == cut.x && a.cuts[last + 1].y > 0) ++last;
-    const PrefillItem it = a.items[cut.x / a.head_blocks];
-    const int h = cut.x % a.head_blocks, per = a.head_blocks / a.Hkv;
-    const int rows = (it.n_tok > a.tok_tile ? 2 : 1) * kPreTile;
-    constexpr int LANES = DV / 4;  // threads of a row
-    for (int r = blockIdx.y * kPreMergeRows + threadIdx.x / LANES; r < min(rows, int(blockIdx.y + 1) * kPreMergeRows);
-         r += kPreMergeThreads / LANES) {
-        const int tile = r / kPreTile, in = r % kPreTile;
-        const int tok = tile * a.tok_tile + in / a.g_tile, head = (h % per) * a.g_tile + in % a.g_tile;
-        if (in / a.g_tile >= a.tok_tile || tok >= it.n_tok || head >= a.G) continue;
-        const int d = threadIdx.x % LANES * 4;
-        float top = -INFINITY;
-        auto none = [&](int x) {  // an empty share between two cuts at one place
-            return x >= w && a.cuts[x].x == a.cuts[x + 1].x && a.cuts[x].y == a.cuts[x + 1].y;
-        };
-        for (int x = w - 1; x <= last; ++x) {
-            if (none(x)) continue;
-            const int slot = x == w - 1 ? 2 * x + 1 : 2 * x;
-            top = fmaxf(top, a.lse_part[slot * 2 * kPreTile + r]);
+    if (int(blockIdx.x) >= a.plan->n_joins) return;
+    const int2 join = a.joins[blockIdx.x];  // first and last worker whose share begins within the item
+    const int number = a.cuts[join.x].x;
+    const PrefillItem it = a.items[number / a.head_blocks];
+    const int r0 = blockIdx.y * kPreMergeRows;
+    if (r0 >= kPreTile && it.n_tok <= a.tok_tile) return;
+    const int h = number % a.head_blocks, per = a.head_blocks / a.Hkv;
+    // part x: what worker first + x did of the item -- the last thing of its share for the first of them, the first for the others
+    const int first = join.x - 1, parts = join.y - first + 1;
+    auto place_of = [&](int x) {
+        const int2 c0 = a.cuts[first + x], c1 = a.cuts[first + x + 1];
+        if (x > 0 && c0.x == c1.x && c0.y == c1.y) return -1;
+        return (x == 0 ? 2 * first + 1 : 2 * (first + x)) * 2 * kPreTile + r0;
+    };
+    const int row = threadIdx.x & (kPreMergeRows - 1), lane_part = threadIdx.x / kPreMergeRows;
+    constexpr int LANES = kPreMergeThreads / kPreMergeRows;  // parts looked at side by side
+    // largest LSE of each row
+    float top = -INFINITY;
+    for (int x = lane_part; x < parts; x += LANES) {
+        const int at = place_of(x);
+        if (at >= 0) top = fmaxf(top, a.lse_part[at + row]);
+    }
+    weight[lane_part][row] = top;
+    __syncthreads();
+    if (threadIdx.x < kPreMergeRows) {
+        for (int x = 1; x < LANES; ++x) top = fmaxf(top, weight[x][row]);
+        top_s[row] = top == -INFINITY ? 0.f : top;
+    }
+    __syncthreads();
+    constexpr int COLS = DV / 4, PASS = kPreMergeThreads / COLS, N = kPreMergeRows / PASS;  // rows at a time, rows of a thread
+    const int d = threadIdx.x % COLS * 4, sub = threadIdx.x / COLS;
+    float4 o[N] = {};
+    float total[N] = {};
+    for (int x0 = 0; x0 < parts; x0 += kPreMergeParts) {
+        const int here = min(kPreMergeParts, parts - x0);
+        for (int x = lane_part; x < here; x += LANES) {
+            const int at = place_of(x0 + x);
+            weight[x][row] = at < 0 ? 0.f : exp2f(a.lse_part[at + row] - top_s[row]);
+            if (row == 0) place[x] = at;
         }
-        const float ref = top == -INFINITY ? 0.f : top;
-        float total = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = w - 1; x <= last; ++x) {
-            if (none(x)) continue;
-            const int at = (x == w - 1 ? 2 * x + 1 : 2 * x) * 2 * kPreTile + r;
-            const float lse = a.lse_part[at], f = exp2f(lse - ref);
-            if (lse == -INFINITY) continue;
-            total += f;
-            const float4 y = *reinterpret_cast<const float4 *>(a.o_part + (long long)at * DV + d);
-            o.x += f * y.x, o.y += f * y.y, o.z += f * y.z, o.w += f * y.w;
+        __syncthreads();
+#pragma unroll 2
+        for (int x = 0; x < here; ++x) {
+            const int at = place[x];
+            if (at < 0) continue;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int r = n * PASS + sub;
+                const float f = weight[x][r];
+                const float4 y = *reinterpret_cast<const float4 *>(a.o_part + (long long)(at + r) * DV + d);
+                total[n] += f;
+                if (f != 0.f) {  // a part without a key for the row has no share, whatever it holds
+                    o[n].x = fmaf(f, y.x, o[n].x), o[n].y = fmaf(f, y.y, o[n].y);
+                    o[n].z = fmaf(f, y.z, o[n].z), o[n].w = fmaf(f, y.w, o[n].w);
+                }
+            }
         }
-        const float inv = total == 0.f ? 0.f : 1.f / total;
-        const long long row = (long long)(it.q_row + tok) * a.Hq + h / per * a.G + head;
-        *reinterpret_cast<uint2 *>(a.out + row * DV + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (a.lse != nullptr && d == 0) a.lse[row] = total == 0.f ? -INFINITY : (ref + log2f(total)) * 0.69314718055994530942f;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int r = r0 + n * PASS + sub, tile = r / kPreTile, in = r % kPreTile;
+        const int tok_in = in / a.g_tile, tok = tile * a.tok_tile + tok_in, head = h % per * a.g_tile + in % a.g_tile;
+        if (tok_in >= a.tok_tile || tok >= it.n_tok || head >= a.G) continue;
+        const float inv = total[n] == 0.f ? 0.f : 1.f / total[n];
+        const long long to = (long long)(it.q_row + tok) * a.Hq + h / per * a.G + head;
+        *reinterpret_cast<uint2 *>(a.out + to * DV + d) =
+            make_uint2(pack_bf16x2(o[n].x * inv, o[n].y * inv), pack_bf16x2(o[n].z * inv, o[n].w * inv));
+        if (a.lse != nullptr && d == 0)
+            a.lse[to] = total[n] == 0.f ? -INFINITY : (top_s[r - r0] + log2f(total[n])) * 0.69314718055994530942f;
     }
 }
 

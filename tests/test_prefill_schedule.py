@@ -4,7 +4,7 @@ import random
 
 import pytest
 
-KEYS, MIN_SPLIT, SNAP, BUCKETS = 128, 4, 2, 64
+KEYS, MIN_SPLIT, SNAP, BUCKETS, EXACT_ROUNDS = 128, 4, 2, 64, 64
 COST_TWO, COST_ONE, COST_ITEM = 4, 3, 4
 
 
@@ -28,25 +28,40 @@ def plan(items, top, HB, W, may_split):
     prefix = [0]
     for i in items:
         prefix.append(prefix[-1] + i["cost"])
-    goal = max(-(-prefix[-1] * HB // W), min(top, COST_ITEM + MIN_SPLIT * COST_TWO))
+    small = min(top, COST_ITEM + MIN_SPLIT * COST_TWO)
+    goal = max(-(-prefix[-1] * HB // W), small)
     number = lambda r, w: r * W + (W - 1 - w if r & 1 else w)  # noqa: E731
-    rounds = 1 << 30
-    for w in range(W):
-        load, r = 0, 0
-        while (r + 1) * W <= total:
-            load += items[number(r, w) // HB]["cost"]
+    cost = lambda k: items[k // HB]["cost"]  # noqa: E731
+    exact = total // W <= EXACT_ROUNDS
+    if exact:
+        rounds = total // W
+        for w in range(W):
+            load = 0
+            for r in range(rounds):
+                load += cost(number(r, w))
+                if load > goal:
+                    rounds = r
+                    break
+    else:
+        rounds, load = 0, 0
+        while (rounds + 2) * W <= total:
+            load += cost(rounds * W) + cost((rounds + 2) * W - 1)
             if load > goal:
                 break
-            r += 1
-        rounds = min(rounds, r)
-    need = [goal - sum(items[number(r, w) // HB]["cost"] for r in range(rounds)) for w in range(W)]
+            rounds += 2
+    n0 = rounds * W
+    line = prefix[n0 // HB] * HB + n0 % HB * items[n0 // HB]["cost"] if n0 < total else prefix[-1] * HB
+    need = []
+    for w in range(W):
+        load = sum(cost(number(r, w)) for r in range(rounds)) if exact else line // W
+        need.append(max(goal - load, small))
     n0, cuts, x = rounds * W, [], 0
     for w in range(W):
         cut = (total, 0)
         if w == 0:
             cut = (n0, 0)
         elif n0 < total:
-            pos = prefix[n0 // HB] * HB + n0 % HB * items[n0 // HB]["cost"] + x
+            pos = line + x
             if pos < prefix[-1] * HB:
                 lo = max(i for i in range(len(items)) if prefix[i] * HB <= pos)
                 it = items[lo]
@@ -122,4 +137,5 @@ def test_plan_covers_every_step_once(seed):
             joined.add(slot)
     assert joined >= set(slots)
     if may_split and items:
-        assert max(loads) <= goal + 2 * COST_ITEM + 2 * SNAP * COST_TWO + min(top, COST_ITEM + MIN_SPLIT * COST_TWO)
+        slack = 2 * COST_ITEM + 2 * SNAP * COST_TWO + min(top, COST_ITEM + MIN_SPLIT * COST_TWO)
+        assert max(loads) <= goal + slack + (0 if len(items) * HB // W <= EXACT_ROUNDS else 2 * top)
