@@ -369,23 +369,24 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     if (!ok) break;
                     bool found = false;
                     uint8_t *tile = smem + C::V_OFF + st * C::V_BYTES;
-                    const int from = max(0, p.first_limit - step * kPreKeys), gone = p.item.L - step * kPreKeys;
+                    const int from = max(0, p.first_limit - step * kPreKeys), gone = max(0, min(kPreKeys, p.item.L - step * kPreKeys));
                     // a quarter warp a 128-byte row piece; the swizzle permutes 16-byte units within it
-                    for (int i = from * 8 + lane; i < kPreKeys * 8; i += 32) {
-                        const int key = i >> 3;
 #pragma unroll
-                        for (int c = 0; c < C::VC; ++c) {
-                            uint4 *x = reinterpret_cast<uint4 *>(tile + c * (kPreKeys * 128) + i * 16);
-                            if (key >= gone) {
-                                *x = make_uint4(0, 0, 0, 0);
-                            } else {
-                                uint4 y = *x;
-                                if (not_finite2<C::F16>(y.x) || not_finite2<C::F16>(y.y) || not_finite2<C::F16>(y.z) ||
-                                    not_finite2<C::F16>(y.w)) {
-                                    found = true;
-                                    *x = make_uint4(finite2<C::F16>(y.x), finite2<C::F16>(y.y), finite2<C::F16>(y.z),
-                                                    finite2<C::F16>(y.w));
-                                }
+                    for (int c = 0; c < C::VC; ++c) {
+                        uint4 *x = reinterpret_cast<uint4 *>(tile + c * (kPreKeys * 128));
+                        for (int i = gone * 8 + lane; i < kPreKeys * 8; i += 32) x[i] = make_uint4(0, 0, 0, 0);
+                        uint32_t most = 0;  // largest magnitude's bits, two 16-bit halves; infinities and NaN are above all others
+#pragma unroll 8
+                        for (int i = from * 8 + lane; i < gone * 8; i += 32) {
+                            const uint4 y = x[i];
+                            most = __vmaxu2(__vmaxu2(most, __vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu)),
+                                            __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+                        }
+                        if (__any_sync(0xffffffffu, not_finite2<C::F16>(most))) {
+                            found = true;
+                            for (int i = from * 8 + lane; i < gone * 8; i += 32) {
+                                const uint4 y = x[i];
+                                x[i] = make_uint4(finite2<C::F16>(y.x), finite2<C::F16>(y.y), finite2<C::F16>(y.z), finite2<C::F16>(y.w));
                             }
                         }
                     }
@@ -421,6 +422,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             const int seen = !real ? 0 : a.causal ? min(max(p.item.limit0 + tok, 0), p.item.L) : p.item.L;
             const bool idle = !__any_sync(0xffffffffu, real);  // nothing in this warp's rows: it only keeps step
             const int all_see = __reduce_min_sync(0xffffffffu, real ? seen : 0x7fffffff);
+            const int most_see = __reduce_max_sync(0xffffffffu, seen);
             const int n_units = p.units == 0 ? 0 : p.units_of(t);
             float alpha = a.alpha, v_scale = a.v_scale;
             if constexpr (C::F16) {
@@ -486,9 +488,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const bool masked = key0 + kPreKeys > all_see;
                     const int left = seen - key0;
                     float m4[4];
-                    uint32_t pk[kPreKeys / 2];
-                    // Scores h * 32 .. of the row as they go into the maximum: 4-bit keys' parameters applied, -inf for keys that the
-                    // row does not see.  The scale enters through the maximum (exact: it is positive) and one fma a weight.
+                    // Scores h * 32 .. of the row as they go into the maximum: 4-bit keys' parameters applied.  The scale enters
+                    // through the maximum (exact: it is positive) and one fma a weight.
                     auto finish = [&](uint32_t (&x)[32], int h) {
                         if constexpr (C::K_PARAMS) {
                             const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512) + h * 8;
@@ -508,13 +509,12 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 }
                             }
                         }
-                        if (masked) {
-                            const int n = left - h * 32;
-                            const uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                    };
+                    auto hide = [&](uint32_t (&x)[32], int h) {
+                        const int n = left - h * 32;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(see & 1u << c)) x[c] = __float_as_uint(-INFINITY);
-                        }
+                        for (int c = 0; c < 32; ++c)
+                            if (c >= n) x[c] = __float_as_uint(-INFINITY);
                     };
                     auto maximum = [&](const uint32_t (&x)[32]) {  // four chains of three-input maxima (exact)
 #pragma unroll
@@ -525,13 +525,13 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in fp32
                     // before they are rounded for the product
                     const float2 al2 = make_float2(alpha, alpha);
-                    auto weigh = [&](const uint32_t (&x)[32], int h, float2 nm2) {
+                    auto weigh = [&](const uint32_t (&x)[32], uint32_t *pk, float2 nm2) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), al2, nm2);
                             const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                             sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], w);
-                            pk[h * 16 + c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                            pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                         }
                     };
                     // A row's reference follows its maximum when that passes it by 2^8; O and the sum then change with it.
@@ -560,8 +560,39 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         if (renew) m_ref = mx;
                         return renew;
                     };
-                    if constexpr (C::TMA) {
+                    if (masked) {
+                        // 32 keys after the other, those that no row of the warp sees left out (in short prompts half of them):
+                        // the maximum, then the weights from scores read once more
+                        const int most = most_see - key0;
+                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+#pragma unroll 1
+                        for (int h = 0; h * 32 < min(most, kPreKeys); ++h) {
+                            uint32_t x[32];
+                            tmem_ld32(s_at + h * 32, x);
+                            tmem_wait_ld();
+                            finish(x, h);
+                            hide(x, h);
+                            maximum(x);
+                        }
+                        follow();
+                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+#pragma unroll 1
+                        for (int h = 0; h < kPreKeys / 32; ++h) {
+                            uint32_t w[16] = {};
+                            if (h * 32 < most) {
+                                uint32_t x[32];
+                                tmem_ld32(s_at + h * 32, x);
+                                tmem_wait_ld();
+                                finish(x, h);
+                                hide(x, h);
+                                weigh(x, w, make_float2(-m_use, -m_use));
+                            }
+                            tmem_st16(s_at + h * 16, w);  // (columns whose scores have been read)
+                        }
+                    } else if constexpr (C::TMA) {
                         // a row's scores in registers: the maximum, then the weights
+                        uint32_t pk[kPreKeys / 2];
                         uint32_t sr[4][32];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
@@ -577,11 +608,16 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            weigh(sr[h], h, make_float2(-m_use, -m_use));
+                            weigh(sr[h], pk + h * 16, make_float2(-m_use, -m_use));
                         }
+                        // All of them at the end: a store holds its registers for some 180 cycles, which stores between the
+                        // pieces would wait for.
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
                     } else {
                         // Registers for half of them: maximum and weights in one pass with the reference as it is, once more in the
                         // few steps whose maximum passes it.
+                        uint32_t pk[kPreKeys / 2];
 #pragma unroll 1
                         for (bool again = true; again;) {
                             const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
@@ -596,15 +632,13 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) & 1]);
                                 finish(sr[h & 1], h);
                                 maximum(sr[h & 1]);
-                                weigh(sr[h & 1], h, nm2);
+                                weigh(sr[h & 1], pk + h * 16, nm2);
                             }
                             again = __any_sync(0xffffffffu, follow());
                         }
-                    }
-                    // All of them at the end: a store holds its registers for some 180 cycles, which stores between the pieces
-                    // of one loop would wait for.
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                    }
                     tmem_wait_st();
                     l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
                     tc_fence_before_sync();
