@@ -89,7 +89,7 @@ struct PrefillArgs {
     PrefillItem *unsorted;   // [max_items]
     int *tile_prefix;        // [B + 1]
     long long *cost_prefix;  // [max_items + 1]
-    int2 *joins;             // [workers]: of a divided item, the first and last worker whose share begins within it
+    int4 *joins;             // [workers]: of a divided item its number, the worker with its beginning and the one with its end
     int2 *cuts;              // [workers + 1]: where a worker's share of the divided part begins (number, step)
     float *o_part;           // [2 workers][2 * kPreTile][Dv]
     float *lse_part;         // [2 workers][2 * kPreTile], log2 domain

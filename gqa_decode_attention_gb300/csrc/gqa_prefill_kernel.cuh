@@ -794,30 +794,24 @@ constexpr int kPreMergeRows = 32, kPreMergeThreads = 256, kPreMergeParts = 64;  
 template <int DV>
 __global__ void __launch_bounds__(kPreMergeThreads) gqa_prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
     __shared__ float weight[kPreMergeParts][kPreMergeRows];
-    __shared__ int place[kPreMergeParts];  // first row of a part's results, -1 for a share without steps
     __shared__ float top_s[kPreMergeRows];
     pdl_wait_primary();
     if (int(blockIdx.x) >= a.plan->n_joins) return;
-    const int2 join = a.joins[blockIdx.x];  // first and last worker whose share begins within the item
-    const int number = a.cuts[join.x].x;
+    const int4 join = a.joins[blockIdx.x];
+    const int number = join.x;
     const PrefillItem it = a.items[number / a.head_blocks];
     const int r0 = blockIdx.y * kPreMergeRows;
     if (r0 >= kPreTile && it.n_tok <= a.tok_tile) return;
     const int h = number % a.head_blocks, per = a.head_blocks / a.Hkv;
     // part x: what worker first + x did of the item -- the last thing of its share for the first of them, the first for the others
-    const int first = join.x - 1, parts = join.y - first + 1;
-    auto place_of = [&](int x) {
-        const int2 c0 = a.cuts[first + x], c1 = a.cuts[first + x + 1];
-        if (x > 0 && c0.x == c1.x && c0.y == c1.y) return -1;
-        return (x == 0 ? 2 * first + 1 : 2 * (first + x)) * 2 * kPreTile + r0;
-    };
+    const int first = join.y, parts = join.z - first + 1;
+    auto place_of = [&](int x) { return (x == 0 ? 2 * first + 1 : 2 * (first + x)) * 2 * kPreTile + r0; };
     const int row = threadIdx.x & (kPreMergeRows - 1), lane_part = threadIdx.x / kPreMergeRows;
     constexpr int LANES = kPreMergeThreads / kPreMergeRows;  // parts looked at side by side
     // largest LSE of each row
     float top = -INFINITY;
     for (int x = lane_part; x < parts; x += LANES) {
-        const int at = place_of(x);
-        if (at >= 0) top = fmaxf(top, a.lse_part[at + row]);
+        top = fmaxf(top, a.lse_part[place_of(x) + row]);
     }
     weight[lane_part][row] = top;
     __syncthreads();
@@ -832,16 +826,12 @@ __global__ void __launch_bounds__(kPreMergeThreads) gqa_prefill_merge_kernel(con
     float total[N] = {};
     for (int x0 = 0; x0 < parts; x0 += kPreMergeParts) {
         const int here = min(kPreMergeParts, parts - x0);
-        for (int x = lane_part; x < here; x += LANES) {
-            const int at = place_of(x0 + x);
-            weight[x][row] = at < 0 ? 0.f : exp2f(a.lse_part[at + row] - top_s[row]);
-            if (row == 0) place[x] = at;
-        }
+        for (int x = lane_part; x < here; x += LANES)
+            weight[x][row] = exp2f(a.lse_part[place_of(x0 + x) + row] - top_s[row]);
         __syncthreads();
 #pragma unroll 2
         for (int x = 0; x < here; ++x) {
-            const int at = place[x];
-            if (at < 0) continue;
+            const int at = place_of(x0 + x);
 #pragma unroll
             for (int n = 0; n < N; ++n) {
                 const int r = n * PASS + sub;

@@ -34,290 +34,391 @@ __device__ __forceinline__ void prefill_range(const int32_t *cu, int per, int b,
     if (*from != f || *to != t) flag_error(err, kErrIndex);
 }
 
-template <typename T>
-__device__ __forceinline__ T block_exclusive_scan(T x, T *total, T *warp_sums) {
+// Sum of x before this thread, and of all; `sums` is shared memory for 33.  Every warp adds the warps' sums up by itself.
+template <typename T, int THREADS>
+__device__ __forceinline__ T block_exclusive_scan(T x, T *total, T *sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int WARPS = THREADS / 32;
     T inc = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const T y = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += y;
     }
-    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();  // (`sums` may be in use by the scan before)
+    if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    if (warp == 0) {
-        T s = lane < kPlanThreads / 32 ? warp_sums[lane] : T(0);
+    T s = lane < WARPS ? sums[lane] : T(0);
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const T y = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += y;
-        }
-        warp_sums[lane] = s;
+    for (int d = 1; d < WARPS; d <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += y;
     }
-    __syncthreads();
-    const T before = warp > 0 ? warp_sums[warp - 1] : T(0);
-    *total = warp_sums[kPlanThreads / 32 - 1];
-    __syncthreads();
-    return before + inc - x;
+    *total = __shfl_sync(0xffffffffu, s, WARPS - 1);
+    const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : T(0)) + inc - x;
 }
 
+// A sequence's rows and keys.
+struct PlanSeq {
+    int q_row, n, k_row, L;
+};
+
 template <bool PAGED>
-__device__ __forceinline__ PrefillItem plan_item(const PrefillArgs &a, int b, int tile, unsigned *err) {
-    int f, t, kf = 0, kt;
-    prefill_range(a.cu_q, a.per_q, b, a.Tq, nullptr, &f, &t);
+__device__ __forceinline__ PlanSeq plan_seq(const PrefillArgs &a, int b, unsigned *err) {
+    PlanSeq s;
+    int t, kt;
     if constexpr (PAGED) {
         const int n = a.seq_lens[b];
+        s.k_row = 0;
         kt = min(max(n, 0), a.pages_per_req * a.page_size);
         if (kt != n) flag_error(err, kErrIndex);
     } else {
-        prefill_range(a.cu_k, a.per_k, b, a.Tk, err, &kf, &kt);
+        prefill_range(a.cu_k, a.per_k, b, a.Tk, err, &s.k_row, &kt);
     }
-    const int tpi = 2 * a.tok_tile;
+    prefill_range(a.cu_q, a.per_q, b, a.Tq, err, &s.q_row, &t);
+    s.n = t - s.q_row;
+    s.L = kt - s.k_row;
+    return s;
+}
+
+__device__ __forceinline__ PrefillItem plan_item(const PrefillArgs &a, int b, const PlanSeq &s, int tile) {
+    const int first = tile * 2 * a.tok_tile;
     PrefillItem it;
-    it.q_row = f + tile * tpi;
-    it.n_tok = min(tpi, t - it.q_row);
+    it.q_row = s.q_row + first;
+    it.n_tok = min(2 * a.tok_tile, s.n - first);
     it.req = b;
-    it.L = kt - kf;
-    it.k_row = kf;
-    it.limit0 = a.causal ? it.L - (t - f) + tile * tpi + 1 : it.L;
-    const int seen = a.causal ? min(max(it.limit0 + it.n_tok - 1, 0), it.L) : it.L;
+    it.L = s.L;
+    it.k_row = s.k_row;
+    it.limit0 = a.causal ? s.L - s.n + first + 1 : s.L;
+    const int seen = a.causal ? min(max(it.limit0 + it.n_tok - 1, 0), s.L) : s.L;
     it.steps = (seen + kPreKeys - 1) / kPreKeys;
     it.cost = kPreCostItem + it.steps * (it.n_tok > a.tok_tile ? kPreCostTwo : kPreCostOne);
     return it;
 }
 
-// SMALL: at most one sequence and one item a thread, nothing but the results in global memory.
-template <bool PAGED, bool SMALL>
-__global__ void __launch_bounds__(kPlanThreads, 1) gqa_prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
-    __shared__ int hist[kPlanThreads / 32][kPlanBuckets];
-    __shared__ int tile_prefix_s[SMALL ? kPlanThreads + 1 : 1];
-    __shared__ long long cost_prefix_s[SMALL ? kPlanThreads + 1 : 1];
-    __shared__ int2 cuts_s[kPlanThreads + 1];
-    __shared__ long long sums[32];
-    __shared__ int isums[32];
-    __shared__ int shared_max;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_launch_dependents();
-    const int tpi = 2 * a.tok_tile;
-    int *tile_prefix = SMALL ? tile_prefix_s : a.tile_prefix;
-    long long *cost_prefix = SMALL ? cost_prefix_s : a.cost_prefix;
+__device__ __forceinline__ int plan_bucket(int cost, int top) {
+    return kPlanBuckets - 1 - int((unsigned long long)unsigned(cost) * (kPlanBuckets - 1) / unsigned(top));
+}
 
-    // tiles before each sequence
-    const int per_thread = SMALL ? 1 : (a.B + kPlanThreads - 1) / kPlanThreads;
-    int mine = 0;
-    for (int i = 0; i < per_thread; ++i) {
-        const int b = tid * per_thread + i;
-        if (b >= a.B) break;
-        int f, t;
-        prefill_range(a.cu_q, a.per_q, b, a.Tq, a.err, &f, &t);
-        mine += (t - f + tpi - 1) / tpi;
+// The last i < n with prefix[i] <= x.
+template <typename T, typename X>
+__device__ __forceinline__ int plan_search(const T *prefix, int n, X x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (X(prefix[mid]) <= x) lo = mid;
+        else hi = mid;
     }
-    if (tid == 0) shared_max = 1;
-    for (int i = tid; i < (kPlanThreads / 32) * kPlanBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
-    int n_items;
-    int at = block_exclusive_scan(mine, &n_items, isums);
-    if constexpr (SMALL) {
-        if (tid < a.B) tile_prefix[tid] = at;
-        if (tid == a.B - 1) tile_prefix[a.B] = at + mine;
+    return lo;
+}
+
+// Shares of the sorted items: rounds of whole ones, the cuts of the line of the rest, and the items that several workers hold
+// steps of.  prefix[i]: cost before item i (of one head block), prefix[n_items] the sum; in shared memory, or not.
+template <typename T, int THREADS>
+__device__ __forceinline__ void plan_shares(const PrefillArgs &a, int n_items, int top, const T *prefix, int2 *cuts, long long *sums,
+                                            int *isums, int *shared_int) {
+    const int tid = threadIdx.x;
+    const int W = a.workers, HB = a.head_blocks;
+    const int total = n_items * HB;
+    const long long all_cost = (long long)prefix[n_items] * HB;
+    // number / HB by a product, exact while number x HB < 2^32
+    const unsigned inv = unsigned((1ull << 32) / unsigned(HB)) + 1;
+    const bool by_product = HB > 1 && (unsigned long long)total * unsigned(HB) < (1ull << 32);
+    auto item_of = [&](int number) { return HB == 1 ? number : by_product ? int(__umulhi(unsigned(number), inv)) : number / HB; };
+    auto cost_of = [&](int number) {
+        const int item = item_of(number);
+        return int(prefix[item + 1] - prefix[item]);
+    };
+    auto number_of = [&](int r, int w) { return r * W + ((r & 1) ? W - 1 - w : w); };
+    const int small = min(top, kPreCostItem + kPreMinSplit * kPreCostTwo);  // no part of an item is planned smaller
+    const long long goal = max((all_cost + W - 1) / W, (long long)small);
+    const int all_rounds = total / W;
+    const bool exact = all_rounds <= kPlanExactRounds;
+    // Whole rounds, as long as no worker passes its share of the total.
+    int rounds = 0;
+    long long load = 0;  // this worker's, after them
+    if (exact) {
+        if (all_rounds > 0) {
+            if (tid == 0) *shared_int = all_rounds;
+            __syncthreads();
+            if (tid < W) {
+                int r = 0;
+                for (long long sum = 0; r < all_rounds; ++r) {
+                    sum += cost_of(number_of(r, tid));
+                    if (sum > goal) break;
+                }
+                atomicMin(shared_int, r);
+            }
+            __syncthreads();
+            rounds = *shared_int;
+            if (tid < W)
+                for (int r = 0; r < rounds; ++r) load += cost_of(number_of(r, tid));
+        }
     } else {
-        for (int i = 0; i < per_thread; ++i) {
-            const int b = tid * per_thread + i;
-            if (b >= a.B) break;
-            int f, t;
-            prefill_range(a.cu_q, a.per_q, b, a.Tq, nullptr, &f, &t);
-            tile_prefix[b] = at;
-            at += (t - f + tpi - 1) / tpi;
-            if (b == a.B - 1) tile_prefix[a.B] = at;
+        // Many rounds: two of them, forth and back, are taken as even, as much as their first and last item together.
+        long long done = 0;
+        for (int r0 = 0;; r0 += THREADS) {
+            const int r = r0 + tid;
+            const long long c = (long long)(2 * r + 2) * W <= total ? cost_of(2 * r * W) + cost_of((2 * r + 2) * W - 1) : goal + 1;
+            long long turn;
+            const long long sum = block_exclusive_scan<long long, THREADS>(c, &turn, sums) + c + done;
+            const int fit = __syncthreads_count(sum <= goal);
+            rounds += 2 * fit;
+            done += turn;
+            if (fit < THREADS) break;
         }
     }
+    // The rest is one line of steps that fills every worker up to its share of the total.
+    const int n0 = rounds * W;
+    const long long line = n0 < total ? (long long)prefix[item_of(n0)] * HB + (long long)(n0 - item_of(n0) * HB) * cost_of(n0) : all_cost;
+    if (!exact) load = line / W;
+    const long long need = tid < W ? max(goal - load, (long long)small) : 0;
+    long long ignored;
+    const long long pos = line + block_exclusive_scan<long long, THREADS>(need, &ignored, sums);
+    if (tid < W) {
+        int2 cut = make_int2(total, 0);
+        if (tid == 0) {
+            cut.x = n0;
+        } else if (pos < all_cost) {
+            // the item whose steps of all head blocks hold the place: prefix x HB <= pos
+            int lo = 0, hi = n_items;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if ((long long)prefix[mid] * HB <= pos) lo = mid;
+                else hi = mid;
+            }
+            const int4 *rec = reinterpret_cast<const int4 *>(a.items + lo);
+            const int cost = int(prefix[lo + 1] - prefix[lo]);
+            const unsigned long long rem = pos - (long long)prefix[lo] * HB;
+            const int head = rem >> 32 ? int(rem / unsigned(cost)) : int(unsigned(rem) / unsigned(cost));
+            const int y = int(rem - (unsigned long long)unsigned(head) * unsigned(cost));
+            const int4 it = rec[0];  // q_row, n_tok, req, steps
+            const int steps = it.w;
+            int step = max(0, y - kPreCostItem);
+            step = it.y > a.tok_tile ? step / kPreCostTwo : step / kPreCostOne;
+            if (!a.may_split) step = 2 * y >= cost ? steps : 0;
+            cut.x = lo * HB + head;
+            if (steps - step < kPreSnap && 2 * y >= cost) cut.x += 1;
+            else if (step >= kPreSnap && steps - step >= kPreSnap) cut.y = step;
+        }
+        cuts[tid] = cut;
+        a.cuts[tid] = cut;
+    }
+    if (tid == 0) a.cuts[W] = cuts[W] = make_int2(total, 0);
+    int n_joins = 0;
+    if (a.may_split) {
+        __syncthreads();
+        // Items that several workers hold steps of.  (Cuts within one item are places apart: a worker's share of the line is
+        // never less than a few steps.)
+        bool first = false;
+        int4 join;
+        if (tid > 0 && tid < W) {
+            const int2 cut = cuts[tid], prev = cuts[tid - 1];
+            first = cut.y > 0 && !(prev.x == cut.x && prev.y > 0);
+            int lo = tid, hi = W;  // the last worker whose share begins within the item
+            while (first && hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cuts[mid].x == cut.x) lo = mid;
+                else hi = mid;
+            }
+            join = make_int4(cut.x, tid - 1, lo, 0);
+        }
+        const int slot = block_exclusive_scan<int, THREADS>(int(first), &n_joins, isums);
+        if (first) a.joins[slot] = join;
+    }
+    if (tid == 0) *reinterpret_cast<int4 *>(a.plan) = make_int4(n_items, rounds, total, n_joins);
+}
+
+// Few sequences and items (THREADS and THREADS x IPT at most, costs that add up in 32 bits): all in shared memory, one thread a
+// sequence and IPT items.
+template <bool PAGED, int THREADS, int IPT>
+__global__ void __launch_bounds__(THREADS, 1) gqa_prefill_plan_small_kernel(const __grid_constant__ PrefillArgs a) {
+    constexpr int WARPS = THREADS / 32, HIST = WARPS * kPlanBuckets, PER = HIST / THREADS;
+    __shared__ int hist[WARPS][kPlanBuckets];
+    __shared__ PlanSeq seq[THREADS];
+    __shared__ int tiles[THREADS + 1];
+    __shared__ unsigned prefix[THREADS * IPT + 1];
+    __shared__ long long sums[33];
+    __shared__ int isums[33], shared_max;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    int mine = 0;
+    if (tid < a.B) {
+        const PlanSeq s = plan_seq<PAGED>(a, tid, a.err);
+        seq[tid] = s;
+        mine = (s.n + 2 * a.tok_tile - 1) / (2 * a.tok_tile);
+    }
+    if (tid == 0) shared_max = 1;
+    for (int i = tid; i < HIST; i += THREADS) (&hist[0][0])[i] = 0;
+    int n_items;
+    const int at = block_exclusive_scan<int, THREADS>(mine, &n_items, isums);
+    if (tid < a.B) tiles[tid] = at;
     // overlapping ranges of bad offsets (flagged already) may hold more than any good ones
     n_items = min(n_items, a.max_items);
     __syncthreads();
-
-    auto item_at = [&](int i) {
-        int lo = 0, hi = a.B;  // the last sequence with tile_prefix <= i
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tile_prefix[mid] <= i) lo = mid;
-            else hi = mid;
-        }
-        return plan_item<PAGED>(a, lo, i - tile_prefix[lo], a.err);
-    };
-    PrefillItem own = {};
+    PrefillItem own[IPT];
     int most = 1;
-    if constexpr (SMALL) {
-        if (tid < n_items) own = item_at(tid);
-        most = max(1, own.cost);
-    } else {
-        for (int i = tid; i < n_items; i += kPlanThreads) {
-            const PrefillItem it = item_at(i);
-            a.unsorted[i] = it;
-            most = max(most, it.cost);
+#pragma unroll
+    for (int k = 0; k < IPT; ++k) {
+        const int i = (warp * IPT + k) * 32 + lane;
+        own[k].cost = 0;
+        if (i < n_items) {
+            const int b = plan_search(tiles, a.B, i);
+            own[k] = plan_item(a, b, seq[b], i - tiles[b]);
+            most = max(most, own[k].cost);
         }
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0 && most > 1) atomicMax(&shared_max, most);
+    __syncthreads();
+    const int top = shared_max;
+    // stable counting sort, longest first: a warp counts and places a run of items
+    const unsigned below = (1u << lane) - 1;
+    int bucket[IPT], rank[IPT];
+#pragma unroll
+    for (int k = 0; k < IPT; ++k) {
+        bucket[k] = own[k].cost > 0 ? plan_bucket(own[k].cost, top) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, bucket[k]);
+        rank[k] = __popc(same & below);
+        if (bucket[k] >= 0) rank[k] += hist[warp][bucket[k]];
+        __syncwarp();
+        if (bucket[k] >= 0 && (same & below) == 0) hist[warp][bucket[k]] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    {
+        int x[PER], sum = 0;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int pos = PER * tid + e;  // bucket-major
+            x[e] = hist[pos % WARPS][pos / WARPS];
+            sum += x[e];
+        }
+        int all;
+        int base = block_exclusive_scan<int, THREADS>(sum, &all, isums);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int pos = PER * tid + e;
+            hist[pos % WARPS][pos / WARPS] = base;
+            base += x[e];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < IPT; ++k) {
+        if (bucket[k] < 0) continue;
+        const int pos = hist[warp][bucket[k]] + rank[k];
+        a.items[pos] = own[k];
+        prefix[pos] = own[k].cost;
+    }
+    __syncthreads();
+    unsigned cost[IPT], sum = 0, all;
+#pragma unroll
+    for (int k = 0; k < IPT; ++k) {
+        const int i = tid * IPT + k;
+        cost[k] = i < n_items ? prefix[i] : 0;
+        sum += cost[k];
+    }
+    unsigned before = block_exclusive_scan<unsigned, THREADS>(sum, &all, reinterpret_cast<unsigned *>(isums));
+#pragma unroll
+    for (int k = 0; k < IPT; ++k) {
+        const int i = tid * IPT + k;
+        if (i < n_items) prefix[i] = before;
+        before += cost[k];
+    }
+    if (tid == 0) prefix[n_items] = all;
+    __syncthreads();
+    plan_shares<unsigned, THREADS>(a, n_items, top, prefix, reinterpret_cast<int2 *>(seq), sums, isums, &shared_max);
+}
+
+// Any number of them, through the workspace.
+template <bool PAGED>
+__global__ void __launch_bounds__(kPlanThreads, 1) gqa_prefill_plan_kernel(const __grid_constant__ PrefillArgs a) {
+    __shared__ int hist[kPlanThreads / 32][kPlanBuckets];
+    __shared__ int2 cuts[kPlanThreads + 1];
+    __shared__ long long sums[33];
+    __shared__ int isums[33], shared_max;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    const int tpi = 2 * a.tok_tile;
+    const int per_thread = (a.B + kPlanThreads - 1) / kPlanThreads;
+    int mine = 0;
+    for (int b = tid * per_thread; b < min((tid + 1) * per_thread, a.B); ++b)
+        mine += (plan_seq<PAGED>(a, b, a.err).n + tpi - 1) / tpi;
+    if (tid == 0) shared_max = 1;
+    for (int i = tid; i < (kPlanThreads / 32) * kPlanBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
+    int n_items;
+    int at = block_exclusive_scan<int, kPlanThreads>(mine, &n_items, isums);
+    for (int b = tid * per_thread; b < min((tid + 1) * per_thread, a.B); ++b) {
+        a.tile_prefix[b] = at;
+        at += (plan_seq<PAGED>(a, b, nullptr).n + tpi - 1) / tpi;
+    }
+    n_items = min(n_items, a.max_items);  // as above
+    __syncthreads();
+    int most = 1;
+    for (int i = tid; i < n_items; i += kPlanThreads) {
+        const int b = plan_search(a.tile_prefix, a.B, i);
+        const PrefillItem it = plan_item(a, b, plan_seq<PAGED>(a, b, nullptr), i - a.tile_prefix[b]);
+        a.unsorted[i] = it;
+        most = max(most, it.cost);
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) atomicMax(&shared_max, most);
     __syncthreads();
     const int top = shared_max;
-
-    // stable counting sort, longest first: a warp counts and places a run of items
     const int run = (n_items + kPlanThreads - 1) / kPlanThreads * 32;
-    auto bucket_of = [&](int cost) { return kPlanBuckets - 1 - int((unsigned long long)unsigned(cost) * (kPlanBuckets - 1) / unsigned(top)); };
     const unsigned below = (1u << lane) - 1;
     for (int i = warp * run + lane; i < (warp + 1) * run; i += 32) {
         const bool there = i < n_items;
-        const int bucket = there ? bucket_of(SMALL ? own.cost : a.unsorted[i].cost) : -1;
+        const int bucket = there ? plan_bucket(a.unsorted[i].cost, top) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, bucket);
         if (there && (same & below) == 0) hist[warp][bucket] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
     {
-        int x[2], sum = 0;
+        constexpr int WARPS = kPlanThreads / 32, PER = kPlanBuckets / 32;
+        int x[PER], sum = 0;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int pos = 2 * tid + e;  // bucket-major
-            x[e] = hist[pos % (kPlanThreads / 32)][pos / (kPlanThreads / 32)];
+        for (int e = 0; e < PER; ++e) {
+            const int pos = PER * tid + e;
+            x[e] = hist[pos % WARPS][pos / WARPS];
             sum += x[e];
         }
         int all;
-        int base = block_exclusive_scan(sum, &all, isums);
+        int base = block_exclusive_scan<int, kPlanThreads>(sum, &all, isums);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int pos = 2 * tid + e;
-            hist[pos % (kPlanThreads / 32)][pos / (kPlanThreads / 32)] = base;
+        for (int e = 0; e < PER; ++e) {
+            const int pos = PER * tid + e;
+            hist[pos % WARPS][pos / WARPS] = base;
             base += x[e];
         }
     }
     __syncthreads();
     for (int i = warp * run + lane; i < (warp + 1) * run; i += 32) {
         const bool there = i < n_items;
-        PrefillItem it = own;
-        if (!SMALL && there) it = a.unsorted[i];
-        const int bucket = there ? bucket_of(it.cost) : -1;
+        PrefillItem it = {};
+        if (there) it = a.unsorted[i];
+        const int bucket = there ? plan_bucket(it.cost, top) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, bucket);
-        if (there) {
-            const int pos = hist[warp][bucket] + __popc(same & below);
-            a.items[pos] = it;
-            if (SMALL) cost_prefix[pos] = it.cost;
-        }
+        if (there) a.items[hist[warp][bucket] + __popc(same & below)] = it;
         __syncwarp();
         if (there && (same & below) == 0) hist[warp][bucket] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
-
-    // cost before each item
-    const int share = SMALL ? 1 : (n_items + kPlanThreads - 1) / kPlanThreads;
+    const int share = (n_items + kPlanThreads - 1) / kPlanThreads;
     long long cost = 0, all_cost;
-    if constexpr (SMALL) cost = tid < n_items ? cost_prefix[tid] : 0;
-    else
-        for (int i = tid * share; i < min((tid + 1) * share, n_items); ++i) cost += a.items[i].cost;
-    long long before = block_exclusive_scan(cost, &all_cost, sums);
+    for (int i = tid * share; i < min((tid + 1) * share, n_items); ++i) cost += a.items[i].cost;
+    long long before = block_exclusive_scan<long long, kPlanThreads>(cost, &all_cost, sums);
     for (int i = tid * share; i < min((tid + 1) * share, n_items); ++i) {
-        cost_prefix[i] = before;
-        if (!SMALL) before += a.items[i].cost;
+        a.cost_prefix[i] = before;
+        before += a.items[i].cost;
     }
-    if (tid == 0) cost_prefix[n_items] = all_cost;
+    if (tid == 0) a.cost_prefix[n_items] = all_cost;
     __syncthreads();
-
-    // Whole rounds, as long as no worker passes its share of the total.
-    const int W = a.workers, HB = a.head_blocks;
-    const int total = n_items * HB;
-    auto cost_of = [&](int number) {
-        const int item = unsigned(number) / unsigned(HB);
-        return int(cost_prefix[item + 1] - cost_prefix[item]);
-    };
-    auto number_of = [&](int r, int w) { return r * W + ((r & 1) ? W - 1 - w : w); };
-    const long long goal = max((all_cost * HB + W - 1) / W, (long long)min(top, kPreCostItem + kPreMinSplit * kPreCostTwo));
-    const bool exact = total / W <= kPlanExactRounds;
-    int rounds = 0;
-    long long load = 0;  // this worker's, after them
-    if (exact) {
-        if (tid == 0) shared_max = total / W;
-        __syncthreads();
-        if (tid < W) {
-            int r = 0;
-            for (long long sum = 0; r < total / W; ++r) {
-                sum += cost_of(number_of(r, tid));
-                if (sum > goal) break;
-            }
-            atomicMin(&shared_max, r);
-        }
-        __syncthreads();
-        rounds = shared_max;
-        if (tid < W)
-            for (int r = 0; r < rounds; ++r) load += cost_of(number_of(r, tid));
-    } else {
-        // Many rounds: two of them, forth and back, are taken as even, as much as their first and last item together.
-        long long done = 0;
-        for (int r0 = 0;; r0 += kPlanThreads) {
-            const int r = r0 + tid;
-            const long long c = (long long)(2 * r + 2) * W <= total ? cost_of(2 * r * W) + cost_of((2 * r + 2) * W - 1) : goal + 1;
-            long long turn;
-            const long long sum = block_exclusive_scan(c, &turn, sums) + c + done;
-            const int fit = __syncthreads_count(sum <= goal);
-            rounds += 2 * fit;
-            done += turn;
-            if (fit < kPlanThreads) break;
-        }
-    }
-    // The rest is one line of steps that fills every worker up to its share of the total; no part of it is too small.
-    const int n0 = rounds * W;
-    const long long line = n0 < total ? cost_prefix[n0 / HB] * HB + (long long)(n0 % HB) * cost_of(n0) : all_cost * HB;
-    if (!exact) load = line / W;
-    const long long need = tid < W ? max(goal - load, (long long)min(top, kPreCostItem + kPreMinSplit * kPreCostTwo)) : 0;
-    long long ignored;
-    const long long skip = block_exclusive_scan(need, &ignored, sums);
-    if (tid < W) {
-        int2 cut = make_int2(total, 0);
-        const long long pos = line + skip;
-        if (tid == 0) {
-            cut.x = n0;
-        } else if (pos < all_cost * HB) {
-            int lo = 0, hi = n_items;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (cost_prefix[mid] * HB <= pos) lo = mid;
-                else hi = mid;
-            }
-            const PrefillItem it = a.items[lo];
-            const long long rem = pos - cost_prefix[lo] * HB;
-            const int head = int(rem / it.cost), y = int(rem % it.cost);
-            int step = max(0, y - kPreCostItem) / (it.n_tok > a.tok_tile ? kPreCostTwo : kPreCostOne);
-            if (!a.may_split) step = 2 * y >= it.cost ? it.steps : 0;
-            cut.x = lo * HB + head;
-            if (it.steps - step < kPreSnap && 2 * y >= it.cost) cut.x += 1;
-            else if (step >= kPreSnap && it.steps - step >= kPreSnap) cut.y = step;
-        }
-        cuts_s[tid] = cut;
-        a.cuts[tid] = cut;
-    }
-    if (tid == 0) a.cuts[W] = cuts_s[W] = make_int2(total, 0);
-    __syncthreads();
-    // items that several workers hold steps of
-    bool first = false;
-    int2 join;
-    if (tid > 0 && tid < W) {
-        const int2 cut = cuts_s[tid], prev = cuts_s[tid - 1];
-        first = cut.y > 0 && !(prev.x == cut.x && prev.y > 0);
-        int lo = tid, hi = W;  // the last worker whose share begins within the item
-        while (first && hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cuts_s[mid].x == cut.x) lo = mid;
-            else hi = mid;
-        }
-        join = make_int2(tid, lo);
-    }
-    int n_joins;
-    const int slot = block_exclusive_scan(int(first), &n_joins, isums);
-    if (first) a.joins[slot] = join;
-    if (tid == 0) {
-        a.plan->n_items = n_items;
-        a.plan->rounds = rounds;
-        a.plan->total = total;
-        a.plan->n_joins = n_joins;
-    }
+    plan_shares<long long, kPlanThreads>(a, n_items, top, a.cost_prefix, cuts, sums, isums, &shared_max);
 }
 
 // One piece of a worker's work.

@@ -91,7 +91,7 @@ def pieces(items, HB, W, rounds, cuts, w):
     return got
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(200))
 def test_plan_covers_every_step_once(seed):
     r = random.Random(seed)
     W = r.choice([1, 2, 7, 152])
@@ -132,10 +132,9 @@ def test_plan_covers_every_step_once(seed):
             last += 1
         for x in range(w - 1, last + 1):
             slot = 2 * x + 1 if x == w - 1 else 2 * x
-            empty = x > w - 1 and cuts[x] == cuts[x + 1]
-            assert empty or slots[slot] == n_
+            assert slots[slot] == n_  # no share without steps among them
             joined.add(slot)
-    assert joined >= set(slots)
+    assert joined == set(slots)
     if may_split and items:
         slack = 2 * COST_ITEM + 2 * SNAP * COST_TWO + min(top, COST_ITEM + MIN_SPLIT * COST_TWO)
         assert max(loads) <= goal + slack + (0 if len(items) * HB // W <= EXACT_ROUNDS else 2 * top)
