@@ -22,8 +22,8 @@ enum PrefillSource {
 
 constexpr int kPreKeys = 128;   // keys of a step
 constexpr int kPreTile = 128;   // query rows of a tile; an item has one or two
-constexpr int kPreMinSplit = 4; // steps that a part of a divided item has at least, as planned
-constexpr int kPreSnap = 2;     // ... and as cut: nearer to an item's end, the cut moves there
+constexpr int kPreMinSplit = 6; // steps that a part of a divided item has at least, as planned
+constexpr int kPreSnap = 3;     // ... and as cut: nearer to an item's end, the cut moves there
 
 // A piece of work is steps [s0, s1) of an item: up to 2 * tok_tile consecutive tokens of one sequence, for one block of
 // query heads of one KV head (the item's rows), over the keys that its last row sees.
