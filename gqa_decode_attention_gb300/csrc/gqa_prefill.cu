@@ -256,6 +256,10 @@ extern "C" gqa_status gqa_prefill_paged(const void *q, long long q_stride, int k
     a.page_table = page_table;
     a.seq_lens = seq_lens;
     a.page_size = page_size, a.pages_per_req = pages_per_req, a.num_pages = num_pages;
+    int lg = 0;
+    while ((1LL << lg) < page_size) ++lg;
+    a.page_mul = unsigned((1ull << (31 + lg)) / unsigned(page_size) + 1);
+    a.page_shift = 31 + lg;
     const bool kv8 = kv_dtype == GQA_KV_FP8_E4M3FN || kv_dtype == GQA_KV_INT8;
     const bool host_scales = kv8 && k_scales == nullptr;
     a.k_scales = kv8 ? k_scales : nullptr;

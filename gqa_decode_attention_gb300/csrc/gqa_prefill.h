@@ -66,6 +66,8 @@ struct PrefillArgs {
     const int32_t *page_table;
     const int32_t *seq_lens;
     int page_size, pages_per_req, num_pages;
+    unsigned page_mul;  // t / page_size = t * page_mul >> page_shift
+    int page_shift;
     int box_rows;  // tokens of a TMA box
     const float *k_scales;
     const float *v_scales;

@@ -488,28 +488,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const bool masked = key0 + kPreKeys > all_see;
                     const int left = seen - key0;
                     float m4[4];
-                    // Scores h * 32 .. of the row as they go into the maximum: 4-bit keys' parameters applied.  The scale enters
-                    // through the maximum (exact: it is positive) and one fma a weight.
-                    auto finish = [&](uint32_t (&x)[32], int h) {
-                        if constexpr (C::K_PARAMS) {
-                            const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512) + h * 8;
-                            const float2 qs2 = make_float2(q_sum, q_sum);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const uint4 y = par[c / 4];
-                                const uint32_t w[4] = {y.x, y.y, y.z, y.w};  // scales of two keys, zeros of two keys, twice
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e]));
-                                    const float2 kz = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e + 1]));
-                                    const float2 z = fma2(make_float2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), ks,
-                                                          mul2(qs2, kz));
-                                    x[c + 2 * e] = __float_as_uint(z.x);
-                                    x[c + 2 * e + 1] = __float_as_uint(z.y);
-                                }
-                            }
-                        }
-                    };
+                    // Scores stay raw: the scale enters through the maximum (exact: it is positive) and one fma a weight.
                     auto hide = [&](uint32_t (&x)[32], int h) {
                         const int n = left - h * 32;
 #pragma unroll
@@ -560,7 +539,60 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         if (renew) m_ref = mx;
                         return renew;
                     };
-                    if (masked) {
+                    if constexpr (C::K_PARAMS) {
+                        // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back; parameters
+                        // and scores of the next are under way meanwhile (beside the tensor core's reads of shared memory theirs
+                        // take hundreds of cycles).
+                        const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512);
+                        const float2 qs2 = make_float2(q_sum, q_sum);
+                        uint4 pr[2][8];
+                        uint32_t x[2][32];
+                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+                        tmem_ld32(s_at, x[0]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) pr[0][e] = par[e];
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            tmem_wait_ld();
+                            if (h < 3) {
+                                tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) pr[(h + 1) & 1][e] = par[(h + 1) * 8 + e];
+                            }
+                            uint32_t (&y)[32] = x[h & 1];
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const uint4 z = pr[h & 1][c / 4];
+                                const uint32_t w[4] = {z.x, z.y, z.z, z.w};  // scales of two keys, zeros of two keys, twice
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e]));
+                                    const float2 kz = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e + 1]));
+                                    const float2 v = fma2(make_float2(__uint_as_float(y[c + 2 * e]), __uint_as_float(y[c + 2 * e + 1])), ks,
+                                                          mul2(qs2, kz));
+                                    y[c + 2 * e] = __float_as_uint(v.x);
+                                    y[c + 2 * e + 1] = __float_as_uint(v.y);
+                                }
+                            }
+                            if (masked) hide(y, h);
+                            maximum(y);
+                            tmem_st32(s_at + h * 32, y);
+                        }
+                        tmem_wait_st();
+                        follow();
+                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+                        uint32_t pk[kPreKeys / 2];
+                        tmem_ld32(s_at, x[0]);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            tmem_wait_ld();
+                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
+                            weigh(x[h & 1], pk + h * 16, make_float2(-m_use, -m_use));
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                    } else if (masked) {
                         // 32 keys after the other, those that no row of the warp sees left out (in short prompts half of them):
                         // the maximum, then the weights from scores read once more
                         const int most = most_see - key0;
@@ -570,7 +602,6 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             uint32_t x[32];
                             tmem_ld32(s_at + h * 32, x);
                             tmem_wait_ld();
-                            finish(x, h);
                             hide(x, h);
                             maximum(x);
                         }
@@ -584,8 +615,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 uint32_t x[32];
                                 tmem_ld32(s_at + h * 32, x);
                                 tmem_wait_ld();
-                                finish(x, h);
-                                hide(x, h);
+                                    hide(x, h);
                                 weigh(x, w, make_float2(-m_use, -m_use));
                             }
                             tmem_st16(s_at + h * 16, w);  // (columns whose scores have been read)
@@ -600,7 +630,6 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
-                            finish(sr[h], h);
                             maximum(sr[h]);
                         }
                         follow();
@@ -630,7 +659,6 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             for (int h = 0; h < 4; ++h) {
                                 tmem_wait_ld();
                                 if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) & 1]);
-                                finish(sr[h & 1], h);
                                 maximum(sr[h & 1]);
                                 weigh(sr[h & 1], pk + h * 16, nm2);
                             }

@@ -68,14 +68,20 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
     return x;
 }
 
+// key / page_size by a product (exact below 2^31).
+__device__ __forceinline__ int prefill_page(const PrefillArgs &a, int key) {
+    return int((unsigned long long)unsigned(key) * a.page_mul >> a.page_shift);
+}
+
 // Pool row of a request's key, or -1 (flagged) where its page is out of range.
 __device__ __forceinline__ int prefill_pool_row(const PrefillArgs &a, int req, int key) {
-    const int page = a.page_table[(long long)req * a.pages_per_req + key / a.page_size];
+    const int in_req = prefill_page(a, key);
+    const int page = a.page_table[(long long)req * a.pages_per_req + in_req];
     if (page < 0 || page >= a.num_pages) {
         flag_error(a.err, kErrIndex);
         return -1;
     }
-    return page * a.page_size + key % a.page_size;
+    return page * a.page_size + key - in_req * a.page_size;
 }
 
 // Four fp16 pairs of eight 8-bit or 4-bit codes.
@@ -208,14 +214,14 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
         const int *table = nullptr;
         auto look_ahead = [&](int step) {
             const int key = step * kPreKeys + lw * 32 + lane;
-            if (key < p.item.L) page = table[key / a.page_size];
+            if (key < p.item.L) page = table[prefill_page(a, key)];
         };
         auto look_up = [&](int step) {
             const int key = step * kPreKeys + lw * 32 + lane;
             next_row = -1;
             if (key < p.item.L && step < p.s1) {
                 if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrIndex);
-                else next_row = page * a.page_size + key % a.page_size;
+                else next_row = (page - prefill_page(a, key)) * a.page_size + key;
             }
             if constexpr (SRC == kPreInt4) {
                 next_par = make_uint2(0, 0);
@@ -235,7 +241,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
         };
         // first_clean: keys of the step from here on may hold what some row must not see
         auto store = [&](auto is_v_t, auto clean_t, uint8_t *tile, int first_clean) {
-            constexpr bool is_v = decltype(is_v_t)::value, clean = decltype(clean_t)::value;
+            constexpr bool is_v = decltype(is_v_t)::value, careful = decltype(clean_t)::value;
             bool found = false;
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the other one's newest copies
 #pragma unroll
@@ -262,16 +268,19 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                         if constexpr (SRC == kPreInt4) {
                             __half2 x = widen_int4(w[u], e);
                             if constexpr (is_v) {
-                                // values past fp16's largest are it; a parameter that is not finite is NaN already
-                                const __half2 big(__half_raw{0x7bff}, __half_raw{0x7bff});
-                                x = __hmin2_nan(__hmax2_nan(__hfma2(x, vs, vz), __hneg2(big)), big);
+                                x = __hfma2(x, vs, vz);
+                                if constexpr (careful) {
+                                    // values past fp16's largest are it; a parameter that is not finite is NaN already
+                                    const __half2 big(__half_raw{0x7bff}, __half_raw{0x7bff});
+                                    x = __hmin2_nan(__hmax2_nan(x, __hneg2(big)), big);
+                                }
                             }
                             o[e] = *reinterpret_cast<const uint32_t *>(&x);
                         } else {
                             o[e] = widen_pair<SRC>(w[2 * u + (e >> 1)], e & 1);
                         }
                     }
-                    if constexpr (clean) {
+                    if constexpr (careful && SRC != kPreInt8) {
                         if (k >= first_clean) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -321,8 +330,14 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 ok = at < C::VST || mbar_wait_bounded(&v_empty[at % C::VST], (at / C::VST - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (SRC != kPreInt8 && p.masked(step))
-                    store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, p.first_limit - step * kPreKeys);
+                bool careful = SRC != kPreInt8 && p.masked(step);
+                if constexpr (SRC == kPreInt4) {  // a value of some key may pass fp16's largest
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
+                    careful |= __any_sync(0xffffffffu, !(fabsf(f.x) * 15.f + fabsf(f.y) <= 65504.f));
+                }
+                if (careful)
+                    store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES,
+                          p.masked(step) ? p.first_limit - step * kPreKeys : kPreKeys);
                 else
                     store(std::true_type(), std::false_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, 0);
                 fence_proxy_async_shared();
