@@ -540,12 +540,12 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         return renew;
                     };
                     if constexpr (C::K_PARAMS) {
-                        // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back; parameters
-                        // and scores of the next are under way meanwhile (beside the tensor core's reads of shared memory theirs
-                        // take hundreds of cycles).
-                        const uint4 *par = reinterpret_cast<const uint4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 512);
+                        // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back (held in
+                        // registers they spilled: 350 us against 331 on chunks of 300 tokens); parameters and scores of the
+                        // next are under way meanwhile (beside the tensor core's reads of shared memory theirs take long).
+                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 1024);
                         const float2 qs2 = make_float2(q_sum, q_sum);
-                        uint4 pr[2][8];
+                        float4 pr[2][8];  // scales and zeros of two keys each
                         uint32_t x[2][32];
                         m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
                         tmem_ld32(s_at, x[0]);
@@ -554,24 +554,22 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             tmem_wait_ld();
-                            if (h < 3) {
-                                tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) pr[(h + 1) & 1][e] = par[(h + 1) * 8 + e];
-                            }
+                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
                             uint32_t (&y)[32] = x[h & 1];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const uint4 z = pr[h & 1][c / 4];
-                                const uint32_t w[4] = {z.x, z.y, z.z, z.w};  // scales of two keys, zeros of two keys, twice
+                            for (int half = 0; half < 2; ++half) {
+                                if (h < 3 || half == 0) {
 #pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const float2 ks = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e]));
-                                    const float2 kz = __half22float2(*reinterpret_cast<const __half2 *>(&w[2 * e + 1]));
-                                    const float2 v = fma2(make_float2(__uint_as_float(y[c + 2 * e]), __uint_as_float(y[c + 2 * e + 1])), ks,
-                                                          mul2(qs2, kz));
-                                    y[c + 2 * e] = __float_as_uint(v.x);
-                                    y[c + 2 * e + 1] = __float_as_uint(v.y);
+                                    for (int e = 0; e < 8; ++e) pr[(half + 1) & 1][e] = par[(h * 2 + half + 1) * 8 + e];
+                                }
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 z = pr[half][e];
+                                    const int c = half * 16 + 2 * e;
+                                    const float2 v = fma2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(z.x, z.y),
+                                                          mul2(qs2, make_float2(z.z, z.w)));
+                                    y[c] = __float_as_uint(v.x);
+                                    y[c + 1] = __float_as_uint(v.y);
                                 }
                             }
                             if (masked) hide(y, h);

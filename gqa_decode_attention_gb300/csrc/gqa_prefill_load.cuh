@@ -26,8 +26,8 @@ struct PrefillCfg {
     static constexpr int K_OFF = 2 * Q_BYTES;
     static constexpr int V_OFF = K_OFF + KST * K_BYTES;
     static constexpr int STAT_OFF = V_OFF + VST * V_BYTES;  // [128] float2: what row group 1 hands over
-    static constexpr int PAR_OFF = STAT_OFF + 1024;         // [PST][64] uint2: fp16 scales of two keys, their zeros
-    static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * 512 : 0);  // codes of K and of V on their way
+    static constexpr int PAR_OFF = STAT_OFF + 1024;         // [PST][64] float4: scales of two keys, their zeros
+    static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * 1024 : 0);  // codes of K and of V on their way
     static constexpr int RAW_BYTES = !F16 ? 0 : kPreKeys * DV / (SRC == kPreInt4 ? 2 : 1);
     static constexpr int BAR_OFF = RAW_OFF + 2 * RAW_BYTES;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;
@@ -310,14 +310,15 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 if constexpr (SRC == kPreInt4) {
                     if ((par.x & 0x7c00u) == 0x7c00u || (par.x & 0x7c000000u) == 0x7c000000u) par.x = 0x7fff7fffu;
                     if ((par.y & 0x7c00u) == 0x7c00u || (par.y & 0x7c000000u) == 0x7c000000u) par.y = 0x7fff7fffu;
-                    const uint32_t of_next = __shfl_down_sync(0xffffffffu, par.x, 1);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.x));
+                    const float scale1 = __shfl_down_sync(0xffffffffu, f.x, 1), zero1 = __shfl_down_sync(0xffffffffu, f.y, 1);
                     // (the ring of parameters is free when the stage of K is, see PST)
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if ((lane & 1) == 0)
-                        reinterpret_cast<uint2 *>(smem + C::PAR_OFF)[at % C::PST * (kPreKeys / 2) + (lw * 32 + lane) / 2] =
-                            make_uint2(__byte_perm(par.x, of_next, 0x5410), __byte_perm(par.x, of_next, 0x7632));
+                        reinterpret_cast<float4 *>(smem + C::PAR_OFF)[at % C::PST * (kPreKeys / 2) + (lw * 32 + lane) / 2] =
+                            make_float4(f.x, scale1, f.y, zero1);
                 } else {
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
