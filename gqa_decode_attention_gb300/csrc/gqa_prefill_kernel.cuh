@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
     uint64_t *q_ready = o_full + 2;        // [2] a tile's rows are fp16
     uint64_t *stat_full = q_ready + 2;      // [1] row group 1's references and sums are in `stat`
     uint64_t *stat_free = stat_full + 1;   // [1] ... and joined, its O too
-    uint64_t *fin = stat_free + 1;         // [1] every product is done
+    uint64_t *piece_full = stat_free + 1;  // [kPrePieces]
+    uint64_t *piece_empty = piece_full + kPrePieces;
+    uint64_t *fin = piece_empty + kPrePieces;  // [1] every product is done
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(fin + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_base_s + 1);
     volatile int *bad_v = abort_flag + 1;  // elements of V that are not finite were cleared, in this piece or an earlier one
@@ -167,6 +169,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         for (int t = 0; t < 2; ++t) mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 128), mbar_init(&o_full[t], 1), mbar_init(&q_ready[t], 128);
         mbar_init(stat_full, 128);
         mbar_init(stat_free, 128);
+        // read by the softmax warps, the issuer, and V's loader and cleaner or the four that convert
+        for (int i = 0; i < kPrePieces; ++i) mbar_init(&piece_full[i], 1), mbar_init(&piece_empty[i], 8 + 1 + (C::TMA ? 2 : 4));
         mbar_init(fin, 1);
         *abort_flag = 0;
         *bad_v = 0;
@@ -184,10 +188,12 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
     pdl_wait_primary();  // the plan, and whatever wrote the inputs
 
     bool ok = true;
+    PrefillPiece *pieces = reinterpret_cast<PrefillPiece *>(smem + C::PIECE_OFF);
+    PieceFeed feed(pieces, piece_full, piece_empty);
     if (!C::TMA && warp >= 12) {
         if constexpr (!C::TMA) {
             set_registers<C::LAUNCH_REGS, C::LOAD_REGS>();
-            ok = prefill_load<DQK, DV, SRC>(a, smem, k_full, k_empty, v_full, v_empty, abort_flag, bad_v);
+            ok = prefill_load<DQK, DV, SRC>(a, smem, k_full, k_empty, v_full, v_empty, feed, abort_flag, bad_v);
         }
         if (!ok && lane == 0) {
             flag_error(a.err, kErrTimeout);
@@ -196,8 +202,6 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         __syncwarp();
     } else if (warp >= 8) {
         set_registers<C::LAUNCH_REGS, C::OTHER_REGS>();
-        PrefillWalk walk(a, blockIdx.x);
-        PrefillPiece p;
         if (warp == 8) {
             // -------------------------------------------------------- products
             // One lane; descriptors are a base and a constant and ring places are counted, so that the next product is issued
@@ -211,16 +215,20 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 const uint32_t v_desc = desc_lo(smem_u32(smem + C::V_OFF), kPreKeys * 128);
                 uint32_t q_phase = 0, p_phase = 0, k_phase = 0, v_phase = 0;
                 int ks = 0, vs = 0;  // stages in turn
-                while (ok && walk.next(&p)) {
-                    if (p.units == 0) continue;
+                while (ok) {
+                    const volatile PrefillPiece *p = feed.next(limit, abort_flag, &ok);
+                    if (p == nullptr) break;
+                    const int units = p->units;
+                    const bool two = p->two;
+                    feed.done();
+                    feed.step();
+                    if (units == 0) continue;
                     if constexpr (C::F16)
                         ok = mbar_wait_bounded(&q_ready[0], q_phase, limit, abort_flag) &&
                              mbar_wait_bounded(&q_ready[1], q_phase, limit, abort_flag);
                     else
                         ok = mbar_wait_bounded(q_full, q_phase, limit, abort_flag);
                     q_phase ^= 1;
-                    const int units = p.units;
-                    const bool two = p.two;
                     auto qk = [&](int u) {
                         const uint32_t t = u & 1;
                         if (!two || t == 0) {
@@ -283,12 +291,12 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             const CUtensorMap *map = is_k ? &tm_k : &tm_v;
             int n_piece = 0, at = 0;
             uint32_t raw_next = 0, raw_last = 0;  // a bit a stage: parity of its next uncleared step, whether its last was one
-            while (ok && walk.next(&p)) {
-                if (p.units == 0) continue;
+            auto load_piece = [&](const PrefillPiece &p) {
+                if (p.units <= 0) return;
                 if (is_k) {
                     ok = n_piece == 0 || mbar_wait_bounded(q_empty, (n_piece - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    if (!ok) return;
                     ++n_piece;
                     if (lane == 0) {
                         const int tiles = p.units > 1 ? 2 : 1;
@@ -297,7 +305,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
 #pragma unroll
                             for (int c = 0; c < C::QC; ++c)
                                 tma_load_3d(smem + C::Q_OFF + t * C::Q_BYTES + c * (kPreTile * 128), &tm_q, q_full, c * 64,
-                                            p.g * a.G + p.hb * a.g_tile, p.item.q_row + (p.two ? t * a.tok_tile : 0));
+                                            p.g * a.G + p.hb * a.g_tile, p.q_row + (p.two ? t * a.tok_tile : 0));
                     }
                     __syncwarp();
                 }
@@ -307,8 +315,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     bool there = false;
                     if constexpr (SRC == kPrePages) {
                         const int key = step * kPreKeys + lane * a.box_rows;
-                        there = lane * a.box_rows < kPreKeys && key < p.item.L;
-                        if (there) row = prefill_pool_row(a, p.item.req, key);
+                        there = lane * a.box_rows < kPreKeys && key < p.L;
+                        if (there) row = prefill_pool_row(a, p.req, key);
                         if (row < 0) row = a.num_pages * a.page_size;  // past the end: zeros
                     }
                     ok = at < stages || mbar_wait_bounded(&empty[st], (at / stages - 1) & 1, limit, abort_flag);
@@ -318,7 +326,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     uint8_t *dst = ring + st * stage_bytes;
                     uint64_t *bar = &full[st];
                     raw_last &= ~(1u << st);
-                    if (!is_k && p.masked(step)) {
+                    if (!is_k && (step + 1) * kPreKeys > p.first_limit) {
                         bar = &v_raw[st];
                         raw_last |= 1u << st;
                         raw_next ^= 1u << st;
@@ -327,7 +335,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         if (lane == 0) {
                             mbar_arrive_expect_tx(bar, stage_bytes);
                             for (int c = 0; c < chunks; ++c)
-                                tma_load_3d(dst + c * (kPreKeys * 128), map, bar, c * 64, p.g, p.item.k_row + step * kPreKeys);
+                                tma_load_3d(dst + c * (kPreKeys * 128), map, bar, c * 64, p.g, p.k_row + step * kPreKeys);
                         }
                     } else {
                         const int boxes = __popc(__ballot_sync(0xffffffffu, there));
@@ -338,6 +346,36 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 tma_load_3d(dst + c * (kPreKeys * 128) + lane * a.box_rows * 128, map, bar, c * 64, p.g, row);
                     }
                     __syncwarp();
+                }
+            };
+            PrefillPiece p;
+            if (is_k) {
+                // This warp walks the plan for all of them, a piece ahead of its own loads.
+                PrefillWalk walk(a, blockIdx.x);
+                for (int n = 0; ok; ++n) {
+                    walk.next(&p);
+                    ok = n < kPrePieces || mbar_wait_bounded(&piece_empty[n % kPrePieces], (n / kPrePieces - 1) & 1, limit, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        pieces[n % kPrePieces] = p;
+                        mbar_arrive(&piece_full[n % kPrePieces]);
+                    }
+                    __syncwarp();
+                    if (p.units < 0) break;
+                    load_piece(p);
+                }
+            } else {
+                while (ok) {
+                    const volatile PrefillPiece *x = feed.next(limit, abort_flag, &ok);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok || x == nullptr) break;
+                    p.units = x->units, p.L = x->L, p.req = x->req, p.k_row = x->k_row, p.g = x->g, p.s0 = x->s0, p.s1 = x->s1;
+                    p.first_limit = x->first_limit;
+                    __syncwarp();
+                    if (lane == 0) feed.done();
+                    feed.step();
+                    load_piece(p);
                 }
             }
             if (!ok && lane == 0) {
@@ -358,18 +396,24 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             // -------------------------------------------------------- V rows that no row may see
             int at = 0;
             uint32_t raw_phase = 0;
-            while (ok && walk.next(&p)) {
-                if (p.units == 0) continue;
-                for (int step = p.s0; ok && step < p.s1; ++step) {
-                    const int st = (at + step - p.s0) % C::VST;
-                    if (!p.masked(step)) continue;
+            while (ok) {
+                const volatile PrefillPiece *x = feed.next(limit, abort_flag, &ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok || x == nullptr) break;
+                const int s0 = x->s0, s1 = x->s1, first_limit = x->first_limit, L = x->L;
+                __syncwarp();
+                if (lane == 0) feed.done();
+                feed.step();
+                for (int step = s0; ok && step < s1; ++step) {
+                    const int st = (at + step - s0) % C::VST;
+                    if ((step + 1) * kPreKeys <= first_limit) continue;
                     ok = mbar_wait_bounded(&v_raw[st], raw_phase >> st & 1, limit, abort_flag);
                     raw_phase ^= 1u << st;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     bool found = false;
                     uint8_t *tile = smem + C::V_OFF + st * C::V_BYTES;
-                    const int from = max(0, p.first_limit - step * kPreKeys), gone = max(0, min(kPreKeys, p.item.L - step * kPreKeys));
+                    const int from = max(0, first_limit - step * kPreKeys), gone = max(0, min(kPreKeys, L - step * kPreKeys));
                     // a quarter warp a 128-byte row piece; the swizzle permutes 16-byte units within it
 #pragma unroll
                     for (int c = 0; c < C::VC; ++c) {
@@ -396,7 +440,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&v_full[st]);
                 }
-                at += p.s1 - p.s0;
+                at += s1 - s0;
             }
             if (!ok && lane == 0) {
                 flag_error(a.err, kErrTimeout);
@@ -412,28 +456,29 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
         const int tok_in = row / a.g_tile, head_in = row - tok_in * a.g_tile;
         const uint32_t lane_base = tbase + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t s_at = lane_base + C::S_COL + t * kPreKeys;
-        PrefillWalk walk(a, blockIdx.x);
-        PrefillPiece p;
         uint32_t s_phase = 0, o_phase = 0, stat_phase = 0, q_phase = 0;
         int par_at = 0;  // steps before this piece
-        while (ok && walk.next(&p)) {
-            const int tok = tok_in + (p.two ? t * a.tok_tile : 0);
-            const bool real = tok_in < a.tok_tile && tok < p.item.n_tok && p.hb * a.g_tile + head_in < a.G;
-            const int seen = !real ? 0 : a.causal ? min(max(p.item.limit0 + tok, 0), p.item.L) : p.item.L;
+        while (ok) {
+            const volatile PrefillPiece *p = feed.next(limit, abort_flag, &ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || p == nullptr) break;
+            const int tok = tok_in + (p->two ? t * a.tok_tile : 0);
+            const bool real = tok_in < a.tok_tile && tok < p->n_tok && p->hb * a.g_tile + head_in < a.G;
+            const int seen = !real ? 0 : a.causal ? min(max(p->limit0 + tok, 0), p->L) : p->L;
             const bool idle = !__any_sync(0xffffffffu, real);  // nothing in this warp's rows: it only keeps step
             const int all_see = __reduce_min_sync(0xffffffffu, real ? seen : 0x7fffffff);
             const int most_see = __reduce_max_sync(0xffffffffu, seen);
-            const int n_units = p.units == 0 ? 0 : p.units_of(t);
+            const int n_units = p->two ? p->s1 - p->s0 : (p->s1 - p->s0 + 1 - t) / 2;
             float alpha = a.alpha, v_scale = a.v_scale;
             if constexpr (C::F16) {
                 if (a.k_scales != nullptr) {
-                    alpha *= a.k_scales[a.n_scales > 1 ? p.g : 0];
-                    v_scale = a.v_scales[a.n_scales > 1 ? p.g : 0];
+                    alpha *= a.k_scales[a.n_scales > 1 ? p->g : 0];
+                    v_scale = a.v_scales[a.n_scales > 1 ? p->g : 0];
                 }
             }
             float q_sum = 0.f;  // of the row as the product takes it
             if constexpr (C::F16) {
-                if (p.units > 0) {
+                if (p->units > 0) {
                     ok = mbar_wait_bounded(q_full, q_phase, limit, abort_flag);
                     q_phase ^= 1;
                     ok = __all_sync(0xffffffffu, ok);
@@ -484,7 +529,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 if (!ok) break;
                 if (!idle) {
                     tc_fence_after_sync();
-                    const int step = p.step_of(p.two ? 2 * i : 2 * i + t), key0 = step * kPreKeys;
+                    const int step = p->s0 + (p->two ? i : 2 * i + t), key0 = step * kPreKeys;
                     const bool masked = key0 + kPreKeys > all_see;
                     const int left = seen - key0;
                     float m4[4];
@@ -543,7 +588,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back (held in
                         // registers they spilled: 350 us against 331 on chunks of 300 tokens); parameters and scores of the
                         // next are under way meanwhile (beside the tensor core's reads of shared memory theirs take long).
-                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p.s0) % C::PST * 1024);
+                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p->s0) % C::PST * 1024);
                         const float2 qs2 = make_float2(q_sum, q_sum);
                         float4 pr[2][8];  // scales and zeros of two keys each
                         uint32_t x[2][32];
@@ -672,10 +717,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
-            par_at += p.s1 - p.s0;
+            par_at += p->s1 - p->s0;
 
             // ---- epilogue: row group t's own rows, or (one tile) group 0 for both
-            const bool join = !p.two && p.units > 1;
+            const bool join = !p->two && p->units > 1;
             if (n_units > 0) {
                 ok = mbar_wait_bounded(&o_full[t], o_phase, limit, abort_flag);
                 o_phase ^= 1;
@@ -695,7 +740,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 stat_phase ^= 1;
                 if (!ok) break;
             }
-            if (p.two || t == 0) {
+            if (p->two || t == 0) {
                 float f0 = 1.f, f1 = 0.f;
                 if (join) {
                     const float2 other = stat[row];
@@ -709,17 +754,17 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     const bool any = real && l != 0.f;  // a row that sees no key is zeros (a sum of NaN is not zero)
                     const float inv = any ? v_scale / l : 0.f;
                     const float lse2 = any ? m_ref + log2f(l) : -INFINITY;
-                    const bool fix = n_units > 0 && p.s1 * kPreKeys > p.first_limit && *bad_v != 0;
-                    const long long out_row = (long long)(p.item.q_row + tok) * a.Hq + p.g * a.G + p.hb * a.g_tile + head_in;
-                    const int part_row = (p.slot * 2 + (p.two ? t : 0)) * kPreTile + row;
+                    const bool fix = n_units > 0 && p->s1 * kPreKeys > p->first_limit && *bad_v != 0;
+                    const long long out_row = (long long)(p->q_row + tok) * a.Hq + p->g * a.G + p->hb * a.g_tile + head_in;
+                    const int part_row = (p->slot * 2 + (p->two ? t : 0)) * kPreTile + row;
                     // A row's 64 bytes go out by four lanes (a 16-byte piece each; a lane alone would touch 32 rows an
                     // instruction): lanes of a quad exchange pieces, and lane q writes piece q of the quad's rows in turn.
-                    const long long mine = p.slot < 0 ? out_row * DV * 2 : (long long)part_row * DV * 4;
+                    const long long mine = p->slot < 0 ? out_row * DV * 2 : (long long)part_row * DV * 4;
                     char *rows[4];
                     const unsigned there = __ballot_sync(0xffffffffu, real) >> (lane & ~3);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        rows[r] = (p.slot < 0 ? reinterpret_cast<char *>(a.out) : reinterpret_cast<char *>(a.o_part)) +
+                        rows[r] = (p->slot < 0 ? reinterpret_cast<char *>(a.out) : reinterpret_cast<char *>(a.o_part)) +
                                   __shfl_sync(0xffffffffu, mine, (lane & ~3) + r) + (lane & 3) * 16;
                     }
 #pragma unroll 1
@@ -752,7 +797,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 o[e + 1] = x2, o[e + 2] = x4, o[e + 3] = x6, o[e + 4] = x1, o[e + 5] = x3, o[e + 6] = x5;
                             }
                         }
-                        if (p.slot < 0) {
+                        if (p->slot < 0) {
                             uint32_t x[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
@@ -778,15 +823,15 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     }
                     __syncwarp();  // a row's elements were written by its quad
                     if (fix && any) {
-                        const int key0 = max(p.first_limit, p.s0 * kPreKeys), key1 = min(seen, p.s1 * kPreKeys);
-                        if (p.slot < 0)
-                            prefill_add_not_finite<DV, SRC>(a, p.item.req, p.item.k_row, p.g, key0, key1, a.out + out_row * DV);
+                        const int key0 = max(p->first_limit, p->s0 * kPreKeys), key1 = min(seen, p->s1 * kPreKeys);
+                        if (p->slot < 0)
+                            prefill_add_not_finite<DV, SRC>(a, p->req, p->k_row, p->g, key0, key1, a.out + out_row * DV);
                         else
-                            prefill_add_not_finite<DV, SRC>(a, p.item.req, p.item.k_row, p.g, key0, key1,
+                            prefill_add_not_finite<DV, SRC>(a, p->req, p->k_row, p->g, key0, key1,
                                                             a.o_part + (long long)part_row * DV);
                     }
                     if (real) {
-                        if (p.slot >= 0) a.lse_part[part_row] = lse2;
+                        if (p->slot >= 0) a.lse_part[part_row] = lse2;
                         else if (a.lse != nullptr) a.lse[out_row] = lse2 * 0.69314718055994530942f;
                     }
                 }
@@ -796,6 +841,9 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 }
             }
             tc_fence_before_sync();  // O is read before the next piece's first weights are handed over
+            __syncwarp();
+            if (lane == 0) feed.done();
+            feed.step();
         }
         if (!ok) {
             flag_error(a.err, kErrTimeout);

@@ -26,7 +26,8 @@ struct PrefillCfg {
     static constexpr int K_OFF = 2 * Q_BYTES;
     static constexpr int V_OFF = K_OFF + KST * K_BYTES;
     static constexpr int STAT_OFF = V_OFF + VST * V_BYTES;  // [128] float2: what row group 1 hands over
-    static constexpr int PAR_OFF = STAT_OFF + 1024;         // [PST][64] float4: scales of two keys, their zeros
+    static constexpr int PIECE_OFF = STAT_OFF + 1024;       // pieces that are known ahead
+    static constexpr int PAR_OFF = PIECE_OFF + kPrePieces * 64;         // [PST][64] float4: scales of two keys, their zeros
     static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * 1024 : 0);  // codes of K and of V on their way
     static constexpr int RAW_BYTES = !F16 ? 0 : kPreKeys * DV / (SRC == kPreInt4 ? 2 : 1);
     static constexpr int BAR_OFF = RAW_OFF + 2 * RAW_BYTES;
@@ -111,15 +112,30 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem_dst, const void
 // that reads are whole sectors and the writes of a quarter warp cover all banks.  Returns false after a wait that ran out.
 template <int DQK, int DV, int SRC>
 __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem, uint64_t *k_full, uint64_t *k_empty,
-                                             uint64_t *v_full, uint64_t *v_empty, volatile int *abort_flag, volatile int *bad_v) {
+                                             uint64_t *v_full, uint64_t *v_empty, PieceFeed feed, volatile int *abort_flag,
+                                             volatile int *bad_v) {
     using C = PrefillCfg<DQK, DV, SRC>;
     static_assert(DQK == DV, "pools");
     const int lane = threadIdx.x & 31, lw = (threadIdx.x >> 5) & 3;
     const uint64_t limit = a.wait_limit_ns;
     constexpr int CHUNK = kPreKeys * 128;  // bytes
     bool ok = true;
-    PrefillWalk walk(a, blockIdx.x);
-    PrefillPiece p;
+    struct { int req, L, g, s0, s1, first_limit; } p;  // of the piece
+    auto masked = [&](int step) { return (step + 1) * kPreKeys > p.first_limit; };
+    auto next = [&]() {
+        const volatile PrefillPiece *x;
+        do {
+            x = feed.next(limit, abort_flag, &ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || x == nullptr) return false;
+            p = {x->req, x->L, x->g, x->s0, x->s1, x->first_limit};
+            const bool some = x->units > 0;
+            __syncwarp();
+            if (lane == 0) feed.done();
+            feed.step();
+            if (some) return true;
+        } while (true);
+    };
     int at = 0;  // steps so far
 
     if constexpr (SRC == kPreCopy) {
@@ -157,10 +173,10 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             pend[0] = pend[1];
             n_pend = keep;
         };
-        while (ok && walk.next(&p)) {
+        while (ok && next()) {
             for (int step = p.s0; ok && step < p.s1; ++step, ++at) {
                 const int key = step * kPreKeys + lw * 32 + lane;
-                const int row = key < p.item.L ? prefill_pool_row(a, p.item.req, key) : -1;
+                const int row = key < p.L ? prefill_pool_row(a, p.req, key) : -1;
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     const int stages = v ? C::VST : C::KST, st = at % stages;
@@ -186,7 +202,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
                     const bool withheld = a.fault_mode == 1 && !v && at == 0;  // test hook: this stage never fills
-                    pend[n_pend] = {withheld ? nullptr : v ? &v_full[st] : &k_full[st], v && p.masked(step) ? dst : nullptr,
+                    pend[n_pend] = {withheld ? nullptr : v ? &v_full[st] : &k_full[st], v && masked(step) ? dst : nullptr,
                                     p.first_limit - step * kPreKeys};
                     ++n_pend;
                     hand_on(1);
@@ -214,12 +230,12 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
         const int *table = nullptr;
         auto look_ahead = [&](int step) {
             const int key = step * kPreKeys + lw * 32 + lane;
-            if (key < p.item.L) page = table[prefill_page(a, key)];
+            if (key < p.L) page = table[prefill_page(a, key)];
         };
         auto look_up = [&](int step) {
             const int key = step * kPreKeys + lw * 32 + lane;
             next_row = -1;
-            if (key < p.item.L && step < p.s1) {
+            if (key < p.L && step < p.s1) {
                 if (page < 0 || page >= a.num_pages) flag_error(a.err, kErrIndex);
                 else next_row = (page - prefill_page(a, key)) * a.page_size + key;
             }
@@ -294,10 +310,9 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             }
             if (found) *bad_v = 1;
         };
-        while (ok && walk.next(&p)) {
-            if (p.units == 0) continue;
+        while (ok && next()) {
             const uint8_t *k_pool = a.k_pool + p.g * ROW_BYTES + in_chunk * 16, *v_pool = a.v_pool + p.g * ROW_BYTES + in_chunk * 16;
-            table = a.page_table + (long long)p.item.req * a.pages_per_req;
+            table = a.page_table + (long long)p.req * a.pages_per_req;
             look_ahead(p.s0);
             look_up(p.s0);
             row = next_row, par = next_par;
@@ -331,14 +346,14 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 ok = at < C::VST || mbar_wait_bounded(&v_empty[at % C::VST], (at / C::VST - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                bool careful = SRC != kPreInt8 && p.masked(step);
+                bool careful = SRC != kPreInt8 && masked(step);
                 if constexpr (SRC == kPreInt4) {  // a value of some key may pass fp16's largest
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
                     careful |= __any_sync(0xffffffffu, !(fabsf(f.x) * 15.f + fabsf(f.y) <= 65504.f));
                 }
                 if (careful)
                     store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES,
-                          p.masked(step) ? p.first_limit - step * kPreKeys : kPreKeys);
+                          masked(step) ? p.first_limit - step * kPreKeys : kPreKeys);
                 else
                     store(std::true_type(), std::false_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, 0);
                 fence_proxy_async_shared();

@@ -421,22 +421,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) gqa_prefill_plan_kernel(const
     plan_shares<long long, kPlanThreads>(a, n_items, top, a.cost_prefix, cuts, sums, isums, &shared_max);
 }
 
-// One piece of a worker's work.
-struct PrefillPiece {
-    PrefillItem item;
-    int g, hb;   // KV head, block of its query heads
-    int s0, s1;
-    int slot;    // of the partial results; -1: the whole item
-    bool two;    // two tiles of rows; one tile otherwise, whose steps the two row groups take in turns
-    int units;   // (tile, step) pairs, in the order of their products
-    int first_limit;  // keys that every row sees
-    __device__ __forceinline__ int units_of(int t) const { return two ? s1 - s0 : (s1 - s0 + 1 - t) / 2; }
-    __device__ __forceinline__ int step_of(int u) const { return s0 + (two ? u >> 1 : u); }
-    // keys past what some row sees lie in this step
-    __device__ __forceinline__ bool masked(int step) const { return (step + 1) * kPreKeys > first_limit; }
+// One piece of a worker's work, as it lies in shared memory for all roles of the CTA.
+struct __align__(16) PrefillPiece {
+    int q_row, n_tok, req, units;  // units: (tile, step) pairs, in the order of their products; negative behind the last piece
+    int limit0, L, k_row, first_limit;  // first_limit: keys that every row sees
+    int g, hb, s0, s1;             // KV head, block of its query heads, steps
+    int slot;                      // of the partial results; -1: the whole item
+    int two;                       // two tiles of rows; one tile otherwise, whose steps the two row groups take in turns
+    int spare[2];
 };
+static_assert(sizeof(PrefillPiece) == 64, "four 16-byte words");
 
-// Walks a worker's pieces; every role of the CTA does so by itself.  The item after the present one is under way meanwhile.
+__device__ __forceinline__ int piece_step(const volatile PrefillPiece *p, int u) { return p->s0 + (p->two ? u >> 1 : u); }
+// keys past what some row sees lie in this step
+__device__ __forceinline__ bool piece_masked(const volatile PrefillPiece *p, int step) { return (step + 1) * kPreKeys > p->first_limit; }
+
+// Walks a worker's pieces.  The item after the present one is under way meanwhile.
 struct PrefillWalk {
     const PrefillArgs &a;
     int w, r, rounds, n, s0;
@@ -470,21 +470,48 @@ struct PrefillWalk {
             y = src[1];
         }
     }
-    __device__ __forceinline__ bool next(PrefillPiece *p) {
-        if (!more) return false;
-        p->item = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    __device__ __forceinline__ void next(PrefillPiece *p) {
+        if (!more) {
+            p->units = -1;
+            return;
+        }
+        const int n_tok = x.y, steps = x.w, limit0 = y.x, L = y.y;
         const int h = n % a.head_blocks;
         const int per = a.head_blocks / a.Hkv;
+        p->q_row = x.x, p->n_tok = n_tok, p->req = x.z;
+        p->limit0 = limit0, p->L = L, p->k_row = y.z;
         p->g = h / per;
         p->hb = h % per;
         p->s0 = s0;
-        p->s1 = line && n == end.x ? end.y : p->item.steps;
-        p->slot = s0 > 0 ? 2 * w : p->s1 < p->item.steps ? 2 * w + 1 : -1;
-        p->two = p->item.n_tok > a.tok_tile;
-        p->units = (p->s1 - p->s0) * (p->two ? 2 : 1);
-        p->first_limit = a.causal ? min(max(p->item.limit0, 0), p->item.L) : p->item.L;
+        p->s1 = line && n == end.x ? end.y : steps;
+        p->slot = s0 > 0 ? 2 * w : p->s1 < steps ? 2 * w + 1 : -1;
+        p->two = n_tok > a.tok_tile;
+        p->units = (p->s1 - s0) * (p->two ? 2 : 1);
+        p->first_limit = a.causal ? min(max(limit0, 0), L) : L;
         ahead();
-        return true;
+    }
+};
+
+constexpr int kPrePieces = 4;  // pieces that are known ahead
+
+// What the roles share to follow the pieces: warp W_LOAD writes them, every other warp reads them and says so.
+struct PieceFeed {
+    PrefillPiece *ring;
+    uint64_t *full, *empty;
+    int at;
+    uint32_t phase;
+    __device__ __forceinline__ PieceFeed(PrefillPiece *r, uint64_t *f, uint64_t *e) : ring(r), full(f), empty(e), at(0), phase(0) {}
+    // The next piece, or null: behind the last one, or a wait that ran out (*ok).
+    __device__ __forceinline__ const volatile PrefillPiece *next(uint64_t limit, volatile int *abort_flag, bool *ok) {
+        *ok = mbar_wait_bounded(&full[at], phase, limit, abort_flag);
+        if (!*ok || const_cast<volatile PrefillPiece *>(ring)[at].units < 0) return nullptr;
+        return ring + at;
+    }
+    __device__ __forceinline__ void done() {  // one lane of the warp, once all are
+        mbar_arrive(&empty[at]);
+    }
+    __device__ __forceinline__ void step() {
+        if (++at == kPrePieces) at = 0, phase ^= 1;
     }
 };
 
