@@ -35,7 +35,7 @@ struct PrefillCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
     // Registers by warp group, shared out anew from the launch's 168 or 128 a thread (softmax, the group of warp 8, loaders).
     static constexpr int THREADS = TMA ? 384 : 512;
-    static constexpr int SOFT_REGS = TMA ? 224 : 176, OTHER_REGS = TMA ? 56 : 64, LOAD_REGS = 96;
+    static constexpr int SOFT_REGS = TMA ? 224 : 192, OTHER_REGS = TMA ? 56 : 48, LOAD_REGS = 80;
     static constexpr int REGS = 256 * SOFT_REGS + 128 * OTHER_REGS + (TMA ? 0 : 128 * LOAD_REGS);
     static constexpr int LAUNCH_REGS = 65536 / THREADS / 8 * 8;
     static_assert(REGS <= LAUNCH_REGS * THREADS, "registers");
@@ -260,14 +260,20 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             constexpr bool is_v = decltype(is_v_t)::value, careful = decltype(clean_t)::value;
             bool found = false;
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the other one's newest copies
+            constexpr int BATCH = N < 4 ? N : 4;  // pieces read before the first is converted
+            uint32_t raw_w[BATCH][4];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int in = i / C::VC * ROWS + in_rows, k = lw * 32 + in;
                 uint8_t *dst = tile + i % C::VC * CHUNK + k * 128;
-                uint32_t w[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                             : "r"(raw + (is_v ? C::RAW_BYTES : 0) + i * 2048));
+                if (i % BATCH == 0) {
+#pragma unroll
+                    for (int x = 0; x < BATCH; ++x)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(raw_w[x][0]), "=r"(raw_w[x][1]), "=r"(raw_w[x][2]), "=r"(raw_w[x][3])
+                                     : "r"(raw + (is_v ? C::RAW_BYTES : 0) + (i + x) * 2048));
+                }
+                const uint32_t (&w)[4] = raw_w[i % BATCH];
                 __half2 vs = {}, vz = {};
                 if constexpr (SRC == kPreInt4) {
                     if constexpr (is_v) {
