@@ -83,6 +83,10 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     a.workers = prefill_workers(dev);
     // Items of fewer steps than a part of one has at least are not divided, and need neither partial results nor a merge.
     a.may_split = (keys + kPreKeys - 1) / kPreKeys >= kPreMinSplit + kPreSnap;
+    // Short keys and no more items than SMs: nothing to share out, each CTA finds its own item (one prompt of 17 tokens 9.6 us
+    // a replayed call with the plan's launch).
+    const long long numbers = (long long)a.max_items * a.head_blocks;
+    a.direct = !a.may_split && numbers <= a.workers;
     CUtensorMap q_map, k_map, v_map;
     bool maps = host_rows_tensor_map(&q_map, a.q, a.Tq, a.Hq, DQK, a.q_stride, a.tok_tile, a.g_tile);
     if (SRC == kPreDense) {
@@ -96,30 +100,33 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
                host_rows_tensor_map(&v_map, a.v_pool, rows, a.Hkv, DV, (long long)a.Hkv * DV, a.box_rows, 1);
     }
     if (!maps) return GQA_ERR_CUDA;
-    const size_t need = prefill_workspace(&a, DV, a.may_split, nullptr);
+    const size_t need = a.direct ? 0 : prefill_workspace(&a, DV, a.may_split, nullptr);
     void *ws = workspace;
     bool owned = false;
     if (ws != nullptr) {
         if (workspace_bytes < prefill_workspace(&a, DV, true, nullptr)) return GQA_ERR_NO_MEMORY;
         if (!host_aligned(ws, 256)) return GQA_ERR_ALIGNMENT;
-    } else {
+    } else if (need > 0) {
         if (host_pool_alloc(&ws, need, dev, cs) != cudaSuccess) {
             cudaGetLastError();
             return GQA_ERR_NO_MEMORY;
         }
         owned = true;
     }
-    prefill_workspace(&a, DV, a.may_split, static_cast<char *>(ws));
+    if (need > 0) prefill_workspace(&a, DV, a.may_split, static_cast<char *>(ws));
     constexpr bool paged = SRC != kPreDense;
     // Measured (us of the plan alone): one request 9.0 with 1024 threads, 16 prompts of up to 4K tokens 19.5 with sums in 64 bits.
     const long long most_cost = a.max_items * (kPreCostItem + kPreCostTwo * ((keys + kPreKeys - 1) / kPreKeys));
     const int seqs = std::max(a.B, a.workers);
-    if (seqs <= 256 && a.max_items <= 256 && most_cost < (1LL << 31))
+    if (a.direct) {
+        // no plan
+    } else if (seqs <= 256 && a.max_items <= 256 && most_cost < (1LL << 31)) {
         gqa_prefill_plan_small_kernel<paged, 256, 1><<<1, 256, 0, cs>>>(a);
-    else if (seqs <= 512 && a.max_items <= 2048 && most_cost < (1LL << 31))
+    } else if (seqs <= 512 && a.max_items <= 2048 && most_cost < (1LL << 31)) {
         gqa_prefill_plan_small_kernel<paged, 512, 4><<<1, 512, 0, cs>>>(a);
-    else
+    } else {
         gqa_prefill_plan_kernel<paged><<<1, kPlanThreads, 0, cs>>>(a);
+    }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
         cudaEvent_t before, after;
@@ -127,7 +134,7 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
         const bool timed = before != nullptr && after != nullptr;
         if (timed) cudaEventRecord(before, cs);
         void *args[] = {&q_map, &k_map, &v_map, &a};
-        e = launch_after(kern, dim3(unsigned(a.workers)), C::THREADS, C::SMEM, args, cs);
+        e = launch_after(kern, dim3(unsigned(a.direct ? numbers : a.workers)), C::THREADS, C::SMEM, args, cs);
         if (timed) cudaEventRecord(after, cs);
     }
     if (e == cudaSuccess && a.may_split && a.workers > 1) {

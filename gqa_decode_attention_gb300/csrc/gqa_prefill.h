@@ -84,6 +84,7 @@ struct PrefillArgs {
     // the plan, in the workspace
     int workers;
     int may_split;
+    int direct;  // no plan: CTA i has item i, whole
     int max_items;
     PrefillPlan *plan;
     PrefillItem *items;      // [max_items], longest first

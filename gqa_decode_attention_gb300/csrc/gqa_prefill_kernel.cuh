@@ -351,19 +351,29 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             PrefillPiece p;
             if (is_k) {
                 // This warp walks the plan for all of them, a piece ahead of its own loads.
-                PrefillWalk walk(a, blockIdx.x);
-                for (int n = 0; ok; ++n) {
-                    walk.next(&p);
+                auto publish = [&](int n) {
                     ok = n < kPrePieces || mbar_wait_bounded(&piece_empty[n % kPrePieces], (n / kPrePieces - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) {
+                    if (ok && lane == 0) {
                         pieces[n % kPrePieces] = p;
                         mbar_arrive(&piece_full[n % kPrePieces]);
                     }
                     __syncwarp();
-                    if (p.units < 0) break;
-                    load_piece(p);
+                };
+                if (a.direct) {
+                    const bool some = direct_piece<SRC != kPreDense>(a, blockIdx.x, &p);
+                    if (some) publish(0);
+                    if (some) load_piece(p);
+                    p.units = -1;
+                    if (ok) publish(some ? 1 : 0);
+                } else {
+                    PrefillWalk walk(a, blockIdx.x);
+                    for (int n = 0; ok; ++n) {
+                        walk.next(&p);
+                        publish(n);
+                        if (!ok || p.units < 0) break;
+                        load_piece(p);
+                    }
                 }
             } else {
                 while (ok) {

@@ -18,8 +18,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 64;
 constexpr int kPlanExactRounds = 64;  // whose sums every worker works out for itself
 
-// A step's cost with two tiles and with one, and what an item costs beside its steps.
-constexpr int kPreCostTwo = 4, kPreCostOne = 3, kPreCostItem = 4;
+// A step's cost with two tiles and with one, and what an item costs beside its steps.  Measured (us a call; 24 chunks of up to
+// 256 tokens over an int8 cache, mixed step over an FP8 cache): 4, 3 and 4 88 and 1135, 4, 3 and 12 76 and 1129, 4, 4 and 4 91 and
+// 1201, 4, 2 and 8 80 and 1184.
+constexpr int kPreCostTwo = 4, kPreCostOne = 3, kPreCostItem = 12;
 
 // First and one past the last row of sequence b, clamped into [0, total].
 __device__ __forceinline__ void prefill_range(const int32_t *cu, int per, int b, int total, unsigned *err, int *from,
@@ -436,6 +438,57 @@ __device__ __forceinline__ int piece_step(const volatile PrefillPiece *p, int u)
 // keys past what some row sees lie in this step
 __device__ __forceinline__ bool piece_masked(const volatile PrefillPiece *p, int step) { return (step + 1) * kPreKeys > p->first_limit; }
 
+__device__ __forceinline__ PrefillPiece piece_of(const PrefillArgs &a, const PrefillItem &it, int h, int s0, int s1, int slot) {
+    const int per = a.head_blocks / a.Hkv;
+    PrefillPiece p;
+    p.q_row = it.q_row, p.n_tok = it.n_tok, p.req = it.req;
+    p.limit0 = it.limit0, p.L = it.L, p.k_row = it.k_row;
+    p.g = h / per;
+    p.hb = h % per;
+    p.s0 = s0;
+    p.s1 = s1;
+    p.slot = slot;
+    p.two = it.n_tok > a.tok_tile;
+    p.units = (s1 - s0) * (p.two ? 2 : 1);
+    p.first_limit = a.causal ? min(max(it.limit0, 0), it.L) : it.L;
+    return p;
+}
+
+// Without a plan: the warp works out which item is number `n`, whole.  Returns false past the last one.
+template <bool PAGED>
+__device__ __forceinline__ bool direct_piece(const PrefillArgs &a, int n, PrefillPiece *p) {
+    const int lane = threadIdx.x & 31, item = n / a.head_blocks;
+    int before = 0, b = -1, tile = 0;
+    PlanSeq found = {};
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        PlanSeq s = {};
+        int tiles = 0;
+        if (b0 + lane < a.B) {
+            s = plan_seq<PAGED>(a, b0 + lane, a.err);
+            tiles = (s.n + 2 * a.tok_tile - 1) / (2 * a.tok_tile);
+        }
+        int inc = tiles;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, before + inc - tiles <= item && item < before + inc);
+        if (here != 0) {
+            const int src = __ffs(here) - 1;
+            b = b0 + src;
+            tile = item - __shfl_sync(0xffffffffu, before + inc - tiles, src);
+            found = {__shfl_sync(0xffffffffu, s.q_row, src), __shfl_sync(0xffffffffu, s.n, src), __shfl_sync(0xffffffffu, s.k_row, src),
+                     __shfl_sync(0xffffffffu, s.L, src)};
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (b < 0) return false;
+    const PrefillItem it = plan_item(a, b, found, tile);
+    *p = piece_of(a, it, n % a.head_blocks, 0, it.steps, -1);
+    return true;
+}
+
 // Walks a worker's pieces.  The item after the present one is under way meanwhile.
 struct PrefillWalk {
     const PrefillArgs &a;
@@ -475,19 +528,9 @@ struct PrefillWalk {
             p->units = -1;
             return;
         }
-        const int n_tok = x.y, steps = x.w, limit0 = y.x, L = y.y;
-        const int h = n % a.head_blocks;
-        const int per = a.head_blocks / a.Hkv;
-        p->q_row = x.x, p->n_tok = n_tok, p->req = x.z;
-        p->limit0 = limit0, p->L = L, p->k_row = y.z;
-        p->g = h / per;
-        p->hb = h % per;
-        p->s0 = s0;
-        p->s1 = line && n == end.x ? end.y : steps;
-        p->slot = s0 > 0 ? 2 * w : p->s1 < steps ? 2 * w + 1 : -1;
-        p->two = n_tok > a.tok_tile;
-        p->units = (p->s1 - s0) * (p->two ? 2 : 1);
-        p->first_limit = a.causal ? min(max(limit0, 0), L) : L;
+        const PrefillItem it = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const int s1 = line && n == end.x ? end.y : it.steps;
+        *p = piece_of(a, it, n % a.head_blocks, s0, s1, s0 > 0 ? 2 * w : s1 < it.steps ? 2 * w + 1 : -1);
         ahead();
     }
 };

@@ -5,7 +5,7 @@ import random
 import pytest
 
 KEYS, MIN_SPLIT, SNAP, BUCKETS, EXACT_ROUNDS = 128, 6, 3, 64, 64
-COST_TWO, COST_ONE, COST_ITEM = 4, 3, 4
+COST_TWO, COST_ONE, COST_ITEM = 4, 3, 12
 
 
 def items_of(n, L, tok_tile, causal):
