@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prefill_plan_small_kernel(cons
     int n_items;
     const int at = block_exclusive_scan<int, THREADS>(mine, &n_items, isums);
     if (tid < a.B) tiles[tid] = at;
-    // overlapping ranges of bad offsets (flagged already) may hold more than any good ones
+    // overlapping ranges of bad offsets (flagged) may hold more items than any good ones: what is past max_items is left out
     n_items = min(n_items, a.max_items);
     __syncthreads();
     PrefillItem own[IPT];
@@ -345,18 +345,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) gqa_prefill_plan_kernel(const
     pdl_launch_dependents();
     const int tpi = 2 * a.tok_tile;
     const int per_thread = (a.B + kPlanThreads - 1) / kPlanThreads;
-    int mine = 0;
+    // overlapping ranges of bad offsets (flagged) may hold more items than any good ones: what is past max_items is left out
+    long long mine = 0, all_items;
     for (int b = tid * per_thread; b < min((tid + 1) * per_thread, a.B); ++b)
         mine += (plan_seq<PAGED>(a, b, a.err).n + tpi - 1) / tpi;
     if (tid == 0) shared_max = 1;
     for (int i = tid; i < (kPlanThreads / 32) * kPlanBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
-    int n_items;
-    int at = block_exclusive_scan<int, kPlanThreads>(mine, &n_items, isums);
+    long long at = block_exclusive_scan<long long, kPlanThreads>(mine, &all_items, sums);
     for (int b = tid * per_thread; b < min((tid + 1) * per_thread, a.B); ++b) {
-        a.tile_prefix[b] = at;
+        a.tile_prefix[b] = int(min(at, (long long)a.max_items));
         at += (plan_seq<PAGED>(a, b, nullptr).n + tpi - 1) / tpi;
     }
-    n_items = min(n_items, a.max_items);  // as above
+    const int n_items = int(min(all_items, (long long)a.max_items));
     __syncthreads();
     int most = 1;
     for (int i = tid; i < n_items; i += kPlanThreads) {

@@ -536,7 +536,8 @@ gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const void *v_pool
  *   1 / sqrt(Dqk).
  * Rounding: weights are rounded to bf16 (2^-8 of each at most, relative to a
  *   reference within 2^8 of the row's largest); their sum is not; sums are fp32.
- * Limits: Tq, Tk >= 0; B <= 65535; Hq / Hkv <= 4096; Tq * Hq < 2^31.
+ * Limits: Tq, Tk >= 0; Tk <= 2^31 - 256; B <= 65535; Hq / Hkv <= 4096; Tq * Hq
+ *   < 2^31.
  * Workspace: NULL = library pool, allocated stream-ordered; otherwise device
  *   memory of at least gqa_prefill_workspace_bytes, 256-byte aligned, not in
  *   use by other work in flight (two graphs that may run at once need one each).
@@ -549,7 +550,8 @@ gqa_status gqa_prefill(const void *q, long long q_stride, const void *k, long lo
                        int Tk, int B, int Hq, int Hkv, int Dqk, int Dv, int causal, float scale, void *workspace,
                        size_t workspace_bytes, gqa_stream_t stream);
 
-/* Workspace bytes of gqa_prefill on the current device (0 on invalid arguments). */
+/* Workspace bytes of gqa_prefill on the current device (0 on invalid arguments);
+ * calls with few items and short keys use none of it. */
 size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int Dv);
 
 /* ------------------------------------------------------------------------
@@ -570,9 +572,12 @@ size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int 
  *   the kernel); pools 16-byte, kv_params 8-byte aligned.
  * Limits: D in {64, 128}; page limits as gqa_decode_paged; pages_per_req *
  *   page_size <= 2^31 - 256; the rest, and the workspace, as gqa_prefill.
- * Rounding: bf16 pools as gqa_prefill; codes enter the products as fp16 values
- *   and weights are rounded to fp16 (2^-11, and by at most 2^-25 of the largest
- *   where they are small); see gqa_decode_paged_int4 for what 4-bit codes stand for.
+ * Rounding: bf16 pools as gqa_prefill.  Others: codes enter the products as fp16,
+ *   8-bit ones and those of a 4-bit K exactly (scale and zero of a 4-bit K are
+ *   applied to the scores), the values of a 4-bit V rounded (2^-11; past 65504
+ *   they are that); queries exactly but for elements below 2^-28 of their
+ *   row's largest; weights rounded to fp16 (2^-11, and by at most 2^-25 of the
+ *   largest where they are small).
  * Device-checked (GQA_ERR_DEVICE_INDEX): offsets as gqa_prefill; a seq_lens[b]
  *   outside [0, pages_per_req * page_size] is clamped; a token whose page id is
  *   out of range reads as zeros.

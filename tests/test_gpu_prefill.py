@@ -194,6 +194,19 @@ def test_bad_offsets(gq):
     assert torch.isfinite(guard).all()
 
 
+def test_bad_offsets_of_many(gq):
+    """Thousands of sequences that each claim all rows: far more items than there is room for."""
+    d = ref.make([90], [90], 8, 8, 64, seed=59, pad=0)
+    cu = torch.tensor([0, 90] * 20000, dtype=torch.int32).cuda()
+    guard = torch.full((270, 8, 64), -7.0, dtype=torch.bfloat16, device="cuda")
+    gq.gqa_prefill(d["q"], d["k"], d["v"], cu, out=guard[90:180])
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 7
+    assert torch.all(guard[:90] == -7) and torch.all(guard[180:] == -7)
+    out, lse = run(gq, d)
+    ref.check(d, out, lse)
+
+
 # ------------------------------------------------------------------------------------------------ what is not finite
 @pytest.mark.parametrize("kind", ["dense", "bf16", "fp8", "int4"])
 def test_keys_not_seen_never_reach_a_row(gq, kind):
@@ -323,6 +336,94 @@ def test_two_calls_at_once(gq):
     for d, runs in zip(ds, got):
         for out, lse in runs:
             ref.check(d, out, lse, untouched=False)
+
+
+# ------------------------------------------------------------------------------------------------ plans and sizes
+def test_many_sequences_through_the_workspace(gq):
+    """More sequences than the planning CTA holds by itself, and more rounds of items than it adds up one by one; one of
+    them long enough to be divided."""
+    g = torch.Generator().manual_seed(50)
+    n = torch.randint(0, 17, (1200,), generator=g).tolist()
+    d = ref.make(n, n, 32, 32, 64, seed=51, fused=True)
+    ref.check(d, *run(gq, d))
+    n[700] = 3000
+    L = list(n)
+    L[20] = 9000
+    d = ref.make(n, L, 4, 2, 64, seed=52)
+    ref.check(d, *run(gq, d))
+    d = ref.make(n[:620], L[:620], 4, 2, 64, seed=53, kind="fp8")
+    ref.check(d, *run(gq, d))
+
+
+def test_many_items(gq):
+    """More items than the planning CTA has threads: a group of 64 heads leaves four tokens an item."""
+    d = ref.make([9001, 3], [9001, 3], 64, 1, 64, seed=54, fused=True)
+    out, lse = run(gq, d)
+    at = [0, 1, 2, 500, 4000, 8191, 8999, 9000]  # rows checked
+    k, v = d["kv"][0]
+    for i in at:
+        e = dict(n=[1], L=[i + 1], q=d["q"][i:i + 1], kv=[(k[:i + 1], v[:i + 1])], kind="dense", Hq=64, Hkv=1, D=64, Dv=64)
+        ref.check(e, out[i:i + 1], lse[i:i + 1], untouched=False, what=f"row {i}")
+    ref.check(dict(n=[3], L=[3], q=d["q"][9001:9004], kv=[d["kv"][1]], kind="dense", Hq=64, Hkv=1, D=64, Dv=64), out[9001:], lse[9001:])
+
+
+@pytest.mark.parametrize("B,n,L", [(1, 3, 40), (19, 5, 300), (37, 1, 1100), (40, 2, 129)])
+def test_items_found_without_a_plan(gq, B, n, L):
+    """No more items than SMs and keys that are not divided: no plan, no workspace (some sequences are empty)."""
+    ns, Ls = [n if b % 5 else 0 for b in range(B)], [max(0, L - 7 * b) if b % 3 else 0 for b in range(B)]
+    ns[-1] = n
+    for kind in ("dense", "int8"):
+        d = ref.make(ns, Ls, 8, 2, 64, seed=55 + B, kind=kind)
+        ref.check(d, *run(gq, d))
+
+
+@pytest.mark.parametrize("kind,ps", [("bf16", 16), ("bf16", 5), ("fp8", 16), ("int4", 16)])
+def test_large_pool(gq, kind, ps):
+    """Pools whose far end is past 4 GB."""
+    Hkv, D, lens = 8, 128, [300, 40]
+    row = Hkv * D * {"bf16": 2, "fp8": 1, "int4": 0.5}[kind]
+    pages = int((1 << 32) / (row * ps)) + 200
+    small = ref.make([20, 3], lens, 16, Hkv, D, seed=56, kind=kind, ps=ps)
+    want = run(gq, small)
+    big = dict(small)
+    for name in ("k_pool", "v_pool", "params"):
+        x = small[name]
+        if x is not None:
+            big[name] = torch.empty(pages, *x.shape[1:], dtype=x.dtype, device="cuda")
+            big[name][pages - x.shape[0]:] = x
+    used = small["table"] >= 0
+    used &= small["table"] < small["k_pool"].shape[0]
+    big["table"] = torch.where(used, small["table"] + (pages - small["k_pool"].shape[0]), small["table"])
+    got = run(gq, big)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_shared_pages(gq):
+    """Two requests whose tables name the same pages."""
+    d = ref.make([30, 30], [400, 400], 16, 4, 128, seed=57, kind="bf16")
+    d["table"][1] = d["table"][0]
+    d["rows"][1] = d["rows"][0]
+    d["kv"][1] = d["kv"][0]
+    d["q"][30:60] = d["q"][:30]
+    out, lse = run(gq, d)
+    ref.check(d, out, lse)
+    assert torch.equal(out[:30], out[30:60]) and torch.equal(lse[:30], lse[30:60])
+
+
+@pytest.mark.parametrize("kind,ps", [("dense", 16), ("bf16", 16), ("bf16", 7), ("fp8", 16), ("int4", 16)])
+def test_wait_limit(gq, kind, ps):
+    """A tile that never comes: the call ends with the error flagged, and the next one is right."""
+    d = ref.make([200, 3], [700, 1500], 16, 4, 128, seed=58, kind=kind, ps=ps)
+    run(gq, d)
+    gq.gqa_set_wait_limit_ns(50_000_000)
+    gq.gqa_debug_set_fault_mode(1)
+    try:
+        ref.call(gq, d)
+        assert gq.gqa_device_status() == 6
+    finally:
+        gq.gqa_debug_set_fault_mode(0)
+        gq.gqa_set_wait_limit_ns(0)
+    ref.check(d, *run(gq, d))
 
 
 def test_nothing_to_do(gq):
