@@ -842,6 +842,7 @@ def gqa_prefill_paged_workspace_bytes(T, B, Hq, Hkv, D) -> int:
 
 
 GQA_MERGE_MAX_PARTS = 8
+_MergePointers = ctypes.c_void_p * GQA_MERGE_MAX_PARTS
 
 
 def gqa_merge(outs, lses, out=None, lse=None, stream=None, with_lse=True):
@@ -856,25 +857,30 @@ def gqa_merge(outs, lses, out=None, lse=None, stream=None, with_lse=True):
     n = len(outs)
     if n < 1 or n != len(lses) or n > GQA_MERGE_MAX_PARTS:
         raise ValueError(f"{fn}: one to {GQA_MERGE_MAX_PARTS} outs, and as many lses")
-    shape = outs[0].shape
+    first = outs[0]
+    shape = first.shape
     if len(shape) < 1:
         raise ValueError(f"{fn}: outs must be [...,D]")
-    dev = outs[0].get_device()
+    rows = shape[:-1]
+    dev = first.get_device()
     guard, cs = _on_device_of(dev, stream)
-    for o, s in zip(outs, lses):
-        _fit(fn, "outs", o, torch.bfloat16, dev, shape)
-        _fit(fn, "lses", s, torch.float32, dev, shape[:-1])
+    bf16, fp32 = torch.bfloat16, torch.float32
+    for o in outs:
+        if o.dtype is not bf16 or o.get_device() != dev or o.shape != shape or not o.is_contiguous():
+            raise _misfit(fn, "outs", o, bf16, dev, shape)
+    for s in lses:
+        if s.dtype is not fp32 or s.get_device() != dev or s.shape != rows or not s.is_contiguous():
+            raise _misfit(fn, "lses", s, fp32, dev, rows)
     if out is None:
-        out = _new(shape, torch.bfloat16, outs[0], stream)
+        out = _new(shape, bf16, first, stream)
     else:
-        _fit(fn, "out", out, torch.bfloat16, dev, shape)
+        _fit(fn, "out", out, bf16, dev, shape)
     if lse is not None:
-        _fit(fn, "lse", lse, torch.float32, dev, shape[:-1])
+        _fit(fn, "lse", lse, fp32, dev, rows)
     elif with_lse:
-        lse = _new(shape[:-1], torch.float32, outs[0], stream)
-    ptrs = ctypes.c_void_p * n
-    st = _guarded(guard, lib.gqa_merge, ptrs(*[o.data_ptr() for o in outs]), ptrs(*[s.data_ptr() for s in lses]), n,
-                  out.data_ptr(), _data(lse), lses[0].numel(), shape[-1], cs)
+        lse = _new(rows, fp32, first, stream)
+    st = _guarded(guard, lib.gqa_merge, _MergePointers(*[o.data_ptr() for o in outs]),
+                  _MergePointers(*[s.data_ptr() for s in lses]), n, out.data_ptr(), _data(lse), lses[0].numel(), shape[-1], cs)
     if st:
         raise GQAError(st, fn)
     return out, lse

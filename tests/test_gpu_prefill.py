@@ -548,3 +548,25 @@ def test_serving_step(gq, kind):
         # and their codes differ by
         assert bool(((out[a].float() - whole).abs() <= 0.05).all()) and bool(((lse[a] - one[1][int(cu[b]) + f:int(cu[b + 1])]).abs() <= 0.02).all())
     assert gq.gqa_device_status() == 0
+
+
+def test_decode_over_a_shared_prefix(gq):
+    """One token a request over a prefix that all share (read once, as one sequence of the batch's rows) and over its own
+    tokens, merged, is the decode over all of them."""
+    B, Hq, Hkv, D, ps, prefix, own = 6, 16, 4, 128, 16, 320, [1, 40, 17, 100, 64, 3]
+    g = torch.Generator().manual_seed(60)
+    ppr = 30
+    k, v = (torch.randn(200, ps, Hkv, D, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    pages = torch.randperm(200, generator=g).int()
+    shared, rest = pages[:prefix // ps], pages[prefix // ps:prefix // ps + B * 8].view(B, 8)
+    table = torch.cat([shared.expand(B, -1), rest], 1).contiguous().cuda()
+    q = torch.randn(B, Hq, D, generator=g).to(torch.bfloat16).cuda()
+    lens = torch.tensor(own, dtype=torch.int32).cuda()
+    whole, whole_lse = gq.gqa_decode_paged(q[:, None].contiguous(), k, v, table, lens + prefix)
+    a = gq.gqa_prefill_paged(q, k, v, shared[None].contiguous().cuda(), torch.tensor([prefix], dtype=torch.int32).cuda(), causal=False)
+    b = gq.gqa_decode_paged(q[:, None].contiguous(), k, v, rest.contiguous().cuda(), lens)
+    out, lse = gq.gqa_merge([a[0], b[0][:, 0].contiguous()], [a[1], b[1][..., 0].contiguous()])
+    # roundings of either side to bf16 (out of about 1 at most: 2^-8 each, and of the parts), of weights on either side
+    assert bool(((out.float() - whole[:, 0].float()).abs() <= 4 * 2.0 ** -8 * (1 + whole[:, 0].float().abs())).all())
+    assert bool(((lse - whole_lse[..., 0]).abs() <= 1e-4).all())
+    assert gq.gqa_device_status() == 0
