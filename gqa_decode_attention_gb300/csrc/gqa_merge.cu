@@ -3,7 +3,8 @@
 //   w_p = exp(lse_p - max),  out = sum_p w_p out_p / sum_p w_p,  lse = max + ln sum_p w_p
 //
 // A thread takes 16 bytes (8 elements) of one row: all parts' pieces and the row's LSEs are loaded before any is used,
-// the weights are worked out by every thread of the row (n exponentials, far less than the loads cost).
+// the weights are worked out by every thread of the row (n exponentials, far less than the loads cost).  Bound by HBM: two
+// parts of 16K tokens, 64 heads of 128, 128 us = 6.4 TB/s, 94 % of the measured copy rate.
 #include "gqa_common.cuh"
 #include "gqa_host.h"
 

@@ -1,5 +1,5 @@
 // gqa_prefill.cu -- attention over packed prompts and of new tokens over the
-// paged cache: kernel, and the C entry points.
+// paged cache: launches, and the C entry points.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -83,8 +83,8 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     a.workers = prefill_workers(dev);
     // Items of fewer steps than a part of one has at least are not divided, and need neither partial results nor a merge.
     a.may_split = (keys + kPreKeys - 1) / kPreKeys >= kPreMinSplit + kPreSnap;
-    // Short keys and no more items than SMs: nothing to share out, each CTA finds its own item (one prompt of 17 tokens 9.6 us
-    // a replayed call with the plan's launch).
+    // Short keys and no more items than SMs: nothing to share out, each CTA finds its own item (a replayed call on one prompt of
+    // 17 tokens 5.9 us, with the plan's launch 9.6; 5 rows over 1K keys 16.8 against 20.4).
     const long long numbers = (long long)a.max_items * a.head_blocks;
     a.direct = !a.may_split && numbers <= a.workers;
     CUtensorMap q_map, k_map, v_map;
@@ -115,7 +115,8 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     }
     if (need > 0) prefill_workspace(&a, DV, a.may_split, static_cast<char *>(ws));
     constexpr bool paged = SRC != kPreDense;
-    // Measured (us of the plan alone): one request 9.0 with 1024 threads, 16 prompts of up to 4K tokens 19.5 with sums in 64 bits.
+    // As few threads as hold the sequences, items and workers (us of the plan: one request 5.2 with 256, 9.0 with 1024), all in
+    // shared memory up to 2048 items (16 prompts of up to 4K tokens 17.0, with 64-bit sums through the workspace 19.5).
     const long long most_cost = a.max_items * (kPreCostItem + kPreCostTwo * ((keys + kPreKeys - 1) / kPreKeys));
     const int seqs = std::max(a.B, a.workers);
     if (a.direct) {

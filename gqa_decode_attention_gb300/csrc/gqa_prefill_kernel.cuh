@@ -20,6 +20,14 @@
 // codes as they are (exact), 4-bit codes of K as they are, with scale and zero applied to the scores, those of V as values.
 // Q is converted to fp16 in place, each row times a power of two (exact but for elements 2^-28 below the row's largest).
 // Tensor products run in the order of their issue, so S_t of a step being there says that O_t of the step before is too.
+//
+// Two tiles because one chain of scores, softmax (1.4K cycles a step), weights and output leaves the tensor core (1K cycles a
+// step and tile at d 128) idle more than half of the time; 128 keys a step because S, P and O of both tiles then fill TMEM.
+// Measured (64/8 heads of 128, GB300): one causal prompt of 16K tokens 2.63 ms = 1.67 PFLOP/s, 2K rows over 128K bf16 keys
+// 5.08 ms = 1.72 PFLOP/s, of 1.89 PFLOP/s measured for a large library product (tensor pipe 69 % active at 8K tokens; its
+// clock stays at 1.95 GHz); 8 rows for each of 16 requests of 8K-32K keys 206 us in the kernel = 6.45 TB/s (HBM); a mixed step
+// over an FP8 cache 1.14 ms = 1.14 PFLOP/s (the converting warps, 2.6K cycles a step).  Short items are bound by their chain:
+// some 8K cycles beside their steps, of which the epilogue is 5K.
 #pragma once
 
 #include "gqa_prefill_load.cuh"
@@ -698,7 +706,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
                     } else {
                         // Registers for half of them: maximum and weights in one pass with the reference as it is, once more in the
-                        // few steps whose maximum passes it.
+                        // few steps whose maximum passes it (read a second time for the weights always: mixed step over an FP8
+                        // cache 1652 us against 1243).
                         uint32_t pk[kPreKeys / 2];
 #pragma unroll 1
                         for (bool again = true; again;) {
