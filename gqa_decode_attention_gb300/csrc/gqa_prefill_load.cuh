@@ -120,7 +120,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
     const uint64_t limit = a.wait_limit_ns;
     constexpr int CHUNK = kPreKeys * 128;  // bytes
     bool ok = true;
-    struct { int req, L, g, s0, s1, first_limit; } p;  // of the piece
+    struct { int req, L, g, s0, s1, first_limit; } p = {};  // of the piece
     auto masked = [&](int step) { return (step + 1) * kPreKeys > p.first_limit; };
     auto next = [&]() {
         const volatile PrefillPiece *x;
@@ -274,7 +274,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                                      : "r"(raw + (is_v ? C::RAW_BYTES : 0) + (i + x) * 2048));
                 }
                 const uint32_t (&w)[4] = raw_w[i % BATCH];
-                __half2 vs = {}, vz = {};
+                [[maybe_unused]] __half2 vs = {}, vz = {};
                 if constexpr (SRC == kPreInt4) {
                     if constexpr (is_v) {
                         const uint32_t x = __shfl_sync(0xffffffffu, par.y, in);
