@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 constexpr int kMaxWorkers = kPlanThreads;
+constexpr unsigned long long kPreWaitStepNs = 32000;
 
 // Tiles of a shape: query heads of a KV head side by side, as many tokens as fit.
 void prefill_tiles(PrefillArgs *a) {
@@ -87,6 +88,9 @@ gqa_status launch_prefill(PrefillArgs a, long long keys, void *workspace, size_t
     // 17 tokens 5.9 us, with the plan's launch 9.6; 5 rows over 1K keys 16.8 against 20.4).
     const long long numbers = (long long)a.max_items * a.head_blocks;
     a.direct = !a.may_split && numbers <= a.workers;
+    // Some waits last for the items under way: the next rows of Q wait for the last scores of those before, V's cleaner for an
+    // item's last steps.  What the limit allows grows with them, at some ten times a step's 1.1 to 1.4 us for three items.
+    a.wait_limit_ns += (unsigned long long)((keys + kPreKeys - 1) / kPreKeys) * kPreWaitStepNs;
     CUtensorMap q_map, k_map, v_map;
     bool maps = host_rows_tensor_map(&q_map, a.q, a.Tq, a.Hq, DQK, a.q_stride, a.tok_tile, a.g_tile);
     if (SRC == kPreDense) {

@@ -638,8 +638,10 @@ gqa_status gqa_device_status(gqa_stream_t stream);
  * and the paged kernels (default 2e9).  Exceeding it aborts the CTA and flags
  * GQA_ERR_DEVICE_TIMEOUT.  0 restores the default; values below 1e6 (1 ms)
  * are raised to 1e6, so that an aborting CTA's bounded drain outlasts every
- * copy still in flight into its shared memory.  Affects later launches on all
- * streams. */
+ * copy still in flight into its shared memory.  gqa_prefill and
+ * gqa_prefill_paged, some of whose waits last for whole items, add 32 us for
+ * each 128 keys that a sequence may have (Tk, or pages_per_req * page_size).
+ * Affects later launches on all streams. */
 void gqa_set_wait_limit_ns(uint64_t ns);
 
 #ifdef __cplusplus

@@ -426,6 +426,26 @@ def test_wait_limit(gq, kind, ps):
     ref.check(d, *run(gq, d))
 
 
+@pytest.mark.parametrize("kind,ps", [("bf16", 64), ("bf16", 7), ("fp8", 16), ("int4", 16)])
+def test_items_longer_than_the_wait_limit(gq, kind, ps):
+    """Two whole items an SM of 4096 steps each, some milliseconds, with the least wait limit that can be set."""
+    Hq, Hkv, D, pages, L = 8, 1, 64, 90, (1 << 19) + 37
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    d = ref.make([1], [pages * ps], Hq, Hkv, D, seed=59, kind=kind, ps=ps)
+    g = torch.Generator(device="cuda").manual_seed(60)
+    d["q"] = torch.randn(2 * 32 * sms, Hq, D, device="cuda", generator=g).to(torch.bfloat16)
+    d["table"] = d["table"][0][torch.randint(0, pages, (1, -(-L // ps)), device="cuda", generator=g)]
+    d["lens"] = torch.tensor([L], dtype=torch.int32, device="cuda")
+    d["cu"] = torch.tensor([0, d["q"].shape[0]], dtype=torch.int32, device="cuda")
+    want = run(gq, d)
+    gq.gqa_set_wait_limit_ns(1)  # raised to 1 ms
+    try:
+        got = run(gq, d)
+    finally:
+        gq.gqa_set_wait_limit_ns(0)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 def test_nothing_to_do(gq):
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     out, lse = gq.gqa_prefill(z(0, 8, 64), z(5, 2, 64), z(5, 2, 64))
