@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 uint32_t x[32];
                                 tmem_ld32(s_at + h * 32, x);
                                 tmem_wait_ld();
-                                    hide(x, h);
+                                hide(x, h);
                                 weigh(x, w, make_float2(-m_use, -m_use));
                             }
                             tmem_st16(s_at + h * 16, w);  // (columns whose scores have been read)
@@ -770,7 +770,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     m_ref = m;
                 }
                 if (!idle) {
-                    const bool any = real && l != 0.f;  // a row that sees no key is zeros (a sum of NaN is not zero)
+                    // a row that sees no key here is zeros, whatever a scale of NaN made of its masked scores (a sum of NaN is not zero)
+                    const bool any = seen > p->s0 * kPreKeys && l != 0.f;
                     const float inv = any ? v_scale / l : 0.f;
                     const float lse2 = any ? m_ref + log2f(l) : -INFINITY;
                     const bool fix = n_units > 0 && p->s1 * kPreKeys > p->first_limit && *bad_v != 0;

@@ -446,6 +446,22 @@ def test_items_longer_than_the_wait_limit(gq, kind, ps):
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+@pytest.mark.parametrize("kind", ["fp8", "int8"])
+@pytest.mark.parametrize("n,L", [([5, 7], [3, 20]), ([1500], [1400])])
+def test_device_scale_of_nan(gq, kind, n, L):
+    """A K scale of NaN is NaN for rows that see a key; rows that see none are zeros all the same."""
+    d = ref.make(n, L, 8, 2, 128, seed=61, kind=kind)
+    nan, one = torch.full((1,), math.nan, device="cuda"), torch.ones(1, device="cuda")
+    out, lse = ref.call(gq, d, k_scales=nan, v_scales=one)
+    assert gq.gqa_device_status() == 0
+    at = 0
+    for ni, Li in zip(n, L):
+        none = max(0, ni - Li)
+        assert torch.all(out[at:at + none] == 0) and torch.all(lse[at:at + none] == -math.inf)
+        assert torch.all(out[at + none:at + ni].isnan()) and torch.all(lse[at + none:at + ni].isnan())
+        at += ni
+
+
 def test_nothing_to_do(gq):
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     out, lse = gq.gqa_prefill(z(0, 8, 64), z(5, 2, 64), z(5, 2, 64))
