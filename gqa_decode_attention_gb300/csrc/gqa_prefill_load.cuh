@@ -122,9 +122,12 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
     bool ok = true;
     struct { int req, L, g, s0, s1, first_limit; } p = {};  // of the piece
     auto masked = [&](int step) { return (step + 1) * kPreKeys > p.first_limit; };
-    auto next = [&]() {
+    // The next piece with steps.  before_wait() runs where it is not there yet: the pieces ahead are published as the softmax
+    // is done with those behind, so nothing that the softmax waits for may be held back during this wait.
+    auto next = [&](auto before_wait) {
         const volatile PrefillPiece *x;
         do {
+            if (!__all_sync(0xffffffffu, feed.ready())) before_wait();
             x = feed.next(limit, abort_flag, &ok);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || x == nullptr) return false;
@@ -140,7 +143,8 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
 
     if constexpr (SRC == kPreCopy) {
         // 16-byte asynchronous copies.  K and V of a step are handed on once the copies after them are under way, or before a
-        // wait that may depend on them.
+        // wait that may depend on them: for a free stage, and for the next piece (behind the last step of a piece, items
+        // without steps may fill the ring of pieces, whose first place is only free once that step's V has been used).
         constexpr int PIECES = DV / 8, ROWS = 32 / 8;  // of a row; rows of a warp's copy (8 pieces of one chunk each)
         struct { uint64_t *bar; uint8_t *clean; int from; } pend[2] = {};
         int n_pend = 0;
@@ -173,7 +177,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             pend[0] = pend[1];
             n_pend = keep;
         };
-        while (ok && next()) {
+        while (ok && next([&]() { hand_on(0); })) {
             for (int step = p.s0; ok && step < p.s1; ++step, ++at) {
                 const int key = step * kPreKeys + lw * 32 + lane;
                 const int row = key < p.L ? prefill_pool_row(a, p.req, key) : -1;
@@ -316,7 +320,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             }
             if (found) *bad_v = 1;
         };
-        while (ok && next()) {
+        while (ok && next([]() {})) {  // (each step hands its own K and V on)
             const uint8_t *k_pool = a.k_pool + p.g * ROW_BYTES + in_chunk * 16, *v_pool = a.v_pool + p.g * ROW_BYTES + in_chunk * 16;
             table = a.page_table + (long long)p.req * a.pages_per_req;
             look_ahead(p.s0);

@@ -544,6 +544,7 @@ struct PieceFeed {
     int at;
     uint32_t phase;
     __device__ __forceinline__ PieceFeed(PrefillPiece *r, uint64_t *f, uint64_t *e) : ring(r), full(f), empty(e), at(0), phase(0) {}
+    __device__ __forceinline__ bool ready() const { return mbar_test_wait(&full[at], phase); }
     // The next piece, or null: behind the last one, or a wait that ran out (*ok).
     __device__ __forceinline__ const volatile PrefillPiece *next(uint64_t limit, volatile int *abort_flag, bool *ok) {
         *ok = mbar_wait_bounded(&full[at], phase, limit, abort_flag);
