@@ -248,9 +248,13 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 if (next_row >= 0) next_par = __ldg(reinterpret_cast<const uint2 *>(a.params) + (long long)next_row * a.Hkv + p.g);
             }
         };
-        auto load = [&](bool is_v, const uint8_t *pool, int r) {
+        // `some` is false behind a piece's last step: nothing is copied, but the group counts for the waits.  (Zeros copied
+        // there could land after the next piece's codes: copies to one place are ordered by a wait alone, and store() waits
+        // for them only where it reads.)
+        auto load = [&](bool is_v, const uint8_t *pool, int r, bool some) {
 #pragma unroll
             for (int i = 0; i < N; i += C::VC) {
+                if (!some) break;
                 const int from = __shfl_sync(0xffffffffu, r, i / C::VC * ROWS + in_rows);
                 const uint8_t *src = pool + (long long)max(from, 0) * row_bytes;
 #pragma unroll
@@ -327,8 +331,8 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
             look_up(p.s0);
             row = next_row, par = next_par;
             look_ahead(p.s0 + 1);
-            load(false, k_pool, row);
-            load(true, v_pool, row);
+            load(false, k_pool, row, true);
+            load(true, v_pool, row, true);
             for (int step = p.s0; step < p.s1; ++step, ++at) {
                 look_up(step + 1);
                 look_ahead(step + 2);
@@ -352,7 +356,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 store(std::false_type(), std::false_type(), smem + C::K_OFF + at % C::KST * C::K_BYTES, 0);
                 fence_proxy_async_shared();
                 if (!(a.fault_mode == 1 && at == 0)) mbar_arrive(&k_full[at % C::KST]);  // test hook: the first stage never fills
-                load(false, k_pool, next_row);
+                load(false, k_pool, next_row, step + 1 < p.s1);
                 ok = at < C::VST || mbar_wait_bounded(&v_empty[at % C::VST], (at / C::VST - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -369,7 +373,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 fence_proxy_async_shared();
                 __threadfence_block();
                 mbar_arrive(&v_full[at % C::VST]);
-                load(true, v_pool, next_row);
+                load(true, v_pool, next_row, step + 1 < p.s1);
                 row = next_row, par = next_par;
             }
         }

@@ -48,3 +48,16 @@ def test_prefixes_of_some(gq, ps):
     assert torch.all(out[:512 * 32] == 0) and torch.all(lse[:512 * 32] == -float("inf"))
     last = dict(d, n=n[32:], L=L[32:], q=d["q"][512 * 32:], kv=d["kv"][32:], rows=d["rows"][32:])
     ref.check(last, out[512 * 32:], lse[512 * 32:], False)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "int4"])
+def test_short_pieces_of_codes(gq, kind):
+    """Many pieces of one to three steps a worker: the codes of each piece's first step come while those before are in use.
+    The same bits every time."""
+    n, L = [1, 20, 3] * 60, [100, 300, 257] * 60
+    d = ref.make(n, L, 32, 8, 128, seed=3, kind=kind)
+    want = run(gq, d)
+    ref.check(d, *want)
+    for _ in range(20):
+        got = run(gq, d)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])

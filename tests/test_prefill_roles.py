@@ -1,6 +1,7 @@
 """The roles of prompt attention's CTA, modelled on the CPU: what each waits for and hands on, over the pieces that the plan
 gives a worker, with bf16 pools whose pages go through registers (the loader hands a step's copies on when later ones are under
-way, or before it waits).  A CTA stalls when every role waits for another."""
+way, or before it waits).  A CTA stalls when every role waits for another.  And the copies of codes by the loader of coded pools,
+whose order only waits give."""
 import random
 
 import pytest
@@ -198,3 +199,44 @@ def test_no_planned_list_stalls(seed):
     L = [0 if r.random() < 0.6 else max(0, x + r.randint(-5, 2000)) for x in n]
     for s, w in enumerate(works(n, L, r.random() < 0.5, r.choice([1, 16, 25, 128]), r.choice([1, 8]), r.choice([2, 7, 152]))):
         assert ends(w, True, s)
+
+
+def copies(pieces, zeros_behind):
+    """A thread's asynchronous copies into its places of K and of V, its waits ("all groups but the newest n are there") and its
+    reads, over pieces of so many steps.  zeros_behind: something is copied behind a piece's last step too."""
+    for steps in pieces:
+        if not steps:
+            continue
+        yield from (("copy", "K"), ("commit",), ("copy", "V"), ("commit",))
+        for step in range(steps):
+            for place in "KV":
+                yield ("wait", 1)
+                yield ("read", place)
+                if step + 1 < steps or zeros_behind:
+                    yield ("copy", place)
+                yield ("commit",)
+
+
+def in_order(events):
+    """No copy to a place that an older one may still reach, no read of a place that one may."""
+    groups, now = [], []
+    for e in events:
+        if e[0] == "copy":
+            if any(e[1] in g for g in groups + [now]):
+                return False
+            now.append(e[1])
+        elif e[0] == "commit":
+            groups.append(now)
+            now = []
+        elif e[0] == "wait":
+            del groups[:max(0, len(groups) - e[1])]
+        elif any(e[1] in g for g in groups + [now]):
+            return False
+    return True
+
+
+@pytest.mark.parametrize("pieces", [[1], [1, 1], [3, 1, 2], [0, 2, 0, 0, 5, 1, 1], [9, 9]])
+def test_copies_of_codes_are_ordered(pieces):
+    assert in_order(copies(pieces, False))
+    # the model sees zeros copied behind a piece, beside the next piece's codes
+    assert in_order(copies(pieces, True)) == (sum(x > 0 for x in pieces) < 2)
