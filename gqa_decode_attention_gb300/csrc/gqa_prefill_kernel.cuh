@@ -35,7 +35,11 @@
 
 namespace gqa {
 
-constexpr float kPreRescaleLog2 = 8.f;  // a row's reference moves when its maximum grows past it by 2^8
+// A row's largest weight is 2^TOP when its reference is set, and the reference moves when a later one would pass 2^8 times that.
+// bf16 weights have fp32's range (TOP 0); fp16 ones lose what lies below 2^-25, so they start at 2^7 and use fp16's range up to
+// 2^15: what is rounded to nothing lies 2^-32 below the largest (from 1 on it lay 2^-25 below, and a row with one large
+// score among 2^20 small ones came out 2 % small, its sum being taken before the rounding).
+constexpr float kPreRescaleLog2 = 8.f, kPreTopF16 = 7.f;
 
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
     asm volatile(
@@ -576,13 +580,18 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
                         }
                     };
-                    // A row's reference follows its maximum when that passes it by 2^8; O and the sum then change with it.
+                    // A row's reference follows its maximum when that passes it by too much; O and the sum then change with it.
                     auto follow = [&]() {
-                        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * alpha;
-                        const bool renew = mx > m_ref + kPreRescaleLog2;
+                        constexpr float top = C::F16 ? kPreTopF16 : 0.f;
+                        // Each operation rounded by itself: contracted to one fma with the product, the difference to a
+                        // reference of great magnitude would not be small once the reference has moved.  (A difference:
+                        // beside a reference past 2^27 the sum with the allowance rounds up.)
+                        const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), alpha);
+                        const bool renew = __fsub_rn(mx, m_ref) > kPreRescaleLog2 + top;
                         const bool rescale = renew && i > 0 && m_ref != -INFINITY;
+                        const float ref = __fsub_rn(mx, top);
                         if (__any_sync(0xffffffffu, rescale)) {
-                            const float corr = rescale ? fast_exp2(m_ref - mx) : 1.f;
+                            const float corr = rescale ? fast_exp2(m_ref - ref) : 1.f;
 #pragma unroll 1
                             for (int c = 0; c < DV / 32; ++c) {
                                 uint32_t ov[32];
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                             }
                             l *= corr;
                         }
-                        if (renew) m_ref = mx;
+                        if (renew) m_ref = ref;
                         return renew;
                     };
                     if constexpr (C::K_PARAMS) {
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         // cache 1652 us against 1243).
                         uint32_t pk[kPreKeys / 2];
 #pragma unroll 1
-                        for (bool again = true; again;) {
+                        for (int pass = 0; pass < 2; ++pass) {
                             const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                             const float2 nm2 = make_float2(-m_use, -m_use);
                             m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
@@ -724,7 +733,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                                 maximum(sr[h & 1]);
                                 weigh(sr[h & 1], pk + h * 16, nm2);
                             }
-                            again = __any_sync(0xffffffffu, follow());
+                            if (!__any_sync(0xffffffffu, follow())) break;
                         }
 #pragma unroll
                         for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));

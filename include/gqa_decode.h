@@ -576,8 +576,9 @@ size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int 
  *   8-bit ones and those of a 4-bit K exactly (scale and zero of a 4-bit K are
  *   applied to the scores), the values of a 4-bit V rounded (2^-11; past 65504
  *   they are that); queries exactly but for elements below 2^-28 of their
- *   row's largest; weights rounded to fp16 (2^-11, and by at most 2^-25 of the
- *   largest where they are small).
+ *   row's largest; weights rounded to fp16 (2^-11, and by at most 2^-32 of the
+ *   largest where they are small).  A row whose scores pass 2^27 in magnitude may
+ *   be NaN.
  * Device-checked (GQA_ERR_DEVICE_INDEX): offsets as gqa_prefill; a seq_lens[b]
  *   outside [0, pages_per_req * page_size] is clamped; a token whose page id is
  *   out of range reads as zeros.

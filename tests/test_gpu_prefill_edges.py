@@ -1,7 +1,10 @@
 """GPU tests of prompt attention at its edges, against plain 64-bit computations."""
+import math
+
 import pytest
 import torch
 
+import cache_ref as cref
 import prefill_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +64,82 @@ def test_short_pieces_of_codes(gq, kind):
     for _ in range(20):
         got = run(gq, d)
         assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+# ------------------------------------------------------------------------------------------------ weights in 16 bits
+def one_large_score(gq, kind, first, large):
+    """One key's weight is 2^25.4 times that of each of the 2^20 - 1 others, which together are 2.3 % of the row: they count in
+    the sum, so they must count in the product with V.  Its value is `large`, theirs 1.  (Whole items, two an SM: parts of a
+    divided one have references of their own.)"""
+    Hq, Hkv, D, ps, L = 8, 1, 64, 16, 1 << 20
+    T = 2 * 32 * torch.cuda.get_device_properties(0).multi_processor_count
+    scale = 1 / 8 if kind in ("fp8", "int8") else 1.0
+    k, v = torch.zeros(2, ps, Hkv, D), torch.ones(2, ps, Hkv, D)
+    at = 0 if first else ps - 1  # page 0 holds the large key, page 1 is all the others
+    k[0, at, 0, 7], v[0, at] = 2.0, large
+    (kc, kp), (vc, vp) = cref.encode(kind, k, scale), cref.encode(kind, v, scale)
+    params = torch.cat([kp, vp], -1).cuda() if kind == "int4" else None
+    table = torch.ones(1, L // ps, dtype=torch.int32)
+    table[0, 0 if first else -1] = 0
+    q = torch.zeros(T, Hq, D)
+    q[..., 7] = 25.4 * math.log(2) * math.sqrt(D) / 2
+    d = dict(kind=kind, q=q.to(torch.bfloat16).cuda(), k_pool=kc.cuda(), v_pool=vc.cuda(), params=params, table=table.cuda(), scale=scale,
+             lens=torch.tensor([L], dtype=torch.int32).cuda(), cu=torch.tensor([0, T], dtype=torch.int32).cuda(), Hq=Hq, Dv=D)
+    out, lse = run(gq, d, causal=False)
+    s = float(d["q"][0, 0, 7].double()) * float(cref.values(kind, kc, kp, scale)[0, at, 0, 7]) / math.sqrt(D)
+    rest = (L - 1) * math.exp(-s)
+    want, mag, want_lse = (rest + large) / (rest + 1), (rest + abs(large)) / (rest + 1), s + math.log1p(rest)
+    # as prefill_ref.bounds, but small weights are off by 2^-32 of the largest at most
+    steps, ds = (L / 128 + 160) * 2.0 ** -23, (D + 8) * 2.0 ** -23 * s
+    half = ref.HALF[torch.bfloat16] if kind == "bf16" else ref.HALF[torch.float16] * (2 if kind == "int4" else 1)
+    rel = half + 2 * ds + 2.0 ** -20 + 2 * steps
+    bound = ref.HALF[torch.bfloat16] * abs(want) + rel * mag + (0.0 if kind == "bf16" else L * 2.0 ** -32)
+    assert bound < 0.5 * rest  # what the others' part is
+    assert float((out.double() - want).abs().max()) <= bound
+    assert float((lse.double() - want_lse).abs().max()) <= ds + steps + 2.0 ** -20 + 2.0 ** -22 * want_lse
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "int4"])
+@pytest.mark.parametrize("first", [True, False])
+def test_many_small_weights(gq, kind, first):
+    """The others' values are all that the row's result consists of: their weights must not be rounded to nothing."""
+    one_large_score(gq, kind, first, 0.0)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int8", "int4"])
+def test_scores_of_great_magnitude(gq, kind):
+    """Scores up to 2^27: a row is the value of its largest score's key."""
+    n, L, Hq, Hkv, D = [70, 5], [70, 900], 8, 2, 64
+    d = ref.make(n, L, Hq, Hkv, D, seed=21, kind=kind, gain=2.0 ** 23)
+    out, lse = run(gq, d)
+    at = 0
+    for (k, v), nb, Lb in zip(d["kv"], n, L):
+        x = torch.einsum("nhgd,lhd->nhgl", d["q"][at:at + nb].double().view(nb, Hkv, Hq // Hkv, D), k) / math.sqrt(D)
+        hide = torch.arange(Lb, device="cuda") > (Lb - nb + torch.arange(nb, device="cuda"))[:, None]
+        x = x.masked_fill(hide[:, None, None], -math.inf)
+        assert 2.0 ** 24 < float(x.nan_to_num(neginf=0.0).abs().max()) < 2.0 ** 27
+        best = x.topk(min(2, Lb), -1)
+        # what the scores may be off by: (D + 8) 2^-23 of their magnitude, below 2^29 with a 4-bit scale and zero apart
+        clear = best.values[..., 0] - best.values[..., 1] > 72 * 2.0 ** -23 * 2.0 ** 29 + 64
+        assert clear.float().mean() > 0.8
+        want = torch.gather(v.permute(1, 0, 2)[None].expand(nb, -1, -1, -1), 2, best.indices[..., :1].expand(-1, -1, -1, D))
+        got = out[at:at + nb].double().view(nb, Hkv, Hq // Hkv, D)
+        assert torch.isfinite(got).all() and torch.isfinite(lse[at:at + nb]).all()
+        e = (got - want).abs() - (2.0 ** -8 + 2 * 2.0 ** -11) * want.abs() - 2.0 ** -20
+        assert float(e[clear].max()) <= 0
+        at += nb
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8", "int4"])
+@pytest.mark.parametrize("ps", [16, 7])
+def test_rows_past_the_scores_range(gq, kind, ps):
+    """A row of queries up to 2^125 may be NaN; the call ends, and every other row is as before."""
+    d = ref.make([50, 3], [50, 500], 12, 4, 64, seed=22, kind=kind, ps=ps)  # (groups that leave rows of a tile empty)
+    want = run(gq, d)
+    for up in (40, 90, 122):
+        e = dict(d, q=d["q"].clone())
+        e["q"][[7, 51]] *= 2.0 ** up
+        got = run(gq, e)
+        keep = [i for i in range(53) if i not in (7, 51)]
+        for a, b in zip(want, got):
+            assert torch.equal(a[keep], b[keep])
