@@ -41,6 +41,13 @@ namespace gqa {
 // score among 2^20 small ones came out 2 % small, its sum being taken before the rounding).
 constexpr float kPreRescaleLog2 = 8.f, kPreTopF16 = 7.f;
 
+// Steps of a row group after which its O goes to global memory, in fp32, and starts anew.  The tensor core cuts a product off some
+// 2^-25 below the sum that it is added to: over 2^20 keys values of one sign came out 0.7 % small, and the others' part was
+// missing where one key's weight was 2^25 times theirs.  Over 128 steps that is 2^-11 of the sum at most; items of up to 16K keys
+// never come to it, and one of 128K keys does 7 times.
+constexpr int kPreDrain = 128;
+static_assert((kPreDrain & (kPreDrain - 1)) == 0 && kPreDrain > kPreMinSplit + kPreSnap, "only items with room for partial results");
+
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         tc_fence_after_sync();
                         const uint32_t d = tbase + C::O_COL + t * DV, w = tbase + C::S_COL + t * kPreKeys;
                         const uint32_t vd = v_desc + vs * (C::V_BYTES >> 4);
-                        if (u > 1) umma_ts<true>(d, w, vd, idesc_pv);
+                        if ((u >> 1) & (kPreDrain - 1)) umma_ts<true>(d, w, vd, idesc_pv);
                         else umma_ts<false>(d, w, vd, idesc_pv);
 #pragma unroll
                         for (int kg = 1; kg < kPreKeys / 16; ++kg) umma_ts<true>(d, w + kg * 8, vd + kg * (2048 >> 4), idesc_pv);
@@ -544,6 +551,38 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             }
             if (alpha < 1e-37f) alpha = 1e-37f;  // a scale of zero must not make NaN of a masked score
             float m_ref = -INFINITY, l = 0.f;  // reference (log2 domain), sum of the weights
+            // What has left O so far, with the reference m_out: the warp's rows of the worker's last place for partial results
+            // (in use by nothing else before the epilogue of the worker's last piece), four elements of each of 32 rows in turn.
+            float m_out = -INFINITY;
+            float4 *out_at = reinterpret_cast<float4 *>(a.o_part + ((2LL * blockIdx.x + 1) * 2 + t) * kPreTile * DV + (warp & 3) * 32 * DV) + lane;
+            // O there, or (last) what is there back into O.
+            auto drain = [&](bool some, bool last) {
+                const float corr = m_out == m_ref ? 1.f : fast_exp2(m_out - m_ref);
+#pragma unroll 1
+                for (int c = 0; c < DV / 32; ++c) {
+                    uint32_t ov[32];
+                    float4 y[8] = {};
+                    tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                    if (some) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = out_at[(c * 8 + e) * 32];
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float *x = reinterpret_cast<float *>(&y[e]);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float o = __uint_as_float(ov[4 * e + z]);
+                            x[z] = some ? fmaf(x[z], corr, o) : o;
+                            ov[4 * e + z] = __float_as_uint(x[z]);
+                        }
+                        if (!last) out_at[(c * 8 + e) * 32] = y[e];
+                    }
+                    if (last) tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                }
+                m_out = m_ref;
+            };
             for (int i = 0; i < n_units; ++i) {
                 ok = mbar_wait_bounded(&s_full[t], s_phase, limit, abort_flag);
                 s_phase ^= 1;
@@ -551,6 +590,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                 if (!ok) break;
                 if (!idle) {
                     tc_fence_after_sync();
+                    if (i > 0 && (i & (kPreDrain - 1)) == 0) drain(i > kPreDrain, false);
                     const int step = p->s0 + (p->two ? i : 2 * i + t), key0 = step * kPreKeys;
                     const bool masked = key0 + kPreKeys > all_see;
                     const int left = seen - key0;
@@ -760,6 +800,11 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
+            if (n_units > kPreDrain && !idle) {
+                drain(true, true);
+                tmem_wait_st();
+                __syncwarp();  // every lane has read its part of the place, which may be this piece's
+            }
             if (join && t == 1) {
                 stat[row] = make_float2(m_ref, l);
                 tc_fence_before_sync();

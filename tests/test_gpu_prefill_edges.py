@@ -143,3 +143,67 @@ def test_rows_past_the_scores_range(gq, kind, ps):
         keep = [i for i in range(53) if i not in (7, 51)]
         for a, b in zip(want, got):
             assert torch.equal(a[keep], b[keep])
+
+
+# ------------------------------------------------------------------------------------------------ sums over many steps
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int8", "int4"])
+@pytest.mark.parametrize("first", [True, False])
+def test_small_weights_beside_a_large_value(gq, kind, first):
+    """As above, and the large key's value is what the row mostly consists of: the others' products lie 2^-25 below."""
+    one_large_score(gq, kind, first, -1.0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_long_sums_of_one_sign(gq, kind):
+    """2^20 keys with values between 1 and 2: nothing is lost on the way (what the tensor core cuts off is always towards zero)."""
+    Hq, Hkv, D, ps, pages, L = 8, 1, 64, 16, 64, 1 << 20
+    T = 2 * 32 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(23)
+    scale = 5 / 448 if kind == "fp8" else 1.0
+    k, v = torch.randn(pages, ps, Hkv, D, generator=g), torch.rand(pages, ps, Hkv, D, generator=g) * 0.3 + torch.linspace(1.0, 1.7, D)
+    (kc, kp), (vc, vp) = cref.encode(kind, k, scale), cref.encode(kind, v, scale)
+    params = torch.cat([kp, vp], -1) if kind == "int4" else None
+    table = torch.randint(0, pages, (1, L // ps), generator=g).int()
+    q = torch.randn(32, Hq, D, generator=g).to(torch.bfloat16).cuda().repeat(T // 32, 1, 1)
+    d = dict(kind=kind, q=q, k_pool=kc.cuda(), v_pool=vc.cuda(), params=None if params is None else params.cuda(), table=table.cuda(), scale=scale,
+             lens=torch.tensor([L], dtype=torch.int32).cuda(), cu=torch.tensor([0, T], dtype=torch.int32).cuda(), Hq=Hq, Dv=D)
+    out, lse = run(gq, d, causal=False)
+    kd, vd = cref.values(kind, kc, kp, scale).view(-1, D).cuda(), cref.values(kind, vc, vp, scale).view(-1, D).cuda()
+    times = torch.bincount(table[0], minlength=pages).double().repeat_interleave(ps).cuda()
+    p = torch.softmax(q[:32].double().view(-1, D) @ kd.T / math.sqrt(D) + times.log(), -1)
+    want = (p @ vd).view(32, Hq, D)
+    # bf16 rounds either way over values between 1 and 2: their mean moves little.  A product loses less than 2^-24 of the sum that
+    # it is added to, over 16384 keys.
+    off = float(((out[:32].double() - want) / want).mean())
+    assert abs(off) <= 2.0 ** -24 * 16384 + 2.0 ** -12
+    assert torch.equal(out[:32], out[32:64]) and torch.equal(lse[:32], lse[-32:])
+
+
+@pytest.mark.parametrize("kind,ps", [("bf16", 16), ("bf16", 7), ("fp8", 16), ("int4", 16)])
+@pytest.mark.parametrize("n", [[1500], [16] * 90])  # items of two tiles, and of one, whose steps the row groups take in turns
+@pytest.mark.parametrize("rise", [False, True])
+def test_sums_that_leave_the_tensor_core(gq, kind, ps, n, rise):
+    """Whole items and parts of more steps than a sum stays in the tensor core for, the largest scores at the end or anywhere."""
+    Hq, Hkv, D, L = 16, 2, 64, 40000
+    d = ref.make([1], [L], Hq, Hkv, D, seed=24, kind=kind, ps=ps, pad=0)
+    B, T = len(n), sum(n)
+    g = torch.Generator().manual_seed(25)
+    if rise:  # keys grow along the sequence
+        up = torch.linspace(0.25, 2.0, L)
+        k = torch.randn(L, Hkv, D, generator=g) * up[:, None, None]
+        kc, kp = cref.encode(kind, k, d["scale"])
+        d["k_pool"].view(-1, *kc.shape[1:])[d["rows"][0]] = kc.cuda()
+        if kind == "int4":
+            d["params"].view(-1, Hkv, 4)[d["rows"][0], :, :2] = kp.cuda()
+        d["kv"] = [ref.held(d, d["rows"][0])]
+    q = torch.randn(T + 3, Hq, D, generator=g)
+    d.update(n=n, L=[L] * B, q=(q * 2).to(torch.bfloat16).cuda(), cu=torch.tensor([0] + n).cumsum(0).int().cuda(), table=d["table"].expand(B, -1).contiguous(),
+             lens=torch.full((B,), L, dtype=torch.int32).cuda(), rows=d["rows"] * B, kv=d["kv"] * B)
+    out, lse = run(gq, d)
+    step = 1 if B == 1 else 13  # requests checked
+    for b in range(0, B, step):
+        at = sum(n[:b])
+        one = dict(d, n=[n[b]], L=[L], q=d["q"][at:at + n[b]], kv=[d["kv"][b]], rows=[d["rows"][b]])
+        ref.check(one, out[at:at + n[b]], lse[at:at + n[b]], untouched=False, what=f"request {b}")
+    again = run(gq, d)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
