@@ -43,9 +43,10 @@ constexpr float kPreRescaleLog2 = 8.f, kPreTopF16 = 7.f;
 
 // Steps of a row group after which its O goes to global memory, in fp32, and starts anew.  The tensor core cuts a product off some
 // 2^-25 below the sum that it is added to: over 2^20 keys values of one sign came out 0.7 % small, and the others' part was
-// missing where one key's weight was 2^25 times theirs.  Over 128 steps that is 2^-11 of the sum at most; items of up to 16K keys
-// never come to it, and one of 128K keys does 7 times.
-constexpr int kPreDrain = 128;
+// missing where one key's weight was 2^25 times theirs.  Over 256 steps that is 2^-10 of the sum at most.  Items of up to 32K keys
+// never come to it.  It takes some 6 us, as all SMs move their 128 KB at about the same time (2K rows over 128K keys: every 128
+// steps 5790 us, every 256 5710, never 5600).
+constexpr int kPreDrain = 256;
 static_assert((kPreDrain & (kPreDrain - 1)) == 0 && kPreDrain > kPreMinSplit + kPreSnap, "only items with room for partial results");
 
 __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, uint64_t *bar, int c0, int c1, int c2) {
@@ -147,6 +148,45 @@ __device__ __forceinline__ uint4 prefill_q_unit(uint4 x, float scale) {
     if constexpr (SRC == kPreInt4)
         return make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
     return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
+}
+
+// A row group's O (at o_at, a thread a row) goes to global memory, added to `corr` times what is there (some); last: that sum goes
+// back into O instead.  The place is the warp's rows of the worker's last place for partial results, which nothing else uses
+// before the epilogue of the worker's last piece; four elements of each of 32 rows in turn, so that a warp's accesses are whole
+// lines.  (Not inline: two copies in the softmax's code cost short items 4 %.)
+template <int DV>
+__device__ __noinline__ void prefill_drain(const PrefillArgs &a, uint32_t o_at, int t, float corr, bool some, bool last) {
+    float4 *at = reinterpret_cast<float4 *>(a.o_part + ((2LL * blockIdx.x + 1) * 2 + t) * kPreTile * DV + (threadIdx.x >> 5 & 3) * 32 * DV) +
+                 (threadIdx.x & 31);
+#pragma unroll 1
+    for (int c = 0; c < DV; c += 64) {
+        uint32_t ov[2][32];
+        float4 y[16] = {};
+        if (some) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = at[(c / 4 + e) * 32];
+        }
+        tmem_ld32(o_at + c, ov[0]);
+        tmem_ld32(o_at + c + 32, ov[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            float *x = reinterpret_cast<float *>(&y[e]);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                uint32_t &o = ov[e / 8][4 * e % 32 + z];
+                x[z] = fmaf(x[z], corr, __uint_as_float(o));
+                o = __float_as_uint(x[z]);
+            }
+            if (!last) at[(c / 4 + e) * 32] = y[e];
+        }
+        if (last) {
+            tmem_st32(o_at + c, ov[0]);
+            tmem_st32(o_at + c + 32, ov[1]);
+        }
+    }
+    if (last) tmem_wait_st();
+    __syncwarp();  // every lane has read its part of the place, which may be the piece's own
 }
 
 template <int DQK, int DV, int SRC>
@@ -551,36 +591,9 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             }
             if (alpha < 1e-37f) alpha = 1e-37f;  // a scale of zero must not make NaN of a masked score
             float m_ref = -INFINITY, l = 0.f;  // reference (log2 domain), sum of the weights
-            // What has left O so far, with the reference m_out: the warp's rows of the worker's last place for partial results
-            // (in use by nothing else before the epilogue of the worker's last piece), four elements of each of 32 rows in turn.
-            float m_out = -INFINITY;
-            float4 *out_at = reinterpret_cast<float4 *>(a.o_part + ((2LL * blockIdx.x + 1) * 2 + t) * kPreTile * DV + (warp & 3) * 32 * DV) + lane;
-            // O there, or (last) what is there back into O.
+            float m_out = -INFINITY;           // the reference of what has left O
             auto drain = [&](bool some, bool last) {
-                const float corr = m_out == m_ref ? 1.f : fast_exp2(m_out - m_ref);
-#pragma unroll 1
-                for (int c = 0; c < DV / 32; ++c) {
-                    uint32_t ov[32];
-                    float4 y[8] = {};
-                    tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
-                    if (some) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = out_at[(c * 8 + e) * 32];
-                    }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float *x = reinterpret_cast<float *>(&y[e]);
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const float o = __uint_as_float(ov[4 * e + z]);
-                            x[z] = some ? fmaf(x[z], corr, o) : o;
-                            ov[4 * e + z] = __float_as_uint(x[z]);
-                        }
-                        if (!last) out_at[(c * 8 + e) * 32] = y[e];
-                    }
-                    if (last) tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
-                }
+                prefill_drain<DV>(a, lane_base + C::O_COL + t * DV, t, !some || m_out == m_ref ? 1.f : fast_exp2(m_out - m_ref), some, last);
                 m_out = m_ref;
             };
             for (int i = 0; i < n_units; ++i) {
@@ -623,13 +636,12 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     // A row's reference follows its maximum when that passes it by too much; O and the sum then change with it.
                     auto follow = [&]() {
                         constexpr float top = C::F16 ? kPreTopF16 : 0.f;
-                        // Each operation rounded by itself: contracted to one fma with the product, the difference to a
-                        // reference of great magnitude would not be small once the reference has moved.  (A difference:
-                        // beside a reference past 2^27 the sum with the allowance rounds up.)
+                        // (Rounded one by one: contracted with the product, a difference to a reference of great magnitude would
+                        // not be small once the reference has moved.  The sum rounds down, so that past 2^27 no weight passes 2^15.)
                         const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), alpha);
-                        const bool renew = __fsub_rn(mx, m_ref) > kPreRescaleLog2 + top;
+                        const bool renew = mx > __fadd_rd(m_ref, kPreRescaleLog2 + top);
                         const bool rescale = renew && i > 0 && m_ref != -INFINITY;
-                        const float ref = __fsub_rn(mx, top);
+                        const float ref = C::F16 ? __fsub_rn(mx, top) : mx;
                         if (__any_sync(0xffffffffu, rescale)) {
                             const float corr = rescale ? fast_exp2(m_ref - ref) : 1.f;
 #pragma unroll 1
@@ -800,11 +812,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
-            if (n_units > kPreDrain && !idle) {
-                drain(true, true);
-                tmem_wait_st();
-                __syncwarp();  // every lane has read its part of the place, which may be this piece's
-            }
+            if (n_units > kPreDrain && !idle) drain(true, true);
             if (join && t == 1) {
                 stat[row] = make_float2(m_ref, l);
                 tc_fence_before_sync();
