@@ -636,10 +636,11 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                     // A row's reference follows its maximum when that passes it by too much; O and the sum then change with it.
                     auto follow = [&]() {
                         constexpr float top = C::F16 ? kPreTopF16 : 0.f;
+                        constexpr float most = kPreRescaleLog2 + top - (C::K_PARAMS ? kPreLargeV : 0);
                         // (Rounded one by one: contracted with the product, a difference to a reference of great magnitude would
                         // not be small once the reference has moved.  The sum rounds down, so that past 2^27 no weight passes 2^15.)
                         const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), alpha);
-                        const bool renew = mx > __fadd_rd(m_ref, kPreRescaleLog2 + top);
+                        const bool renew = mx > __fadd_rd(m_ref, most);
                         const bool rescale = renew && i > 0 && m_ref != -INFINITY;
                         const float ref = C::F16 ? __fsub_rn(mx, top) : mx;
                         if (__any_sync(0xffffffffu, rescale)) {
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back (held in
                         // registers they spilled: 350 us against 331 on chunks of 300 tokens); parameters and scores of the
                         // next are under way meanwhile (beside the tensor core's reads of shared memory theirs take long).
-                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p->s0) % C::PST * 1024);
+                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p->s0) % C::PST * C::PAR_BYTES);
                         const float2 qs2 = make_float2(q_sum, q_sum);
                         float4 pr[2][8];  // scales and zeros of two keys each
                         uint32_t x[2][32];
@@ -703,14 +704,22 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
                         tmem_wait_st();
                         follow();
                         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
                         uint32_t pk[kPreKeys / 2];
                         tmem_ld32(s_at, x[0]);
+                        const uint4 large = *reinterpret_cast<const uint4 *>(&par[kPreKeys / 2]);  // 32 keys each, values divided
+                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             tmem_wait_ld();
                             if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
                             weigh(x[h & 1], pk + h * 16, make_float2(-m_use, -m_use));
+                            if (h == 0 ? large.x : h == 1 ? large.y : h == 2 ? large.z : large.w) {
+#pragma unroll
+                                for (int c = h * 16; c < h * 16 + 16; ++c) {
+                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&pk[c]), __half2(__half_raw{0x4c00}, __half_raw{0x4c00}));  // 2^4
+                                    pk[c] = *reinterpret_cast<const uint32_t *>(&y);
+                                }
+                            }
                         }
 #pragma unroll
                         for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));

@@ -8,6 +8,10 @@
 
 namespace gqa {
 
+// 4-bit values may pass fp16's largest (15 scales and a zero: up to 2^20).  32 keys one of whose values may enter the product
+// divided by 2^kPreLargeV, and their weights times that.
+constexpr int kPreLargeV = 4;
+
 template <int DQK, int DV, int SRC>
 struct PrefillCfg {
     static constexpr bool F16 = SRC >= kPreFp8;  // operands: fp16 (codes), else bf16
@@ -22,13 +26,14 @@ struct PrefillCfg {
     // A key's parameters are read until its step's weights are out: when a stage of K is free for the KST-th step after it,
     // the weights of the second step before that one are (one tile an item; of the first with two).
     static constexpr int PST = KST + 2;
+    static constexpr int PAR_BYTES = kPreKeys * 8 + 16;  // scales of two keys and their zeros, 64 times; whether each 32 keys' values are divided
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = 2 * Q_BYTES;
     static constexpr int V_OFF = K_OFF + KST * K_BYTES;
     static constexpr int STAT_OFF = V_OFF + VST * V_BYTES;  // [128] float2: what row group 1 hands over
     static constexpr int PIECE_OFF = STAT_OFF + 1024;       // pieces that are known ahead
-    static constexpr int PAR_OFF = PIECE_OFF + kPrePieces * 64;         // [PST][64] float4: scales of two keys, their zeros
-    static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * 1024 : 0);  // codes of K and of V on their way
+    static constexpr int PAR_OFF = PIECE_OFF + kPrePieces * 64;  // [PST] parameters of a step
+    static constexpr int RAW_OFF = PAR_OFF + (K_PARAMS ? PST * PAR_BYTES : 0);  // codes of K and of V on their way
     static constexpr int RAW_BYTES = !F16 ? 0 : kPreKeys * DV / (SRC == kPreInt4 ? 2 : 1);
     static constexpr int BAR_OFF = RAW_OFF + 2 * RAW_BYTES;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;
@@ -297,14 +302,7 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                     for (int e = 0; e < 4; ++e) {
                         if constexpr (SRC == kPreInt4) {
                             __half2 x = widen_int4(w[u], e);
-                            if constexpr (is_v) {
-                                x = __hfma2(x, vs, vz);
-                                if constexpr (careful) {
-                                    // values past fp16's largest are it; a parameter that is not finite is NaN already
-                                    const __half2 big(__half_raw{0x7bff}, __half_raw{0x7bff});
-                                    x = __hmin2_nan(__hmax2_nan(x, __hneg2(big)), big);
-                                }
-                            }
+                            if constexpr (is_v) x = __hfma2(x, vs, vz);
                             o[e] = *reinterpret_cast<const uint32_t *>(&x);
                         } else {
                             o[e] = widen_pair<SRC>(w[2 * u + (e >> 1)], e & 1);
@@ -345,9 +343,15 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    if ((lane & 1) == 0)
-                        reinterpret_cast<float4 *>(smem + C::PAR_OFF)[at % C::PST * (kPreKeys / 2) + (lw * 32 + lane) / 2] =
-                            make_float4(f.x, scale1, f.y, zero1);
+                    uint8_t *par_at = smem + C::PAR_OFF + at % C::PST * C::PAR_BYTES;
+                    if ((lane & 1) == 0) reinterpret_cast<float4 *>(par_at)[(lw * 32 + lane) / 2] = make_float4(f.x, scale1, f.y, zero1);
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
+                    const bool large = __any_sync(0xffffffffu, fabsf(v.x) * 15.f + fabsf(v.y) > 65504.f);  // (not for NaN)
+                    if (lane == 0) reinterpret_cast<unsigned *>(par_at + kPreKeys * 8)[lw] = large;
+                    if (large) {  // times 2^-4
+                        const __half2 less = __hmul2(*reinterpret_cast<const __half2 *>(&par.y), __half2(__half_raw{0x2c00}, __half_raw{0x2c00}));
+                        par.y = *reinterpret_cast<const uint32_t *>(&less);
+                    }
                 } else {
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
@@ -360,14 +364,8 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                 ok = at < C::VST || mbar_wait_bounded(&v_empty[at % C::VST], (at / C::VST - 1) & 1, limit, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                bool careful = SRC != kPreInt8 && masked(step);
-                if constexpr (SRC == kPreInt4) {  // a value of some key may pass fp16's largest
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
-                    careful |= __any_sync(0xffffffffu, !(fabsf(f.x) * 15.f + fabsf(f.y) <= 65504.f));
-                }
-                if (careful)
-                    store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES,
-                          masked(step) ? p.first_limit - step * kPreKeys : kPreKeys);
+                if (SRC != kPreInt8 && masked(step))
+                    store(std::true_type(), std::true_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, p.first_limit - step * kPreKeys);
                 else
                     store(std::true_type(), std::false_type(), smem + C::V_OFF + at % C::VST * C::V_BYTES, 0);
                 fence_proxy_async_shared();

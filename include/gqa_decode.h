@@ -574,11 +574,12 @@ size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int 
  *   page_size <= 2^31 - 256; the rest, and the workspace, as gqa_prefill.
  * Rounding: bf16 pools as gqa_prefill.  Others: codes enter the products as fp16,
  *   8-bit ones and those of a 4-bit K exactly (scale and zero of a 4-bit K are
- *   applied to the scores), the values of a 4-bit V rounded (2^-11; past 65504
- *   they are that); queries exactly but for elements below 2^-28 of their
- *   row's largest; weights rounded to fp16 (2^-11, and by at most 2^-32 of the
- *   largest where they are small).  A row whose scores pass 2^27 in magnitude may
- *   be NaN.
+ *   applied to the scores), the values of a 4-bit V rounded to fp16 (2^-11, or by
+ *   2^-25 where they are small; by 2^-16 in the tokens 32 i .. 32 i + 31 of a
+ *   request one of whose values may pass 65504); queries exactly but for
+ *   elements below 2^-28 of their row's largest; weights rounded to fp16 (2^-11,
+ *   and by at most 2^-32 of the largest where they are small).  A row whose scores
+ *   pass 2^27 in magnitude may be NaN.
  * Device-checked (GQA_ERR_DEVICE_INDEX): offsets as gqa_prefill; a seq_lens[b]
  *   outside [0, pages_per_req * page_size] is clamped; a token whose page id is
  *   out of range reads as zeros.

@@ -207,3 +207,37 @@ def test_sums_that_leave_the_tensor_core(gq, kind, ps, n, rise):
         ref.check(one, out[at:at + n[b]], lse[at:at + n[b]], untouched=False, what=f"request {b}")
     again = run(gq, d)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+# ------------------------------------------------------------------------------------------------ values past fp16's largest
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,L,Hq,Hkv,D", [([150, 20], [400, 20], 8, 4, 64), ([3, 40], [1500, 700], 16, 2, 128)])
+def test_large_values_of_4_bits(gq, n, L, Hq, Hkv, D, causal):
+    """15 scales and a zero reach 2^20: tokens here and there, fp16's largest parameters among them."""
+    d = ref.make(n, L, Hq, Hkv, D, seed=26, kind="int4")
+    base = run(gq, d, causal)
+    params = d["params"].flatten(0, 1)
+    at = d["rows"][0][100:]
+    for i, (vs, vz) in enumerate([(65504.0, 65504.0), (30000.0, -225000.0 / 15), (65504.0, -65504.0), (4400.0, -500.0), (9000.0, -65504.0), (0.0, 65504.0)]):
+        params[at[i * 41], i % Hkv, 2:] = torch.tensor([vs, vz]).half().cuda()
+    params[d["rows"][1][7], :, 2] = 50000.0
+    d["kv"] = [ref.held(d, r) for r in d["rows"]]
+    assert float(d["kv"][0][1].abs().max()) == 16 * 65504.0
+    out, lse = run(gq, d, causal)
+    assert torch.equal(lse, base[1])
+    t = 0
+    for b, (nb, Lb) in enumerate(zip(n, L)):
+        q, (k, v) = d["q"][t:t + nb].double(), d["kv"][b]
+        want, want_lse, mag, _, v_max = ref.attend(q, k, v, causal)
+        p = params[d["rows"][b]].double()
+        s_mag = q.abs().sum(-1) * (15 * p[..., 0] + p[..., 1].abs()).amax(0).repeat_interleave(Hq // Hkv) / math.sqrt(D)
+        steps, ds = (Lb / 128 + 160) * 2.0 ** -23, (D + 8) * 2.0 ** -23 * s_mag
+        # weights and values are off by 2^-11 each; small weights by 2^-32 of the largest, small values beside a large one by 2^-16
+        rel = 2 * ref.HALF[torch.float16] + 2 * ds + 2.0 ** -20 + 2 * steps
+        bound = 1.01 * (ref.HALF[torch.bfloat16] * want.abs() + rel[..., None] * mag) + (Lb * 2.0 ** -32 * v_max)[..., None] + 2.0 ** -16
+        e = (out[t:t + nb].double() - want).abs()
+        assert bool((e <= bound).all()), f"request {b}: {float((e - bound).max())} past the bound"
+        t += nb
+    if causal and L[0] > n[0]:  # rows that see no large value stay within what they were
+        before = max(0, 96 - (L[0] - n[0]))
+        assert torch.equal(out[:before], base[0][:before])
