@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prefill_plan_small_kernel(cons
     constexpr int WARPS = THREADS / 32, HIST = WARPS * kPlanBuckets, PER = HIST / THREADS;
     __shared__ int hist[WARPS][kPlanBuckets];
     __shared__ PlanSeq seq[THREADS];
+    __shared__ int2 cuts[THREADS + 1];
     __shared__ int tiles[THREADS + 1];
     __shared__ unsigned prefix[THREADS * IPT + 1];
     __shared__ long long sums[33];
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1) gqa_prefill_plan_small_kernel(cons
     }
     if (tid == 0) prefix[n_items] = all;
     __syncthreads();
-    plan_shares<unsigned, THREADS>(a, n_items, top, prefix, reinterpret_cast<int2 *>(seq), sums, isums, &shared_max);
+    plan_shares<unsigned, THREADS>(a, n_items, top, prefix, cuts, sums, isums, &shared_max);
 }
 
 // Any number of them, through the workspace.
