@@ -435,10 +435,6 @@ struct __align__(16) PrefillPiece {
 };
 static_assert(sizeof(PrefillPiece) == 64, "four 16-byte words");
 
-__device__ __forceinline__ int piece_step(const volatile PrefillPiece *p, int u) { return p->s0 + (p->two ? u >> 1 : u); }
-// keys past what some row sees lie in this step
-__device__ __forceinline__ bool piece_masked(const volatile PrefillPiece *p, int step) { return (step + 1) * kPreKeys > p->first_limit; }
-
 __device__ __forceinline__ PrefillPiece piece_of(const PrefillArgs &a, const PrefillItem &it, int h, int s0, int s1, int slot) {
     const int per = a.head_blocks / a.Hkv;
     PrefillPiece p;
