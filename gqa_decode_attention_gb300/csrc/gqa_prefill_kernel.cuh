@@ -58,31 +58,66 @@ __device__ __forceinline__ void tma_load_3d(void *smem_dst, const void *tmap, ui
 }
 
 // Adds to a row's result (bf16 out, or fp32 part) the elements of V's rows key0 .. key1 - 1 that are not finite: the
-// products had zeros there.  (What is added is the value without its scale and weight: infinite or NaN all the same.)
+// products had zeros there.  (What is added is the value without its scale and weight: infinite or NaN all the same.)  Eight
+// elements of eight keys at a time, then into the result: where all of V is NaN a batch of 256 prompts of 128 tokens takes 4.4 ms
+// (element by element into the result 71, which is longer than the least limit of the other warps' waits).
 template <int DV, int SRC, typename T>
 __device__ __noinline__ void prefill_add_not_finite(const PrefillArgs &a, int req, int k_row, int g, int key0, int key1, T *dst) {
-    for (int key = key0; key < key1; ++key) {
-        long long head;
-        if constexpr (SRC != kPreDense) {
-            const int row = prefill_pool_row(a, req, key);
-            if (row < 0) continue;
-            head = (long long)row * a.Hkv + g;
-        }
-        for (int d = 0; d < DV; ++d) {
-            float x;
-            if constexpr (SRC == kPreDense) {
-                x = __bfloat162float(a.v[(long long)(k_row + key) * a.v_stride + g * DV + d]);
-            } else if constexpr (SRC == kPreFp8) {
-                x = (a.v_pool[head * DV + d] & 0x7f) == 0x7f ? NAN : 0.f;
-            } else if constexpr (SRC == kPreInt4) {
-                x = __half2float(a.params[head * 4 + 2]) + __half2float(a.params[head * 4 + 3]);
-            } else if constexpr (SRC == kPreInt8) {
-                x = 0.f;
-            } else {
-                x = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.v_pool)[head * DV + d]);
+    if constexpr (SRC == kPreInt8) return;  // every code is finite
+    constexpr int KEYS = 8, WORDS = SRC == kPreInt4 ? 1 : SRC == kPreFp8 ? 2 : 4;  // keys on their way, words of one's elements
+#pragma unroll 1
+    for (int d = 0; d < DV; d += 8) {
+        float add[8] = {};
+        bool some = false;
+#pragma unroll 1
+        for (int key = key0; key < key1; key += KEYS) {
+            long long at[KEYS];
+            uint32_t w[KEYS][WORDS] = {};
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) {
+                at[i] = -1;
+                if (key + i < key1) at[i] = SRC == kPreDense ? k_row + key + i : prefill_pool_row(a, req, key + i);
             }
-            if (!isfinite(x)) dst[d] = T(float(dst[d]) + (SRC == kPreInt4 ? NAN : x));
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) {
+                if (at[i] < 0) continue;
+                const long long head = at[i] * a.Hkv + g;
+                if constexpr (SRC == kPreInt4) {
+                    w[i][0] = reinterpret_cast<const uint32_t *>(a.params)[head * 2 + 1];
+                } else if constexpr (SRC == kPreFp8) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(a.v_pool + head * DV + d);
+                    w[i][0] = x.x, w[i][1] = x.y;
+                } else {
+                    const __nv_bfloat16 *v = SRC == kPreDense ? a.v + at[i] * a.v_stride + g * DV : reinterpret_cast<const __nv_bfloat16 *>(a.v_pool) + head * DV;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(v + d);
+                    w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                }
+            }
+            bool found = false;
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i)
+#pragma unroll
+                for (int x = 0; x < WORDS; ++x)
+                    found |= SRC == kPreFp8 ? __vcmpeq4(w[i][x] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0 : not_finite2<SRC == kPreInt4>(w[i][x]);
+            if (!found) continue;
+            some = true;
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if constexpr (SRC == kPreInt4) {
+                        if (not_finite2<true>(w[i][0])) add[e] = NAN;
+                    } else if constexpr (SRC == kPreFp8) {
+                        if ((w[i][e >> 2] >> (e & 3) * 8 & 0x7f) == 0x7f) add[e] = NAN;
+                    } else {
+                        const float f = __uint_as_float(e & 1 ? w[i][e >> 1] & 0xffff0000u : w[i][e >> 1] << 16);
+                        if (!isfinite(f)) add[e] += f;
+                    }
+                }
         }
+        if (!some) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dst[d + e] = T(float(dst[d + e]) + add[e]);
     }
 }
 

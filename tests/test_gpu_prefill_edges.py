@@ -241,3 +241,49 @@ def test_large_values_of_4_bits(gq, n, L, Hq, Hkv, D, causal):
     if causal and L[0] > n[0]:  # rows that see no large value stay within what they were
         before = max(0, 96 - (L[0] - n[0]))
         assert torch.equal(out[:before], base[0][:before])
+
+
+# ------------------------------------------------------------------------------------------------ V that is not finite
+@pytest.mark.parametrize("kind,ps", [("bf16", 16), ("bf16", 7), ("fp8", 16), ("int4", 16)])
+def test_values_of_nan_under_the_least_wait_limit(gq, kind, ps):
+    """Every element of V is NaN: rows get theirs back in the epilogue, which must not take so long that the warps that wait for
+    it give up (many items an SM, each of short keys, and the least limit that can be set)."""
+    d = ref.make([256] * 4, [256] * 4, 8, 8, 128, seed=27, kind=kind, ps=ps)
+    if kind == "int4":
+        d["params"][..., 2] = math.nan
+    else:
+        d["v_pool"].fill_(127 if kind == "fp8" else math.nan)
+    B = 300
+    d["q"] = torch.cat([d["q"][:1024]] * (B // 4))
+    e = dict(d, cu=(torch.arange(B + 1) * 256).int().cuda(), table=d["table"].repeat(B // 4, 1), lens=d["lens"].repeat(B // 4))
+    gq.gqa_set_wait_limit_ns(1)  # raised to 1 ms
+    try:
+        out, lse = run(gq, e)
+    finally:
+        gq.gqa_set_wait_limit_ns(0)
+    assert torch.isnan(out).all()
+    for b in range(4):
+        want = ref.attend(d["q"][256 * b:256 * b + 256].double(), d["kv"][b][0], torch.zeros_like(d["kv"][b][0]), True)[1]
+        assert bool(((lse[256 * b:256 * b + 256].double() - want).abs() < 1e-4).all())
+    assert torch.equal(lse, lse[:1024].repeat(B // 4, 1))
+
+
+@pytest.mark.parametrize("kind", ["dense", "bf16", "fp8"])
+def test_some_values_not_finite(gq, kind):
+    """Single elements in the last tokens, each sign and NaN: they reach that element of the rows that see them."""
+    L = [200, 60]
+    d = ref.make(L, L, 8, 4, 64, seed=28, kind=kind)
+    base = run(gq, d)
+    bad = [(150, 1, 3, math.inf), (151, 1, 3, -math.inf), (160, 2, 63, -math.inf), (161, 3, 8, math.nan), (199, 0, 0, math.inf), (170, 2, 62, math.inf)]
+    want = base[0][:200].float().clone()
+    for t, g, e, x in bad:
+        x = math.nan if kind == "fp8" else x
+        if kind == "dense":
+            d["v"][t, g, e] = x
+        else:
+            d["v_pool"].flatten(0, 1)[d["rows"][0][t], g, e] = 127 if kind == "fp8" else x
+        want[t:, 2 * g:2 * g + 2, e] += x
+    out, lse = run(gq, d)
+    assert torch.equal(lse, base[1]) and torch.equal(out[200:], base[0][200:])
+    got = out[:200].float()
+    assert torch.equal(torch.nan_to_num(got, nan=9e9), torch.nan_to_num(want, nan=9e9))
