@@ -44,8 +44,8 @@ constexpr float kPreRescaleLog2 = 8.f, kPreTopF16 = 7.f;
 // Steps of a row group after which its O goes to global memory, in fp32, and starts anew.  The tensor core cuts a product off some
 // 2^-25 below the sum that it is added to: over 2^20 keys values of one sign came out 0.7 % small, and the others' part was
 // missing where one key's weight was 2^25 times theirs.  Over 256 steps that is 2^-10 of the sum at most.  Items of up to 32K keys
-// never come to it.  It takes some 6 us, as all SMs move their 128 KB at about the same time (2K rows over 128K keys: every 128
-// steps 5790 us, every 256 5710, never 5600).
+// never come to it.  It takes some 6 us, as all SMs move their 128 KB at about the same time (2K rows over 128K keys: every 256
+// steps 5690 us, every 128 some 60 more, never 5610).
 constexpr int kPreDrain = 256;
 static_assert((kPreDrain & (kPreDrain - 1)) == 0 && kPreDrain > kPreMinSplit + kPreSnap, "only items with room for partial results");
 
@@ -185,14 +185,18 @@ __device__ __forceinline__ uint4 prefill_q_unit(uint4 x, float scale) {
     return make_uint4(pack_f16x2(f[0], f[1]), pack_f16x2(f[2], f[3]), pack_f16x2(f[4], f[5]), pack_f16x2(f[6], f[7]));
 }
 
-// A row group's O (at o_at, a thread a row) goes to global memory, added to `corr` times what is there (some); last: that sum goes
-// back into O instead.  The place is the warp's rows of the worker's last place for partial results, which nothing else uses
-// before the epilogue of the worker's last piece; four elements of each of 32 rows in turn, so that a warp's accesses are whole
-// lines.  (Not inline: two copies in the softmax's code cost short items 4 %.)
+// A row group's O (at o_at, a thread a row) goes to global memory with the row's reference, added to what is there (some); last:
+// that sum goes back into O instead.  The place is the warp's rows of the worker's last place for partial results, which nothing
+// else uses before the epilogue of the worker's last piece; four elements of each of 32 rows in turn, so that a warp's
+// accesses are whole lines.  (Not inline: two copies in the softmax's code cost short items 4 %.)
 template <int DV>
-__device__ __noinline__ void prefill_drain(const PrefillArgs &a, uint32_t o_at, int t, float corr, bool some, bool last) {
-    float4 *at = reinterpret_cast<float4 *>(a.o_part + ((2LL * blockIdx.x + 1) * 2 + t) * kPreTile * DV + (threadIdx.x >> 5 & 3) * 32 * DV) +
-                 (threadIdx.x & 31);
+__device__ __noinline__ void prefill_drain(const PrefillArgs &a, uint32_t o_at, int t, float m_ref, bool some, bool last) {
+    const long long place = ((2LL * blockIdx.x + 1) * 2 + t) * kPreTile + (threadIdx.x >> 5 & 3) * 32;  // of the warp's rows
+    float4 *at = reinterpret_cast<float4 *>(a.o_part + place * DV) + (threadIdx.x & 31);
+    float *ref = a.lse_part + place + (threadIdx.x & 31);
+    float corr = 1.f;
+    if (some && *ref != m_ref) corr = fast_exp2(*ref - m_ref);
+    if (!last) *ref = m_ref;
 #pragma unroll 1
     for (int c = 0; c < DV; c += 64) {
         uint32_t ov[2][32];
@@ -626,219 +630,235 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             }
             if (alpha < 1e-37f) alpha = 1e-37f;  // a scale of zero must not make NaN of a masked score
             float m_ref = -INFINITY, l = 0.f;  // reference (log2 domain), sum of the weights
-            float m_out = -INFINITY;           // the reference of what has left O
-            auto drain = [&](bool some, bool last) {
-                prefill_drain<DV>(a, lane_base + C::O_COL + t * DV, t, !some || m_out == m_ref ? 1.f : fast_exp2(m_out - m_ref), some, last);
-                m_out = m_ref;
-            };
-            for (int i = 0; i < n_units; ++i) {
-                ok = mbar_wait_bounded(&s_full[t], s_phase, limit, abort_flag);
-                s_phase ^= 1;
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (!idle) {
-                    tc_fence_after_sync();
-                    if (i > 0 && (i & (kPreDrain - 1)) == 0) drain(i > kPreDrain, false);
-                    const int step = p->s0 + (p->two ? i : 2 * i + t), key0 = step * kPreKeys;
-                    const bool masked = key0 + kPreKeys > all_see;
-                    const int left = seen - key0;
-                    float m4[4];
-                    // Scores stay raw: the scale enters through the maximum (exact: it is positive) and one fma a weight.
-                    auto hide = [&](uint32_t (&x)[32], int h) {
-                        const int n = left - h * 32;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c >= n) x[c] = __float_as_uint(-INFINITY);
-                    };
-                    auto maximum = [&](const uint32_t (&x)[32]) {  // four chains of three-input maxima (exact)
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2)
-                            m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                    };
-                    float2 sum2[2];
-                    // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in fp32
-                    // before they are rounded for the product
-                    const float2 al2 = make_float2(alpha, alpha);
-                    auto weigh = [&](const uint32_t (&x)[32], uint32_t *pk, float2 nm2) {
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), al2, nm2);
-                            const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], w);
-                            pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
-                        }
-                    };
-                    // A row's reference follows its maximum when that passes it by too much; O and the sum then change with it.
-                    auto follow = [&]() {
-                        constexpr float top = C::F16 ? kPreTopF16 : 0.f;
-                        constexpr float most = kPreRescaleLog2 + top - (C::K_PARAMS ? kPreLargeV : 0);
-                        // (Rounded one by one: contracted with the product, a difference to a reference of great magnitude would
-                        // not be small once the reference has moved.  The sum rounds down, so that past 2^27 no weight passes 2^15.)
-                        const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), alpha);
-                        const bool renew = mx > __fadd_rd(m_ref, most);
-                        const bool rescale = renew && i > 0 && m_ref != -INFINITY;
-                        const float ref = C::F16 ? __fsub_rn(mx, top) : mx;
-                        if (__any_sync(0xffffffffu, rescale)) {
-                            const float corr = rescale ? fast_exp2(m_ref - ref) : 1.f;
+            for (int first = 0; ok && first < n_units; first += kPreDrain) {
+                if (first > 0) {  // (a look at the next step's scores, which the loop below waits for)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[t], s_phase, limit, abort_flag));
+                    if (!ok) break;
+                    if (!idle) {
+                        tc_fence_after_sync();
+                        prefill_drain<DV>(a, lane_base + C::O_COL + t * DV, t, m_ref, first > kPreDrain, false);
+                    }
+                }
+                const int stop = min(n_units, first + kPreDrain);
 #pragma unroll 1
-                            for (int c = 0; c < DV / 32; ++c) {
-                                uint32_t ov[32];
-                                tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                for (int i = first; i < stop; ++i) {
+                    ok = mbar_wait_bounded(&s_full[t], s_phase, limit, abort_flag);
+                    s_phase ^= 1;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (!idle) {
+                        tc_fence_after_sync();
+                        const int step = p->s0 + (p->two ? i : 2 * i + t), key0 = step * kPreKeys;
+                        const bool masked = key0 + kPreKeys > all_see;
+                        const int left = seen - key0;
+                        float m4[4];
+                        // Scores stay raw: the scale enters through the maximum (exact: it is positive) and one fma a weight.
+                        auto hide = [&](uint32_t (&x)[32], int h) {
+                            const int n = left - h * 32;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c >= n) x[c] = __float_as_uint(-INFINITY);
+                        };
+                        auto maximum = [&](const uint32_t (&x)[32]) {  // four chains of three-input maxima (exact)
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2)
+                                m4[(c >> 1) & 3] = fmax3(m4[(c >> 1) & 3], __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        };
+                        float2 sum2[2];
+                        // weights exp2(alpha s - reference), two keys at a time (each lane rounded as fmaf would), summed in fp32
+                        // before they are rounded for the product
+                        const float2 al2 = make_float2(alpha, alpha);
+                        auto weigh = [&](const uint32_t (&x)[32], uint32_t *pk, float2 nm2) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float2 y = fma2(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), al2, nm2);
+                                const float2 w = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                                sum2[(c >> 1) & 1] = add2(sum2[(c >> 1) & 1], w);
+                                pk[c / 2] = C::F16 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+                            }
+                        };
+                        // A row's reference follows its maximum when that passes it by too much; O and the sum then change with it.
+                        auto follow = [&]() {
+                            constexpr float top = C::F16 ? kPreTopF16 : 0.f;
+                            constexpr float most = kPreRescaleLog2 + top - (C::K_PARAMS ? kPreLargeV : 0);
+                            // (Rounded one by one: contracted with the product, a difference to a reference of great magnitude would
+                            // not be small once the reference has moved.  The sum rounds down, so that past 2^27 no weight passes 2^15.)
+                            const float mx = __fmul_rn(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), alpha);
+                            const bool renew = mx > __fadd_rd(m_ref, most);
+                            const bool rescale = renew && i > 0 && m_ref != -INFINITY;
+                            const float ref = C::F16 ? __fsub_rn(mx, top) : mx;
+                            if (__any_sync(0xffffffffu, rescale)) {
+                                const float corr = rescale ? fast_exp2(m_ref - ref) : 1.f;
+#pragma unroll 1
+                                for (int c = 0; c < DV / 32; ++c) {
+                                    uint32_t ov[32];
+                                    tmem_ld32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) {
+                                        const float2 o2 = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
+                                                               make_float2(corr, corr));
+                                        ov[e] = __float_as_uint(o2.x);
+                                        ov[e + 1] = __float_as_uint(o2.y);
+                                    }
+                                    tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                                }
+                                l *= corr;
+                            }
+                            if (renew) m_ref = ref;
+                            return renew;
+                        };
+                        if constexpr (C::K_PARAMS) {
+                            // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back (held in
+                            // registers they spilled: 350 us against 331 on chunks of 300 tokens); parameters and scores of the
+                            // next are under way meanwhile (beside the tensor core's reads of shared memory theirs take long).
+                            const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p->s0) % C::PST * C::PAR_BYTES);
+                            const float2 qs2 = make_float2(q_sum, q_sum);
+                            float4 pr[2][8];  // scales and zeros of two keys each
+                            uint32_t x[2][32];
+                            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+                            tmem_ld32(s_at, x[0]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) pr[0][e] = par[e];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
                                 tmem_wait_ld();
+                                if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
+                                uint32_t (&y)[32] = x[h & 1];
 #pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    const float2 o2 = mul2(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])),
-                                                           make_float2(corr, corr));
-                                    ov[e] = __float_as_uint(o2.x);
-                                    ov[e + 1] = __float_as_uint(o2.y);
+                                for (int half = 0; half < 2; ++half) {
+                                    if (h < 3 || half == 0) {
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) pr[(half + 1) & 1][e] = par[(h * 2 + half + 1) * 8 + e];
+                                    }
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) {
+                                        const float4 z = pr[half][e];
+                                        const int c = half * 16 + 2 * e;
+                                        const float2 v = fma2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(z.x, z.y),
+                                                              mul2(qs2, make_float2(z.z, z.w)));
+                                        y[c] = __float_as_uint(v.x);
+                                        y[c + 1] = __float_as_uint(v.y);
+                                    }
                                 }
-                                tmem_st32(lane_base + C::O_COL + t * DV + c * 32, ov);
+                                if (masked) hide(y, h);
+                                maximum(y);
+                                tmem_st32(s_at + h * 32, y);
                             }
-                            l *= corr;
-                        }
-                        if (renew) m_ref = ref;
-                        return renew;
-                    };
-                    if constexpr (C::K_PARAMS) {
-                        // Scale and zero of the keys applied first, 32 keys after the other, and the scores put back (held in
-                        // registers they spilled: 350 us against 331 on chunks of 300 tokens); parameters and scores of the
-                        // next are under way meanwhile (beside the tensor core's reads of shared memory theirs take long).
-                        const float4 *par = reinterpret_cast<const float4 *>(smem + C::PAR_OFF + (par_at + step - p->s0) % C::PST * C::PAR_BYTES);
-                        const float2 qs2 = make_float2(q_sum, q_sum);
-                        float4 pr[2][8];  // scales and zeros of two keys each
-                        uint32_t x[2][32];
-                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
-                        tmem_ld32(s_at, x[0]);
+                            tmem_wait_st();
+                            follow();
+                            const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                            uint32_t pk[kPreKeys / 2];
+                            tmem_ld32(s_at, x[0]);
+                            sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) pr[0][e] = par[e];
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            tmem_wait_ld();
-                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
-                            uint32_t (&y)[32] = x[h & 1];
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                if (h < 3 || half == 0) {
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) pr[(half + 1) & 1][e] = par[(h * 2 + half + 1) * 8 + e];
-                                }
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float4 z = pr[half][e];
-                                    const int c = half * 16 + 2 * e;
-                                    const float2 v = fma2(make_float2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), make_float2(z.x, z.y),
-                                                          mul2(qs2, make_float2(z.z, z.w)));
-                                    y[c] = __float_as_uint(v.x);
-                                    y[c + 1] = __float_as_uint(v.y);
-                                }
+                            for (int h = 0; h < 4; ++h) {
+                                tmem_wait_ld();
+                                if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
+                                weigh(x[h & 1], pk + h * 16, make_float2(-m_use, -m_use));
                             }
-                            if (masked) hide(y, h);
-                            maximum(y);
-                            tmem_st32(s_at + h * 32, y);
-                        }
-                        tmem_wait_st();
-                        follow();
-                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                        uint32_t pk[kPreKeys / 2];
-                        tmem_ld32(s_at, x[0]);
-                        const uint4 large = *reinterpret_cast<const uint4 *>(&par[kPreKeys / 2]);  // 32 keys each, values divided
-                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            tmem_wait_ld();
-                            if (h < 3) tmem_ld32(s_at + (h + 1) * 32, x[(h + 1) & 1]);
-                            weigh(x[h & 1], pk + h * 16, make_float2(-m_use, -m_use));
-                            if (h == 0 ? large.x : h == 1 ? large.y : h == 2 ? large.z : large.w) {
-#pragma unroll
-                                for (int c = h * 16; c < h * 16 + 16; ++c) {
-                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&pk[c]), __half2(__half_raw{0x4c00}, __half_raw{0x4c00}));  // 2^4
-                                    pk[c] = *reinterpret_cast<const uint32_t *>(&y);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
-                    } else if (masked) {
-                        // 32 keys after the other, those that no row of the warp sees left out (in short prompts half of them):
-                        // the maximum, then the weights from scores read once more
-                        const int most = most_see - key0;
-                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+                            for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                            // 32 keys each whose values are divided: their weights once more, times 2^4 (in the loop above, or in
+                            // registers behind it, this cost every step 3 to 6 %)
+                            const unsigned large = *reinterpret_cast<const unsigned *>(&par[kPreKeys / 2]);
+                            if (large != 0) {
+                                tmem_wait_st();
 #pragma unroll 1
-                        for (int h = 0; h * 32 < min(most, kPreKeys); ++h) {
-                            uint32_t x[32];
-                            tmem_ld32(s_at + h * 32, x);
-                            tmem_wait_ld();
-                            hide(x, h);
-                            maximum(x);
-                        }
-                        follow();
-                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+                                for (int h = 0; h < 2; ++h) {
+                                    tmem_ld32(s_at + h * 32, x[0]);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) {
+                                        const __half2 by = __float2half2_rn(large >> (h * 16 + c / 16 * 8) & 1 ? 16.f : 1.f);
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[0][c]), by);
+                                        x[0][c] = *reinterpret_cast<const uint32_t *>(&y);
+                                    }
+                                    tmem_st32(s_at + h * 32, x[0]);
+                                }
+                            }
+                        } else if (masked) {
+                            // 32 keys after the other, those that no row of the warp sees left out (in short prompts half of them):
+                            // the maximum, then the weights from scores read once more
+                            const int most = most_see - key0;
+                            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
 #pragma unroll 1
-                        for (int h = 0; h < kPreKeys / 32; ++h) {
-                            uint32_t w[16] = {};
-                            if (h * 32 < most) {
+                            for (int h = 0; h * 32 < min(most, kPreKeys); ++h) {
                                 uint32_t x[32];
                                 tmem_ld32(s_at + h * 32, x);
                                 tmem_wait_ld();
                                 hide(x, h);
-                                weigh(x, w, make_float2(-m_use, -m_use));
+                                maximum(x);
                             }
-                            tmem_st16(s_at + h * 16, w);  // (columns whose scores have been read)
-                        }
-                    } else if constexpr (C::TMA) {
-                        // a row's scores in registers: the maximum, then the weights
-                        uint32_t pk[kPreKeys / 2];
-                        uint32_t sr[4][32];
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
-                        tmem_wait_ld();
-                        m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            maximum(sr[h]);
-                        }
-                        follow();
-                        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                        sum2[0] = sum2[1] = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            weigh(sr[h], pk + h * 16, make_float2(-m_use, -m_use));
-                        }
-                        // All of them at the end: a store holds its registers for some 180 cycles, which stores between the
-                        // pieces would wait for.
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
-                    } else {
-                        // Registers for half of them: maximum and weights in one pass with the reference as it is, once more in the
-                        // few steps whose maximum passes it (read a second time for the weights always: mixed step over an FP8
-                        // cache 1652 us against 1243).
-                        uint32_t pk[kPreKeys / 2];
-#pragma unroll 1
-                        for (int pass = 0; pass < 2; ++pass) {
+                            follow();
                             const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                            const float2 nm2 = make_float2(-m_use, -m_use);
-                            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
                             sum2[0] = sum2[1] = make_float2(0.f, 0.f);
-                            uint32_t sr[2][32];
-                            tmem_ld32(s_at, sr[0]);
+#pragma unroll 1
+                            for (int h = 0; h < kPreKeys / 32; ++h) {
+                                uint32_t w[16] = {};
+                                if (h * 32 < most) {
+                                    uint32_t x[32];
+                                    tmem_ld32(s_at + h * 32, x);
+                                    tmem_wait_ld();
+                                    hide(x, h);
+                                    weigh(x, w, make_float2(-m_use, -m_use));
+                                }
+                                tmem_st16(s_at + h * 16, w);  // (columns whose scores have been read)
+                            }
+                        } else if constexpr (C::TMA) {
+                            // a row's scores in registers: the maximum, then the weights
+                            uint32_t pk[kPreKeys / 2];
+                            uint32_t sr[4][32];
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tmem_ld32(s_at + h * 32, sr[h]);
+                            tmem_wait_ld();
+                            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
 #pragma unroll
                             for (int h = 0; h < 4; ++h) {
-                                tmem_wait_ld();
-                                if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) & 1]);
-                                maximum(sr[h & 1]);
-                                weigh(sr[h & 1], pk + h * 16, nm2);
+                                maximum(sr[h]);
                             }
-                            if (!__any_sync(0xffffffffu, follow())) break;
-                        }
+                            follow();
+                            const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                            sum2[0] = sum2[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                            for (int h = 0; h < 4; ++h) {
+                                weigh(sr[h], pk + h * 16, make_float2(-m_use, -m_use));
+                            }
+                            // All of them at the end: a store holds its registers for some 180 cycles, which stores between the
+                            // pieces would wait for.
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                        } else {
+                            // Registers for half of them: maximum and weights in one pass with the reference as it is, once more in the
+                            // few steps whose maximum passes it (read a second time for the weights always: mixed step over an FP8
+                            // cache 1652 us against 1243).
+                            uint32_t pk[kPreKeys / 2];
+#pragma unroll 1
+                            for (int pass = 0; pass < 2; ++pass) {
+                                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                                const float2 nm2 = make_float2(-m_use, -m_use);
+                                m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+                                sum2[0] = sum2[1] = make_float2(0.f, 0.f);
+                                uint32_t sr[2][32];
+                                tmem_ld32(s_at, sr[0]);
+#pragma unroll
+                                for (int h = 0; h < 4; ++h) {
+                                    tmem_wait_ld();
+                                    if (h < 3) tmem_ld32(s_at + (h + 1) * 32, sr[(h + 1) & 1]);
+                                    maximum(sr[h & 1]);
+                                    weigh(sr[h & 1], pk + h * 16, nm2);
+                                }
+                                if (!__any_sync(0xffffffffu, follow())) break;
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<const uint32_t (*)[32]>(&pk[h * 32]));
+                        }
+                        tmem_wait_st();
+                        l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
+                        tc_fence_before_sync();
                     }
-                    tmem_wait_st();
-                    l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
-                    tc_fence_before_sync();
+                    mbar_arrive(&p_full[t]);
                 }
-                mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
             par_at += p->s1 - p->s0;
@@ -856,7 +876,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, SRC>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after_sync();
-            if (n_units > kPreDrain && !idle) drain(true, true);
+            if (n_units > kPreDrain && !idle) prefill_drain<DV>(a, lane_base + C::O_COL + t * DV, t, m_ref, true, true);
             if (join && t == 1) {
                 stat[row] = make_float2(m_ref, l);
                 tc_fence_before_sync();

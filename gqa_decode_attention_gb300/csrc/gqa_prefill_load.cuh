@@ -26,7 +26,7 @@ struct PrefillCfg {
     // A key's parameters are read until its step's weights are out: when a stage of K is free for the KST-th step after it,
     // the weights of the second step before that one are (one tile an item; of the first with two).
     static constexpr int PST = KST + 2;
-    static constexpr int PAR_BYTES = kPreKeys * 8 + 16;  // scales of two keys and their zeros, 64 times; whether each 32 keys' values are divided
+    static constexpr int PAR_BYTES = kPreKeys * 8 + 16;  // scales of two keys and their zeros, 64 times; a byte for each 32 keys: values divided
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = 2 * Q_BYTES;
     static constexpr int V_OFF = K_OFF + KST * K_BYTES;
@@ -339,19 +339,19 @@ __device__ __forceinline__ bool prefill_load(const PrefillArgs &a, uint8_t *smem
                     if ((par.y & 0x7c00u) == 0x7c00u || (par.y & 0x7c000000u) == 0x7c000000u) par.y = 0x7fff7fffu;
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&par.x));
                     const float scale1 = __shfl_down_sync(0xffffffffu, f.x, 1), zero1 = __shfl_down_sync(0xffffffffu, f.y, 1);
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
+                    const bool large = __any_sync(0xffffffffu, fabsf(v.x) * 15.f + fabsf(v.y) > 65504.f);  // (not for NaN)
+                    if (large) {  // times 2^-4
+                        const __half2 less = __hmul2(*reinterpret_cast<const __half2 *>(&par.y), __half2(__half_raw{0x2c00}, __half_raw{0x2c00}));
+                        par.y = *reinterpret_cast<const uint32_t *>(&less);
+                    }
                     // (the ring of parameters is free when the stage of K is, see PST)
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     uint8_t *par_at = smem + C::PAR_OFF + at % C::PST * C::PAR_BYTES;
                     if ((lane & 1) == 0) reinterpret_cast<float4 *>(par_at)[(lw * 32 + lane) / 2] = make_float4(f.x, scale1, f.y, zero1);
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&par.y));
-                    const bool large = __any_sync(0xffffffffu, fabsf(v.x) * 15.f + fabsf(v.y) > 65504.f);  // (not for NaN)
-                    if (lane == 0) reinterpret_cast<unsigned *>(par_at + kPreKeys * 8)[lw] = large;
-                    if (large) {  // times 2^-4
-                        const __half2 less = __hmul2(*reinterpret_cast<const __half2 *>(&par.y), __half2(__half_raw{0x2c00}, __half_raw{0x2c00}));
-                        par.y = *reinterpret_cast<const uint32_t *>(&less);
-                    }
+                    if (lane == 0) par_at[kPreKeys * 8 + lw] = large;
                 } else {
                     ok = at < C::KST || mbar_wait_bounded(&k_empty[at % C::KST], (at / C::KST - 1) & 1, limit, abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
