@@ -805,7 +805,8 @@ def gqa_prefill_workspace_bytes(Tq, B, Hq, Hkv, Dqk, Dv) -> int:
 def gqa_prefill_paged(q, k_pool, v_pool, page_table, seq_lens, cu_tokens=None, out=None, lse=None, causal=True,
                       scale=None, kv_params=None, k_scale=1.0, v_scale=1.0, k_scales=None, v_scales=None, workspace=None,
                       stream=None, with_lse=True):
-    """Attention of new tokens over the paged cache that holds them, any number of tokens a request.
+    """Attention of new tokens over the paged cache that holds them, any number of tokens a request.  (Single tokens alone
+    over an FP8, int8 or 4-bit cache: gqa_decode_paged and gqa_decode_paged_int4 are 1.7 to 5 times faster.)
 
     q [T,Hq,D] bf16 with a free token stride; cu_tokens int32 [B+1]: request b owns rows cu_tokens[b] ..
     cu_tokens[b+1]-1 (None: T / B each); seq_lens int32 [B] counts the new tokens too.  causal: row i of n sees the

@@ -23,11 +23,15 @@
 //
 // Two tiles because one chain of scores, softmax (1.4K cycles a step), weights and output leaves the tensor core (1K cycles a
 // step and tile at d 128) idle more than half of the time; 128 keys a step because S, P and O of both tiles then fill TMEM.
-// Measured (64/8 heads of 128, GB300): one causal prompt of 16K tokens 2.63 ms = 1.67 PFLOP/s, 2K rows over 128K bf16 keys
-// 5.08 ms = 1.72 PFLOP/s, of 1.89 PFLOP/s measured for a large library product (tensor pipe 69 % active at 8K tokens; its
-// clock stays at 1.95 GHz); 8 rows for each of 16 requests of 8K-32K keys 206 us in the kernel = 6.45 TB/s (HBM); a mixed step
-// over an FP8 cache 1.14 ms = 1.14 PFLOP/s (the converting warps, 2.6K cycles a step).  Short items are bound by their chain:
-// some 8K cycles beside their steps, of which the epilogue is 5K.
+// Measured (GB300; a call alone after an L2 flush, and in brackets among others, where the power limit holds the long ones; of
+// 1.89 PFLOP/s measured for a large library product).  64/8 heads of 128: one causal prompt of 16K tokens 2.64 (2.76-2.89) ms =
+// 1.67 (1.53-1.59) PFLOP/s, 2K rows over 128K bf16 keys 5.12 (5.52-5.71) ms = 1.70 (1.53-1.58) PFLOP/s; the tensor pipe is 69 %
+// active at 8K tokens; 8 rows for each of 16 requests of 8K-32K keys 240 (226) us, 206 in the kernel = 6.45 TB/s (HBM); a
+// mixed step over an FP8 cache 1.23 (1.15-1.18) ms = 1.1 PFLOP/s (the converting warps, 2.6K cycles a step).  Short items are bound
+// by their chain: some 8K cycles beside their steps, of which the epilogue is 5K.  At d 64 a step's products halve and its
+// softmax does not: one prompt of 8K tokens 658 (611) us = 0.84-0.89 PFLOP/s.  Single tokens over codes convert every code for a
+// tile that is a sixteenth full: 32 tokens over 16K-32K keys FP8 459 (451) us, 4 bits 750 (745), where the paged decode calls
+// take 273 and 141-146.
 #pragma once
 
 #include "gqa_prefill_load.cuh"

@@ -18,9 +18,10 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBuckets = 64;
 constexpr int kPlanExactRounds = 64;  // whose sums every worker works out for itself
 
-// A step's cost with two tiles and with one, and what an item costs beside its steps.  Measured (us a call; 24 chunks of up to
-// 256 tokens over an int8 cache, mixed step over an FP8 cache): 4, 3 and 4 88 and 1135, 4, 3 and 12 76 and 1129, 4, 4 and 4 91 and
-// 1201, 4, 2 and 8 80 and 1184.
+// A step's cost with two tiles and with one, and what an item costs beside its steps, for all types and head sizes alike (a 4-bit step
+// takes twice a bf16 one, one of d 64 less than one of d 128; only the balance is at stake).  Measured on two (us a call; 24 chunks of
+// up to 256 tokens over an int8 cache, mixed step over an FP8 cache): 4, 3 and 4 88 and 1135, 4, 3 and 12 76 and 1129, 4, 4 and 4
+// 91 and 1201, 4, 2 and 8 80 and 1184.
 constexpr int kPreCostTwo = 4, kPreCostOne = 3, kPreCostItem = 12;
 
 // First and one past the last row of sequence b, clamped into [0, total].

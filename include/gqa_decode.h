@@ -535,7 +535,9 @@ gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const void *v_pool
  * (Dqk, Dv): (64, 64), (128, 128), (192, 128).  scale <= 0 or NaN selects
  *   1 / sqrt(Dqk).
  * Rounding: weights are rounded to bf16 (2^-8 of each at most, relative to a
- *   reference within 2^8 of the row's largest); their sum is not; sums are fp32.
+ *   reference within 2^8 of the row's largest); their sum is not; sums are fp32,
+ *   where a product loses what lies some 2^-25 below the sum over at most 32K
+ *   keys that it is added to.
  * Limits: Tq, Tk >= 0; Tk <= 2^31 - 256; B <= 65535; Hq / Hkv <= 4096; Tq * Hq
  *   < 2^31.
  * Workspace: NULL = library pool, allocated stream-ordered; otherwise device
@@ -557,6 +559,9 @@ size_t gqa_prefill_workspace_bytes(int Tq, int B, int Hq, int Hkv, int Dqk, int 
 /* ------------------------------------------------------------------------
  * Attention of new tokens over the paged cache that holds them: a chunk of a
  * prompt, draft tokens to check, or the one token of a decode step, in any mix.
+ * (A batch of single tokens alone over coded pools is faster through the decode
+ * calls: 32 tokens over 16K to 32K keys in FP8 273 us, here 451; in 4 bits
+ * 141 to 146, here 745.)
  *
  * gqa_prefill's operation with the keys in a paged cache: request b has the
  * query rows cu_tokens[b] .. cu_tokens[b+1]-1 (NULL: T / B each) and L_b =

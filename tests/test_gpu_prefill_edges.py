@@ -287,3 +287,23 @@ def test_some_values_not_finite(gq, kind):
     assert torch.equal(lse, base[1]) and torch.equal(out[200:], base[0][200:])
     got = out[:200].float()
     assert torch.equal(torch.nan_to_num(got, nan=9e9), torch.nan_to_num(want, nan=9e9))
+
+
+@pytest.mark.parametrize("D,Dv", [(64, 64), (128, 128), (192, 128)])
+def test_packed_sums_that_leave_the_tensor_core(gq, D, Dv):
+    """The same over packed keys, in a workspace of NaN, called and as a captured graph."""
+    n, L, Hq, Hkv = [1500], [70000], 16, 2
+    d = ref.make(n, L, Hq, Hkv, D, seed=29, Dv=Dv)
+    need = gq.gqa_prefill_workspace_bytes(d["q"].shape[0], 1, Hq, Hkv, D, Dv)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = run(gq, d, workspace=ws)
+    ref.check(d, out, lse)
+    got = torch.full_like(out, -7.0), torch.full_like(lse, -7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ref.call(gq, d, workspace=ws, out=got[0], lse=got[1])
+    ws.fill_(255)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert gq.gqa_device_status() == 0
+    assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
