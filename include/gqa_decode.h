@@ -537,7 +537,8 @@ gqa_status gqa_paged_gather(int kv_dtype, const void *k_pool, const void *v_pool
  * Rounding: weights are rounded to bf16 (2^-8 of each at most, relative to a
  *   reference within 2^8 of the row's largest); their sum is not; sums are fp32,
  *   where a product loses what lies some 2^-25 below the sum over at most 32K
- *   keys that it is added to.
+ *   keys that it is added to.  A row whose scores pass 2^30 in magnitude may be
+ *   NaN.
  * Limits: Tq, Tk >= 0; Tk <= 2^31 - 256; B <= 65535; Hq / Hkv <= 4096; Tq * Hq
  *   < 2^31.
  * Workspace: NULL = library pool, allocated stream-ordered; otherwise device
